@@ -86,6 +86,11 @@ extern "C" {
 #define DSPARK_ST_Q_PADDING 16         /* dense padding past V that is not +0.0 */
 #define DSPARK_ST_Q_MASS 17            /* a value above 1, or counts not summing to M */
 #define DSPARK_ST_Q_TOKEN 18           /* proposed token outside [0, V) or with q = 0 */
+/* refusals of dspark_shape_logits; a row breaking several rules gets the smallest code */
+#define DSPARK_ST_BAD_HISTORY 19       /* a history or prompt length out of range, or a token outside [0, V) */
+#define DSPARK_ST_BAD_PENALTY 20       /* a penalty or temperature outside its range */
+#define DSPARK_ST_BAD_BIAS 21          /* bias offsets out of order, ids not strictly ascending in [0, V), or a NaN / +inf value */
+#define DSPARK_ST_BAD_MASK 22          /* a mask row index outside [-1, n_masks) */
 
 typedef enum { DSPARK_F32 = 0, DSPARK_BF16 = 1 } dspark_dtype;
 typedef enum { DSPARK_GREEDY = 0, DSPARK_SAMPLED = 1 } dspark_mode;
@@ -348,6 +353,141 @@ size_t dspark_sharded_q_workspace(int64_t n_rows, int32_t n_shards, int32_t k_ma
 int dspark_sharded_q(const dspark_rows* rows, int32_t n_shards, const dspark_q* q, const uint32_t* draws,
                      int32_t* argmax, int32_t* sample, int32_t* row_status, void* ws, size_t ws_bytes,
                      void* stream);
+
+/* How dspark_shape_logits changes the logits of each request.  Request r owns
+ * the rows r * rows_per_request + i, i = 0 .. rows_per_request - 1 (1 when one
+ * token is decoded, DSPARK_N_DRAFT / DSPARK_N_TARGET for a block).  Every
+ * array is a device array; NULL leaves its step out.
+ *   history, history_len, prompt_len: the request's tokens so far, ids
+ *           history[r * history_stride .. + history_len[r]), of which the
+ *           first prompt_len[r] are the prompt's and the rest were generated
+ *           (prompt_len NULL: all were).  0 <= prompt_len[r] <=
+ *           history_len[r] <= history_max <= history_stride.
+ *   draft:  the drafted tokens; row i counts draft[r * draft_stride .. + i)
+ *           as generated (draft_stride >= rows_per_request - 1).
+ *   repetition (> 0), frequency, presence: the request's penalties (finite;
+ *           NULL = 1, 0, 0).  Where all three are neutral, history and draft
+ *           are not read.
+ *   temperature: > 0, finite, and with a finite reciprocal (NULL = 1).
+ *   bias_offset (int64[n_requests + 1]), bias_ids, bias_values: request r's
+ *           biases are the entries bias_offset[r] .. bias_offset[r + 1) of
+ *           ids (strictly ascending) and values (finite, or -inf to ban a
+ *           token); bias_total entries in all.
+ *   mask:   packed bits, bit v & 31 of word v >> 5 set where token v is
+ *           allowed (bits past V are ignored); n_masks rows of (V + 31) / 32
+ *           words, mask_stride words apart.  mask_row (int32[n_rows]): the
+ *           mask of row j, -1 for none; NULL: row j has mask j.           */
+typedef struct {
+  int32_t rows_per_request;
+  int32_t reserved;
+  const int32_t* history;
+  int64_t history_max;
+  int64_t history_stride;
+  const int32_t* history_len;
+  const int32_t* prompt_len;
+  const int32_t* draft;
+  int64_t draft_stride;
+  const float* repetition;
+  const float* frequency;
+  const float* presence;
+  const float* temperature;
+  const int64_t* bias_offset;
+  const int32_t* bias_ids;
+  const float* bias_values;
+  int64_t bias_total;
+  const uint32_t* mask;
+  int64_t mask_stride;
+  int64_t n_masks;
+  const int32_t* mask_row;
+} dspark_shaping;
+
+/* Final logits from a model's raw ones, for the steps that read final logits
+ * (propose, q, verification).  For token v of a row with logit x, generated
+ * count c_v and s_v = "v is in the prompt or was generated":
+ *   z = x / repetition if s_v and x > 0;  x * repetition if s_v and x <= 0;
+ *   z = z - frequency c_v - presence [c_v > 0];
+ *   z = (z + bias_v) / temperature;
+ *   z = -inf where the row's mask does not allow v, whatever x is.
+ * Computed in binary32 and rounded once to out_dtype (the rows' own type, or
+ * DSPARK_F32 for bf16 rows).  out: rows of vocab values, out_stride elements
+ * apart, 16-byte aligned like the input rows; either the input itself (same
+ * type and stride: in place) or memory apart from it.  What lies between
+ * rows is not written.  row_status[j]: OK, or BAD_HISTORY, BAD_PENALTY,
+ * BAD_BIAS, BAD_MASK (a bad drafted token: the rows that count it); a refused
+ * row is -inf throughout, which every later step refuses too.  A row whose
+ * mask allows nothing is OK and -inf throughout.  Logits may be NaN or
+ * infinite: the arithmetic above applies to them. */
+int dspark_shape_logits(const dspark_rows* rows, const dspark_shaping* how, void* out, int32_t out_dtype,
+                        int64_t out_stride, int32_t* row_status, void* stream);
+
+/* The largest logits of every row and the log-sum-exp of the whole row: what
+ * a teacher hands to dspark_distill.  Row r lists its k = topk[r] (0 <= k <=
+ * min(k_max, V), else BAD_TOPK; topk NULL: min(k_max, V)) largest finite
+ * logits by (logit desc, id asc), fewer when it has fewer: ids (int32
+ * [n_rows][k_max], ascending) with logits (float[n_rows][k_max], the row's
+ * values), zeros past len[r] (int32[n_rows]).  lse[r] (float, may be NULL) =
+ * log sum_v exp(x_v / temperature) over the whole row.  k_max: 0 ..
+ * DSPARK_K_MAX (0: ids and logits may be NULL); temperature > 0, finite, with
+ * a finite reciprocal.  row_status[r]: OK, ROW_NAN, ROW_POSINF,
+ * ROW_ZERO_MASS or BAD_TOPK; a refused row has len 0, lse 0 and zeros. */
+int dspark_top_logits(const dspark_rows* rows, const int32_t* topk, int32_t k_max, float temperature, int32_t* ids,
+                      float* logits, int32_t* len, float* lse, int32_t* row_status, void* ws, size_t ws_bytes,
+                      void* stream);
+/* Workspace of dspark_top_logits (16-byte aligned). */
+size_t dspark_top_logits_workspace(int64_t n_rows, int64_t vocab, int32_t k_max);
+
+/* A teacher's rows for dspark_distill: row r lists len[r] tokens (0 <= len[r]
+ * <= k_max <= DSPARK_K_MAX) by strictly ascending id with finite logits, as
+ * dspark_top_logits writes them.  lse: log sum_v exp(z_v / temperature) of
+ * the teacher's whole row at the loss's temperature, or NULL to renormalise
+ * the teacher over the list. */
+typedef struct {
+  const int32_t* ids;
+  const float* logits;
+  const int32_t* len;
+  const float* lse;
+  int32_t k_max;
+  int32_t reserved;
+} dspark_teacher;
+
+/* Distillation loss of student rows s against a teacher's top logits z, at
+ * temperature T: with q = softmax(s / T) over the whole vocabulary and, on
+ * the list J, p_j = exp(z_j / T - lse) (lse NULL: softmax of z / T over J),
+ *   loss = sum_J p_j (log p_j - log q_j) + P log(P / Q),
+ *   P = max(0, 1 - sum_J p_j), Q = sum of q off the list.
+ * The last term is there only with lse, and only where P > 0 and the student
+ * has a finite logit off the list.  Its
+ * gradient with respect to s, computed by dspark_distill_backward:
+ *   (q_v - p_v) / T on the list;  q_v (1 - P / Q) / T off it (q_v / T
+ *   without the last term).
+ * A row with len[r] = 0 teaches nothing: loss 0, gradient 0, its student row
+ * is not read.  A student's -inf at a token with p > 0 gives loss +inf.
+ * loss: float[n_rows].  stats: double[n_rows][DSPARK_DISTILL_STATS], what
+ * the backward call takes (opaque).  row_status[r]: OK, Q_BAD_LEN, Q_BAD_ID,
+ * Q_UNSORTED, Q_NONFINITE (a listed logit or lse that is not finite) for the
+ * teacher's list (the smallest), then ROW_NAN, ROW_POSINF or ROW_ZERO_MASS for
+ * the student's row; a refused row has loss 0 and gradient 0.
+ * ws: dspark_distill_workspace() bytes, 16-byte aligned. */
+#define DSPARK_DISTILL_STATS 5
+size_t dspark_distill_workspace(int64_t n_rows, int64_t vocab);
+int dspark_distill(const dspark_rows* student, const dspark_teacher* teacher, float temperature, float* loss,
+                   double* stats, int32_t* row_status, void* ws, size_t ws_bytes, void* stream);
+
+/* Gradient of sum_r grad_loss[r] loss[r] (grad_loss: float[n_rows]) with
+ * respect to the student rows, from the same student and teacher rows and
+ * temperature and the stats and row_status that dspark_distill wrote.  grad: rows of the
+ * student's type and vocab, grad_stride elements apart and 16-byte aligned;
+ * either the student rows themselves (same stride: they are overwritten) or
+ * memory apart from them.  What lies between rows is not written. */
+int dspark_distill_backward(const dspark_rows* student, const dspark_teacher* teacher, float temperature,
+                            const double* stats, const int32_t* row_status, const float* grad_loss, void* grad,
+                            int64_t grad_stride, void* stream);
+
+/* Both in one call, for row weights known beforehand: loss (unweighted) and
+ * grad of sum_r weight[r] loss[r], as the two calls above give them. */
+int dspark_distill_step(const dspark_rows* student, const dspark_teacher* teacher, float temperature,
+                        const float* weight, float* loss, void* grad, int64_t grad_stride, int32_t* row_status,
+                        void* ws, size_t ws_bytes, void* stream);
 
 /* Test entry: the dense allocation steps of dspark_q_alloc applied to
  * caller-given float32 weights (normalised weights in [0, 1]), so that the

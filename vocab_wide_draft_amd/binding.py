@@ -21,7 +21,8 @@ K_MAX = 1024
 STATUS_NAMES = {0: "OK", 1: "ROW_NAN", 2: "ROW_POSINF", 3: "ROW_ZERO_MASS", 4: "DRAW_RANGE",
                 5: "ALLOC_INCONSISTENT", 6: "TARGET_INVALID", 7: "DRAFT_INVALID", 8: "BAD_WEIGHT",
                 9: "BAD_TOPK", 10: "Q_BAD_LEN", 11: "Q_BAD_ID", 12: "Q_UNSORTED", 13: "Q_NONFINITE",
-                14: "Q_NEGATIVE", 15: "Q_NOT_DYADIC", 16: "Q_PADDING", 17: "Q_MASS", 18: "Q_TOKEN"}
+                14: "Q_NEGATIVE", 15: "Q_NOT_DYADIC", 16: "Q_PADDING", 17: "Q_MASS", 18: "Q_TOKEN",
+                19: "BAD_HISTORY", 20: "BAD_PENALTY", 21: "BAD_BIAS", 22: "BAD_MASK"}
 
 
 class DsparkError(RuntimeError):
@@ -45,8 +46,30 @@ class QWire(ctypes.Structure):
                 ("sp_ids", ctypes.c_void_p), ("sp_val", ctypes.c_void_p), ("sp_len", ctypes.c_void_p)]
 
 
+class Shaping(ctypes.Structure):
+    _fields_ = [("rows_per_request", ctypes.c_int32), ("reserved", ctypes.c_int32),
+                ("history", ctypes.c_void_p), ("history_max", ctypes.c_int64), ("history_stride", ctypes.c_int64),
+                ("history_len", ctypes.c_void_p), ("prompt_len", ctypes.c_void_p),
+                ("draft", ctypes.c_void_p), ("draft_stride", ctypes.c_int64),
+                ("repetition", ctypes.c_void_p), ("frequency", ctypes.c_void_p), ("presence", ctypes.c_void_p),
+                ("temperature", ctypes.c_void_p),
+                ("bias_offset", ctypes.c_void_p), ("bias_ids", ctypes.c_void_p), ("bias_values", ctypes.c_void_p),
+                ("bias_total", ctypes.c_int64),
+                ("mask", ctypes.c_void_p), ("mask_stride", ctypes.c_int64), ("n_masks", ctypes.c_int64),
+                ("mask_row", ctypes.c_void_p)]
+
+
+class Teacher(ctypes.Structure):
+    _fields_ = [("ids", ctypes.c_void_p), ("logits", ctypes.c_void_p), ("len", ctypes.c_void_p),
+                ("lse", ctypes.c_void_p), ("k_max", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+DISTILL_STATS = 5
+
 EXPORTS = ["dspark_propose", "dspark_q_alloc", "dspark_sample", "dspark_verify_greedy", "dspark_fused",
            "dspark_q_alloc_weights", "dspark_cr_expf", "dspark_q_encode", "dspark_q_validate", "dspark_margin", "dspark_verify_stochastic", "dspark_verify_ratio", "dspark_sharded_propose", "dspark_sharded_propose_noalloc", "dspark_sharded_q", "dspark_sharded_q_workspace", "dspark_workspace_bytes", "dspark_q_semantic_id",
+           "dspark_shape_logits", "dspark_top_logits", "dspark_top_logits_workspace", "dspark_distill",
+           "dspark_distill_backward", "dspark_distill_step", "dspark_distill_workspace",
            "dspark_status_name", "dspark_last_error", "dspark_abi_version"]
 
 
@@ -65,6 +88,7 @@ def load_library():
     lib = ctypes.CDLL(path)
     P, I32, I64, SZ = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
     RP, QP = ctypes.POINTER(Rows), ctypes.POINTER(Q)
+    TP, F32 = ctypes.POINTER(Teacher), ctypes.c_float
     sig = {
         "dspark_propose": (ctypes.c_int, [RP, P, P, P, P, SZ, P]),
         "dspark_q_alloc": (ctypes.c_int, [RP, QP, P, P, SZ, P]),
@@ -83,6 +107,13 @@ def load_library():
         "dspark_verify_ratio": (ctypes.c_int, [RP, P, P, QP, I64, P, P, P, P, P, P]),
         "dspark_q_validate": (ctypes.c_int, [ctypes.POINTER(QWire), I64, I64, P, P, P, P, P]),
         "dspark_workspace_bytes": (SZ, [I32, I64, I64, I32]),
+        "dspark_shape_logits": (ctypes.c_int, [RP, ctypes.POINTER(Shaping), P, I32, I64, P, P]),
+        "dspark_top_logits": (ctypes.c_int, [RP, P, I32, F32, P, P, P, P, P, P, SZ, P]),
+        "dspark_top_logits_workspace": (SZ, [I64, I64, I32]),
+        "dspark_distill": (ctypes.c_int, [RP, TP, F32, P, P, P, P, SZ, P]),
+        "dspark_distill_backward": (ctypes.c_int, [RP, TP, F32, P, P, P, P, I64, P]),
+        "dspark_distill_step": (ctypes.c_int, [RP, TP, F32, P, P, P, I64, P, P, SZ, P]),
+        "dspark_distill_workspace": (SZ, [I64, I64]),
         "dspark_q_semantic_id": (ctypes.c_char_p, []),
         "dspark_status_name": (ctypes.c_char_p, [I32]),
         "dspark_last_error": (ctypes.c_char_p, []),
@@ -432,3 +463,217 @@ def sharded_q(rows: torch.Tensor, n_shards: int, topk=None, k_max: int = 0, draw
                                 _p(out["sample"]), _p(out["status"]), ctypes.c_void_p(out["_ws_ptr"]),
                                 out["_ws_bytes"], _stream()))
     return out
+
+
+# ---- operators on logit rows: shaping, a teacher's top logits, distillation.
+# Their work runs on the rows' device and on that device's current stream.
+
+
+def _arg(t, name, dtype, shape, dev):
+    """Address of a contiguous argument tensor (None stays None)."""
+    if t is None:
+        return None
+    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or t.device != dev or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {dev}, "
+                         f"not {t.dtype} {tuple(t.shape)} on {t.device}")
+    return t.data_ptr()
+
+
+def _matrix(t, name, dtype, n, dev):
+    """(address, columns, row stride) of an [n, columns] argument with unit column stride."""
+    if t is None:
+        return None, 0, 0
+    if t.dtype != dtype or t.dim() != 2 or t.shape[0] != n or t.device != dev:
+        raise ValueError(f"{name} must be a 2-D {dtype} tensor with {n} rows on {dev}")
+    if (t.shape[1] > 1 and t.stride(1) != 1) or (n > 1 and t.stride(0) < t.shape[1]):
+        raise ValueError(f"{name} must have unit column stride and rows that do not overlap")
+    return t.data_ptr(), t.shape[1], max(t.stride(0), t.shape[1])
+
+
+def _empty_rows(n, V, dtype, dev):
+    """Rows [n, V] that start 16-byte aligned."""
+    per = 16 // dtype.itemsize
+    return torch.empty((n, -(-V // per) * per), dtype=dtype, device=dev)[:, :V]
+
+
+def _out_rows(out, like, dtype):
+    if out is None:
+        return _empty_rows(like.shape[0], like.shape[1], dtype, like.device)
+    if out.shape != like.shape or out.dtype != dtype or out.device != like.device or out.stride(1) != 1:
+        raise ValueError(f"out must be a {dtype} tensor of shape {tuple(like.shape)} with unit column stride on {like.device}")
+    return out
+
+
+def _call(dev, f, *args):
+    """The library call on dev's current stream, with dev current."""
+    if dev.index == torch.cuda.current_device():
+        _check(f(*args, ctypes.c_void_p(torch.cuda.current_stream(dev).cuda_stream)))
+    else:
+        with torch.cuda.device(dev):
+            _check(f(*args, ctypes.c_void_p(torch.cuda.current_stream(dev).cuda_stream)))
+
+
+def shape_logits(rows: torch.Tensor, rows_per_request: int = 1, *, history=None, history_len=None, prompt_len=None,
+                 draft=None, repetition=None, frequency=None, presence=None, temperature=None, bias=None, mask=None,
+                 mask_row=None, out=None, out_dtype=None):
+    """Final logits from raw ones: penalties for repeated tokens, biases,
+    temperature and grammar masks (see dspark_shape_logits).  rows [n, V],
+    rows_per_request of them for each of the n / rows_per_request requests.
+    history int32 [requests, most] with history_len and prompt_len int32
+    [requests] (history_len None: every row is full); draft int32 [requests,
+    at least rows_per_request - 1]; the penalties and temperature float32
+    [requests]; bias (offsets int64 [requests + 1], ids int32, values float32);
+    mask int32 (packed bits) [masks, at least (V + 31) // 32] with mask_row
+    int32 [n].  out: rows to write, which may be `rows` itself; out_dtype: the
+    rows' type (default) or float32.  Returns {"logits", "status"}."""
+    lib = load_library()
+    r = _rows(rows)
+    n, V, dev = rows.shape[0], rows.shape[1], rows.device
+    P = int(rows_per_request)
+    if P < 1 or n % P:
+        raise ValueError("the number of rows must be a multiple of rows_per_request")
+    R = n // P
+    o = _out_rows(out, rows, out_dtype or (rows.dtype if out is None else out.dtype))
+    if o.dtype not in (torch.float32, rows.dtype):
+        raise ValueError("out_dtype must be the rows' type or float32")
+    h, h_max, h_stride = _matrix(history, "history", torch.int32, R, dev)
+    if history is not None and history_len is None:
+        history_len = torch.full((R,), h_max, dtype=torch.int32, device=dev)
+    d, d_cols, d_stride = _matrix(draft, "draft", torch.int32, R, dev)
+    if draft is not None and d_cols < P - 1:
+        raise ValueError("draft must have at least rows_per_request - 1 columns")
+    m, m_cols, m_stride = (None, 0, 0) if mask is None else _matrix(mask, "mask", torch.int32, mask.shape[0], dev)
+    if mask is not None and m_cols < (V + 31) // 32:
+        raise ValueError("mask must have at least (V + 31) // 32 columns")
+    offsets, ids, values = bias if bias is not None else (None, None, None)
+    total = 0 if ids is None else ids.numel()
+    i32, f32 = torch.int32, torch.float32
+    how = Shaping(P, 0, h, h_max, h_stride, _arg(history_len, "history_len", i32, (R,), dev),
+                  _arg(prompt_len, "prompt_len", i32, (R,), dev), d, d_stride,
+                  _arg(repetition, "repetition", f32, (R,), dev), _arg(frequency, "frequency", f32, (R,), dev),
+                  _arg(presence, "presence", f32, (R,), dev), _arg(temperature, "temperature", f32, (R,), dev),
+                  _arg(offsets, "bias offsets", torch.int64, (R + 1,), dev), _arg(ids, "bias ids", i32, (total,), dev),
+                  _arg(values, "bias values", f32, (total,), dev), total,
+                  m, m_stride, 0 if mask is None else mask.shape[0], _arg(mask_row, "mask_row", i32, (n,), dev))
+    st = _i32(n, dev)
+    _call(dev, lib.dspark_shape_logits, ctypes.byref(r), ctypes.byref(how), _p(o),
+          DTYPE_F32 if o.dtype == torch.float32 else DTYPE_BF16, o.stride(0), _p(st))
+    return {"logits": o, "status": st}
+
+
+def top_logits(rows: torch.Tensor, k_max: int, topk=None, temperature: float = 1.0):
+    """The k_max (or per row topk, int32 [n]) largest finite logits of every
+    row by ascending id, and the log-sum-exp of the row over temperature (see
+    dspark_top_logits): {"ids", "logits", "len", "lse", "status"}, a teacher
+    for distill at that temperature."""
+    lib = load_library()
+    r = _rows(rows)
+    n, V, dev = rows.shape[0], rows.shape[1], rows.device
+    k = int(k_max)
+    if k < 0 or k > K_MAX:
+        raise ValueError("k_max must be in [0, K_MAX]")
+    out = {"ids": torch.empty((n, k), dtype=torch.int32, device=dev),
+           "logits": torch.empty((n, k), dtype=torch.float32, device=dev),
+           "len": _i32(n, dev), "lse": torch.empty(n, dtype=torch.float32, device=dev), "status": _i32(n, dev)}
+    nbytes = int(lib.dspark_top_logits_workspace(n, V, k))
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
+    tk = None if topk is None else ctypes.c_void_p(_arg(topk, "topk", torch.int32, (n,), dev))
+    _call(dev, lib.dspark_top_logits, ctypes.byref(r), tk, k, float(temperature), _p(out["ids"]), _p(out["logits"]),
+          _p(out["len"]), _p(out["lse"]), _p(out["status"]), _p(ws), nbytes)
+    return out
+
+
+def _teacher(t, n, dev) -> Teacher:
+    ids = t["ids"]
+    if ids.dim() != 2 or ids.shape[1] > K_MAX:
+        raise ValueError("teacher ids must be [rows, at most K_MAX]")
+    k = ids.shape[1]
+    return Teacher(_arg(ids, "teacher ids", torch.int32, (n, k), dev),
+                   _arg(t["logits"], "teacher logits", torch.float32, (n, k), dev),
+                   _arg(t["len"], "teacher len", torch.int32, (n,), dev),
+                   _arg(t.get("lse"), "teacher lse", torch.float32, (n,), dev), k, 0)
+
+
+def _distill_ws(lib, n, V, dev):
+    nbytes = int(lib.dspark_distill_workspace(n, V))
+    return (torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None), nbytes
+
+
+def distill(student: torch.Tensor, teacher, temperature: float = 1.0):
+    """Distillation loss of every student row [n, V] against a teacher's top
+    logits (see dspark_distill).  teacher: {"ids", "logits", "len", "lse"} as
+    top_logits returns it at the same temperature; without "lse" (or None)
+    the teacher is renormalised over its list.  Returns {"loss", "stats",
+    "status"}; stats and status go to distill_backward."""
+    lib = load_library()
+    r = _rows(student)
+    n, V, dev = student.shape[0], student.shape[1], student.device
+    t = _teacher(teacher, n, dev)
+    out = {"loss": torch.empty(n, dtype=torch.float32, device=dev),
+           "stats": torch.empty((n, DISTILL_STATS), dtype=torch.float64, device=dev), "status": _i32(n, dev)}
+    ws, nbytes = _distill_ws(lib, n, V, dev)
+    _call(dev, lib.dspark_distill, ctypes.byref(r), ctypes.byref(t), float(temperature), _p(out["loss"]),
+          _p(out["stats"]), _p(out["status"]), _p(ws), nbytes)
+    return out
+
+
+def distill_backward(student: torch.Tensor, teacher, forward, grad_loss: torch.Tensor, temperature: float = 1.0,
+                     out=None):
+    """Gradient of sum(grad_loss * loss) with respect to the student rows;
+    forward: what distill returned for the same arguments.  out may be the
+    student rows themselves (overwritten)."""
+    lib = load_library()
+    r = _rows(student)
+    n, dev = student.shape[0], student.device
+    t = _teacher(teacher, n, dev)
+    g = _out_rows(out, student, student.dtype)
+    st = ctypes.c_void_p(_arg(forward["stats"], "stats", torch.float64, (n, DISTILL_STATS), dev))
+    rs = ctypes.c_void_p(_arg(forward["status"], "status", torch.int32, (n,), dev))
+    gl = ctypes.c_void_p(_arg(grad_loss, "grad_loss", torch.float32, (n,), dev))
+    _call(dev, lib.dspark_distill_backward, ctypes.byref(r), ctypes.byref(t), float(temperature), st, rs, gl, _p(g),
+          g.stride(0))
+    return g
+
+
+def distill_step(student: torch.Tensor, teacher, weight: torch.Tensor, temperature: float = 1.0, out=None):
+    """Loss of every row (unweighted) and the gradient of sum(weight * loss)
+    in one call: {"loss", "grad", "status"}.  out as in distill_backward."""
+    lib = load_library()
+    r = _rows(student)
+    n, V, dev = student.shape[0], student.shape[1], student.device
+    t = _teacher(teacher, n, dev)
+    g = _out_rows(out, student, student.dtype)
+    loss, st = torch.empty(n, dtype=torch.float32, device=dev), _i32(n, dev)
+    w = ctypes.c_void_p(_arg(weight, "weight", torch.float32, (n,), dev))
+    ws, nbytes = _distill_ws(lib, n, V, dev)
+    _call(dev, lib.dspark_distill_step, ctypes.byref(r), ctypes.byref(t), float(temperature), w, _p(loss), _p(g),
+          g.stride(0), _p(st), _p(ws), nbytes)
+    return {"loss": loss, "grad": g, "status": st}
+
+
+class _Distill(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, student, ids, logits, length, lse, temperature):
+        out = distill(student, {"ids": ids, "logits": logits, "len": length, "lse": lse}, temperature)
+        ctx.save_for_backward(student, ids, logits, length, lse, out["stats"], out["status"])
+        ctx.temperature = temperature
+        return out["loss"]
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, grad_loss):
+        student, ids, logits, length, lse, stats, status = ctx.saved_tensors
+        teacher = {"ids": ids, "logits": logits, "len": length, "lse": lse}
+        g = distill_backward(student, teacher, {"stats": stats, "status": status},
+                             grad_loss.to(torch.float32).contiguous(), ctx.temperature)
+        return g, None, None, None, None, None
+
+
+def distill_loss(student: torch.Tensor, teacher, temperature: float = 1.0) -> torch.Tensor:
+    """distill's loss (float32 [n]) as a differentiable function of the
+    student rows.  The teacher is constant: its logits must not require a
+    gradient.  Rows that the call refuses have loss 0 and gradient 0."""
+    if teacher["logits"].requires_grad or (teacher.get("lse") is not None and teacher["lse"].requires_grad):
+        raise ValueError("the teacher is constant: detach its logits and lse")
+    return _Distill.apply(student, teacher["ids"], teacher["logits"], teacher["len"], teacher.get("lse"),
+                          float(temperature))

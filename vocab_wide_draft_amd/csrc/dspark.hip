@@ -15,6 +15,7 @@
 #include "dense_vd.hpp"
 #include "draw.hpp"
 #include "fast_q.hpp"
+#include "host_checks.hpp"
 #include "margin.hpp"
 #include "q_wire.hpp"
 #include "sharded.hpp"
@@ -1083,6 +1084,11 @@ void set_q(RowsArgs& a, const dspark_q* q) {
 }
 }  // namespace
 
+// the same checks and error message for the entry points of the other source files
+int dspark::host_fail(int code, const char* msg) { return fail(code, msg); }
+int dspark::host_check_launch() { return check_launch(); }
+int dspark::host_check_rows(const dspark_rows* r, const char* what) { return check_rows(r, what); }
+
 extern "C" {
 
 int32_t dspark_abi_version(void) { return DSPARK_ABI_VERSION; }
@@ -1110,6 +1116,10 @@ const char* dspark_status_name(int32_t code) {
     case DSPARK_ST_Q_PADDING: return "Q_PADDING";
     case DSPARK_ST_Q_MASS: return "Q_MASS";
     case DSPARK_ST_Q_TOKEN: return "Q_TOKEN";
+    case DSPARK_ST_BAD_HISTORY: return "BAD_HISTORY";
+    case DSPARK_ST_BAD_PENALTY: return "BAD_PENALTY";
+    case DSPARK_ST_BAD_BIAS: return "BAD_BIAS";
+    case DSPARK_ST_BAD_MASK: return "BAD_MASK";
     default: return "UNKNOWN";
   }
 }

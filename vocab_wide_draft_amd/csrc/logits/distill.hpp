@@ -1,0 +1,360 @@
+// Distillation loss against a teacher's top logits, and its gradient
+// (dspark_distill, dspark_distill_backward, dspark_distill_step).
+//
+// Mathematics.  u = s / T.  Off the list, a row needs M_off = max s and S_off =
+// sum exp(u - M_off / T); on the list M_on and S_on, and, with w_j = exp(z_j / T
+// - zm) (zm: the teacher's lse, or the list's maximum when it is
+// renormalised), B0 = sum w_j and B1 = sum w_j (z_j / T - zm - u_j).  The two
+// sides are kept apart, each with its own maximum: S - S_on would cancel
+// where the list holds nearly all mass, and with one maximum S_off would
+// underflow where the list lies far above the rest, while the loss still
+// holds the logarithm of that mass and the gradient its distribution.  With
+// M = max(M_off, M_on) and S = S_off e^((M_off - M) / T) + S_on e^((M_on - M) / T),
+//   lse_u = M / T + log S,  log Q = M_off / T + log S_off - lse_u
+//   with lse:    loss = B1 + B0 lse_u + P (log P - log Q),  P = 1 - B0
+//                off the list dL/du_v = e^(u_v - M_off / T) (e^((M_off - M) / T) / S - P / S_off)
+//   normalised:  loss = B1 / B0 - log B0 + lse_u  (every id counts as off the list in the sums)
+// Every term is a sum over slices of the vocabulary once each slice's
+// maximum is put back, so slices are worked on apart and joined.  Sums over
+// a thread's logits are binary32, everything joined is binary64, as is the
+// list's side (P = 1 - B0 loses what binary32 would keep of it).  The hardware
+// exponential gives 0 below 2^-126 relative to a maximum.
+#pragma once
+#include "slices.hpp"
+
+namespace dspark {
+
+struct DistillPart {  // one slice of one row
+  double s_off, s_on, b0, b1, zm;
+  float m_off, m_on;
+  int32_t flags;  // 1: a NaN, 2: a +inf
+  int32_t reserved;
+};
+
+struct DistillArgs {
+  const void* x;
+  int64_t x_stride;
+  int64_t n;
+  int V;
+  int slices, slice;
+  const int32_t* ids;
+  const float* logits;
+  const int32_t* len;
+  const float* lse;
+  int k_max;
+  double inv_t;
+  DistillPart* part;  // [n][slices]
+  int32_t* list_status;  // [n] (the list's refusal)
+  float* loss;
+  double* stats;
+  int32_t* row_status;
+  const int32_t* status_in;  // backward
+  const double* stats_in;
+  const float* weight;
+  void* grad;
+  int64_t grad_stride;
+};
+
+constexpr int kListPer = DSPARK_K_MAX / kSliceBS;  // list entries per thread
+constexpr float kLog2e = 1.4426950408889634f;
+
+__device__ __forceinline__ bool finite_row_value(float x) { return (__float_as_uint(x) & 0x7f800000u) != 0x7f800000u; }
+
+// The slice's part of a row (see above).  Returns with the whole workgroup.
+template <int DT>
+__device__ void distill_slice(const DistillArgs& a, int64_t r, int s, uint32_t* lds) {
+  __shared__ double red[kSliceNW];
+  __shared__ float redf[kSliceNW];
+  __shared__ uint32_t redu[kSliceNW];
+  typedef typename El<DT>::T XT;
+  const int start = s * a.slice, V = a.V;
+  const int size = V - start < a.slice ? V - start : a.slice;
+  const int words = (a.slice + 31) / 32;
+  const XT* x = static_cast<const XT*>(a.x) + r * a.x_stride;
+  const int32_t* ids = a.ids + r * a.k_max;
+  const float* zl = a.logits + r * a.k_max;
+  int len = a.len[r];
+  uint32_t wrong = 0;
+  if (len < 0 || len > a.k_max) {
+    wrong = 1u;
+    len = 0;
+  }
+  const bool tail = a.lse != nullptr;
+  IdSet on{lds, lds + words};
+  if (len > 0 && tail) on.clear(words);
+  // the list: which entries are ours, and (slice 0) whether it may be used
+  int32_t id[kListPer];
+  float z[kListPer];
+  float zmax = -__builtin_inff();
+#pragma unroll
+  for (int j = 0; j < kListPer; ++j) {
+    const int e = j * kSliceBS + (int)threadIdx.x;
+    id[j] = -1;
+    z[j] = -__builtin_inff();
+    if (e < len) {
+      id[j] = ids[e];
+      z[j] = zl[e];
+      zmax = __builtin_fmaxf(zmax, z[j]);
+      if (s == 0) {
+        if ((uint32_t)id[j] >= (uint32_t)V) wrong |= 2u;
+        if (e > 0 && ids[e - 1] >= id[j]) wrong |= 4u;
+        if (!finite_row_value(z[j])) wrong |= 8u;
+      }
+    }
+  }
+  if (s == 0) {
+    if (len > 0 && tail && !finite_row_value(a.lse[r])) wrong |= 8u;
+    wrong = group_reduce<kSliceNW>(wrong, 0u, [](uint32_t p, uint32_t q) { return p | q; }, redu);
+    if (threadIdx.x == 0) a.list_status[r] = wrong ? DSPARK_ST_Q_BAD_LEN + (wrong & 1u ? 0 : wrong & 2u ? 1 : wrong & 4u ? 2 : 3) : DSPARK_ST_OK;
+  }
+  if (len == 0) return;  // (uniform)
+  double zm;
+  if (tail) {
+    zm = (double)a.lse[r];
+  } else {
+    zm = (double)group_reduce<kSliceNW>(zmax, -__builtin_inff(), [](float p, float q) { return __builtin_fmaxf(p, q); }, redf) * a.inv_t;
+  }
+  __syncthreads();
+  const float c = (float)(a.inv_t * (double)kLog2e);
+  double b0 = 0.0, b1 = 0.0;
+  float m_on = -__builtin_inff(), s_on = 0.0f, on_x[kListPer];
+  uint32_t flags = 0;
+#pragma unroll
+  for (int j = 0; j < kListPer; ++j) {
+    const uint32_t t = (uint32_t)(id[j] - start);
+    on_x[j] = -__builtin_inff();
+    if (id[j] >= 0 && t < (uint32_t)size) {
+      const float xj = El<DT>::get(x, id[j]);
+      if (tail) {
+        atomicOr(&on.bits[t >> 5], 1u << (t & 31));
+        on_x[j] = xj;
+        m_on = __builtin_fmaxf(m_on, xj);
+        flags |= xj != xj ? 1u : xj == __builtin_inff() ? 2u : 0u;
+      }
+      const double lp = (double)z[j] * a.inv_t - zm;
+      const double w = exp(lp);
+      if (w > 0.0) {
+        b0 += w;
+        b1 += w * (lp - (double)xj * a.inv_t);
+      }
+    }
+  }
+  if (m_on > -__builtin_inff()) {
+#pragma unroll
+    for (int j = 0; j < kListPer; ++j) s_on += __builtin_amdgcn_exp2f((on_x[j] - m_on) * c);
+  }
+  __syncthreads();
+  // the row off the list: running maximum and sum; a group of eight logits
+  // moves the maximum at most once
+  float m = -__builtin_inff(), s_off = 0.0f;
+  for (int t = threadIdx.x * 8; t < size; t += kSliceStep) {
+    float v[8];
+    load8<DT, false>(x, start + t, V, v);
+    const uint32_t bits = tail ? on.byte(t) : 0u;
+    if (bits) {
+#pragma unroll
+      for (int l = 0; l < 8; ++l) v[l] = (bits >> l) & 1u ? -__builtin_inff() : v[l];
+    }
+    float top = v[0];
+#pragma unroll
+    for (int l = 1; l < 8; ++l) top = __builtin_fmaxf(top, v[l]);
+    if (top > m) {
+      s_off *= __builtin_amdgcn_exp2f((m - top) * c);  // (by 0 the first time)
+      m = top;
+    }
+    const float ref = m == -__builtin_inff() ? 0.0f : m;
+#pragma unroll
+    for (int l = 0; l < 8; ++l) s_off += __builtin_amdgcn_exp2f((v[l] - ref) * c);
+  }
+  // a NaN or +inf shows in the sum or the maximum; which of the two, the thread's own logits tell
+  if (s_off != s_off || m == __builtin_inff()) {
+    for (int t = threadIdx.x * 8; t < size; t += kSliceStep) {
+      float v[8];
+      load8<DT, false>(x, start + t, V, v);
+#pragma unroll
+      for (int l = 0; l < 8; ++l) flags |= v[l] != v[l] ? 1u : v[l] == __builtin_inff() ? 2u : 0u;
+    }
+  }
+  const auto larger = [](float p, float q) { return __builtin_fmaxf(p, q); };
+  const auto plus = [](double p, double q) { return p + q; };
+  const float M_off = group_reduce<kSliceNW>(m, -__builtin_inff(), larger, redf);
+  const float M_on = group_reduce<kSliceNW>(m_on, -__builtin_inff(), larger, redf);
+  flags = group_reduce<kSliceNW>(flags, 0u, [](uint32_t p, uint32_t q) { return p | q; }, redu);
+  const double f = m == -__builtin_inff() ? 0.0 : (double)__builtin_amdgcn_exp2f((m - M_off) * c);
+  const double g = m_on == -__builtin_inff() ? 0.0 : (double)__builtin_amdgcn_exp2f((m_on - M_on) * c);
+  const double t_off = group_reduce<kSliceNW>((double)s_off * f, 0.0, plus, red);
+  const double t_on = group_reduce<kSliceNW>((double)s_on * g, 0.0, plus, red);
+  b0 = group_reduce<kSliceNW>(b0, 0.0, plus, red);
+  b1 = group_reduce<kSliceNW>(b1, 0.0, plus, red);
+  if (threadIdx.x == 0) {
+    DistillPart& p = a.part[r * a.slices + s];
+    p.s_off = t_off;
+    p.s_on = t_on;
+    p.b0 = b0;
+    p.b1 = b1;
+    p.zm = zm;
+    p.m_off = M_off;
+    p.m_on = M_on;
+    p.flags = (int32_t)flags;
+    p.reserved = 0;
+  }
+}
+
+struct DistillRow {  // what the gradient needs of a row
+  int status;
+  double M;      // the row's maximum
+  double inv_s;  // 1 / S
+  double M_off;  // the maximum off the list
+  double f_off;  // dL/du off the list over e^(u - M_off / T)
+  double zm;     // log of the teacher's normaliser
+  double loss;
+};
+
+// One wave joins the slices of a row (every lane gets the result).
+__device__ __forceinline__ DistillRow distill_join(const DistillArgs& a, int64_t r) {
+  DistillRow o{a.list_status[r], 0.0, 0.0, 0.0, 0.0, 0.0, 0.0};
+  if (o.status != DSPARK_ST_OK || a.len[r] == 0) return o;
+  const int l = lane_id();
+  constexpr float kNone = -__builtin_inff();
+  DistillPart p{0.0, 0.0, 0.0, 0.0, 0.0, kNone, kNone, 0, 0};
+  if (l < a.slices) p = a.part[r * a.slices + l];
+  const auto larger = [](float x, float y) { return __builtin_fmaxf(x, y); };
+  const uint32_t flags = wave_reduce((uint32_t)p.flags, 0u, [](uint32_t x, uint32_t y) { return x | y; });
+  const float m_off = wave_reduce(p.m_off, kNone, larger), m_on = wave_reduce(p.m_on, kNone, larger);
+  const float m = __builtin_fmaxf(m_off, m_on);
+  if (flags & 1u) o.status = DSPARK_ST_ROW_NAN;
+  else if (flags & 2u) o.status = DSPARK_ST_ROW_POSINF;
+  else if (m == kNone) o.status = DSPARK_ST_ROW_ZERO_MASS;
+  if (o.status != DSPARK_ST_OK) return o;
+  // e^((x - y) / T) of two maxima, 0 where x is none
+  const auto shift = [&](float x, float y) { return x == kNone ? 0.0 : exp(((double)x - (double)y) * a.inv_t); };
+  const double off = wave_sum(p.s_off * shift(p.m_off, m_off)), on = wave_sum(p.s_on * shift(p.m_on, m_on));
+  const double b0 = wave_sum(p.b0), b1 = wave_sum(p.b1);
+  const double zm = a.part[r * a.slices].zm;
+  const double q_off = off * shift(m_off, m);  // underflows where the rest is out of sight
+  const double S = q_off + on * shift(m_on, m);
+  const double log_s = log(S), lse_u = (double)m * a.inv_t + log_s;
+  o.M = m;
+  o.inv_s = 1.0 / S;
+  o.M_off = m_off == kNone ? 0.0 : m_off;
+  o.f_off = shift(m_off, m) * o.inv_s;
+  if (a.lse) {
+    o.zm = zm;
+    o.loss = b1 + b0 * lse_u;
+    const double P = 1.0 - b0;
+    if (P > 0.0 && off > 0.0) {
+      o.loss += P * (log(P) - (((double)m_off - (double)m) * a.inv_t + log(off) - log_s));
+      o.f_off -= P / off;
+    }
+  } else {
+    const double lz = log(b0);
+    o.zm = zm + lz;
+    o.loss = b1 / b0 - lz + lse_u;
+  }
+  return o;
+}
+
+__device__ __forceinline__ void distill_row_out(const DistillArgs& a, int64_t r, const DistillRow& o) {
+  a.loss[r] = (float)o.loss;
+  a.row_status[r] = o.status;
+  if (a.stats) {
+    double* st = a.stats + r * DSPARK_DISTILL_STATS;
+    st[0] = o.M;
+    st[1] = o.inv_s;
+    st[2] = o.M_off;
+    st[3] = o.f_off;
+    st[4] = o.zm;
+  }
+}
+
+template <int DT>
+__global__ void __launch_bounds__(kSliceBS) distill_part_kernel(DistillArgs a) {
+  extern __shared__ uint32_t lds[];
+  const int64_t b = block_number(a.n * a.slices);
+  if (b < 0) return;
+  const int64_t r = b / a.slices;
+  distill_slice<DT>(a, r, (int)(b - r * a.slices), lds);
+}
+
+// one wave per row
+__global__ void __launch_bounds__(kSliceBS) distill_join_kernel(DistillArgs a) {
+  const int64_t b = block_number((a.n + kSliceNW - 1) / kSliceNW);
+  if (b < 0) return;
+  const int64_t r = b * kSliceNW + wave_id();
+  if (r >= a.n) return;
+  const DistillRow o = distill_join(a, r);
+  if (lane_id() == 0) distill_row_out(a, r, o);
+}
+
+// The gradient of one slice of one row; FROM_STATS: the row's numbers come
+// from the forward call, otherwise they are joined here (and slice 0 writes
+// the row's outputs).
+template <int DT, bool FROM_STATS>
+__global__ void __launch_bounds__(kSliceBS) distill_grad_kernel(DistillArgs a) {
+  extern __shared__ uint32_t lds[];
+  __shared__ DistillRow sh;
+  __shared__ float p[DSPARK_K_MAX];
+  typedef typename El<DT>::T XT;
+  const int64_t b = block_number(a.n * a.slices);
+  if (b < 0) return;
+  const int64_t r = b / a.slices;
+  const int s = (int)(b - r * a.slices);
+  const int start = s * a.slice, V = a.V;
+  const int size = V - start < a.slice ? V - start : a.slice;
+  const int words = (a.slice + 31) / 32;
+  const XT* x = static_cast<const XT*>(a.x) + r * a.x_stride;
+  XT* g = static_cast<XT*>(a.grad) + r * a.grad_stride;
+  IdSet on{lds, lds + words};
+  if constexpr (FROM_STATS) {
+    if (threadIdx.x == 0) {
+      const double* st = a.stats_in + r * DSPARK_DISTILL_STATS;
+      sh = DistillRow{a.status_in[r], st[0], st[1], st[2], st[3], st[4], 0.0};
+    }
+  } else if (wave_id() == 0) {
+    const DistillRow o = distill_join(a, r);
+    if (lane_id() == 0) {
+      sh = o;
+      if (s == 0) distill_row_out(a, r, o);
+    }
+  }
+  on.clear(words);
+  __syncthreads();
+  int len = a.len[r];
+  if (len < 0 || len > a.k_max) len = 0;
+  if (sh.status != DSPARK_ST_OK || len == 0) {  // (uniform)
+    const float z[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+    for (int t = threadIdx.x * 8; t < size; t += kSliceStep) store8<DT>(g, start + t, V, z);
+    return;
+  }
+  const int32_t* ids = a.ids + r * a.k_max;
+  const float* zl = a.logits + r * a.k_max;
+  for (int e = threadIdx.x; e < len; e += kSliceBS) {
+    const int32_t id = ids[e];
+    const uint32_t t = (uint32_t)(id - start);
+    if (id >= 0 && t < (uint32_t)size) {
+      const int32_t prev = e > 0 ? ids[e - 1] : -1;
+      on.add((int)t, prev < start ? -1 : prev - start, (uint32_t)e);
+      p[e] = (float)exp((double)zl[e] * a.inv_t - sh.zm);
+    }
+  }
+  __syncthreads();
+  const float c = (float)(a.inv_t * (double)kLog2e);
+  const float M = (float)sh.M, M_off = (float)sh.M_off, inv_s = (float)sh.inv_s;
+  const double w = (double)a.weight[r] * a.inv_t;
+  const float w_on = (float)w, f_off = (float)(sh.f_off * w);
+  for (int t = threadIdx.x * 8; t < size; t += kSliceStep) {
+    float v[8];
+    load8<DT, true>(x, start + t, V, v);
+    const uint32_t bits = on.byte(t);
+#pragma unroll
+    for (int l = 0; l < 8; ++l) {
+      const bool listed = (bits >> l) & 1u;
+      const float e = __builtin_amdgcn_exp2f((v[l] - (listed ? M : M_off)) * c);
+      v[l] = e * f_off;
+      if (listed) v[l] = (e * inv_s - p[on.entry(t + l) & (DSPARK_K_MAX - 1)]) * w_on;
+    }
+    store8<DT>(g, start + t, V, v);
+  }
+}
+
+}  // namespace dspark

@@ -1,0 +1,297 @@
+// Operators on logit rows around the draft and verify step: shaping of raw
+// logits, a teacher's top logits, and the distillation loss against them
+// (the entry points declared in include/dspark.h).
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+
+#include "../host_checks.hpp"
+#include "distill.hpp"
+#include "dspark.h"
+#include "shape.hpp"
+#include "top.hpp"
+
+namespace dspark {
+namespace {
+
+int fail(int code, const char* msg) { return host_fail(code, msg); }
+
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+// a temperature whose reciprocal is a finite binary32 above 0
+bool temperature_ok(float t) { return t > 0.0f && std::isfinite(t) && std::isfinite(1.0f / t) && 1.0f / t > 0.0f; }
+
+// a grid of at least n workgroups in two dimensions (a launch takes fewer
+// than 2^32 threads per dimension)
+dim3 grid_of(int64_t n) {
+  const int64_t x = std::min<int64_t>(n, 1 << 20);
+  return dim3((unsigned)x, (unsigned)((n + x - 1) / x));
+}
+
+// Output rows beside input rows: the same memory (same type and stride) or
+// memory apart.
+int check_out(const dspark_rows* in, const void* out, int32_t dtype, int64_t stride) {
+  if (stride < in->vocab) return fail(DSPARK_EINVAL, "output stride < vocab");
+  const int64_t es = dtype == DSPARK_BF16 ? 2 : 4, ei = in->dtype == DSPARK_BF16 ? 2 : 4;
+  if (!aligned16(out) || ((stride * es) & 15) != 0)
+    return fail(DSPARK_EALIGN, "output rows must start 16-byte aligned (data and stride * element size)");
+  if (in->n_rows == 0) return DSPARK_SUCCESS;
+  if (!out) return fail(DSPARK_EINVAL, "NULL output rows");
+  if (out == in->data) {
+    if (dtype != in->dtype || stride != in->row_stride)
+      return fail(DSPARK_EINVAL, "in place needs the input's type and row stride");
+    return DSPARK_SUCCESS;
+  }
+  const char *a = static_cast<const char*>(in->data), *b = static_cast<const char*>(out);
+  const char* ae = a + ((in->n_rows - 1) * in->row_stride + in->vocab) * ei;
+  const char* be = b + ((in->n_rows - 1) * stride + in->vocab) * es;
+  if (a < be && b < ae) return fail(DSPARK_EINVAL, "output rows overlap the input rows");
+  return DSPARK_SUCCESS;
+}
+
+// ids per slice for `owners` workgroup owners (requests or rows) of V ids
+int slice_of(int64_t owners, int64_t V, int64_t most, int64_t want) {
+  const int64_t all = (V + kSliceStep - 1) / kSliceStep;                       // groups of a row
+  const int64_t n = std::max<int64_t>(1, std::min(all, want / std::max<int64_t>(owners, 1)));  // slices wanted
+  const int64_t groups = (all + n - 1) / n;
+  return (int)(std::min<int64_t>(groups, most / kSliceStep) * kSliceStep);
+}
+
+template <int TI, int TO>
+void launch_shape(const ShapeArgs& a, size_t lds, hipStream_t s) {
+  hipLaunchKernelGGL(HIP_KERNEL_NAME(shape_kernel<TI, TO>), grid_of(a.n_requests * a.slices), dim3(kSliceBS), lds, s, a);
+}
+
+}  // namespace
+}  // namespace dspark
+
+using namespace dspark;
+
+extern "C" {
+
+int dspark_shape_logits(const dspark_rows* rows, const dspark_shaping* how, void* out, int32_t out_dtype,
+                        int64_t out_stride, int32_t* row_status, void* stream) {
+  int rc = host_check_rows(rows, "rows NULL");
+  if (rc) return rc;
+  if (!how) return fail(DSPARK_EINVAL, "NULL shaping");
+  if (out_dtype != rows->dtype && out_dtype != DSPARK_F32)
+    return fail(DSPARK_EINVAL, "out_dtype must be the rows' type or F32");
+  if (how->rows_per_request < 1) return fail(DSPARK_EINVAL, "rows_per_request must be at least 1");
+  if (rows->n_rows % how->rows_per_request != 0) return fail(DSPARK_EINVAL, "n_rows is not a multiple of rows_per_request");
+  rc = check_out(rows, out, out_dtype, out_stride);
+  if (rc) return rc;
+  if (how->history && (how->history_max < 0 || how->history_stride < how->history_max || how->history_max > 0x7fffffff))
+    return fail(DSPARK_EINVAL, "history_max must be in [0, history_stride]");
+  if (how->draft && how->draft_stride < how->rows_per_request - 1)
+    return fail(DSPARK_EINVAL, "draft_stride < rows_per_request - 1");
+  if (how->bias_offset && how->bias_total < 0) return fail(DSPARK_EINVAL, "bias_total < 0");
+  if (how->mask && (how->n_masks < 0 || how->mask_stride < (rows->vocab + 31) / 32))
+    return fail(DSPARK_EINVAL, "mask_stride is shorter than the vocabulary's bits");
+  if (rows->n_rows == 0) return DSPARK_SUCCESS;
+  if (!row_status) return fail(DSPARK_EINVAL, "NULL row_status");
+  if (how->history && !how->history_len) return fail(DSPARK_EINVAL, "history needs history_len");
+  if (how->bias_offset && how->bias_total > 0 && (!how->bias_ids || !how->bias_values))
+    return fail(DSPARK_EINVAL, "bias_offset needs bias_ids and bias_values");
+  if (how->mask && !how->mask_row && how->n_masks < rows->n_rows)
+    return fail(DSPARK_EINVAL, "fewer masks than rows and no mask_row");
+  ShapeArgs a;
+  a.x = rows->data;
+  a.x_stride = rows->row_stride;
+  a.out = out;
+  a.out_stride = out_stride;
+  a.row_status = row_status;
+  a.n_requests = rows->n_rows / how->rows_per_request;
+  a.V = (int)rows->vocab;
+  a.how = *how;
+  a.slice = slice_of(a.n_requests, a.V, 8192, 2048);
+  a.slices = (a.V + a.slice - 1) / a.slice;
+  const size_t lds = 4u * ((size_t)a.slice + 2u * ((size_t)a.slice / 32));
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  if (rows->dtype == DSPARK_F32) launch_shape<DSPARK_F32, DSPARK_F32>(a, lds, s);
+  else if (out_dtype == DSPARK_BF16) launch_shape<DSPARK_BF16, DSPARK_BF16>(a, lds, s);
+  else launch_shape<DSPARK_BF16, DSPARK_F32>(a, lds, s);
+  return host_check_launch();
+}
+
+size_t dspark_top_logits_workspace(int64_t n_rows, int64_t vocab, int32_t k_max) {
+  (void)n_rows;
+  (void)vocab;
+  (void)k_max;
+  return 0;
+}
+
+int dspark_top_logits(const dspark_rows* rows, const int32_t* topk, int32_t k_max, float temperature, int32_t* ids,
+                      float* logits, int32_t* len, float* lse, int32_t* row_status, void* ws, size_t ws_bytes,
+                      void* stream) {
+  (void)ws;
+  (void)ws_bytes;
+  int rc = host_check_rows(rows, "rows NULL");
+  if (rc) return rc;
+  if (k_max < 0 || k_max > DSPARK_K_MAX) return fail(DSPARK_EINVAL, "k_max must be in [0, DSPARK_K_MAX]");
+  if (!temperature_ok(temperature)) return fail(DSPARK_EINVAL, "temperature must be above 0 with a finite reciprocal");
+  if (rows->n_rows == 0) return DSPARK_SUCCESS;
+  if (!len || !row_status || (k_max > 0 && (!ids || !logits))) return fail(DSPARK_EINVAL, "NULL output");
+  TopArgs a;
+  a.n = rows->n_rows;
+  a.x = rows->data;
+  a.stride = rows->row_stride;
+  a.V = (int)rows->vocab;
+  a.topk = topk;
+  a.k_max = k_max;
+  a.inv_t = 1.0 / (double)temperature;
+  a.ids = ids;
+  a.logits = logits;
+  a.len = len;
+  a.lse = lse;
+  a.row_status = row_status;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  const dim3 grid = grid_of(a.n);
+  if (rows->dtype == DSPARK_F32) hipLaunchKernelGGL(top_stream_kernel<DSPARK_F32>, grid, dim3(BS), 0, s, a);
+  else if (a.V > NI * BS * 8) hipLaunchKernelGGL(top_stream_kernel<DSPARK_BF16>, grid, dim3(BS), 0, s, a);
+  else hipLaunchKernelGGL(top_bf16_kernel, grid, dim3(BS), 0, s, a);
+  return host_check_launch();
+}
+
+}  // extern "C"
+
+namespace dspark {
+namespace {
+
+constexpr int kDistillSliceMost = 32768;
+
+int distill_slice_ids(int64_t n, int64_t V) {
+  const int s = slice_of(n, V, kDistillSliceMost, 2048);
+  // at most 64 slices: one lane each when a row is joined
+  const int64_t least = ((V + 63) / 64 + kSliceStep - 1) / kSliceStep * kSliceStep;
+  return (int)std::max<int64_t>(s, least);
+}
+size_t distill_part_bytes(int64_t n, int64_t V) {
+  const int64_t s = distill_slice_ids(n, V);
+  return (size_t)n * (size_t)((V + s - 1) / s) * sizeof(DistillPart);
+}
+
+int check_distill(const dspark_rows* student, const dspark_teacher* t, float temperature) {
+  int rc = host_check_rows(student, "student rows NULL");
+  if (rc) return rc;
+  if (!t) return fail(DSPARK_EINVAL, "NULL teacher");
+  if (t->k_max < 0 || t->k_max > DSPARK_K_MAX) return fail(DSPARK_EINVAL, "k_max must be in [0, DSPARK_K_MAX]");
+  if (!temperature_ok(temperature)) return fail(DSPARK_EINVAL, "temperature must be above 0 with a finite reciprocal");
+  if (student->n_rows > 0 && (!t->len || (t->k_max > 0 && (!t->ids || !t->logits))))
+    return fail(DSPARK_EINVAL, "NULL teacher list");
+  return DSPARK_SUCCESS;
+}
+
+int check_distill_ws(const dspark_rows* student, const void* ws, size_t ws_bytes) {
+  if (!aligned16(ws)) return fail(DSPARK_EALIGN, "workspace must be 16-byte aligned");
+  if (!ws || ws_bytes < dspark_distill_workspace(student->n_rows, student->vocab))
+    return fail(DSPARK_EWORKSPACE, "workspace smaller than dspark_distill_workspace()");
+  return DSPARK_SUCCESS;
+}
+
+DistillArgs distill_args(const dspark_rows* student, const dspark_teacher* t, float temperature, void* ws) {
+  DistillArgs a{};
+  a.x = student->data;
+  a.x_stride = student->row_stride;
+  a.n = student->n_rows;
+  a.V = (int)student->vocab;
+  a.slice = distill_slice_ids(a.n, a.V);
+  a.slices = (a.V + a.slice - 1) / a.slice;
+  a.ids = t->ids;
+  a.logits = t->logits;
+  a.len = t->len;
+  a.lse = t->lse;
+  a.k_max = t->k_max;
+  a.inv_t = 1.0 / (double)temperature;
+  a.part = static_cast<DistillPart*>(ws);
+  if (ws) a.list_status = reinterpret_cast<int32_t*>(static_cast<char*>(ws) + distill_part_bytes(a.n, a.V));
+  return a;
+}
+
+size_t distill_lds(const DistillArgs& a) { return 2u * 4u * ((size_t)a.slice / 32); }
+
+void launch_part(const DistillArgs& a, int dtype, hipStream_t s) {
+  const dim3 grid = grid_of(a.n * a.slices);
+  if (dtype == DSPARK_BF16) hipLaunchKernelGGL(distill_part_kernel<DSPARK_BF16>, grid, dim3(kSliceBS), distill_lds(a), s, a);
+  else hipLaunchKernelGGL(distill_part_kernel<DSPARK_F32>, grid, dim3(kSliceBS), distill_lds(a), s, a);
+}
+template <bool FROM_STATS>
+void launch_grad(const DistillArgs& a, int dtype, hipStream_t s) {
+  const dim3 grid = grid_of(a.n * a.slices);
+  if (dtype == DSPARK_BF16)
+    hipLaunchKernelGGL(HIP_KERNEL_NAME(distill_grad_kernel<DSPARK_BF16, FROM_STATS>), grid, dim3(kSliceBS), distill_lds(a), s, a);
+  else
+    hipLaunchKernelGGL(HIP_KERNEL_NAME(distill_grad_kernel<DSPARK_F32, FROM_STATS>), grid, dim3(kSliceBS), distill_lds(a), s, a);
+}
+
+}  // namespace
+}  // namespace dspark
+
+extern "C" {
+
+size_t dspark_distill_workspace(int64_t n_rows, int64_t vocab) {
+  if (n_rows <= 0 || n_rows > (1 << 24) || vocab < 1 || vocab > DSPARK_V_MAX) return 0;
+  return distill_part_bytes(n_rows, vocab) + 4u * (size_t)n_rows;
+}
+
+int dspark_distill(const dspark_rows* student, const dspark_teacher* teacher, float temperature, float* loss,
+                   double* stats, int32_t* row_status, void* ws, size_t ws_bytes, void* stream) {
+  int rc = check_distill(student, teacher, temperature);
+  if (rc) return rc;
+  if (student->n_rows == 0) return DSPARK_SUCCESS;
+  if (!loss || !stats || !row_status) return fail(DSPARK_EINVAL, "NULL output");
+  rc = check_distill_ws(student, ws, ws_bytes);
+  if (rc) return rc;
+  DistillArgs a = distill_args(student, teacher, temperature, ws);
+  a.loss = loss;
+  a.stats = stats;
+  a.row_status = row_status;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  launch_part(a, student->dtype, s);
+  hipLaunchKernelGGL(distill_join_kernel, grid_of((a.n + kSliceNW - 1) / kSliceNW), dim3(kSliceBS), 0, s, a);
+  return host_check_launch();
+}
+
+int dspark_distill_backward(const dspark_rows* student, const dspark_teacher* teacher, float temperature,
+                            const double* stats, const int32_t* row_status, const float* grad_loss, void* grad,
+                            int64_t grad_stride, void* stream) {
+  int rc = check_distill(student, teacher, temperature);
+  if (rc) return rc;
+  rc = check_out(student, grad, student->dtype, grad_stride);
+  if (rc) return rc;
+  if (student->n_rows == 0) return DSPARK_SUCCESS;
+  if (!stats || !row_status || !grad_loss) return fail(DSPARK_EINVAL, "NULL stats, row_status or grad_loss");
+  DistillArgs a = distill_args(student, teacher, temperature, nullptr);
+  a.stats_in = stats;
+  a.status_in = row_status;
+  a.weight = grad_loss;
+  a.grad = grad;
+  a.grad_stride = grad_stride;
+  launch_grad<true>(a, student->dtype, static_cast<hipStream_t>(stream));
+  return host_check_launch();
+}
+
+int dspark_distill_step(const dspark_rows* student, const dspark_teacher* teacher, float temperature,
+                        const float* weight, float* loss, void* grad, int64_t grad_stride, int32_t* row_status,
+                        void* ws, size_t ws_bytes, void* stream) {
+  int rc = check_distill(student, teacher, temperature);
+  if (rc) return rc;
+  rc = check_out(student, grad, student->dtype, grad_stride);
+  if (rc) return rc;
+  if (student->n_rows == 0) return DSPARK_SUCCESS;
+  if (!weight || !loss || !row_status) return fail(DSPARK_EINVAL, "NULL weight or output");
+  rc = check_distill_ws(student, ws, ws_bytes);
+  if (rc) return rc;
+  DistillArgs a = distill_args(student, teacher, temperature, ws);
+  a.loss = loss;
+  a.row_status = row_status;
+  a.weight = weight;
+  a.grad = grad;
+  a.grad_stride = grad_stride;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  launch_part(a, student->dtype, s);
+  launch_grad<false>(a, student->dtype, s);
+  return host_check_launch();
+}
+
+}  // extern "C"

@@ -1,0 +1,131 @@
+// What the operators on vocabulary slices share: a workgroup of 256 threads
+// works on one slice of a row's ids, in groups of eight consecutive logits
+// per thread (one 16-byte load of bf16, two of float32).
+#pragma once
+#include "../device_common.hpp"
+
+namespace dspark {
+
+constexpr int kSliceBS = 256;
+constexpr int kSliceNW = kSliceBS / 64;
+constexpr int kSliceStep = kSliceBS * 8;  // ids of one group per thread
+
+// The workgroup's number in a grid of `total` workgroups laid out by grid_of
+// (host side); -1 past the end (uniform).
+__device__ __forceinline__ int64_t block_number(int64_t total) {
+  const int64_t b = (int64_t)blockIdx.y * gridDim.x + blockIdx.x;
+  return b < total ? b : -1;
+}
+
+typedef unsigned int v4u __attribute__((ext_vector_type(4)));
+typedef float v4f __attribute__((ext_vector_type(4)));
+
+__device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+// two binary32 values rounded to nearest even bf16 (NaN stays NaN)
+__device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
+  typedef __bf16 b2 __attribute__((ext_vector_type(2)));
+  const b2 r = {(__bf16)lo, (__bf16)hi};
+  return __builtin_bit_cast(uint32_t, r);
+}
+
+template <int DT>
+struct El;
+template <>
+struct El<DSPARK_BF16> {
+  typedef uint16_t T;
+  static __device__ __forceinline__ float get(const T* p, int64_t i) { return __uint_as_float((uint32_t)p[i] << 16); }
+  static __device__ __forceinline__ void put(T* p, int64_t i, float x) { p[i] = (T)(bf16_pair(x, x) & 0xffffu); }
+};
+template <>
+struct El<DSPARK_F32> {
+  typedef float T;
+  static __device__ __forceinline__ float get(const T* p, int64_t i) { return p[i]; }
+  static __device__ __forceinline__ void put(T* p, int64_t i, float x) { p[i] = x; }
+};
+
+// The eight logits of a row from id v on (v a multiple of 8; ids past V read
+// as -inf and touch no memory).  NT: streamed, not read again soon.
+template <int DT, bool NT>
+__device__ __forceinline__ void load8(const typename El<DT>::T* row, int v, int V, float (&x)[8]) {
+  if (v + 8 <= V) {
+    if constexpr (DT == DSPARK_BF16) {
+      const v4u* p = reinterpret_cast<const v4u*>(row + v);
+      const v4u u = NT ? __builtin_nontemporal_load(p) : *p;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        x[2 * i] = bf16_lo(u[i]);
+        x[2 * i + 1] = bf16_hi(u[i]);
+      }
+    } else {
+      const v4f* p = reinterpret_cast<const v4f*>(row + v);
+      const v4f a = NT ? __builtin_nontemporal_load(p) : p[0];
+      const v4f b = NT ? __builtin_nontemporal_load(p + 1) : p[1];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        x[i] = a[i];
+        x[4 + i] = b[i];
+      }
+    }
+  } else {
+#pragma unroll
+    for (int l = 0; l < 8; ++l) x[l] = v + l < V ? El<DT>::get(row, v + l) : -__builtin_inff();
+  }
+}
+
+template <int DT>
+__device__ __forceinline__ void store8(typename El<DT>::T* row, int v, int V, const float (&x)[8]) {
+  if (v + 8 <= V) {
+    if constexpr (DT == DSPARK_BF16) {
+      const v4u u = {bf16_pair(x[0], x[1]), bf16_pair(x[2], x[3]), bf16_pair(x[4], x[5]), bf16_pair(x[6], x[7])};
+      __builtin_nontemporal_store(u, reinterpret_cast<v4u*>(row + v));
+    } else {
+      const v4f a = {x[0], x[1], x[2], x[3]}, b = {x[4], x[5], x[6], x[7]};
+      __builtin_nontemporal_store(a, reinterpret_cast<v4f*>(row + v));
+      __builtin_nontemporal_store(b, reinterpret_cast<v4f*>(row + v) + 1);
+    }
+  } else {
+#pragma unroll
+    for (int l = 0; l < 8; ++l)
+      if (v + l < V) El<DT>::put(row, v + l, x[l]);
+  }
+}
+
+// Reductions over a workgroup of NWV waves (every thread calls, every thread
+// gets the result; scratch: NWV values in LDS, free again after the barrier
+// that the next use starts with).
+template <int NWV, class T, class OP>
+__device__ __forceinline__ T group_reduce(T v, T id, OP op, T* scratch) {
+  v = wave_reduce(v, id, op);
+  __syncthreads();
+  if (lane_id() == 0) scratch[wave_id()] = v;
+  __syncthreads();
+  T r = scratch[0];
+#pragma unroll
+  for (int w = 1; w < NWV; ++w) r = op(r, scratch[w]);
+  return r;
+}
+
+// A set of a slice's ids as a bitmap, with the number of the list entry that
+// each word's first id has: the entry of a member is its word's number plus
+// the members before it in the word (the list is ascending).
+struct IdSet {
+  uint32_t* bits;   // one per id
+  uint32_t* first;  // one per word of bits, set where the word is not empty
+  __device__ __forceinline__ void clear(int words) {
+    for (int i = threadIdx.x; i < words; i += blockDim.x) bits[i] = 0u;
+  }
+  // entry e has slice-local id t; prev: the id of the entry before it, relative to the same start (negative: none here)
+  __device__ __forceinline__ void add(int t, int prev, uint32_t e) {
+    atomicOr(&bits[t >> 5], 1u << (t & 31));
+    if (prev < 0 || (prev >> 5) != (t >> 5)) first[t >> 5] = e;
+  }
+  __device__ __forceinline__ uint32_t byte(int t) const {  // members among t .. t + 7 (t a multiple of 8)
+    return (bits[t >> 5] >> (t & 31)) & 0xffu;
+  }
+  __device__ __forceinline__ uint32_t entry(int t) const {
+    return first[t >> 5] + (uint32_t)__builtin_popcount(bits[t >> 5] & ((1u << (t & 31)) - 1u));
+  }
+};
+
+}  // namespace dspark
