@@ -63,6 +63,29 @@ void launch_shape(const ShapeArgs& a, size_t lds, hipStream_t s) {
   hipLaunchKernelGGL(HIP_KERNEL_NAME(shape_kernel<TI, TO>), grid_of(a.n_requests * a.slices), dim3(kSliceBS), lds, s, a);
 }
 
+// How dspark_top_logits cuts rows: none (bytes 0) where the sample cannot
+// place the threshold or the lists would be long.  The sample's rank leaves
+// four standard deviations above the count expected of the top k.
+struct TopPlan {
+  int slices, cap, rank;
+  size_t bytes, part_bytes;
+};
+TopPlan top_plan(int64_t n, int64_t V, int64_t k_max) {
+  TopPlan p{};
+  if (V < 2 * kTopSample) return p;
+  const double mu = (double)std::max<int64_t>(std::min(k_max, V), 1) * kTopSample / (double)V;
+  p.rank = (int)std::ceil(mu + 4.0 * std::sqrt(mu) + 4.0);
+  if (p.rank > 160) return p;
+  // logits of the sample above the rank-th of its 256 maxima, and so of a slice and of the row
+  const double above = -std::log(1.0 - p.rank / 256.0) * 256.0;
+  if (above * (double)V / kTopSample > 0.6 * kTopPer * BS) return p;
+  p.slices = (int)((V + kTopSlice - 1) / kTopSlice);
+  p.cap = (int)std::min<double>(kTopSlice, std::ceil((3.0 * above * kTopSlice / kTopSample + 64.0) / 64.0) * 64.0);
+  p.part_bytes = (size_t)n * (size_t)p.slices * sizeof(TopPart);
+  p.bytes = (size_t)n * (size_t)p.slices * (size_t)p.cap * 8u + p.part_bytes;
+  return p;
+}
+
 }  // namespace
 }  // namespace dspark
 
@@ -115,24 +138,25 @@ int dspark_shape_logits(const dspark_rows* rows, const dspark_shaping* how, void
 }
 
 size_t dspark_top_logits_workspace(int64_t n_rows, int64_t vocab, int32_t k_max) {
-  (void)n_rows;
-  (void)vocab;
-  (void)k_max;
-  return 0;
+  if (n_rows <= 0 || n_rows > (1 << 24) || vocab < 1 || vocab > DSPARK_V_MAX || k_max < 0 || k_max > DSPARK_K_MAX) return 0;
+  return top_plan(n_rows, vocab, k_max).bytes;
 }
 
 int dspark_top_logits(const dspark_rows* rows, const int32_t* topk, int32_t k_max, float temperature, int32_t* ids,
                       float* logits, int32_t* len, float* lse, int32_t* row_status, void* ws, size_t ws_bytes,
                       void* stream) {
-  (void)ws;
-  (void)ws_bytes;
   int rc = host_check_rows(rows, "rows NULL");
   if (rc) return rc;
   if (k_max < 0 || k_max > DSPARK_K_MAX) return fail(DSPARK_EINVAL, "k_max must be in [0, DSPARK_K_MAX]");
   if (!temperature_ok(temperature)) return fail(DSPARK_EINVAL, "temperature must be above 0 with a finite reciprocal");
   if (rows->n_rows == 0) return DSPARK_SUCCESS;
   if (!len || !row_status || (k_max > 0 && (!ids || !logits))) return fail(DSPARK_EINVAL, "NULL output");
-  TopArgs a;
+  const TopPlan plan = top_plan(rows->n_rows, rows->vocab, k_max);
+  if (!aligned16(ws)) return fail(DSPARK_EALIGN, "workspace must be 16-byte aligned");
+  if (plan.bytes > 0 && (!ws || ws_bytes < plan.bytes))
+    return fail(DSPARK_EWORKSPACE, "workspace smaller than dspark_top_logits_workspace()");
+  TopSliceArgs q{};
+  TopArgs& a = q.a;
   a.n = rows->n_rows;
   a.x = rows->data;
   a.stride = rows->row_stride;
@@ -147,9 +171,27 @@ int dspark_top_logits(const dspark_rows* rows, const int32_t* topk, int32_t k_ma
   a.row_status = row_status;
   hipStream_t s = static_cast<hipStream_t>(stream);
   const dim3 grid = grid_of(a.n);
-  if (rows->dtype == DSPARK_F32) hipLaunchKernelGGL(top_stream_kernel<DSPARK_F32>, grid, dim3(BS), 0, s, a);
-  else if (a.V > NI * BS * 8) hipLaunchKernelGGL(top_stream_kernel<DSPARK_BF16>, grid, dim3(BS), 0, s, a);
-  else hipLaunchKernelGGL(top_bf16_kernel, grid, dim3(BS), 0, s, a);
+  if (plan.bytes > 0) {
+    q.slices = plan.slices;
+    q.cap = plan.cap;
+    q.rank = plan.rank;
+    q.cand = ws;
+    q.part = reinterpret_cast<TopPart*>(static_cast<char*>(ws) + plan.bytes - plan.part_bytes);
+    const dim3 slices = grid_of(a.n * plan.slices);
+    if (rows->dtype == DSPARK_F32) {
+      hipLaunchKernelGGL(top_slice_kernel<DSPARK_F32>, slices, dim3(kSliceBS), 0, s, q);
+      hipLaunchKernelGGL(top_select_kernel<DSPARK_F32>, grid, dim3(BS), 0, s, q);
+    } else {
+      hipLaunchKernelGGL(top_slice_kernel<DSPARK_BF16>, slices, dim3(kSliceBS), 0, s, q);
+      hipLaunchKernelGGL(top_select_kernel<DSPARK_BF16>, grid, dim3(BS), 0, s, q);
+    }
+  } else if (rows->dtype == DSPARK_F32) {
+    hipLaunchKernelGGL(top_stream_kernel<DSPARK_F32>, grid, dim3(BS), 0, s, a);
+  } else if (a.V > NI * BS * 8) {
+    hipLaunchKernelGGL(top_stream_kernel<DSPARK_BF16>, grid, dim3(BS), 0, s, a);
+  } else {
+    hipLaunchKernelGGL(top_bf16_kernel, grid, dim3(BS), 0, s, a);
+  }
   return host_check_launch();
 }
 
