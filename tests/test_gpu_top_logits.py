@@ -64,6 +64,35 @@ def test_top_long(dtype, V, n):
     check_rows(a, dtype, ks, 2.0, g)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("V", [2048, 2049, 4096, 8192, 8193, 16384, 16385, 16391, 24577])
+@pytest.mark.parametrize("k", [7, 1024])
+def test_top_around_the_sizes_where_the_kernel_changes(dtype, V, k):
+    rng = np.random.default_rng(V + k)
+    a = rows_of(rng, 3, V, dtype)
+    g = B.top_logits(to_dev(a, dtype), k, temperature=1.3)
+    check_rows(a, dtype, [k] * 3, 1.3, g)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_top_where_the_sample_misleads(dtype):
+    """The largest logits all inside, or all outside, the sampled runs."""
+    rng = np.random.default_rng(77)
+    V, k = 40003, 600
+    step = (V // 64) & ~7
+    sampled = np.zeros(V, bool)
+    for c in range(64):
+        sampled[c * step:c * step + 32] = True
+    x = (rng.standard_normal((4, V)) * 2).astype(np.float32)
+    x[0, sampled] += 40.0                       # a threshold above nearly all of the top k
+    x[1, ~sampled] += 40.0                      # one below nearly all logits
+    x[2, 100:100 + k] += 60.0                   # the top k in one slice
+    x[3, ::2] = -np.inf
+    a = W.f32_to_bf16_bits(x) if dtype == "bf16" else x
+    g = B.top_logits(to_dev(a, dtype), k)
+    check_rows(a, dtype, [k] * 4, 1.0, g)
+
+
 def special_rows(rng, V, dtype):
     x = (rng.standard_normal((14, V)) * 2).astype(np.float32)
     x[0, rng.random(V) < 0.5] = -np.inf

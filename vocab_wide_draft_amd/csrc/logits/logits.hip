@@ -63,27 +63,45 @@ void launch_shape(const ShapeArgs& a, size_t lds, hipStream_t s) {
   hipLaunchKernelGGL(HIP_KERNEL_NAME(shape_kernel<TI, TO>), grid_of(a.n_requests * a.slices), dim3(kSliceBS), lds, s, a);
 }
 
-// How dspark_top_logits cuts rows: none (bytes 0) where the sample cannot
-// place the threshold or the lists would be long.  The sample's rank leaves
-// four standard deviations above the count expected of the top k.
+// How dspark_top_logits cuts rows longer than kTopSmall (bytes 0: not at
+// all).  The sample's rank leaves four standard deviations above the count
+// expected of the top k.
 struct TopPlan {
-  int slices, cap, rank;
+  int slices, cap, rank, waves;
   size_t bytes, part_bytes;
 };
 TopPlan top_plan(int64_t n, int64_t V, int64_t k_max) {
   TopPlan p{};
-  if (V < 2 * kTopSample) return p;
-  const double mu = (double)std::max<int64_t>(std::min(k_max, V), 1) * kTopSample / (double)V;
-  p.rank = (int)std::ceil(mu + 4.0 * std::sqrt(mu) + 4.0);
-  if (p.rank > 160) return p;
+  if (V <= kTopSmall) return p;
+  const double mu = (double)std::max<int64_t>(k_max, 1) * kTopSample / (double)V;  // < 128
+  p.rank = (int)std::ceil(mu + 4.0 * std::sqrt(mu) + 4.0);                         // < 178
   // logits of the sample above the rank-th of its 256 maxima, and so of a slice and of the row
   const double above = -std::log(1.0 - p.rank / 256.0) * 256.0;
-  if (above * (double)V / kTopSample > 0.6 * kTopPer * BS) return p;
+  const double row = above * (double)V / kTopSample;
+  p.waves = row * 2.5 <= kTopPer * 256 ? 4 : row * 2.5 <= kTopPer * 512 ? 8 : 16;
   p.slices = (int)((V + kTopSlice - 1) / kTopSlice);
   p.cap = (int)std::min<double>(kTopSlice, std::ceil((3.0 * above * kTopSlice / kTopSample + 64.0) / 64.0) * 64.0);
   p.part_bytes = (size_t)n * (size_t)p.slices * sizeof(TopPart);
   p.bytes = (size_t)n * (size_t)p.slices * (size_t)p.cap * 8u + p.part_bytes;
   return p;
+}
+
+template <int DT>
+void launch_top_slices(const TopSliceArgs& q, const TopPlan& plan, hipStream_t s) {
+  hipLaunchKernelGGL(top_slice_kernel<DT>, grid_of(q.a.n * plan.slices), dim3(kSliceBS), 0, s, q);
+  const dim3 grid = grid_of(q.a.n);
+  if (plan.waves == 4) hipLaunchKernelGGL(HIP_KERNEL_NAME(top_select_kernel<DT, 4>), grid, dim3(256), 0, s, q);
+  else if (plan.waves == 8) hipLaunchKernelGGL(HIP_KERNEL_NAME(top_select_kernel<DT, 8>), grid, dim3(512), 0, s, q);
+  else hipLaunchKernelGGL(HIP_KERNEL_NAME(top_select_kernel<DT, 16>), grid, dim3(1024), 0, s, q);
+}
+
+template <int DT>
+void launch_top_small(const TopArgs& a, hipStream_t s) {
+  const dim3 grid = grid_of(a.n);
+  if (a.V <= 2048) hipLaunchKernelGGL(HIP_KERNEL_NAME(top_small_kernel<DT, 4, 1>), grid, dim3(256), 0, s, a);
+  else if (a.V <= 4096) hipLaunchKernelGGL(HIP_KERNEL_NAME(top_small_kernel<DT, 8, 1>), grid, dim3(512), 0, s, a);
+  else if (a.V <= 8192) hipLaunchKernelGGL(HIP_KERNEL_NAME(top_small_kernel<DT, 16, 1>), grid, dim3(1024), 0, s, a);
+  else hipLaunchKernelGGL(HIP_KERNEL_NAME(top_small_kernel<DT, 16, 2>), grid, dim3(1024), 0, s, a);
 }
 
 }  // namespace
@@ -164,33 +182,25 @@ int dspark_top_logits(const dspark_rows* rows, const int32_t* topk, int32_t k_ma
   a.topk = topk;
   a.k_max = k_max;
   a.inv_t = 1.0 / (double)temperature;
+  a.c = (float)(1.4426950408889634 * a.inv_t);
   a.ids = ids;
   a.logits = logits;
   a.len = len;
   a.lse = lse;
   a.row_status = row_status;
   hipStream_t s = static_cast<hipStream_t>(stream);
-  const dim3 grid = grid_of(a.n);
   if (plan.bytes > 0) {
     q.slices = plan.slices;
     q.cap = plan.cap;
     q.rank = plan.rank;
     q.cand = ws;
     q.part = reinterpret_cast<TopPart*>(static_cast<char*>(ws) + plan.bytes - plan.part_bytes);
-    const dim3 slices = grid_of(a.n * plan.slices);
-    if (rows->dtype == DSPARK_F32) {
-      hipLaunchKernelGGL(top_slice_kernel<DSPARK_F32>, slices, dim3(kSliceBS), 0, s, q);
-      hipLaunchKernelGGL(top_select_kernel<DSPARK_F32>, grid, dim3(BS), 0, s, q);
-    } else {
-      hipLaunchKernelGGL(top_slice_kernel<DSPARK_BF16>, slices, dim3(kSliceBS), 0, s, q);
-      hipLaunchKernelGGL(top_select_kernel<DSPARK_BF16>, grid, dim3(BS), 0, s, q);
-    }
+    if (rows->dtype == DSPARK_F32) launch_top_slices<DSPARK_F32>(q, plan, s);
+    else launch_top_slices<DSPARK_BF16>(q, plan, s);
   } else if (rows->dtype == DSPARK_F32) {
-    hipLaunchKernelGGL(top_stream_kernel<DSPARK_F32>, grid, dim3(BS), 0, s, a);
-  } else if (a.V > NI * BS * 8) {
-    hipLaunchKernelGGL(top_stream_kernel<DSPARK_BF16>, grid, dim3(BS), 0, s, a);
+    launch_top_small<DSPARK_F32>(a, s);
   } else {
-    hipLaunchKernelGGL(top_bf16_kernel, grid, dim3(BS), 0, s, a);
+    launch_top_small<DSPARK_BF16>(a, s);
   }
   return host_check_launch();
 }

@@ -73,6 +73,12 @@ __device__ __forceinline__ void load8(const typename El<DT>::T* row, int v, int 
   }
 }
 
+// the same where all eight are there: no branch between one load and the next
+template <int DT, bool NT>
+__device__ __forceinline__ void load8_whole(const typename El<DT>::T* row, int v, float (&x)[8]) {
+  load8<DT, NT>(row, v, v + 8, x);
+}
+
 template <int DT>
 __device__ __forceinline__ void store8(typename El<DT>::T* row, int v, int V, const float (&x)[8]) {
   if (v + 8 <= V) {
@@ -104,6 +110,25 @@ __device__ __forceinline__ T group_reduce(T v, T id, OP op, T* scratch) {
 #pragma unroll
   for (int w = 1; w < NWV; ++w) r = op(r, scratch[w]);
   return r;
+}
+
+// Sum of the values of the threads before this one, over a workgroup of NWV
+// waves; *total: of all.  scratch as in group_reduce.
+template <int NWV, class T>
+__device__ __forceinline__ T group_excl_scan(T v, T* scratch, T* total) {
+  const T inc = wave_incl_scan(v);
+  __syncthreads();
+  if (lane_id() == 63) scratch[wave_id()] = inc;
+  __syncthreads();
+  T before = inc - v, all = T(0);
+#pragma unroll
+  for (int w = 0; w < NWV; ++w) {
+    const T o = scratch[w];
+    if (w < wave_id()) before += o;
+    all += o;
+  }
+  *total = all;
+  return before;
 }
 
 // A set of a slice's ids as a bitmap, with the number of the list entry that

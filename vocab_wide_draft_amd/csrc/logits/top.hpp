@@ -1,7 +1,7 @@
 // The top logits of a row with the log-sum-exp of the whole row
 // (dspark_top_logits).
 //
-// Rows of ordinary size are cut into slices of 8,192 ids, one workgroup each,
+// Rows of more than kTopSmall ids are cut into slices of 8,192 ids, one workgroup each,
 // which reads its slice once into registers.  A threshold that the k-th
 // largest logit lies above with good odds comes from a sample of the row
 // (2,048 logits, the same for every slice of the row), so that one pass
@@ -10,10 +10,14 @@
 // selects exactly among those candidates.  A row whose candidates are too
 // few or too many for their list (heavy ties, a sample that misleads) is
 // selected from memory by that kernel's workgroup instead: slower, the same
-// answer.
+// answer.  Shorter rows are held whole in one workgroup's registers.
+//
+// Exponentials are exp2(x c - K), one fused multiply-add each, with c the
+// binary32 rounding of log2(e) / T and K = c times a maximum: the reference
+// K is exact as it stands (the sum is over 2^(x c) / 2^K), and what the
+// rounding of c does to the row's largest logits is put back in binary64
+// (sum_reference).  Where K would leave binary32 they are exp2((x - m) c).
 #pragma once
-#include "../fast_q.hpp"
-#include "../resident.hpp"
 #include "slices.hpp"
 
 namespace dspark {
@@ -26,12 +30,15 @@ struct TopArgs {
   const int32_t* topk;
   int k_max;
   double inv_t;
+  float c;  // binary32 log2(e) / T
   int32_t* ids;
   float* logits;
   int32_t* len;
   float* lse;
   int32_t* row_status;
 };
+
+constexpr double kLn2 = 0.69314718055994530942;
 
 // k of row r: -1 when out of range
 __device__ __forceinline__ int row_k(const TopArgs& a, int64_t r) {
@@ -40,103 +47,297 @@ __device__ __forceinline__ int row_k(const TopArgs& a, int64_t r) {
   return k < 0 || k > cap ? -1 : k;
 }
 
-// writes the n entries of (sh.cid, sh.sx) and zeros behind them
-__device__ __forceinline__ void write_top(const TopArgs& a, int64_t r, int n, const RowShared& sh) {
-  for (int e = threadIdx.x; e < a.k_max; e += BS) {
-    a.ids[r * a.k_max + e] = e < n ? (int32_t)sh.cid[e] : 0;
-    a.logits[r * a.k_max + e] = e < n ? sh.sx[e] : 0.0f;
+// whether K = m c stays far inside binary32
+__device__ __forceinline__ bool reference_fits(const TopArgs& a, float m) { return __builtin_fabsf(m) * a.c < 1e30f; }
+// log of what a sum of exponentials relative to the maximum m is to be multiplied by
+__device__ __forceinline__ double sum_reference(const TopArgs& a, float m) {
+  if (!reference_fits(a, m)) return (double)m * a.inv_t;
+  return (double)(m * a.c) * kLn2 + (a.inv_t - (double)a.c * kLn2) * (double)m;
+}
+// the sum of the exponentials of N logits relative to the maximum m
+template <int N>
+__device__ __forceinline__ float exp_sum(const TopArgs& a, float m, const float (&x)[N]) {
+  float sum = 0.0f;
+  if (reference_fits(a, m)) {  // (uniform)
+    const float K = m * a.c;
+#pragma unroll
+    for (int l = 0; l < N; ++l) sum += __builtin_amdgcn_exp2f(__builtin_fmaf(x[l], a.c, -K));
+  } else {
+#pragma unroll
+    for (int l = 0; l < N; ++l) sum += __builtin_amdgcn_exp2f((x[l] - m) * a.c);
+  }
+  return sum;
+}
+
+__device__ __forceinline__ int top_status(uint32_t flags, float m, int k) {
+  return flags & 1u ? DSPARK_ST_ROW_NAN
+         : flags & 2u ? DSPARK_ST_ROW_POSINF
+         : m == -__builtin_inff() ? DSPARK_ST_ROW_ZERO_MASS
+         : k < 0 ? DSPARK_ST_BAD_TOPK : DSPARK_ST_OK;
+}
+
+template <int DT>
+__device__ __forceinline__ uint32_t top_key(float x) {  // order-preserving, 0 below every finite logit's
+  return DT == DSPARK_BF16 ? key32(x) >> 16 : key32(x);
+}
+template <int DT>
+__device__ __forceinline__ float top_key_value(uint32_t k) {  // the smallest value with that key
+  const uint32_t b = DT == DSPARK_BF16 ? k << 16 : k;
+  return __uint_as_float(b & 0x80000000u ? b & 0x7fffffffu : ~b);
+}
+
+constexpr int kTopBins = 2048;
+
+// Scratch of a selection by NWV waves.
+template <int NWV>
+struct TopScratch {
+  uint32_t hist[kTopBins];
+  uint32_t scan[NWV];
+  double red[NWV];
+  uint32_t bin, above;
+};
+
+// The bin where the running count from bin 0 on reaches `need` (which the
+// bins hold at least), and the count of the bins before it.
+template <int NWV>
+__device__ __forceinline__ uint32_t top_crossing(TopScratch<NWV>& sh, uint32_t need, uint32_t* above) {
+  constexpr int PER = kTopBins / (64 * NWV);
+  uint32_t c[PER], sum = 0, total;
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    c[i] = sh.hist[threadIdx.x * PER + i];
+    sum += c[i];
+  }
+  uint32_t run = group_excl_scan<NWV>(sum, sh.scan, &total);
+  if (run < need && need <= run + sum) {
+    int hit = -1;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      if (hit < 0) {
+        if (run + c[i] >= need) {
+          hit = i;
+          sh.bin = threadIdx.x * PER + i;
+          sh.above = run;
+        }
+        run += c[i];
+      }
+    }
+  }
+  __syncthreads();
+  *above = sh.above;
+  return sh.bin;
+}
+
+// The n largest keys (1 <= n <= how many there are; key 0: none): every key
+// above T and, of the keys equal to T, the first `ties` by id.
+struct TopCut {
+  uint32_t T, ties;
+};
+
+// Cut among keys held PER to a thread, all of them 0 or in [lo, hi]:
+// histograms of a range, narrowed to one key or to a bin taken whole.
+template <int NWV, int PER>
+__device__ __forceinline__ TopCut top_cut(const uint32_t (&key)[PER], uint32_t lo, uint32_t hi, uint32_t n, TopScratch<NWV>& sh) {
+  for (;;) {
+    const uint32_t range = hi - lo;
+    const int shift = range < (uint32_t)kTopBins ? 0 : (32 - __builtin_clz(range)) - 11;
+    for (int i = threadIdx.x; i < kTopBins; i += 64 * NWV) sh.hist[i] = 0u;
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < PER; ++j)
+      if (key[j] >= lo && key[j] <= hi) atomicAdd(&sh.hist[(hi - key[j]) >> shift], 1u);
+    __syncthreads();
+    uint32_t above;
+    const uint32_t bin = top_crossing<NWV>(sh, n, &above);
+    n -= above;
+    const uint32_t held = sh.hist[bin];
+    const uint32_t bhi = hi - (bin << shift), width = (1u << shift) - 1u;
+    const uint32_t blo = bhi - lo > width ? bhi - width : lo;
+    __syncthreads();
+    if (held == n) return TopCut{blo - 1u, 0u};  // all keys from blo on (blo >= 1)
+    if (shift == 0) return TopCut{bhi, n};
+    hi = bhi;
+    lo = blo;
   }
 }
 
-__device__ __forceinline__ void finish_top(const TopArgs& a, int64_t r, int status, int n, float m, double sum) {
+// Writes the chosen ones of a thread-major list in its order, zeros behind
+// them up to k_max.
+template <int NWV, int PER, class ID, class VALUE>
+__device__ __forceinline__ void top_write(const TopArgs& a, int64_t r, const uint32_t (&key)[PER], TopCut cut, int n,
+                                          TopScratch<NWV>& sh, ID id, VALUE value) {
+  uint32_t cnt = 0, total;  // low half: above the cut, high half: ties (each at most PER 64 NWV <= 2^14)
+#pragma unroll
+  for (int j = 0; j < PER; ++j) cnt += key[j] > cut.T ? 1u : key[j] == cut.T && cut.T ? 0x10000u : 0u;
+  uint32_t pre = group_excl_scan<NWV>(cnt, sh.scan, &total);
+  int32_t* ids = a.ids + r * a.k_max;
+  float* logits = a.logits + r * a.k_max;
+#pragma unroll
+  for (int j = 0; j < PER; ++j) {
+    const bool sure = key[j] > cut.T, tie = !sure && key[j] == cut.T && cut.T;
+    const uint32_t tb = pre >> 16;
+    if (sure || (tie && tb < cut.ties)) {
+      const uint32_t pos = (pre & 0xffffu) + (tb < cut.ties ? tb : cut.ties);
+      if (pos < (uint32_t)a.k_max) {
+        ids[pos] = id(j);
+        logits[pos] = value(j);
+      }
+    }
+    pre += sure ? 1u : tie ? 0x10000u : 0u;
+  }
+  for (int e = n + (int)threadIdx.x; e < a.k_max; e += 64 * NWV) {
+    ids[e] = 0;
+    logits[e] = 0.0f;
+  }
+}
+
+__device__ __forceinline__ void top_row_out(const TopArgs& a, int64_t r, int status, int n, float lse) {
   if (threadIdx.x != 0) return;
   const bool ok = status == DSPARK_ST_OK;
   a.row_status[r] = status;
   a.len[r] = ok ? n : 0;
-  if (a.lse) a.lse[r] = ok ? (float)((double)m * a.inv_t + log(sum)) : 0.0f;
+  if (a.lse) a.lse[r] = ok ? lse : 0.0f;
 }
 
-// bf16 rows of up to NI * BS * 8 ids, held in registers
-__global__ void __launch_bounds__(BS) top_bf16_kernel(TopArgs a) {
-  __shared__ RowShared sh;
-  const int64_t r = block_number(a.n);
-  if (r < 0) return;
-  Res R;
-  res_load(R, static_cast<const uint16_t*>(a.x) + r * a.stride, a.V);
-  const RStats st = res_stats(R, sh);
-  const int k = row_k(a, r);
-  int status = st.status;
-  if (status == DSPARK_ST_OK && k < 0) status = DSPARK_ST_BAD_TOPK;
-  int n = 0;
-  double sum = 1.0;
-  const float m = bf16_to_f32(st.m_raw);
-  if (status == DSPARK_ST_OK) {
-    if (a.lse) {
-      const float c = (float)(a.inv_t * 1.4426950408889634);
-      touch(R);
-      double acc = 0.0;
+// --------------------------------------------- rows selected from memory
+// The top k of a good row whose candidates do not fit, by one workgroup:
+// digit histograms over passes of the row, then an ordered pass that writes.
+template <int DT, int NWV>
+__device__ __forceinline__ int top_from_memory(const TopArgs& a, int64_t r, int k, TopScratch<NWV>& sh) {
+  typedef typename El<DT>::T XT;
+  const XT* row = static_cast<const XT*>(a.x) + r * a.stride;
+  const int V = a.V;
+  constexpr int kStep = 64 * NWV * 8;
+  const uint32_t none = top_key<DT>(-__builtin_inff());  // -inf is not listed
+  uint32_t prefix = 0, pmask = 0, need = (uint32_t)k, n = (uint32_t)k;
+  bool first = true;
+  for (int shift = DT == DSPARK_BF16 ? 8 : 24; shift >= 0; shift -= 8) {
+    for (int i = threadIdx.x; i < kTopBins; i += 64 * NWV) sh.hist[i] = 0u;
+    __syncthreads();
+    for (int v = (int)threadIdx.x * 8; v < V; v += kStep) {
+      float x[8];
+      load8<DT, false>(row, v, V, x);
 #pragma unroll
-      for (int i = 0; i < NI; ++i) {
-        const u32x4 v = fetch(R, i);
-        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-        float part = 0.0f;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          part += __builtin_amdgcn_exp2f((bf16_lo(w[j]) - m) * c);
-          part += __builtin_amdgcn_exp2f((bf16_hi(w[j]) - m) * c);
-        }
-        acc += (double)part;
+      for (int l = 0; l < 8; ++l) {
+        const uint32_t key = top_key<DT>(x[l]);
+        const bool in = v + l < V && key > none && (key & pmask) == prefix;
+        const uint32_t bin = 255u - ((key >> shift) & 255u);  // the largest digits first
+        // equal logits meet in one bin: lanes that share the first lane's are counted together
+        const uint64_t act = __ballot(in);
+        if (!act) continue;
+        const int lead = __builtin_ctzll(act);
+        const uint32_t b0 = (uint32_t)__builtin_amdgcn_readlane((int)bin, lead);
+        const uint64_t same = __ballot(in && bin == b0);
+        if (lane_id() == lead) atomicAdd(&sh.hist[b0], (uint32_t)__builtin_popcountll(same));
+        if (in && bin != b0) atomicAdd(&sh.hist[bin], 1u);
       }
-      sum = block_sum<double>(acc, sh.bs);
     }
-    if (k > 0) n = res_topk_support(R, st, k, sh);
+    __syncthreads();
+    if (first) {  // fewer finite logits than k
+      uint32_t mine = 0, total;
+      for (int i = threadIdx.x; i < 256; i += 64 * NWV) mine += sh.hist[i];
+      (void)group_excl_scan<NWV>(mine, sh.scan, &total);
+      if (total < need) need = n = total;
+      first = false;
+    }
+    uint32_t above;
+    const uint32_t bin = top_crossing<NWV>(sh, need, &above);
+    need -= above;
+    prefix |= (255u - bin) << shift;
+    pmask |= 255u << shift;
+    __syncthreads();
   }
-  __syncthreads();
-  write_top(a, r, n, sh);
-  finish_top(a, r, status, n, m, sum);
-}
-
-// a row streamed from memory
-template <int DT>
-__device__ __forceinline__ void top_stream_row(const TopArgs& a, int64_t r, RowShared& sh) {
-  constexpr int ES = DT == DSPARK_BF16 ? 2 : 4;
-  const Row<DT> row{static_cast<const char*>(a.x) + (size_t)r * (size_t)a.stride * ES, a.V};
-  const Stats st = row_stats(row, sh.bs);
-  const int k = row_k(a, r);
-  int status = st.status;
-  if (status == DSPARK_ST_OK && k < 0) status = DSPARK_ST_BAD_TOPK;
-  int n = 0;
-  double sum = 1.0;
-  if (status == DSPARK_ST_OK) {
-    const float c = (float)(a.inv_t * 1.4426950408889634);
-    double acc = 0.0;
-    uint32_t fin = 0;
-    for_vecs<kPF, float, Row<DT>::EPV>(row.nvec(), [&](int q, float (&x)[Row<DT>::EPV]) { return row.load(q, x); },
-                                       [&](int, const float (&x)[Row<DT>::EPV], int nv) {
-      float part = 0.0f;
+  // keys above the prefix and the first `need` equal to it, in id order
+  uint32_t placed = 0, tied = 0;
+  for (int base = 0; base < V; base += kStep) {
+    const int v = base + (int)threadIdx.x * 8;
+    float x[8];
+    if (v < V) load8<DT, false>(row, v, V, x);
+    uint32_t cnt = 0, total;
 #pragma unroll
-      for (int l = 0; l < Row<DT>::EPV; ++l) {
-        part += __builtin_amdgcn_exp2f((x[l] - st.m) * c);  // (lanes past the end hold -inf)
-        fin += l < nv && x[l] > -__builtin_inff() ? 1u : 0u;
+    for (int l = 0; l < 8; ++l) {
+      const uint32_t key = v + l < V ? top_key<DT>(x[l]) : 0u;
+      cnt += key > prefix ? 1u : key == prefix ? 0x10000u : 0u;
+    }
+    uint32_t pre = group_excl_scan<NWV>(cnt, sh.scan, &total);
+#pragma unroll
+    for (int l = 0; l < 8; ++l) {
+      const uint32_t key = v + l < V ? top_key<DT>(x[l]) : 0u;
+      const uint32_t tb = tied + (pre >> 16);
+      if (key > prefix || (key == prefix && tb < need)) {
+        const uint32_t pos = placed + (pre & 0xffffu) + (tb < need ? tb : need);
+        if (pos < (uint32_t)a.k_max) {
+          a.ids[r * a.k_max + pos] = v + l;
+          a.logits[r * a.k_max + pos] = x[l];
+        }
       }
-      acc += (double)part;
-    });
-    sum = block_sum<double>(acc, sh.bs);
-    const uint32_t finite = block_sum<uint32_t>(fin, sh.bs);
-    const int take = (uint32_t)k < finite ? k : (int)finite;  // -inf entries are not listed
-    if (take > 0) n = stream_topk_support(row, st.m, st.tkey, take, sh);
+      pre += key > prefix ? 1u : key == prefix ? 0x10000u : 0u;
+    }
+    placed += total & 0xffffu;
+    tied += total >> 16;
   }
-  __syncthreads();
-  write_top(a, r, n, sh);
-  finish_top(a, r, status, n, st.m, sum);
+  for (int e = (int)n + (int)threadIdx.x; e < a.k_max; e += 64 * NWV) {
+    a.ids[r * a.k_max + e] = 0;
+    a.logits[r * a.k_max + e] = 0.0f;
+  }
+  return (int)n;
 }
 
-template <int DT>
-__global__ void __launch_bounds__(BS) top_stream_kernel(TopArgs a) {
-  __shared__ RowShared sh;
+// ------------------------------------------------------------ short rows
+constexpr int kTopSmall = 16384;  // 1,024 threads of 16 logits
+
+// A row of at most 64 NWV 8 G ids in the workgroup's registers, 8 G
+// neighbouring ones to a thread.
+template <int DT, int NWV, int G>
+__global__ void __launch_bounds__(64 * NWV) top_small_kernel(TopArgs a) {
+  __shared__ TopScratch<NWV> sh;
+  typedef typename El<DT>::T XT;
   const int64_t r = block_number(a.n);
   if (r < 0) return;
-  top_stream_row<DT>(a, r, sh);
+  const XT* row = static_cast<const XT*>(a.x) + r * a.stride;
+  const int v0 = (int)threadIdx.x * 8 * G;
+  float x[8 * G];
+  float m = -__builtin_inff();
+  uint32_t flags = 0;
+#pragma unroll
+  for (int g = 0; g < G; ++g) {
+    float y[8];
+    load8<DT, true>(row, v0 + 8 * g, a.V, y);
+#pragma unroll
+    for (int l = 0; l < 8; ++l) {
+      x[8 * g + l] = y[l];
+      m = __builtin_fmaxf(m, y[l]);
+      flags |= y[l] != y[l] ? 1u : y[l] == __builtin_inff() ? 2u : 0u;
+    }
+  }
+  const float M = group_reduce<NWV>(m, -__builtin_inff(), [](float u, float v) { return __builtin_fmaxf(u, v); },
+                                    reinterpret_cast<float*>(sh.red));
+  flags = group_reduce<NWV>(flags, 0u, [](uint32_t u, uint32_t v) { return u | v; }, sh.scan);
+  const int k = row_k(a, r);
+  const int status = top_status(flags, M, k);
+  int n = 0;
+  float lse = 0.0f;
+  uint32_t key[8 * G];
+  TopCut cut{0xffffffffu, 0u};
+  if (status == DSPARK_ST_OK) {
+    const float part = exp_sum(a, M, x);
+    uint32_t fin = 0, total;
+#pragma unroll
+    for (int j = 0; j < 8 * G; ++j) {
+      key[j] = x[j] > -__builtin_inff() ? top_key<DT>(x[j]) : 0u;
+      fin += key[j] ? 1u : 0u;
+    }
+    const double sum = group_reduce<NWV>((double)part, 0.0, [](double u, double v) { return u + v; }, sh.red);
+    lse = (float)(sum_reference(a, M) + log(sum));
+    (void)group_excl_scan<NWV>(fin, sh.scan, &total);
+    n = (uint32_t)k < total ? k : (int)total;
+    if (n > 0) cut = top_cut<NWV>(key, 1u, top_key<DT>(M), (uint32_t)n, sh);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8 * G; ++j) key[j] = 0u;
+  }
+  top_write<NWV>(a, r, key, cut, n, sh, [&](int j) { return v0 + j; }, [&](int j) { return x[j]; });
+  top_row_out(a, r, status, n, lse);
 }
 
 // ------------------------------------------------------- rows in slices
@@ -147,7 +348,7 @@ constexpr int kTopSample = kSliceBS * 8;                   // logits sampled of 
 constexpr int kTopPer = 8;                                 // candidates per thread of the selection, at most
 
 struct TopPart {
-  double sum;    // of exp((x - m) / T)
+  double sum;    // of the exponentials relative to m
   float m, t;    // the slice's maximum; the row's threshold
   int32_t flags; // 1: a NaN, 2: a +inf
   int32_t count; // candidates (more than the list holds: too many)
@@ -162,7 +363,6 @@ struct Cand<DSPARK_BF16> {
   static __device__ __forceinline__ T make(float x, int t) { return (__float_as_uint(x) & 0xffff0000u) | (uint32_t)t; }
   static __device__ __forceinline__ float value(T c) { return __uint_as_float(c & 0xffff0000u); }
   static __device__ __forceinline__ int place(T c) { return (int)(c & 0xffffu); }
-  static __device__ __forceinline__ uint32_t key(float x) { return key32(x) >> 16; }
 };
 template <>
 struct Cand<DSPARK_F32> {
@@ -170,21 +370,20 @@ struct Cand<DSPARK_F32> {
   static __device__ __forceinline__ T make(float x, int t) { return make_uint2(__float_as_uint(x), (uint32_t)t); }
   static __device__ __forceinline__ float value(T c) { return __uint_as_float(c.x); }
   static __device__ __forceinline__ int place(T c) { return (int)c.y; }
-  static __device__ __forceinline__ uint32_t key(float x) { return key32(x); }
 };
 
 struct TopSliceArgs {
   TopArgs a;
   int slices;
   int cap;      // candidates a slice's list holds
-  int rank;     // the threshold is the rank-th largest of the sample's 256 maxima
+  int rank;     // the threshold is about the rank-th largest of the sample's 256 maxima
   TopPart* part;  // [n][slices]
   void* cand;     // [n][slices][cap]
 };
 
 template <int DT>
 __global__ void __launch_bounds__(kSliceBS) top_slice_kernel(TopSliceArgs q) {
-  __shared__ __align__(16) float sample[kSliceBS];
+  __shared__ __align__(16) uint32_t sample[kSliceBS];
   __shared__ float thr;
   __shared__ uint64_t scan[kSliceNW];
   __shared__ double red[kSliceNW];
@@ -198,44 +397,52 @@ __global__ void __launch_bounds__(kSliceBS) top_slice_kernel(TopSliceArgs q) {
   const XT* row = static_cast<const XT*>(q.a.x) + r * q.a.stride;
   const int step = (V / 64) & ~7;
   float smp[8], x[kTopGroups][8];
-  load8<DT, false>(row, (tid >> 2) * step + (tid & 3) * 8, V, smp);
+  load8_whole<DT, false>(row, (tid >> 2) * step + (tid & 3) * 8, smp);
+  if (start + kTopSlice <= V) {  // (uniform)
 #pragma unroll
-  for (int i = 0; i < kTopGroups; ++i) load8<DT, true>(row, start + (i * kSliceBS + tid) * 8, V, x[i]);
+    for (int i = 0; i < kTopGroups; ++i) load8_whole<DT, true>(row, start + (i * kSliceBS + tid) * 8, x[i]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < kTopGroups; ++i) load8<DT, true>(row, start + (i * kSliceBS + tid) * 8, V, x[i]);
+  }
   float top = smp[0];
 #pragma unroll
   for (int l = 1; l < 8; ++l) top = __builtin_fmaxf(top, smp[l]);
-  if (top != top) top = -__builtin_inff();
-  sample[tid] = top;
-  if (tid == 0) thr = -__builtin_inff();
-  __syncthreads();
-  int above = 0;
-  for (int u = 0; u < kSliceBS; u += 4) {
-    const float4 o = *reinterpret_cast<const float4*>(sample + u);
-    above += (o.x > top || (o.x == top && u < tid)) ? 1 : 0;
-    above += (o.y > top || (o.y == top && u + 1 < tid)) ? 1 : 0;
-    above += (o.z > top || (o.z == top && u + 2 < tid)) ? 1 : 0;
-    above += (o.w > top || (o.w == top && u + 3 < tid)) ? 1 : 0;
-  }
-  if (above == q.rank - 1) thr = top;
+  sample[tid] = top != top ? 0u : key32(top) >> 16;
   float m = -__builtin_inff();
+  __syncthreads();
+  if (wave_id() == 0) {
+    // the largest 16-bit key that at least `rank` of the maxima reach: four
+    // maxima a lane, sixteen steps of ballots
+    const uint4 o = *reinterpret_cast<const uint4*>(sample + 4 * lane_id());
+    uint32_t T = 0;
+#pragma unroll
+    for (int bit = 15; bit >= 0; --bit) {
+      const uint32_t up = T | (1u << bit);
+      const int reach = __builtin_popcountll(__ballot(o.x >= up)) + __builtin_popcountll(__ballot(o.y >= up)) +
+                        __builtin_popcountll(__ballot(o.z >= up)) + __builtin_popcountll(__ballot(o.w >= up));
+      if (reach >= q.rank) T = up;
+    }
+    // -inf is no candidate: the threshold is the lowest finite value at least
+    const float t = top_key_value<DSPARK_BF16>(T);
+    if (lane_id() == 0) thr = t >= -3.4028235e38f ? t : -3.4028235e38f;
+  }
 #pragma unroll
   for (int i = 0; i < kTopGroups; ++i) {
 #pragma unroll
     for (int l = 0; l < 8; ++l) m = __builtin_fmaxf(m, x[i][l]);
   }
   const float M = group_reduce<kSliceNW>(m, -__builtin_inff(), [](float u, float v) { return __builtin_fmaxf(u, v); }, redf);
-  const float t = thr, c = (float)(q.a.inv_t * 1.4426950408889634), ref = M == -__builtin_inff() ? 0.0f : M;
+  const float t = thr, ref = M == -__builtin_inff() ? 0.0f : M;
   float sum = 0.0f;
   uint32_t mask[kTopGroups];
   uint64_t counts = 0;  // four 16-bit fields
 #pragma unroll
   for (int i = 0; i < kTopGroups; ++i) {
+    sum += exp_sum(q.a, ref, x[i]);
     mask[i] = 0u;
 #pragma unroll
-    for (int l = 0; l < 8; ++l) {
-      sum += __builtin_amdgcn_exp2f((x[i][l] - ref) * c);
-      mask[i] |= x[i][l] >= t && x[i][l] > -__builtin_inff() ? 1u << l : 0u;
-    }
+    for (int l = 7; l >= 0; --l) mask[i] = mask[i] + mask[i] + (x[i][l] >= t ? 1u : 0u);
     counts |= (uint64_t)__builtin_popcount(mask[i]) << (16 * i);
   }
   uint32_t flags = 0;
@@ -284,18 +491,18 @@ __global__ void __launch_bounds__(kSliceBS) top_slice_kernel(TopSliceArgs q) {
 }
 
 // One workgroup per row: joins its slices and selects among the candidates.
-template <int DT>
-__global__ void __launch_bounds__(BS) top_select_kernel(TopSliceArgs q) {
-  __shared__ RowShared sh;
+template <int DT, int NWV>
+__global__ void __launch_bounds__(64 * NWV) top_select_kernel(TopSliceArgs q) {
+  __shared__ TopScratch<NWV> sh;
   __shared__ uint32_t first[kTopSlices + 1];  // candidates before each slice
   __shared__ double row_sum;
   __shared__ float row_m;
-  __shared__ int row_flags, row_over;
+  __shared__ uint32_t row_flags, row_over;
   const TopArgs& a = q.a;
   const int64_t r = block_number(a.n);
   if (r < 0) return;
   const TopPart* part = q.part + r * q.slices;
-  if (threadIdx.x < 64) {  // two slices per lane
+  if (wave_id() == 0) {  // two slices per lane
     const int l = lane_id();
     float m = -__builtin_inff(), mm[2] = {m, m};
     double ss[2] = {0.0, 0.0};
@@ -316,7 +523,7 @@ __global__ void __launch_bounds__(BS) top_select_kernel(TopSliceArgs q) {
     double sum = 0.0;
 #pragma unroll
     for (int j = 0; j < 2; ++j)
-      if (mm[j] > -__builtin_inff()) sum += ss[j] * exp(((double)mm[j] - (double)M) * a.inv_t);
+      if (mm[j] > -__builtin_inff()) sum += ss[j] * exp(sum_reference(a, mm[j]) - sum_reference(a, M));
     sum = wave_sum(sum);
     flags = wave_reduce(flags, 0u, [](uint32_t u, uint32_t v) { return u | v; });
     over = wave_reduce(over, 0u, [](uint32_t u, uint32_t v) { return u | v; });
@@ -327,37 +534,41 @@ __global__ void __launch_bounds__(BS) top_select_kernel(TopSliceArgs q) {
     if (l == 0) {
       row_sum = sum;
       row_m = M;
-      row_flags = (int)flags;
-      row_over = (int)over;
+      row_flags = flags;
+      row_over = over;
     }
   }
   __syncthreads();
   const uint32_t total = first[kTopSlices];
-  const float M = row_m;
+  const float M = row_m, t = part[0].t;
   const int k = row_k(a, r);
-  int status = row_flags & 1 ? DSPARK_ST_ROW_NAN
-               : row_flags & 2 ? DSPARK_ST_ROW_POSINF
-               : M == -__builtin_inff() ? DSPARK_ST_ROW_ZERO_MASS
-               : k < 0 ? DSPARK_ST_BAD_TOPK : DSPARK_ST_OK;
+  const int status = top_status(row_flags, M, k);
+  float lse = 0.0f;
+  if (threadIdx.x == 0 && status == DSPARK_ST_OK) lse = (float)(sum_reference(a, M) + log(row_sum));
   int n = 0;
+  uint32_t key[kTopPer], id[kTopPer];
+  float v[kTopPer];
+#pragma unroll
+  for (int j = 0; j < kTopPer; ++j) {
+    key[j] = 0u;
+    id[j] = 0u;
+    v[j] = 0.0f;
+  }
+  TopCut cut{0xffffffffu, 0u};
   if (status == DSPARK_ST_OK && k > 0) {
-    if (row_over || total > (uint32_t)(kTopPer * BS) || (total < (uint32_t)k && part[0].t > -__builtin_inff())) {
-      top_stream_row<DT>(a, r, sh);  // (uniform)
+    if (row_over || total > (uint32_t)(kTopPer * 64 * NWV) || (total < (uint32_t)k && t > -3.4028235e38f)) {
+      n = top_from_memory<DT, NWV>(a, r, k, sh);  // (uniform)
+      top_row_out(a, r, status, n, lse);
       return;
     }
     n = total < (uint32_t)k ? (int)total : k;
-    // this thread's candidates, in id order
-    const int per = (int)((total + BS - 1) / BS);
-    float v[kTopPer];
-    uint32_t id[kTopPer], key[kTopPer];
+    // this thread's candidates: neighbours in id order
+    const int per = (int)((total + 64 * NWV - 1) / (64 * NWV));
 #pragma unroll
     for (int j = 0; j < kTopPer; ++j) {
       const uint32_t g = threadIdx.x * (uint32_t)per + (uint32_t)j;
-      key[j] = 0u;  // (below every finite logit's key)
-      v[j] = 0.0f;
-      id[j] = 0u;
       if (j < per && g < total) {
-        int lo = 0, hi = q.slices - 1;  // the last slice with first <= g
+        int lo = 0, hi = q.slices - 1;  // the last slice that starts at or before g
         while (lo < hi) {
           const int mid = (lo + hi + 1) >> 1;
           if (first[mid] <= g) lo = mid;
@@ -366,67 +577,13 @@ __global__ void __launch_bounds__(BS) top_select_kernel(TopSliceArgs q) {
         const typename Cand<DT>::T e = (static_cast<const typename Cand<DT>::T*>(q.cand) + (r * q.slices + lo) * q.cap)[g - first[lo]];
         v[j] = Cand<DT>::value(e);
         id[j] = (uint32_t)(lo * kTopSlice + Cand<DT>::place(e));
-        key[j] = Cand<DT>::key(v[j]);
+        key[j] = top_key<DT>(v[j]);
       }
     }
-    // the n-th largest key: histograms of a range of keys, narrowed to one key or one full bin
-    uint32_t hi = Cand<DT>::key(M), lo = 1u, T;
-    if (part[0].t > -__builtin_inff()) lo = Cand<DT>::key(part[0].t);
-    uint32_t need = (uint32_t)n, ties;  // of the keys equal to T, the first `ties` by id
-    bool all_ge = false;
-    for (;;) {
-      const uint32_t range = hi - lo;
-      const int shift = range < (uint32_t)kHistBins ? 0 : (32 - __builtin_clz(range)) - 12;
-      const int nb = (int)(range >> shift) + 1;
-      for (int i = threadIdx.x; i < nb; i += BS) sh.hist[i] = 0u;
-      __syncthreads();
-#pragma unroll
-      for (int j = 0; j < kTopPer; ++j)
-        if (key[j] >= lo && key[j] <= hi) atomicAdd(&sh.hist[(hi - key[j]) >> shift], 1u);
-      __syncthreads();
-      uint64_t above;
-      const int bin = block_find_crossing(sh.hist, nb, need, true, sh, &above);
-      need -= (uint32_t)above;
-      const uint32_t in_bin = sh.hist[bin];
-      __syncthreads();
-      const uint32_t bhi = hi - ((uint32_t)bin << shift), width = (1u << shift) - 1u;
-      const uint32_t blo = bhi - lo > width ? bhi - width : lo;
-      if (in_bin == need || shift == 0) {
-        all_ge = in_bin == need;
-        T = all_ge ? blo : bhi;
-        ties = need;
-        break;
-      }
-      hi = bhi;
-      lo = blo;
-    }
-    // places of the chosen ones: those above T (or all from T on), and the first ties, in id order
-    uint32_t cnt = 0;  // low half: chosen for sure, high half: ties
-#pragma unroll
-    for (int j = 0; j < kTopPer; ++j) {
-      if (all_ge ? key[j] >= T : key[j] > T) cnt += 1u;
-      else if (!all_ge && key[j] == T) cnt += 0x10000u;
-    }
-    uint32_t pre = block_excl_scan<uint32_t>(cnt, sh.bs, nullptr);
-#pragma unroll
-    for (int j = 0; j < kTopPer; ++j) {
-      const bool sure = all_ge ? key[j] >= T : key[j] > T, tie = !all_ge && key[j] == T;
-      const uint32_t tb = pre >> 16;
-      if (sure || (tie && tb < ties)) {
-        const uint32_t pos = (pre & 0xffffu) + (tb < ties ? tb : ties);
-        if (pos < (uint32_t)a.k_max) {
-          a.ids[r * a.k_max + pos] = (int32_t)id[j];
-          a.logits[r * a.k_max + pos] = v[j];
-        }
-      }
-      pre += sure ? 1u : tie ? 0x10000u : 0u;
-    }
+    if (n > 0) cut = top_cut<NWV>(key, top_key<DT>(t), top_key<DT>(M), (uint32_t)n, sh);
   }
-  for (int e = n + (int)threadIdx.x; e < a.k_max; e += BS) {
-    a.ids[r * a.k_max + e] = 0;
-    a.logits[r * a.k_max + e] = 0.0f;
-  }
-  finish_top(a, r, status, n, M, row_sum);
+  top_write<NWV>(a, r, key, cut, n, sh, [&](int j) { return (int32_t)id[j]; }, [&](int j) { return v[j]; });
+  top_row_out(a, r, status, n, lse);
 }
 
 }  // namespace dspark
