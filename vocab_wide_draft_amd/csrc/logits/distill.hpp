@@ -144,35 +144,36 @@ __device__ void distill_slice(const DistillArgs& a, int64_t r, int s, uint32_t* 
     for (int j = 0; j < kListPer; ++j) s_on += __builtin_amdgcn_exp2f((on_x[j] - m_on) * c);
   }
   __syncthreads();
-  // the row off the list: running maximum and sum; a group of eight logits
+  // the row off the list: running maximum and sum; a vector
   // moves the maximum at most once
+  constexpr int N = kVec<DT>;
   float m = -__builtin_inff(), s_off = 0.0f;
-  for (int t = threadIdx.x * 8; t < size; t += kSliceStep) {
-    float v[8];
-    load8<DT, false>(x, start + t, V, v);
-    const uint32_t bits = tail ? on.byte(t) : 0u;
+  for (int t = threadIdx.x * N; t < size; t += kSliceBS * N) {
+    float v[N];
+    load_vec<DT, N, false>(x, start + t, V, v);
+    const uint32_t bits = tail ? on.members<N>(t) : 0u;
     if (bits) {
 #pragma unroll
-      for (int l = 0; l < 8; ++l) v[l] = (bits >> l) & 1u ? -__builtin_inff() : v[l];
+      for (int l = 0; l < N; ++l) v[l] = (bits >> l) & 1u ? -__builtin_inff() : v[l];
     }
     float top = v[0];
 #pragma unroll
-    for (int l = 1; l < 8; ++l) top = __builtin_fmaxf(top, v[l]);
+    for (int l = 1; l < N; ++l) top = __builtin_fmaxf(top, v[l]);
     if (top > m) {
       s_off *= __builtin_amdgcn_exp2f((m - top) * c);  // (by 0 the first time)
       m = top;
     }
     const float ref = m == -__builtin_inff() ? 0.0f : m;
 #pragma unroll
-    for (int l = 0; l < 8; ++l) s_off += __builtin_amdgcn_exp2f((v[l] - ref) * c);
+    for (int l = 0; l < N; ++l) s_off += __builtin_amdgcn_exp2f((v[l] - ref) * c);
   }
   // a NaN or +inf shows in the sum or the maximum; which of the two, the thread's own logits tell
   if (s_off != s_off || m == __builtin_inff()) {
-    for (int t = threadIdx.x * 8; t < size; t += kSliceStep) {
-      float v[8];
-      load8<DT, false>(x, start + t, V, v);
+    for (int t = threadIdx.x * N; t < size; t += kSliceBS * N) {
+      float v[N];
+      load_vec<DT, N, false>(x, start + t, V, v);
 #pragma unroll
-      for (int l = 0; l < 8; ++l) flags |= v[l] != v[l] ? 1u : v[l] == __builtin_inff() ? 2u : 0u;
+      for (int l = 0; l < N; ++l) flags |= v[l] != v[l] ? 1u : v[l] == __builtin_inff() ? 2u : 0u;
     }
   }
   const auto larger = [](float p, float q) { return __builtin_fmaxf(p, q); };
@@ -292,6 +293,7 @@ __global__ void __launch_bounds__(kSliceBS) distill_join_kernel(DistillArgs a) {
 template <int DT, bool FROM_STATS>
 __global__ void __launch_bounds__(kSliceBS) distill_grad_kernel(DistillArgs a) {
   extern __shared__ uint32_t lds[];
+  constexpr int N = kVec<DT>;
   __shared__ DistillRow sh;
   __shared__ float p[DSPARK_K_MAX];
   typedef typename El<DT>::T XT;
@@ -322,8 +324,10 @@ __global__ void __launch_bounds__(kSliceBS) distill_grad_kernel(DistillArgs a) {
   int len = a.len[r];
   if (len < 0 || len > a.k_max) len = 0;
   if (sh.status != DSPARK_ST_OK || len == 0) {  // (uniform)
-    const float z[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
-    for (int t = threadIdx.x * 8; t < size; t += kSliceStep) store8<DT>(g, start + t, V, z);
+    float z[N];
+#pragma unroll
+    for (int l = 0; l < N; ++l) z[l] = 0.0f;
+    for (int t = threadIdx.x * N; t < size; t += kSliceBS * N) store_vec<DT, N>(g, start + t, V, z);
     return;
   }
   const int32_t* ids = a.ids + r * a.k_max;
@@ -342,18 +346,18 @@ __global__ void __launch_bounds__(kSliceBS) distill_grad_kernel(DistillArgs a) {
   const float M = (float)sh.M, M_off = (float)sh.M_off, inv_s = (float)sh.inv_s;
   const double w = (double)a.weight[r] * a.inv_t;
   const float w_on = (float)w, f_off = (float)(sh.f_off * w);
-  for (int t = threadIdx.x * 8; t < size; t += kSliceStep) {
-    float v[8];
-    load8<DT, true>(x, start + t, V, v);
-    const uint32_t bits = on.byte(t);
+  for (int t = threadIdx.x * N; t < size; t += kSliceBS * N) {
+    float v[N];
+    load_vec<DT, N, true>(x, start + t, V, v);
+    const uint32_t bits = on.members<N>(t);
 #pragma unroll
-    for (int l = 0; l < 8; ++l) {
+    for (int l = 0; l < N; ++l) {
       const bool listed = (bits >> l) & 1u;
       const float e = __builtin_amdgcn_exp2f((v[l] - (listed ? M : M_off)) * c);
       v[l] = e * f_off;
       if (listed) v[l] = (e * inv_s - p[on.entry(t + l) & (DSPARK_K_MAX - 1)]) * w_on;
     }
-    store8<DT>(g, start + t, V, v);
+    store_vec<DT, N>(g, start + t, V, v);
   }
 }
 

@@ -29,6 +29,12 @@ dim3 grid_of(int64_t n) {
   return dim3((unsigned)x, (unsigned)((n + x - 1) / x));
 }
 
+// a grid of `slices` workgroups for each of n rows (see row_slice)
+dim3 row_slice_grid(int64_t n, int slices) {
+  const int64_t line = std::min<int64_t>((n + 7) & ~int64_t(7), kRowsPerY);
+  return dim3((unsigned)(line * slices), (unsigned)((n + kRowsPerY - 1) / kRowsPerY));
+}
+
 // Output rows beside input rows: the same memory (same type and stride) or
 // memory apart.
 int check_out(const dspark_rows* in, const void* out, int32_t dtype, int64_t stride) {
@@ -88,7 +94,7 @@ TopPlan top_plan(int64_t n, int64_t V, int64_t k_max) {
 
 template <int DT>
 void launch_top_slices(const TopSliceArgs& q, const TopPlan& plan, hipStream_t s) {
-  hipLaunchKernelGGL(top_slice_kernel<DT>, grid_of(q.a.n * plan.slices), dim3(kSliceBS), 0, s, q);
+  hipLaunchKernelGGL(top_slice_kernel<DT>, row_slice_grid(q.a.n, plan.slices), dim3(kSliceBS), 0, s, q);
   const dim3 grid = grid_of(q.a.n);
   if (plan.waves == 4) hipLaunchKernelGGL(HIP_KERNEL_NAME(top_select_kernel<DT, 4>), grid, dim3(256), 0, s, q);
   else if (plan.waves == 8) hipLaunchKernelGGL(HIP_KERNEL_NAME(top_select_kernel<DT, 8>), grid, dim3(512), 0, s, q);

@@ -99,6 +99,7 @@ __global__ void __launch_bounds__(kSliceBS) shape_kernel(ShapeArgs a) {
 
   typedef typename El<TI>::T XT;
   typedef typename El<TO>::T OT;
+  constexpr int N = kVec<TO>;
   const int P = h.rows_per_request;
   const bool lookup = counted || drafted || b1 > b0;
   for (int i = 0; i < P; ++i) {
@@ -124,29 +125,31 @@ __global__ void __launch_bounds__(kSliceBS) shape_kernel(ShapeArgs a) {
     if (s == 0 && threadIdx.x == 0) a.row_status[row] = status;
     const XT* x = static_cast<const XT*>(a.x) + row * a.x_stride;
     OT* o = static_cast<OT*>(a.out) + row * a.out_stride;
-    for (int t = threadIdx.x * 8; t < size; t += kSliceStep) {
+    for (int t = threadIdx.x * N; t < size; t += kSliceBS * N) {
       const int v = start + t;
-      float z[8];
+      float z[N];
       if (status != DSPARK_ST_OK) {
 #pragma unroll
-        for (int l = 0; l < 8; ++l) z[l] = -__builtin_inff();
-        store8<TO>(o, v, V, z);
+        for (int l = 0; l < N; ++l) z[l] = -__builtin_inff();
+        store_vec<TO, N>(o, v, V, z);
         continue;
       }
-      load8<TI, true>(x, v, V, z);
+      load_vec<TI, N, true>(x, v, V, z);
       if (lookup) {
-        uint32_t c[8];
+        uint32_t c[N];
         uint32_t any = 0;
         if (counted || drafted) {
-          const uint4 c0 = *reinterpret_cast<const uint4*>(count + t), c1 = *reinterpret_cast<const uint4*>(count + t + 4);
-          c[0] = c0.x; c[1] = c0.y; c[2] = c0.z; c[3] = c0.w;
-          c[4] = c1.x; c[5] = c1.y; c[6] = c1.z; c[7] = c1.w;
 #pragma unroll
-          for (int l = 0; l < 8; ++l) any |= c[l];
+          for (int l = 0; l < N; l += 4) {
+            const uint4 q = *reinterpret_cast<const uint4*>(count + t + l);
+            c[l] = q.x; c[l + 1] = q.y; c[l + 2] = q.z; c[l + 3] = q.w;
+          }
+#pragma unroll
+          for (int l = 0; l < N; ++l) any |= c[l];
         }
         if (any) {
 #pragma unroll
-          for (int l = 0; l < 8; ++l) {
+          for (int l = 0; l < N; ++l) {
             if (c[l]) {
               const uint32_t n = c[l] & ~kPrompt;
               float y = z[l] > 0.0f ? z[l] / rep : z[l] * rep;
@@ -155,21 +158,21 @@ __global__ void __launch_bounds__(kSliceBS) shape_kernel(ShapeArgs a) {
             }
           }
         }
-        const uint32_t bb = b1 > b0 ? biased.byte(t) : 0u;
+        const uint32_t bb = b1 > b0 ? biased.members<N>(t) : 0u;
         if (bb) {
 #pragma unroll
-          for (int l = 0; l < 8; ++l)
+          for (int l = 0; l < N; ++l)
             if ((bb >> l) & 1u) z[l] += h.bias_values[b0 + biased.entry(t + l)];
         }
       }
 #pragma unroll
-      for (int l = 0; l < 8; ++l) z[l] *= inv_t;
+      for (int l = 0; l < N; ++l) z[l] *= inv_t;
       if (mask) {
-        const uint32_t m = reinterpret_cast<const uint8_t*>(mask)[v >> 3];
+        const uint32_t m = reinterpret_cast<const uint8_t*>(mask)[v >> 3] >> (v & 7);
 #pragma unroll
-        for (int l = 0; l < 8; ++l) z[l] = (m >> l) & 1u ? z[l] : -__builtin_inff();
+        for (int l = 0; l < N; ++l) z[l] = (m >> l) & 1u ? z[l] : -__builtin_inff();
       }
-      store8<TO>(o, v, V, z);
+      store_vec<TO, N>(o, v, V, z);
     }
   }
 }

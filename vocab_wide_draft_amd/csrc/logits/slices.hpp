@@ -1,6 +1,6 @@
 // What the operators on vocabulary slices share: a workgroup of 256 threads
-// works on one slice of a row's ids, in groups of eight consecutive logits
-// per thread (one 16-byte load of bf16, two of float32).
+// works on one slice of a row's ids, a vector of neighbouring logits per
+// thread at a time.
 #pragma once
 #include "../device_common.hpp"
 
@@ -8,7 +8,8 @@ namespace dspark {
 
 constexpr int kSliceBS = 256;
 constexpr int kSliceNW = kSliceBS / 64;
-constexpr int kSliceStep = kSliceBS * 8;  // ids of one group per thread
+constexpr int kSliceStep = kSliceBS * 8;  // slices are whole multiples of it
+constexpr int64_t kRowsPerY = 1 << 14;    // rows of one grid line (a multiple of 8)
 
 // The workgroup's number in a grid of `total` workgroups laid out by grid_of
 // (host side); -1 past the end (uniform).
@@ -17,6 +18,18 @@ __device__ __forceinline__ int64_t block_number(int64_t total) {
   return b < total ? b : -1;
 }
 
+// The row and slice of a workgroup of a grid laid out by row_slice_grid (host
+// side): the slices of one row go to workgroups eight apart, which run on one
+// of the eight XCDs, so that what they all read of the row stays in its L2.
+// False past the last row (uniform).
+__device__ __forceinline__ bool row_slice(int64_t n, int slices, int64_t& r, int& s) {
+  const uint32_t x = blockIdx.x >> 3, rows = x / (uint32_t)slices;
+  s = (int)(x - rows * (uint32_t)slices);
+  r = (int64_t)blockIdx.y * kRowsPerY + (int64_t)rows * 8 + (blockIdx.x & 7u);
+  return r < n;
+}
+
+typedef unsigned int v2u __attribute__((ext_vector_type(2)));
 typedef unsigned int v4u __attribute__((ext_vector_type(4)));
 typedef float v4f __attribute__((ext_vector_type(4)));
 
@@ -44,58 +57,72 @@ struct El<DSPARK_F32> {
   static __device__ __forceinline__ void put(T* p, int64_t i, float x) { p[i] = x; }
 };
 
-// The eight logits of a row from id v on (v a multiple of 8; ids past V read
-// as -inf and touch no memory).  NT: streamed, not read again soon.
-template <int DT, bool NT>
-__device__ __forceinline__ void load8(const typename El<DT>::T* row, int v, int V, float (&x)[8]) {
-  if (v + 8 <= V) {
-    if constexpr (DT == DSPARK_BF16) {
-      const v4u* p = reinterpret_cast<const v4u*>(row + v);
-      const v4u u = NT ? __builtin_nontemporal_load(p) : *p;
+// N neighbouring logits of a row, from id v on (v a multiple of N), as one
+// load of a thread: N = 8 or 4 of bf16, 4 of float32, so that the lanes of a
+// wave read one unbroken stretch.  (Two loads of 16 bytes at a stride of 32,
+// eight float32 per thread, fetch every line twice when they are streamed.)
+// NT: streamed, not read again soon.
+template <int DT, int N, bool NT>
+__device__ __forceinline__ void load_whole(const typename El<DT>::T* row, int v, float (&x)[N]) {
+  static_assert(N == 4 || (N == 8 && DT == DSPARK_BF16), "one load of at most 16 bytes");
+  if constexpr (DT == DSPARK_F32) {
+    const v4f* p = reinterpret_cast<const v4f*>(row + v);
+    const v4f a = NT ? __builtin_nontemporal_load(p) : *p;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        x[2 * i] = bf16_lo(u[i]);
-        x[2 * i + 1] = bf16_hi(u[i]);
-      }
-    } else {
-      const v4f* p = reinterpret_cast<const v4f*>(row + v);
-      const v4f a = NT ? __builtin_nontemporal_load(p) : p[0];
-      const v4f b = NT ? __builtin_nontemporal_load(p + 1) : p[1];
+    for (int i = 0; i < 4; ++i) x[i] = a[i];
+  } else if constexpr (N == 8) {
+    const v4u* p = reinterpret_cast<const v4u*>(row + v);
+    const v4u u = NT ? __builtin_nontemporal_load(p) : *p;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        x[i] = a[i];
-        x[4 + i] = b[i];
-      }
+    for (int i = 0; i < 4; ++i) {
+      x[2 * i] = bf16_lo(u[i]);
+      x[2 * i + 1] = bf16_hi(u[i]);
     }
   } else {
+    const v2u* p = reinterpret_cast<const v2u*>(row + v);
+    const v2u u = NT ? __builtin_nontemporal_load(p) : *p;
 #pragma unroll
-    for (int l = 0; l < 8; ++l) x[l] = v + l < V ? El<DT>::get(row, v + l) : -__builtin_inff();
+    for (int i = 0; i < 2; ++i) {
+      x[2 * i] = bf16_lo(u[i]);
+      x[2 * i + 1] = bf16_hi(u[i]);
+    }
+  }
+}
+// the same at the end of a row: ids past V read as -inf and touch no memory
+template <int DT, int N, bool NT>
+__device__ __forceinline__ void load_vec(const typename El<DT>::T* row, int v, int V, float (&x)[N]) {
+  if (v + N <= V) {
+    load_whole<DT, N, NT>(row, v, x);
+  } else {
+#pragma unroll
+    for (int l = 0; l < N; ++l) x[l] = v + l < V ? El<DT>::get(row, v + l) : -__builtin_inff();
   }
 }
 
-// the same where all eight are there: no branch between one load and the next
-template <int DT, bool NT>
-__device__ __forceinline__ void load8_whole(const typename El<DT>::T* row, int v, float (&x)[8]) {
-  load8<DT, NT>(row, v, v + 8, x);
-}
-
-template <int DT>
-__device__ __forceinline__ void store8(typename El<DT>::T* row, int v, int V, const float (&x)[8]) {
-  if (v + 8 <= V) {
-    if constexpr (DT == DSPARK_BF16) {
+template <int DT, int N>
+__device__ __forceinline__ void store_vec(typename El<DT>::T* row, int v, int V, const float (&x)[N]) {
+  static_assert(N == 4 || (N == 8 && DT == DSPARK_BF16), "one store of at most 16 bytes");
+  if (v + N <= V) {
+    if constexpr (DT == DSPARK_F32) {
+      const v4f a = {x[0], x[1], x[2], x[3]};
+      __builtin_nontemporal_store(a, reinterpret_cast<v4f*>(row + v));
+    } else if constexpr (N == 8) {
       const v4u u = {bf16_pair(x[0], x[1]), bf16_pair(x[2], x[3]), bf16_pair(x[4], x[5]), bf16_pair(x[6], x[7])};
       __builtin_nontemporal_store(u, reinterpret_cast<v4u*>(row + v));
     } else {
-      const v4f a = {x[0], x[1], x[2], x[3]}, b = {x[4], x[5], x[6], x[7]};
-      __builtin_nontemporal_store(a, reinterpret_cast<v4f*>(row + v));
-      __builtin_nontemporal_store(b, reinterpret_cast<v4f*>(row + v) + 1);
+      const v2u u = {bf16_pair(x[0], x[1]), bf16_pair(x[2], x[3])};
+      __builtin_nontemporal_store(u, reinterpret_cast<v2u*>(row + v));
     }
   } else {
 #pragma unroll
-    for (int l = 0; l < 8; ++l)
+    for (int l = 0; l < N; ++l)
       if (v + l < V) El<DT>::put(row, v + l, x[l]);
   }
 }
+
+// logits of one vector of a thread
+template <int DT>
+constexpr int kVec = DT == DSPARK_BF16 ? 8 : 4;
 
 // Reductions over a workgroup of NWV waves (every thread calls, every thread
 // gets the result; scratch: NWV values in LDS, free again after the barrier
@@ -145,8 +172,9 @@ struct IdSet {
     atomicOr(&bits[t >> 5], 1u << (t & 31));
     if (prev < 0 || (prev >> 5) != (t >> 5)) first[t >> 5] = e;
   }
-  __device__ __forceinline__ uint32_t byte(int t) const {  // members among t .. t + 7 (t a multiple of 8)
-    return (bits[t >> 5] >> (t & 31)) & 0xffu;
+  template <int N>
+  __device__ __forceinline__ uint32_t members(int t) const {  // among t .. t + N - 1 (t a multiple of N, N of 4 or 8)
+    return (bits[t >> 5] >> (t & 31)) & ((1u << N) - 1u);
   }
   __device__ __forceinline__ uint32_t entry(int t) const {
     return first[t >> 5] + (uint32_t)__builtin_popcount(bits[t >> 5] & ((1u << (t & 31)) - 1u));

@@ -1,8 +1,8 @@
 // The top logits of a row with the log-sum-exp of the whole row
 // (dspark_top_logits).
 //
-// Rows of more than kTopSmall ids are cut into slices of 8,192 ids, one workgroup each,
-// which reads its slice once into registers.  A threshold that the k-th
+// Rows of more than kTopSmall ids are cut into slices of 8,192 ids, one
+// workgroup each, which reads its slice once into registers.  A threshold that the k-th
 // largest logit lies above with good odds comes from a sample of the row
 // (2,048 logits, the same for every slice of the row), so that one pass
 // yields the slice's maximum, its sum of exponentials and the few logits
@@ -207,18 +207,18 @@ __device__ __forceinline__ int top_from_memory(const TopArgs& a, int64_t r, int 
   typedef typename El<DT>::T XT;
   const XT* row = static_cast<const XT*>(a.x) + r * a.stride;
   const int V = a.V;
-  constexpr int kStep = 64 * NWV * 8;
+  constexpr int N = kVec<DT>, kStep = 64 * NWV * N;
   const uint32_t none = top_key<DT>(-__builtin_inff());  // -inf is not listed
   uint32_t prefix = 0, pmask = 0, need = (uint32_t)k, n = (uint32_t)k;
   bool first = true;
   for (int shift = DT == DSPARK_BF16 ? 8 : 24; shift >= 0; shift -= 8) {
     for (int i = threadIdx.x; i < kTopBins; i += 64 * NWV) sh.hist[i] = 0u;
     __syncthreads();
-    for (int v = (int)threadIdx.x * 8; v < V; v += kStep) {
-      float x[8];
-      load8<DT, false>(row, v, V, x);
+    for (int v = (int)threadIdx.x * N; v < V; v += kStep) {
+      float x[N];
+      load_vec<DT, N, false>(row, v, V, x);
 #pragma unroll
-      for (int l = 0; l < 8; ++l) {
+      for (int l = 0; l < N; ++l) {
         const uint32_t key = top_key<DT>(x[l]);
         const bool in = v + l < V && key > none && (key & pmask) == prefix;
         const uint32_t bin = 255u - ((key >> shift) & 255u);  // the largest digits first
@@ -250,18 +250,18 @@ __device__ __forceinline__ int top_from_memory(const TopArgs& a, int64_t r, int 
   // keys above the prefix and the first `need` equal to it, in id order
   uint32_t placed = 0, tied = 0;
   for (int base = 0; base < V; base += kStep) {
-    const int v = base + (int)threadIdx.x * 8;
-    float x[8];
-    if (v < V) load8<DT, false>(row, v, V, x);
+    const int v = base + (int)threadIdx.x * N;
+    float x[N];
+    if (v < V) load_vec<DT, N, false>(row, v, V, x);
     uint32_t cnt = 0, total;
 #pragma unroll
-    for (int l = 0; l < 8; ++l) {
+    for (int l = 0; l < N; ++l) {
       const uint32_t key = v + l < V ? top_key<DT>(x[l]) : 0u;
       cnt += key > prefix ? 1u : key == prefix ? 0x10000u : 0u;
     }
     uint32_t pre = group_excl_scan<NWV>(cnt, sh.scan, &total);
 #pragma unroll
-    for (int l = 0; l < 8; ++l) {
+    for (int l = 0; l < N; ++l) {
       const uint32_t key = v + l < V ? top_key<DT>(x[l]) : 0u;
       const uint32_t tb = tied + (pre >> 16);
       if (key > prefix || (key == prefix && tb < need)) {
@@ -299,13 +299,14 @@ __global__ void __launch_bounds__(64 * NWV) top_small_kernel(TopArgs a) {
   float x[8 * G];
   float m = -__builtin_inff();
   uint32_t flags = 0;
+  constexpr int N = kVec<DT>;
 #pragma unroll
-  for (int g = 0; g < G; ++g) {
-    float y[8];
-    load8<DT, true>(row, v0 + 8 * g, a.V, y);
+  for (int g = 0; g < 8 * G / N; ++g) {
+    float y[N];
+    load_vec<DT, N, false>(row, v0 + N * g, a.V, y);
 #pragma unroll
-    for (int l = 0; l < 8; ++l) {
-      x[8 * g + l] = y[l];
+    for (int l = 0; l < N; ++l) {
+      x[N * g + l] = y[l];
       m = __builtin_fmaxf(m, y[l]);
       flags |= y[l] != y[l] ? 1u : y[l] == __builtin_inff() ? 2u : 0u;
     }
@@ -341,17 +342,17 @@ __global__ void __launch_bounds__(64 * NWV) top_small_kernel(TopArgs a) {
 }
 
 // ------------------------------------------------------- rows in slices
-constexpr int kTopGroups = 4;                              // groups of eight logits per thread
-constexpr int kTopSlice = kSliceStep * kTopGroups;         // ids of a slice
+constexpr int kTopSlice = 4 * kSliceStep;                  // ids of a slice
 constexpr int kTopSlices = DSPARK_V_MAX / kTopSlice;       // slices of the longest row
 constexpr int kTopSample = kSliceBS * 8;                   // logits sampled of a row: 64 runs of 32
 constexpr int kTopPer = 8;                                 // candidates per thread of the selection, at most
 
 struct TopPart {
-  double sum;    // of the exponentials relative to m
-  float m, t;    // the slice's maximum; the row's threshold
+  float m[kSliceNW], sum[kSliceNW];  // of each wave: its maximum, the sum of exponentials relative to it
+  float t;       // the row's threshold
   int32_t flags; // 1: a NaN, 2: a +inf
   int32_t count; // candidates (more than the list holds: too many)
+  int32_t reserved;
 };
 
 // A candidate of a slice: its logit and its place in the slice.
@@ -381,35 +382,51 @@ struct TopSliceArgs {
   void* cand;     // [n][slices][cap]
 };
 
+// mask = 2 mask + (x >= t): a compare and an add with its carry
+__device__ __forceinline__ void push_ge(uint32_t& mask, float x, float t) {
+  asm("v_cmp_ge_f32 vcc, %1, %2\n\tv_addc_co_u32 %0, vcc, %0, %0, vcc" : "+v"(mask) : "v"(x), "v"(t) : "vcc");
+}
+
+// What bounds it is the number of instructions (bf16: an unpack, half a
+// maximum, a multiply-add, an exponential of four cycles' issue, an addition
+// and two for the mask per logit), so everything per thread is kept small:
+// each wave has a reference of its own, the order of the candidates comes
+// from one scan of packed counts, and a candidate's logit is read again.
 template <int DT>
 __global__ void __launch_bounds__(kSliceBS) top_slice_kernel(TopSliceArgs q) {
   __shared__ __align__(16) uint32_t sample[kSliceBS];
   __shared__ float thr;
-  __shared__ uint64_t scan[kSliceNW];
-  __shared__ double red[kSliceNW];
-  __shared__ float redf[kSliceNW];
-  __shared__ uint32_t redu[kSliceNW];
+  constexpr int N = kVec<DT>, U = kTopSlice / (kSliceBS * N);  // U vectors per thread: 32 logits
+  constexpr int W = U / 4;                                     // words of four 16-bit counts
+  __shared__ uint64_t scan[W][kSliceNW];
+  __shared__ uint32_t any_flags;
   typedef typename El<DT>::T XT;
-  const int64_t b = block_number(q.a.n * q.slices);
-  if (b < 0) return;
-  const int64_t r = b / q.slices;
-  const int s = (int)(b - r * q.slices), start = s * kTopSlice, V = q.a.V, tid = (int)threadIdx.x;
+  int64_t r;
+  int s;
+  if (!row_slice(q.a.n, q.slices, r, s)) return;
+  const int start = s * kTopSlice, V = q.a.V, tid = (int)threadIdx.x;
   const XT* row = static_cast<const XT*>(q.a.x) + r * q.a.stride;
-  const int step = (V / 64) & ~7;
-  float smp[8], x[kTopGroups][8];
-  load8_whole<DT, false>(row, (tid >> 2) * step + (tid & 3) * 8, smp);
+  const int run = (V / 64) & ~7;  // the sample: 64 runs of 32 logits, four threads each
+  float smp[8], x[U][N];
+#pragma unroll
+  for (int i = 0; i < 8 / N; ++i) {
+    float y[N];
+    load_whole<DT, N, false>(row, (tid >> 2) * run + (i * 4 + (tid & 3)) * N, y);
+#pragma unroll
+    for (int l = 0; l < N; ++l) smp[i * N + l] = y[l];
+  }
   if (start + kTopSlice <= V) {  // (uniform)
 #pragma unroll
-    for (int i = 0; i < kTopGroups; ++i) load8_whole<DT, true>(row, start + (i * kSliceBS + tid) * 8, x[i]);
+    for (int i = 0; i < U; ++i) load_whole<DT, N, true>(row, start + (i * kSliceBS + tid) * N, x[i]);
   } else {
 #pragma unroll
-    for (int i = 0; i < kTopGroups; ++i) load8<DT, true>(row, start + (i * kSliceBS + tid) * 8, V, x[i]);
+    for (int i = 0; i < U; ++i) load_vec<DT, N, true>(row, start + (i * kSliceBS + tid) * N, V, x[i]);
   }
   float top = smp[0];
 #pragma unroll
   for (int l = 1; l < 8; ++l) top = __builtin_fmaxf(top, smp[l]);
   sample[tid] = top != top ? 0u : key32(top) >> 16;
-  float m = -__builtin_inff();
+  if (tid == 0) any_flags = 0u;
   __syncthreads();
   if (wave_id() == 0) {
     // the largest 16-bit key that at least `rank` of the maxima reach: four
@@ -427,66 +444,84 @@ __global__ void __launch_bounds__(kSliceBS) top_slice_kernel(TopSliceArgs q) {
     const float t = top_key_value<DSPARK_BF16>(T);
     if (lane_id() == 0) thr = t >= -3.4028235e38f ? t : -3.4028235e38f;
   }
+  float m = x[0][0];
 #pragma unroll
-  for (int i = 0; i < kTopGroups; ++i) {
+  for (int i = 0; i < U; ++i) {
 #pragma unroll
-    for (int l = 0; l < 8; ++l) m = __builtin_fmaxf(m, x[i][l]);
+    for (int l = 0; l < N; ++l) m = __builtin_fmaxf(m, x[i][l]);
   }
-  const float M = group_reduce<kSliceNW>(m, -__builtin_inff(), [](float u, float v) { return __builtin_fmaxf(u, v); }, redf);
-  const float t = thr, ref = M == -__builtin_inff() ? 0.0f : M;
+  const float M = wave_reduce(m, -__builtin_inff(), [](float u, float v) { return __builtin_fmaxf(u, v); });
+  const float ref = M == -__builtin_inff() ? 0.0f : M;
   float sum = 0.0f;
-  uint32_t mask[kTopGroups];
-  uint64_t counts = 0;  // four 16-bit fields
 #pragma unroll
-  for (int i = 0; i < kTopGroups; ++i) {
-    sum += exp_sum(q.a, ref, x[i]);
-    mask[i] = 0u;
+  for (int i = 0; i < U; ++i) sum += exp_sum(q.a, ref, x[i]);
+  if (sum != sum || M == __builtin_inff()) {  // a NaN or a +inf in this thread, or the wave's
+    uint32_t flags = 0;
 #pragma unroll
-    for (int l = 7; l >= 0; --l) mask[i] = mask[i] + mask[i] + (x[i][l] >= t ? 1u : 0u);
-    counts |= (uint64_t)__builtin_popcount(mask[i]) << (16 * i);
-  }
-  uint32_t flags = 0;
-  if (sum != sum || m == __builtin_inff()) {
+    for (int i = 0; i < U; ++i) {
 #pragma unroll
-    for (int i = 0; i < kTopGroups; ++i) {
-#pragma unroll
-      for (int l = 0; l < 8; ++l) flags |= x[i][l] != x[i][l] ? 1u : x[i][l] == __builtin_inff() ? 2u : 0u;
+      for (int l = 0; l < N; ++l) flags |= x[i][l] != x[i][l] ? 1u : x[i][l] == __builtin_inff() ? 2u : 0u;
     }
+    if (flags) atomicOr(&any_flags, flags);
   }
-  // places in the list: by group, then thread, then element -- id order
-  const uint64_t inc = wave_incl_scan(counts);
-  if (lane_id() == 63) scan[wave_id()] = inc;
-  flags = group_reduce<kSliceNW>(flags, 0u, [](uint32_t u, uint32_t v) { return u | v; }, redu);
-  const double total = group_reduce<kSliceNW>((double)sum, 0.0, [](double u, double v) { return u + v; }, red);
-  uint64_t before = inc - counts, all = 0;
+  const float wsum = wave_sum(sum);
+  __syncthreads();
+  const float t = thr;
+  uint32_t mask = 0;  // element l of vector i at bit N i + N - 1 - l
 #pragma unroll
-  for (int w = 0; w < kSliceNW; ++w) {
-    if (w < wave_id()) before += scan[w];
-    all += scan[w];
+  for (int i = U - 1; i >= 0; --i) {
+#pragma unroll
+    for (int l = 0; l < N; ++l) push_ge(mask, x[i][l], t);
   }
-  uint32_t base = 0;
+  // places in the list: by vector, then thread, then element -- id order
+  constexpr uint32_t kOnes = (1u << N) - 1u;
+  TopPart& p = q.part[r * q.slices + s];
+  uint64_t before[W];
+#pragma unroll
+  for (int w = 0; w < W; ++w) {
+    uint64_t count = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) count |= (uint64_t)__builtin_popcount((mask >> (N * (4 * w + i))) & kOnes) << (16 * i);
+    const uint64_t inc = wave_incl_scan(count);
+    before[w] = inc - count;
+    if (lane_id() == 63) scan[w][wave_id()] = inc;
+  }
+  if (lane_id() == 63) {
+    p.m[wave_id()] = M;
+    p.sum[wave_id()] = wsum;
+  }
+  __syncthreads();
   typename Cand<DT>::T* list = static_cast<typename Cand<DT>::T*>(q.cand) + (r * q.slices + s) * q.cap;
+  uint32_t base = 0;
 #pragma unroll
-  for (int i = 0; i < kTopGroups; ++i) {
-    uint32_t pos = base + ((uint32_t)(before >> (16 * i)) & 0xffffu);
-    base += (uint32_t)(all >> (16 * i)) & 0xffffu;
-    if (mask[i]) {
+  for (int w = 0; w < W; ++w) {
+    uint64_t all = 0;
 #pragma unroll
-      for (int l = 0; l < 8; ++l) {
-        if ((mask[i] >> l) & 1u) {
-          if (pos < (uint32_t)q.cap) list[pos] = Cand<DT>::make(x[i][l], (i * kSliceBS + tid) * 8 + l);
-          ++pos;
-        }
-      }
+    for (int v = 0; v < kSliceNW; ++v) {
+      const uint64_t o = scan[w][v];
+      before[w] += v < wave_id() ? o : 0ull;
+      all += o;
+    }
+    // the vectors before: every field stays below 2^14
+    before[w] += (all << 16) + (all << 32) + (all << 48) + (uint64_t)base * 0x0001000100010001ull;
+    base += (uint32_t)((all >> 48) + (all >> 32) + (all >> 16) + all) & 0xffffu;
+    uint32_t left = W == 1 ? mask : (mask >> (16 * w)) & 0xffffu;
+    while (left) {
+      const int i = __builtin_ctz(left) / N;  // the lowest vector left
+      const uint32_t own = (left >> (N * i)) & kOnes;
+      const int l = __builtin_clz(own) - (32 - N);
+      const uint32_t pos = (uint32_t)(before[w] >> (16 * i)) & 0xffffu;
+      before[w] += 1ull << (16 * i);
+      left &= ~((1u << (N - 1)) >> l << (N * i));
+      const int place = ((4 * w + i) * kSliceBS + tid) * N + l;
+      if (pos < (uint32_t)q.cap) list[pos] = Cand<DT>::make(El<DT>::get(row, start + place), place);
     }
   }
   if (tid == 0) {
-    TopPart& p = q.part[r * q.slices + s];
-    p.sum = total;
-    p.m = M;
     p.t = t;
-    p.flags = (int32_t)flags;
+    p.flags = (int32_t)any_flags;
     p.count = (int32_t)base;
+    p.reserved = 0;
   }
 }
 
@@ -502,31 +537,33 @@ __global__ void __launch_bounds__(64 * NWV) top_select_kernel(TopSliceArgs q) {
   const int64_t r = block_number(a.n);
   if (r < 0) return;
   const TopPart* part = q.part + r * q.slices;
-  if (wave_id() == 0) {  // two slices per lane
+  if (wave_id() == 0) {
     const int l = lane_id();
-    float m = -__builtin_inff(), mm[2] = {m, m};
-    double ss[2] = {0.0, 0.0};
+    constexpr float kNone = -__builtin_inff();
+    const auto either = [](uint32_t u, uint32_t v) { return u | v; };
+    // the sums: one wave's record per lane
+    float m = kNone;
+    for (int i = l; i < q.slices * kSliceNW; i += 64) m = __builtin_fmaxf(m, part[i / kSliceNW].m[i % kSliceNW]);
+    const float M = wave_reduce(m, kNone, [](float u, float v) { return __builtin_fmaxf(u, v); });
+    const double top = sum_reference(a, M);
+    double sum = 0.0;
+    for (int i = l; i < q.slices * kSliceNW; i += 64) {
+      const float mi = part[i / kSliceNW].m[i % kSliceNW];
+      if (mi > kNone) sum += (double)part[i / kSliceNW].sum[i % kSliceNW] * exp(sum_reference(a, mi) - top);
+    }
+    sum = wave_sum(sum);
+    // the lists: two slices per lane
     uint32_t n[2] = {0u, 0u}, flags = 0u, over = 0u;
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
       if (2 * l + j < q.slices) {
-        const TopPart p = part[2 * l + j];
-        mm[j] = p.m;
-        ss[j] = p.sum;
-        n[j] = (uint32_t)p.count;
-        flags |= (uint32_t)p.flags;
-        over |= p.count > q.cap ? 1u : 0u;
-        m = __builtin_fmaxf(m, p.m);
+        n[j] = (uint32_t)part[2 * l + j].count;
+        flags |= (uint32_t)part[2 * l + j].flags;
+        over |= part[2 * l + j].count > q.cap ? 1u : 0u;
       }
     }
-    const float M = wave_reduce(m, -__builtin_inff(), [](float u, float v) { return __builtin_fmaxf(u, v); });
-    double sum = 0.0;
-#pragma unroll
-    for (int j = 0; j < 2; ++j)
-      if (mm[j] > -__builtin_inff()) sum += ss[j] * exp(sum_reference(a, mm[j]) - sum_reference(a, M));
-    sum = wave_sum(sum);
-    flags = wave_reduce(flags, 0u, [](uint32_t u, uint32_t v) { return u | v; });
-    over = wave_reduce(over, 0u, [](uint32_t u, uint32_t v) { return u | v; });
+    flags = wave_reduce(flags, 0u, either);
+    over = wave_reduce(over, 0u, either);
     const uint32_t inc = wave_incl_scan(n[0] + n[1]);
     first[2 * l] = inc - n[0] - n[1];
     first[2 * l + 1] = inc - n[1];
