@@ -281,6 +281,28 @@ def test_shape_refused_rows():
     assert g["status"].tolist() == [0, L.ST_BAD_BIAS, L.ST_BAD_BIAS, L.ST_BAD_BIAS]
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_shape_many_rows_of_one_request(dtype):
+    """More rows than a wave has lanes, each with a mask and a drafted token of its own."""
+    rng = np.random.default_rng(44)
+    R, P, V = 2, 150, 2500
+    a = rows_of(rng, R * P, V, dtype)
+    c = case(rng, R, P, V, 30, 10, False)
+    c["allowed"] = rng.random((40, V)) < 0.7
+    c["mask_row"] = rng.integers(-1, 40, R * P)
+    c["draft"][1, 100] = V  # the rows after it are refused
+    g = call(c, to_dev(a, dtype), P)
+    st = g["status"].cpu().numpy().reshape(R, P)
+    assert not st[0].any() and not st[1, :101].any() and (st[1, 101:] == L.ST_BAD_HISTORY).all()
+    got = host64(g["logits"])
+    for j in range(R * P):
+        if st.flat[j]:
+            assert (got[j] == -np.inf).all()
+        else:
+            w, mag = want(c, f64(a, dtype), P, j)
+            check(got[j], w, mag, dtype == "bf16", j)
+
+
 def test_shape_mask_per_row_without_index():
     rng = np.random.default_rng(2)
     a = rows_of(rng, 4, 129, "bf16")

@@ -64,9 +64,15 @@ int slice_of(int64_t owners, int64_t V, int64_t most, int64_t want) {
   return (int)(std::min<int64_t>(groups, most / kSliceStep) * kSliceStep);
 }
 
+// Vocabularies of at most 2,048 ids take one workgroup of 256 threads per
+// request, longer ones workgroups of 1,024.
 template <int TI, int TO>
-void launch_shape(const ShapeArgs& a, size_t lds, hipStream_t s) {
-  hipLaunchKernelGGL(HIP_KERNEL_NAME(shape_kernel<TI, TO>), grid_of(a.n_requests * a.slices), dim3(kSliceBS), lds, s, a);
+void launch_shape(ShapeArgs a, hipStream_t s) {
+  const int waves = a.V <= 64 * 4 * 8 ? 4 : 16;
+  a.slices = (a.V + 64 * waves * 8 - 1) / (64 * waves * 8);
+  const dim3 grid = row_slice_grid(a.n_requests, a.slices);
+  if (waves == 4) hipLaunchKernelGGL(HIP_KERNEL_NAME(shape_kernel<TI, TO, 4>), grid, dim3(256), 0, s, a);
+  else hipLaunchKernelGGL(HIP_KERNEL_NAME(shape_kernel<TI, TO, 16>), grid, dim3(1024), 0, s, a);
 }
 
 // How dspark_top_logits cuts rows longer than kTopSmall (bytes 0: not at
@@ -151,13 +157,10 @@ int dspark_shape_logits(const dspark_rows* rows, const dspark_shaping* how, void
   a.n_requests = rows->n_rows / how->rows_per_request;
   a.V = (int)rows->vocab;
   a.how = *how;
-  a.slice = slice_of(a.n_requests, a.V, 8192, 2048);
-  a.slices = (a.V + a.slice - 1) / a.slice;
-  const size_t lds = 4u * ((size_t)a.slice + 2u * ((size_t)a.slice / 32));
   hipStream_t s = static_cast<hipStream_t>(stream);
-  if (rows->dtype == DSPARK_F32) launch_shape<DSPARK_F32, DSPARK_F32>(a, lds, s);
-  else if (out_dtype == DSPARK_BF16) launch_shape<DSPARK_BF16, DSPARK_BF16>(a, lds, s);
-  else launch_shape<DSPARK_BF16, DSPARK_F32>(a, lds, s);
+  if (rows->dtype == DSPARK_F32) launch_shape<DSPARK_F32, DSPARK_F32>(a, s);
+  else if (out_dtype == DSPARK_BF16) launch_shape<DSPARK_BF16, DSPARK_BF16>(a, s);
+  else launch_shape<DSPARK_BF16, DSPARK_F32>(a, s);
   return host_check_launch();
 }
 

@@ -102,22 +102,66 @@ __device__ __forceinline__ void load_vec(const typename El<DT>::T* row, int v, i
 template <int DT, int N>
 __device__ __forceinline__ void store_vec(typename El<DT>::T* row, int v, int V, const float (&x)[N]) {
   static_assert(N == 4 || (N == 8 && DT == DSPARK_BF16), "one store of at most 16 bytes");
+  char* at = reinterpret_cast<char*>(row) + (uint32_t)v * (uint32_t)sizeof(*row);
   if (v + N <= V) {
     if constexpr (DT == DSPARK_F32) {
       const v4f a = {x[0], x[1], x[2], x[3]};
-      __builtin_nontemporal_store(a, reinterpret_cast<v4f*>(row + v));
+      __builtin_nontemporal_store(a, reinterpret_cast<v4f*>(at));
     } else if constexpr (N == 8) {
       const v4u u = {bf16_pair(x[0], x[1]), bf16_pair(x[2], x[3]), bf16_pair(x[4], x[5]), bf16_pair(x[6], x[7])};
-      __builtin_nontemporal_store(u, reinterpret_cast<v4u*>(row + v));
+      __builtin_nontemporal_store(u, reinterpret_cast<v4u*>(at));
     } else {
       const v2u u = {bf16_pair(x[0], x[1]), bf16_pair(x[2], x[3])};
-      __builtin_nontemporal_store(u, reinterpret_cast<v2u*>(row + v));
+      __builtin_nontemporal_store(u, reinterpret_cast<v2u*>(at));
     }
   } else {
 #pragma unroll
     for (int l = 0; l < N; ++l)
       if (v + l < V) El<DT>::put(row, v + l, x[l]);
   }
+}
+
+// A vector as it is loaded, to be unpacked where it is used: a load that is
+// to stay in flight must not be touched before.
+template <int DT, int N>
+struct Raw {
+  uint32_t w[DT == DSPARK_F32 ? N : N / 2];
+};
+template <int DT, int N, bool NT>
+__device__ __forceinline__ Raw<DT, N> raw_whole(const typename El<DT>::T* row, uint32_t v) {
+  Raw<DT, N> q;
+  const char* at = reinterpret_cast<const char*>(row) + v * (uint32_t)sizeof(*row);  // (scalar base, 32-bit offset)
+  if constexpr (sizeof(q) == 16) {
+    const v4u* p = reinterpret_cast<const v4u*>(at);
+    const v4u u = NT ? __builtin_nontemporal_load(p) : *p;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) q.w[i] = u[i];
+  } else {
+    const v2u* p = reinterpret_cast<const v2u*>(at);
+    const v2u u = NT ? __builtin_nontemporal_load(p) : *p;
+    q.w[0] = u[0];
+    q.w[1] = u[1];
+  }
+  return q;
+}
+template <int DT, int N, bool NT>
+__device__ __forceinline__ Raw<DT, N> raw_vec(const typename El<DT>::T* row, int v, int V) {
+  if (v + N <= V) return raw_whole<DT, N, NT>(row, v);
+  Raw<DT, N> q;
+#pragma unroll
+  for (int l = 0; l < N; ++l) {
+    const uint32_t b = __float_as_uint(v + l < V ? El<DT>::get(row, v + l) : -__builtin_inff());
+    if constexpr (DT == DSPARK_F32) q.w[l] = b;
+    else if (l & 1) q.w[l >> 1] |= b;
+    else q.w[l >> 1] = b >> 16;
+  }
+  return q;
+}
+template <int DT, int N>
+__device__ __forceinline__ void unpack(const Raw<DT, N>& q, float (&x)[N]) {
+#pragma unroll
+  for (int l = 0; l < N; ++l)
+    x[l] = DT == DSPARK_F32 ? __uint_as_float(q.w[l]) : l & 1 ? bf16_hi(q.w[l >> 1]) : bf16_lo(q.w[l >> 1]);
 }
 
 // logits of one vector of a thread
