@@ -2,17 +2,19 @@
 // grammar masks (dspark_shape_logits).
 //
 // A workgroup owns one slice of the vocabulary of one request and all rows
-// of the request there.  It counts the request's tokens of its slice in LDS
-// (bit 31: in the prompt; the other bits: times generated; integer additions,
-// so the order does not matter), turns the counts into what a row needs of a
-// token -- whether it was seen, and d = frequency c + presence [c > 0] - bias
-// -- and streams the slice of each row through that: z = x m - d with m = 1
-// for an unseen token, 1 / repetition or repetition for a seen one, then
-// z / T.  Both quotients are products with a reciprocal rounded once.  The
-// drafted token is added between rows.  Every slice scans the whole history,
-// so slices are wide (8,192 ids, 1,024 threads with eight logits of a row
-// each) and a row's loads are issued a row ahead, the first before the
-// history is read.
+// of the request there; a thread owns eight of its tokens in every row.  The
+// workgroup counts the request's tokens of its slice in LDS (bit 31: in the
+// prompt; the other bits: times generated; integer additions, so the order
+// does not matter) and lays the slice's biases beside them.  Each thread turns
+// that into what a row needs of its tokens, in registers -- whether each was
+// seen, and d = frequency c + presence [c > 0] - bias -- and streams its part
+// of the rows through it: z = x m - d with m = 1 for an unseen token,
+// 1 / repetition or repetition for a seen one, then z / T.  Both quotients
+// are products with a reciprocal rounded once.  A drafted token changes its
+// owner's registers between rows.  Every slice scans the whole history, so
+// slices are not narrow (4,096 ids, 512 threads), and what is read from
+// memory is asked for early: up to three rows ahead, the first rows and the
+// first of the history before anything else.
 #pragma once
 #include "slices.hpp"
 
@@ -41,14 +43,12 @@ __device__ __forceinline__ float pick_bit(uint32_t bits, int l, float a, float b
 }
 
 template <int TI, int TO, int NWV>
-__global__ void __launch_bounds__(64 * NWV, NWV == 16 ? 8 : 1) shape_kernel(ShapeArgs a) {
+__global__ void __launch_bounds__(64 * NWV) shape_kernel(ShapeArgs a) {
   constexpr int T = 64 * NWV, SLICE = 8 * T;
   constexpr int N = kVec<TO>, Q = 8 / N;  // Q vectors of N logits per thread and row
   __shared__ __align__(16) uint32_t count[SLICE];
-  __shared__ __align__(16) float minus[SLICE];             // d of each token
-  __shared__ __align__(16) uint8_t seen[SLICE / 8], hit[SLICE / 8];  // bits: seen; seen or biased
+  __shared__ __align__(16) float bias[SLICE];
   __shared__ uint32_t bad;  // refusals of the whole request: bit code - BAD_HISTORY
-  __shared__ float draft_bias;
   typedef typename El<TI>::T XT;
   typedef typename El<TO>::T OT;
   int64_t r;
@@ -72,7 +72,7 @@ __global__ void __launch_bounds__(64 * NWV, NWV == 16 ? 8 : 1) shape_kernel(Shap
   constexpr int kDepth = TI == DSPARK_F32 ? 2 : 3;
   Raw<TI, N> ahead[kDepth][Q];
   uint32_t ahead_allowed[kDepth][Q];
-  const auto fetch = [&](int i, int64_t m, Raw<TI, N> (&q)[Q], uint32_t (&allowed)[Q]) {
+  const auto fetch = [&](int i, Raw<TI, N> (&q)[Q]) {
     const XT* x = static_cast<const XT*>(a.x) + (r * P + i) * a.x_stride + start;
     if (size == SLICE) {  // (uniform)
 #pragma unroll
@@ -84,6 +84,8 @@ __global__ void __launch_bounds__(64 * NWV, NWV == 16 ? 8 : 1) shape_kernel(Shap
         if (t < size) q[j] = raw_vec<TI, N, true>(x, t, size);
       }
     }
+  };
+  const auto fetch_mask = [&](int64_t m, uint32_t (&allowed)[Q]) {
 #pragma unroll
     for (int j = 0; j < Q; ++j) allowed[j] = 0xffu;
     if (m >= 0 && m < h.n_masks) {
@@ -101,16 +103,16 @@ __global__ void __launch_bounds__(64 * NWV, NWV == 16 ? 8 : 1) shape_kernel(Shap
     if (!h.mask_row) return r * P + i;
     return __builtin_amdgcn_readlane(lane_mask, i & 63);
   };
-  int64_t ahead_mask[kDepth];
-  int32_t ahead_draft[kDepth];
 #pragma unroll
-  for (int k = 0; k < kDepth; ++k) {
-    if (k < P) {
-      ahead_mask[k] = mask_of(k);
-      ahead_draft[k] = __builtin_amdgcn_readlane(lane_draft, k);
-      fetch(k, ahead_mask[k], ahead[k], ahead_allowed[k]);
-    }
-  }
+  for (int k = 0; k < kDepth; ++k)
+    if (k < P) fetch(k, ahead[k]);
+
+  // the first of the history (history_max of it may be read, whatever its length)
+  constexpr int U = 4;
+  const int32_t* hist = h.history + r * h.history_stride;
+  int32_t token[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u) token[u] = h.history && u * T + tid < h.history_max ? hist[u * T + tid] : 0;
 
   const float rep = h.repetition ? h.repetition[r] : 1.0f;
   const float freq = h.frequency ? h.frequency[r] : 0.0f;
@@ -136,71 +138,88 @@ __global__ void __launch_bounds__(64 * NWV, NWV == 16 ? 8 : 1) shape_kernel(Shap
     }
   }
   const bool biased = bias_ok && b1 > b0;
-  const bool changed = counted || drafted || biased;
-  if (tid == 0) bad = 0u;
-  if (changed) {
+  // the first of the biases and of the rows' masks, on their way while LDS is cleared
+  int32_t bias_id = 0, bias_prev = -1;
+  float bias_value = 0.0f;
+  const auto fetch_bias = [&](int64_t e) {
+    bias_id = h.bias_ids[e];
+    bias_prev = e > b0 ? h.bias_ids[e - 1] : -1;
+    bias_value = h.bias_values[e];
+  };
+  if (biased && b0 + tid < b1) fetch_bias(b0 + tid);
+  int64_t ahead_mask[kDepth];
+  int32_t ahead_draft[kDepth];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) reinterpret_cast<uint4*>(count)[i * T + tid] = make_uint4(0u, 0u, 0u, 0u);
+  for (int k = 0; k < kDepth; ++k) {
+    if (k < P) {
+      ahead_mask[k] = mask_of(k);
+      ahead_draft[k] = __builtin_amdgcn_readlane(lane_draft, k);
+      fetch_mask(ahead_mask[k], ahead_allowed[k]);
+    }
+  }
+  if (tid == 0) bad = 0u;
+  const float4 none = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    if (counted || drafted) reinterpret_cast<float4*>(count)[i * T + tid] = none;
+    if (biased) reinterpret_cast<float4*>(bias)[i * T + tid] = none;
   }
   __syncthreads();
 
-  if (counted) {
-    const int32_t* hist = h.history + r * h.history_stride;
-    constexpr int U = 4;  // loads in flight
-    for (int i0 = tid; i0 < len; i0 += U * T) {
-      int32_t id[U];
+  for (int i0 = tid; i0 < len; i0 += U * T) {
 #pragma unroll
-      for (int u = 0; u < U; ++u) id[u] = i0 + u * T < len ? hist[i0 + u * T] : start;
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int i = i0 + u * T;
-        if (i < len) {
-          if ((uint32_t)id[u] >= (uint32_t)V) wrong |= 1u;
-          const uint32_t t = (uint32_t)(id[u] - start);
-          if (t < (uint32_t)size) {
-            if (i < plen) atomicOr(&count[t], kPrompt);
-            else atomicAdd(&count[t], 1u);
-          }
+    for (int u = 0; u < U; ++u) {
+      const int i = i0 + u * T;
+      if (i < len) {
+        if ((uint32_t)token[u] >= (uint32_t)V) wrong |= 1u;
+        const uint32_t t = (uint32_t)(token[u] - start);
+        if (t < (uint32_t)size) {
+          if (i < plen) atomicOr(&count[t], kPrompt);
+          else atomicAdd(&count[t], 1u);
         }
       }
     }
-  }
-  if (changed) {  // this thread's eight tokens: from counts to what a row needs
-    __syncthreads();
-    uint32_t c[8], bits = 0;
-    float d[8];
 #pragma unroll
-    for (int l = 0; l < 8; l += 4) {
-      const uint4 q = *reinterpret_cast<const uint4*>(count + tid * 8 + l);
-      c[l] = q.x; c[l + 1] = q.y; c[l + 2] = q.z; c[l + 3] = q.w;
+    for (int u = 0; u < U; ++u) {
+      const int64_t i = (int64_t)i0 + (U + u) * T;
+      token[u] = i < len ? hist[i] : 0;
     }
-#pragma unroll
-    for (int l = 0; l < 8; ++l) {
-      const uint32_t n = c[l] & ~kPrompt;
-      d[l] = n ? freq * (float)n + pres : 0.0f;
-      bits |= c[l] ? 1u << l : 0u;
-    }
-#pragma unroll
-    for (int l = 0; l < 8; l += 4) *reinterpret_cast<float4*>(minus + tid * 8 + l) = make_float4(d[l], d[l + 1], d[l + 2], d[l + 3]);
-    seen[tid] = hit[tid] = (uint8_t)bits;
-    __syncthreads();
   }
   if (biased) {
     for (int64_t e = b0 + tid; e < b1; e += T) {
-      const int32_t id = h.bias_ids[e], prev = e > b0 ? h.bias_ids[e - 1] : -1;
-      const float v = h.bias_values[e];
-      if ((uint32_t)id >= (uint32_t)V || prev >= id || v != v || v == __builtin_inff())
+      if (e != b0 + tid) fetch_bias(e);
+      if ((uint32_t)bias_id >= (uint32_t)V || bias_prev >= bias_id || bias_value != bias_value || bias_value == __builtin_inff())
         wrong |= 1u << (DSPARK_ST_BAD_BIAS - DSPARK_ST_BAD_HISTORY);
-      const uint32_t t = (uint32_t)(id - start);
-      if (t < (uint32_t)size) {  // (one entry per token in a list that is not refused)
-        minus[t] -= v;
-        atomicOr(reinterpret_cast<uint32_t*>(hit) + (t >> 5), 1u << (t & 31));
-      }
+      const uint32_t t = (uint32_t)(bias_id - start);
+      if (t < (uint32_t)size) bias[t] = bias_value;  // (one entry per token in a list that is not refused)
     }
   }
   if (wrong) atomicOr(&bad, wrong);
   __syncthreads();
   wrong = bad;
+  // this thread's tokens
+  uint32_t seen = 0, hit = 0;  // bit 8 j + l: token l of vector j was seen; seen or biased
+  float minus[Q][N];           // d
+#pragma unroll
+  for (int j = 0; j < Q; ++j) {
+#pragma unroll
+    for (int l = 0; l < N; l += 4) {
+      const int t = (j * T + tid) * N + l;
+      uint4 c = make_uint4(0u, 0u, 0u, 0u);
+      float4 f = none;
+      if (counted || drafted) c = *reinterpret_cast<const uint4*>(count + t);
+      if (biased) f = *reinterpret_cast<const float4*>(bias + t);
+      const uint32_t cs[4] = {c.x, c.y, c.z, c.w};
+      const float fs[4] = {f.x, f.y, f.z, f.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t n = cs[i] & ~kPrompt;
+        minus[j][l + i] = (n ? freq * (float)n + pres : 0.0f) - fs[i];
+        seen |= cs[i] ? 1u << (8 * j + l + i) : 0u;
+        hit |= cs[i] || fs[i] != 0.0f ? 1u << (8 * j + l + i) : 0u;
+      }
+    }
+  }
 
   for (int i0 = 0; i0 < P; i0 += kDepth) {
 #pragma unroll
@@ -221,27 +240,24 @@ __global__ void __launch_bounds__(64 * NWV, NWV == 16 ? 8 : 1) shape_kernel(Shap
       if (((i + kDepth) & 63) == 0) fetch_lanes(i + kDepth);
       ahead_mask[k] = mask_of(i + kDepth);
       ahead_draft[k] = __builtin_amdgcn_readlane(lane_draft, (i + kDepth) & 63);
-      fetch(i + kDepth, ahead_mask[k], ahead[k], ahead_allowed[k]);
+      fetch(i + kDepth, ahead[k]);
+      fetch_mask(ahead_mask[k], ahead_allowed[k]);
     }
     if (i > 0 && drafted) {
       if ((uint32_t)id >= (uint32_t)V) {
         wrong |= 1u;
       } else if ((uint32_t)(id - start) < (uint32_t)size) {
-        const int t = id - start;
-        if (tid == 0) draft_bias = 0.0f;
-        __syncthreads();  // the row before has read the table
-        if (biased) {
-          for (int64_t e = b0 + tid; e < b1; e += T)
-            if (h.bias_ids[e] == id) draft_bias = h.bias_values[e];
-          __syncthreads();
-        }
-        if (tid == 0) {
+        const int t = id - start, l = t & (N - 1), v = t / N;  // (uniform)
+        if (tid == v % T) {
+          const int j = v / T;
           const uint32_t n = (count[t] += 1u) & ~kPrompt;
-          minus[t] = (freq * (float)n + pres) - draft_bias;
-          seen[t >> 3] |= (uint8_t)(1u << (t & 7));
-          hit[t >> 3] |= (uint8_t)(1u << (t & 7));
+          const float d = (freq * (float)n + pres) - (biased ? bias[t] : 0.0f);
+#pragma unroll
+          for (int k = 0; k < Q * N; ++k)
+            if (k == j * N + l) minus[k / N][k % N] = d;
+          seen |= 1u << (8 * j + l);
+          hit |= 1u << (8 * j + l);
         }
-        __syncthreads();
       }
     }
     uint32_t now = wrong;
@@ -256,18 +272,11 @@ __global__ void __launch_bounds__(64 * NWV, NWV == 16 ? 8 : 1) shape_kernel(Shap
         if (status != DSPARK_ST_OK) {
           allowed[j] = 0u;
         } else {
-          if (changed && ((uint32_t)hit[t >> 3] >> (t & 7) & ((1u << N) - 1u))) {
-            const uint32_t sb = (uint32_t)seen[t >> 3] >> (t & 7);
-            float d[N];
-#pragma unroll
-            for (int l = 0; l < N; l += 4) {
-              const float4 q = *reinterpret_cast<const float4*>(minus + t + l);
-              d[l] = q.x; d[l + 1] = q.y; d[l + 2] = q.z; d[l + 3] = q.w;
-            }
+          if ((hit >> (8 * j)) & 0xffu) {
 #pragma unroll
             for (int l = 0; l < N; ++l) {
-              const float m = pick_bit(sb, l, z[j][l] > 0.0f ? inv_rep : rep, 1.0f);
-              z[j][l] = __builtin_fmaf(z[j][l], m, -d[l]);
+              const float m = pick_bit(seen, 8 * j + l, z[j][l] > 0.0f ? inv_rep : rep, 1.0f);
+              z[j][l] = __builtin_fmaf(z[j][l], m, -minus[j][l]);
             }
           }
 #pragma unroll
