@@ -211,6 +211,35 @@ struct DistillRow {  // what the gradient needs of a row
   double loss;
 };
 
+// The loss and the gradient's numbers from a row's sums (a finite maximum, no NaN, no +inf).
+__device__ __forceinline__ void distill_finish(double inv_t, bool tail, float m_off, float m_on, double off, double on,
+                                               double b0, double b1, double zm, DistillRow& o) {
+  constexpr float kNone = -__builtin_inff();
+  const float m = __builtin_fmaxf(m_off, m_on);
+  // e^((x - m) / T), 0 where x is none
+  const double e_off = m_off == kNone ? 0.0 : exp(((double)m_off - (double)m) * inv_t);
+  const double e_on = m_on == kNone ? 0.0 : exp(((double)m_on - (double)m) * inv_t);
+  const double S = off * e_off + on * e_on;  // (the first underflows where the rest is out of sight)
+  const double log_s = log(S), lse_u = (double)m * inv_t + log_s;
+  o.M = m;
+  o.inv_s = 1.0 / S;
+  o.M_off = m_off == kNone ? 0.0 : m_off;
+  o.f_off = e_off * o.inv_s;
+  if (tail) {
+    o.zm = zm;
+    o.loss = b1 + b0 * lse_u;
+    const double P = 1.0 - b0;
+    if (P > 0.0 && off > 0.0) {
+      o.loss += P * (log(P) - (((double)m_off - (double)m) * inv_t + log(off) - log_s));
+      o.f_off -= P / off;
+    }
+  } else {
+    const double lz = log(b0);
+    o.zm = zm + lz;
+    o.loss = b1 / b0 - lz + lse_u;
+  }
+}
+
 // One wave joins the slices of a row (every lane gets the result).
 __device__ __forceinline__ DistillRow distill_join(const DistillArgs& a, int64_t r) {
   DistillRow o{a.list_status[r], 0.0, 0.0, 0.0, 0.0, 0.0, 0.0};
@@ -231,27 +260,7 @@ __device__ __forceinline__ DistillRow distill_join(const DistillArgs& a, int64_t
   const auto shift = [&](float x, float y) { return x == kNone ? 0.0 : exp(((double)x - (double)y) * a.inv_t); };
   const double off = wave_sum(p.s_off * shift(p.m_off, m_off)), on = wave_sum(p.s_on * shift(p.m_on, m_on));
   const double b0 = wave_sum(p.b0), b1 = wave_sum(p.b1);
-  const double zm = a.part[r * a.slices].zm;
-  const double q_off = off * shift(m_off, m);  // underflows where the rest is out of sight
-  const double S = q_off + on * shift(m_on, m);
-  const double log_s = log(S), lse_u = (double)m * a.inv_t + log_s;
-  o.M = m;
-  o.inv_s = 1.0 / S;
-  o.M_off = m_off == kNone ? 0.0 : m_off;
-  o.f_off = shift(m_off, m) * o.inv_s;
-  if (a.lse) {
-    o.zm = zm;
-    o.loss = b1 + b0 * lse_u;
-    const double P = 1.0 - b0;
-    if (P > 0.0 && off > 0.0) {
-      o.loss += P * (log(P) - (((double)m_off - (double)m) * a.inv_t + log(off) - log_s));
-      o.f_off -= P / off;
-    }
-  } else {
-    const double lz = log(b0);
-    o.zm = zm + lz;
-    o.loss = b1 / b0 - lz + lse_u;
-  }
+  distill_finish(a.inv_t, a.lse != nullptr, m_off, m_on, off, on, b0, b1, a.part[r * a.slices].zm, o);
   return o;
 }
 
@@ -271,10 +280,10 @@ __device__ __forceinline__ void distill_row_out(const DistillArgs& a, int64_t r,
 template <int DT>
 __global__ void __launch_bounds__(kSliceBS) distill_part_kernel(DistillArgs a) {
   extern __shared__ uint32_t lds[];
-  const int64_t b = block_number(a.n * a.slices);
-  if (b < 0) return;
-  const int64_t r = b / a.slices;
-  distill_slice<DT>(a, r, (int)(b - r * a.slices), lds);
+  int64_t r;
+  int s;
+  if (!row_slice(a.n, a.slices, r, s)) return;
+  distill_slice<DT>(a, r, s, lds);
 }
 
 // one wave per row
@@ -297,10 +306,9 @@ __global__ void __launch_bounds__(kSliceBS) distill_grad_kernel(DistillArgs a) {
   __shared__ DistillRow sh;
   __shared__ float p[DSPARK_K_MAX];
   typedef typename El<DT>::T XT;
-  const int64_t b = block_number(a.n * a.slices);
-  if (b < 0) return;
-  const int64_t r = b / a.slices;
-  const int s = (int)(b - r * a.slices);
+  int64_t r;
+  int s;
+  if (!row_slice(a.n, a.slices, r, s)) return;
   const int start = s * a.slice, V = a.V;
   const int size = V - start < a.slice ? V - start : a.slice;
   const int words = (a.slice + 31) / 32;
@@ -359,6 +367,202 @@ __global__ void __launch_bounds__(kSliceBS) distill_grad_kernel(DistillArgs a) {
     }
     store_vec<DT, N>(g, start + t, V, v);
   }
+}
+
+// body(t, v) for every vector of a row's ids [start, start + size) that this
+// thread of T owns, t counted from start; kAhead loads are on their way at a
+// time.  BACK: from the end back, streamed (the last use of the row).
+constexpr int kAhead = 4;
+template <int DT, bool BACK, int T, class BODY>
+__device__ __forceinline__ void for_row(const typename El<DT>::T* x, int start, int size, BODY body) {
+  constexpr int N = kVec<DT>, STEP = T * N;
+  const typename El<DT>::T* row = x + start;
+  const int whole = size / (kAhead * STEP) * (kAhead * STEP);
+  const auto rest = [&] {
+    for (int t = whole + (int)threadIdx.x * N; t < size; t += STEP) {
+      float v[N];
+      unpack<DT, N>(raw_vec<DT, N, BACK>(row, t, size), v);
+      body(t, v);
+    }
+  };
+  if (BACK) rest();
+  for (int i = 0; i < whole; i += kAhead * STEP) {
+    const int base = BACK ? whole - kAhead * STEP - i : i;
+    Raw<DT, N> q[kAhead];
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) q[k] = raw_whole<DT, N, BACK>(row, (uint32_t)(base + k * STEP + (int)threadIdx.x * N));
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      float v[N];
+      unpack<DT, N>(q[k], v);
+      body(base + k * STEP + (int)threadIdx.x * N, v);
+    }
+  }
+  if (!BACK) rest();
+}
+
+// Loss and gradient of one row by one workgroup, where the rows fill the
+// chip: the row is read twice, the second time, from its end back, out of
+// the caches (the rows in work at once are about half of the last-level
+// cache), so that HBM sees one read and one write.
+template <int DT, int NWV>
+__global__ void __launch_bounds__(64 * NWV, 8) distill_row_kernel(DistillArgs a) {
+  constexpr int T = 64 * NWV, N = kVec<DT>, PER = DSPARK_K_MAX / T;
+  extern __shared__ uint32_t lds[];
+  __shared__ double red[NWV];
+  __shared__ float redf[NWV];
+  __shared__ uint32_t redu[NWV];
+  __shared__ float p[DSPARK_K_MAX];
+  __shared__ DistillRow sh;
+  typedef typename El<DT>::T XT;
+  const int64_t r = block_number(a.n);
+  if (r < 0) return;
+  const int V = a.V, tid = (int)threadIdx.x, words = (V + 31) / 32;
+  const XT* x = static_cast<const XT*>(a.x) + r * a.x_stride;
+  XT* g = static_cast<XT*>(a.grad) + r * a.grad_stride;
+  const int32_t* ids = a.ids + r * a.k_max;
+  const float* zl = a.logits + r * a.k_max;
+  const bool tail = a.lse != nullptr;
+  const auto larger = [](float u, float v) { return __builtin_fmaxf(u, v); };
+  const auto plus = [](double u, double v) { return u + v; };
+  const auto either = [](uint32_t u, uint32_t v) { return u | v; };
+  constexpr float kNone = -__builtin_inff();
+
+  int len = a.len[r];
+  uint32_t wrong = 0;
+  if (len < 0 || len > a.k_max) {
+    wrong = 1u;
+    len = 0;
+  }
+  if (len > 0 && tail && !finite_row_value(a.lse[r])) wrong |= 8u;
+  IdSet on{lds, lds + words};
+  on.clear(words);
+  int32_t id[PER], prev[PER];
+  float z[PER], zmax = kNone;
+#pragma unroll
+  for (int j = 0; j < PER; ++j) {
+    const int e = j * T + tid;
+    id[j] = prev[j] = -1;
+    z[j] = kNone;
+    if (e < len) {
+      id[j] = ids[e];
+      z[j] = zl[e];
+      zmax = __builtin_fmaxf(zmax, z[j]);
+      if (e > 0) prev[j] = ids[e - 1];
+      if ((uint32_t)id[j] >= (uint32_t)V) wrong |= 2u;
+      if (e > 0 && prev[j] >= id[j]) wrong |= 4u;
+      if (!finite_row_value(z[j])) wrong |= 8u;
+    }
+  }
+  wrong = group_reduce<NWV>(wrong, 0u, either, redu);
+  int status = wrong ? DSPARK_ST_Q_BAD_LEN + (wrong & 1u ? 0 : wrong & 2u ? 1 : wrong & 4u ? 2 : 3) : DSPARK_ST_OK;
+  const float c = (float)(a.inv_t * (double)kLog2e);
+  if (status == DSPARK_ST_OK && len > 0) {  // (uniform)
+    const double zm = tail ? (double)a.lse[r] : (double)group_reduce<NWV>(zmax, kNone, larger, redf) * a.inv_t;
+    __syncthreads();  // the set is clear
+    double b0 = 0.0, b1 = 0.0;
+    float m_on = kNone, s_on = 0.0f, on_x[PER];
+    uint32_t flags = 0;
+#pragma unroll
+    for (int j = 0; j < PER; ++j) {
+      on_x[j] = kNone;
+      if (id[j] >= 0) {
+        const float xj = El<DT>::get(x, id[j]);
+        on.add(id[j], prev[j], (uint32_t)(j * T + tid));
+        if (tail) {
+          on_x[j] = xj;
+          m_on = __builtin_fmaxf(m_on, xj);
+          flags |= xj != xj ? 1u : xj == __builtin_inff() ? 2u : 0u;
+        }
+        const double lp = (double)z[j] * a.inv_t - zm;
+        const double w = exp(lp);
+        if (w > 0.0) {
+          b0 += w;
+          b1 += w * (lp - (double)xj * a.inv_t);
+        }
+      }
+    }
+    if (m_on > kNone) {
+#pragma unroll
+      for (int j = 0; j < PER; ++j) s_on += __builtin_amdgcn_exp2f((on_x[j] - m_on) * c);
+    }
+    __syncthreads();
+    // off the list: running maximum and sum, a vector moves the maximum at most once
+    float m = kNone, s_off = 0.0f;
+    for_row<DT, false, T>(x, 0, V, [&](int t, float (&v)[N]) {
+      const uint32_t bits = tail ? on.members<N>(t) : 0u;
+      if (bits) {
+#pragma unroll
+        for (int l = 0; l < N; ++l) v[l] = (bits >> l) & 1u ? kNone : v[l];
+      }
+      float top = v[0];
+#pragma unroll
+      for (int l = 1; l < N; ++l) top = __builtin_fmaxf(top, v[l]);
+      if (top > m) {
+        s_off *= __builtin_amdgcn_exp2f((m - top) * c);  // (by 0 the first time)
+        m = top;
+      }
+      const float ref = m == kNone ? 0.0f : m;
+#pragma unroll
+      for (int l = 0; l < N; ++l) s_off += __builtin_amdgcn_exp2f((v[l] - ref) * c);
+    });
+    if (s_off != s_off || m == __builtin_inff()) {  // a NaN or +inf: which, the logits tell
+      for (int t = tid * N; t < V; t += T * N) {
+        float v[N];
+        load_vec<DT, N, false>(x, t, V, v);
+#pragma unroll
+        for (int l = 0; l < N; ++l) flags |= v[l] != v[l] ? 1u : v[l] == __builtin_inff() ? 2u : 0u;
+      }
+    }
+    const float M_off = group_reduce<NWV>(m, kNone, larger, redf);
+    const float M_on = group_reduce<NWV>(m_on, kNone, larger, redf);
+    flags = group_reduce<NWV>(flags, 0u, either, redu);
+    const double f = m == kNone ? 0.0 : (double)__builtin_amdgcn_exp2f((m - M_off) * c);
+    const double h = m_on == kNone ? 0.0 : (double)__builtin_amdgcn_exp2f((m_on - M_on) * c);
+    const double off = group_reduce<NWV>((double)s_off * f, 0.0, plus, red);
+    const double sum_on = group_reduce<NWV>((double)s_on * h, 0.0, plus, red);
+    b0 = group_reduce<NWV>(b0, 0.0, plus, red);
+    b1 = group_reduce<NWV>(b1, 0.0, plus, red);
+    status = flags & 1u ? DSPARK_ST_ROW_NAN
+             : flags & 2u ? DSPARK_ST_ROW_POSINF
+             : M_off == kNone && M_on == kNone ? DSPARK_ST_ROW_ZERO_MASS : DSPARK_ST_OK;
+    if (tid == 0 && status == DSPARK_ST_OK) {
+      DistillRow o{};
+      distill_finish(a.inv_t, tail, M_off, M_on, off, sum_on, b0, b1, zm, o);
+      sh = o;
+    }
+  }
+  __syncthreads();
+  const bool live = status == DSPARK_ST_OK && len > 0;  // (uniform)
+  if (tid == 0) {
+    a.loss[r] = live ? (float)sh.loss : 0.0f;
+    a.row_status[r] = status;
+  }
+  if (!live) {
+    float v[N];
+#pragma unroll
+    for (int l = 0; l < N; ++l) v[l] = 0.0f;
+    for (int t = tid * N; t < V; t += T * N) store_vec<DT, N>(g, t, V, v);
+    return;
+  }
+#pragma unroll
+  for (int j = 0; j < PER; ++j)
+    if (id[j] >= 0) p[j * T + tid] = (float)exp((double)z[j] * a.inv_t - sh.zm);
+  __syncthreads();
+  const float M = (float)sh.M, M_off = (float)sh.M_off, inv_s = (float)sh.inv_s;
+  const double w = (double)a.weight[r] * a.inv_t;
+  const float w_on = (float)w, f_off = (float)(sh.f_off * w);
+  for_row<DT, true, T>(x, 0, V, [&](int t, float (&v)[N]) {
+    const uint32_t bits = on.members<N>(t);
+#pragma unroll
+    for (int l = 0; l < N; ++l) {
+      const bool listed = (bits >> l) & 1u;
+      const float e = __builtin_amdgcn_exp2f((v[l] - (listed ? M : M_off)) * c);
+      v[l] = e * f_off;
+      if (listed) v[l] = (e * inv_s - p[on.entry(t + l) & (DSPARK_K_MAX - 1)]) * w_on;
+    }
+    store_vec<DT, N>(g, t, V, v);
+  });
 }
 
 }  // namespace dspark

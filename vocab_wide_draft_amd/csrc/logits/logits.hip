@@ -223,6 +223,11 @@ namespace dspark {
 namespace {
 
 constexpr int kDistillSliceMost = 32768;
+constexpr int kRowMost = 131072;  // ids of a row that one workgroup takes: its set of ids stays below 33 KB of LDS
+#ifndef ROWW
+#define ROWW 16
+#endif
+constexpr int kRowWaves = ROWW;
 
 int distill_slice_ids(int64_t n, int64_t V) {
   const int s = slice_of(n, V, kDistillSliceMost, 2048);
@@ -275,13 +280,22 @@ DistillArgs distill_args(const dspark_rows* student, const dspark_teacher* t, fl
 size_t distill_lds(const DistillArgs& a) { return 2u * 4u * ((size_t)a.slice / 32); }
 
 void launch_part(const DistillArgs& a, int dtype, hipStream_t s) {
-  const dim3 grid = grid_of(a.n * a.slices);
+  const dim3 grid = row_slice_grid(a.n, a.slices);
   if (dtype == DSPARK_BF16) hipLaunchKernelGGL(distill_part_kernel<DSPARK_BF16>, grid, dim3(kSliceBS), distill_lds(a), s, a);
   else hipLaunchKernelGGL(distill_part_kernel<DSPARK_F32>, grid, dim3(kSliceBS), distill_lds(a), s, a);
 }
+// Whether dspark_distill_step gives each row one workgroup.
+bool rows_fill(int64_t n, int64_t V) { return n >= 512 && V <= kRowMost; }
+template <int NWV>
+void launch_rows(const DistillArgs& a, int dtype, hipStream_t s) {
+  const size_t lds = 2u * 4u * (((size_t)a.V + 31) / 32);
+  const dim3 grid = grid_of(a.n), block(64 * NWV);
+  if (dtype == DSPARK_BF16) hipLaunchKernelGGL(HIP_KERNEL_NAME(distill_row_kernel<DSPARK_BF16, NWV>), grid, block, lds, s, a);
+  else hipLaunchKernelGGL(HIP_KERNEL_NAME(distill_row_kernel<DSPARK_F32, NWV>), grid, block, lds, s, a);
+}
 template <bool FROM_STATS>
 void launch_grad(const DistillArgs& a, int dtype, hipStream_t s) {
-  const dim3 grid = grid_of(a.n * a.slices);
+  const dim3 grid = row_slice_grid(a.n, a.slices);
   if (dtype == DSPARK_BF16)
     hipLaunchKernelGGL(HIP_KERNEL_NAME(distill_grad_kernel<DSPARK_BF16, FROM_STATS>), grid, dim3(kSliceBS), distill_lds(a), s, a);
   else
@@ -353,8 +367,12 @@ int dspark_distill_step(const dspark_rows* student, const dspark_teacher* teache
   a.grad = grad;
   a.grad_stride = grad_stride;
   hipStream_t s = static_cast<hipStream_t>(stream);
-  launch_part(a, student->dtype, s);
-  launch_grad<false>(a, student->dtype, s);
+  if (rows_fill(a.n, a.V)) {
+    launch_rows<kRowWaves>(a, student->dtype, s);
+  } else {
+    launch_part(a, student->dtype, s);
+    launch_grad<false>(a, student->dtype, s);
+  }
   return host_check_launch();
 }
 

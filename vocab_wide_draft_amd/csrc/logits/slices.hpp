@@ -177,10 +177,14 @@ __device__ __forceinline__ T group_reduce(T v, T id, OP op, T* scratch) {
   __syncthreads();
   if (lane_id() == 0) scratch[wave_id()] = v;
   __syncthreads();
-  T r = scratch[0];
+  if constexpr (NWV <= 4) {
+    T r = scratch[0];
 #pragma unroll
-  for (int w = 1; w < NWV; ++w) r = op(r, scratch[w]);
-  return r;
+    for (int w = 1; w < NWV; ++w) r = op(r, scratch[w]);
+    return r;
+  } else {  // (few registers: every wave reduces the waves' results)
+    return wave_reduce(lane_id() < NWV ? scratch[lane_id()] : id, id, op);
+  }
 }
 
 // Sum of the values of the threads before this one, over a workgroup of NWV
