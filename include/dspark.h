@@ -484,7 +484,9 @@ int dspark_distill_backward(const dspark_rows* student, const dspark_teacher* te
                             int64_t grad_stride, void* stream);
 
 /* Both in one call, for row weights known beforehand: loss (unweighted) and
- * grad of sum_r weight[r] loss[r], as the two calls above give them. */
+ * grad of sum_r weight[r] loss[r], as the two calls above give them.  ws:
+ * dspark_distill_step_workspace() bytes, 16-byte aligned (NULL where it is 0). */
+size_t dspark_distill_step_workspace(int64_t n_rows, int64_t vocab);
 int dspark_distill_step(const dspark_rows* student, const dspark_teacher* teacher, float temperature,
                         const float* weight, float* loss, void* grad, int64_t grad_stride, int32_t* row_status,
                         void* ws, size_t ws_bytes, void* stream);

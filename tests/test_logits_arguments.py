@@ -71,18 +71,22 @@ def test_top_refusals():
 def test_distill_refusals():
     lib = B.load_library()
     r = B.Rows(0x100000, 1, 0, 6, 64, 64)
-    need = lib.dspark_distill_workspace(6, 64)
-    assert need > 0 and lib.dspark_distill_workspace(0, 64) == 0 and lib.dspark_distill_workspace(6, 0) == 0
+    V = 65536
+    r = B.Rows(0x100000, 1, 0, 6, V, V)  # long enough for a workspace in every entry point
+    need = lib.dspark_distill_workspace(6, V)
+    assert lib.dspark_distill_step_workspace(6, V) == need
+    assert lib.dspark_distill_step_workspace(6, 64) == 0 and lib.dspark_distill_step_workspace(4096, V) == 0
+    assert need > 0 and lib.dspark_distill_workspace(0, V) == 0 and lib.dspark_distill_workspace(6, 0) == 0
     t = B.Teacher(0x10000, 0x10000, 0x10000, None, 8, 0)
 
     def fwd(r=r, t=t, T=1.0, loss=fake, ws=0x40000, n=need):
         return lib.dspark_distill(ctypes.byref(r), ctypes.byref(t), T, loss, fake, fake, ctypes.c_void_p(ws), n, None)
 
-    def bwd(r=r, t=t, T=1.0, st=fake, grad=0x900000, stride=64):
+    def bwd(r=r, t=t, T=1.0, st=fake, grad=0x900000, stride=65536):
         return lib.dspark_distill_backward(ctypes.byref(r), ctypes.byref(t), T, st, fake, fake, ctypes.c_void_p(grad),
                                            stride, None)
 
-    def step(r=r, t=t, T=1.0, w=fake, grad=0x900000, stride=64, ws=0x40000, n=need):
+    def step(r=r, t=t, T=1.0, w=fake, grad=0x900000, stride=65536, ws=0x40000, n=need):
         return lib.dspark_distill_step(ctypes.byref(r), ctypes.byref(t), T, w, fake, ctypes.c_void_p(grad), stride, fake,
                                        ctypes.c_void_p(ws), n, None)
 
@@ -92,14 +96,14 @@ def test_distill_refusals():
         for x in bad_t:
             assert f(t=x) == -1
         assert f(T=0.0) == -1 and f(T=float("nan")) == -1
-        assert f(r=B.Rows(0x100000, 1, 0, 6, 64, 68)) == -2
+        assert f(r=B.Rows(0x100000, 1, 0, 6, V, V + 4)) == -2
     assert fwd(loss=None) == -1 and bwd(st=None) == -1 and step(w=None) == -1
     for f in (fwd, step):
         assert f(n=need - 1) == -3 and f(ws=0) == -3 and f(ws=0x40008) == -2
     for f in (bwd, step):
-        assert f(grad=0x900008) == -2 and f(stride=63) == -1 and f(grad=0) == -1
+        assert f(grad=0x900008) == -2 and f(stride=V - 1) == -1 and f(grad=0) == -1
         assert f(grad=0x100080) == -1                          # overlaps the student rows
-        assert f(grad=0x100000, stride=72) == -1               # in place with another stride
+        assert f(grad=0x100000, stride=V + 8) == -1               # in place with another stride
     empty = B.Rows(None, 1, 0, 0, 64, 64)
     t0 = B.Teacher(None, None, None, None, 8, 0)
     assert fwd(r=empty, t=t0, loss=None, ws=0, n=0) == 0 and bwd(r=empty, t=t0, st=None, grad=0) == 0

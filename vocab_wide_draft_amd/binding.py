@@ -70,6 +70,7 @@ EXPORTS = ["dspark_propose", "dspark_q_alloc", "dspark_sample", "dspark_verify_g
            "dspark_q_alloc_weights", "dspark_cr_expf", "dspark_q_encode", "dspark_q_validate", "dspark_margin", "dspark_verify_stochastic", "dspark_verify_ratio", "dspark_sharded_propose", "dspark_sharded_propose_noalloc", "dspark_sharded_q", "dspark_sharded_q_workspace", "dspark_workspace_bytes", "dspark_q_semantic_id",
            "dspark_shape_logits", "dspark_top_logits", "dspark_top_logits_workspace", "dspark_distill",
            "dspark_distill_backward", "dspark_distill_step", "dspark_distill_workspace",
+           "dspark_distill_step_workspace",
            "dspark_status_name", "dspark_last_error", "dspark_abi_version"]
 
 
@@ -114,6 +115,7 @@ def load_library():
         "dspark_distill_backward": (ctypes.c_int, [RP, TP, F32, P, P, P, P, I64, P]),
         "dspark_distill_step": (ctypes.c_int, [RP, TP, F32, P, P, P, I64, P, P, SZ, P]),
         "dspark_distill_workspace": (SZ, [I64, I64]),
+        "dspark_distill_step_workspace": (SZ, [I64, I64]),
         "dspark_q_semantic_id": (ctypes.c_char_p, []),
         "dspark_status_name": (ctypes.c_char_p, [I32]),
         "dspark_last_error": (ctypes.c_char_p, []),
@@ -473,7 +475,7 @@ def _arg(t, name, dtype, shape, dev):
     """Address of a contiguous argument tensor (None stays None)."""
     if t is None:
         return None
-    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or t.device != dev or not t.is_contiguous():
+    if t.dtype != dtype or t.shape != shape or t.device != dev or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {dev}, "
                          f"not {t.dtype} {tuple(t.shape)} on {t.device}")
     return t.data_ptr()
@@ -492,8 +494,9 @@ def _matrix(t, name, dtype, n, dev):
 
 def _empty_rows(n, V, dtype, dev):
     """Rows [n, V] that start 16-byte aligned."""
-    per = 16 // dtype.itemsize
-    return torch.empty((n, -(-V // per) * per), dtype=dtype, device=dev)[:, :V]
+    wide = -(-V * dtype.itemsize // 16) * 16 // dtype.itemsize
+    rows = torch.empty((n, wide), dtype=dtype, device=dev)
+    return rows if wide == V else rows[:, :V]
 
 
 def _out_rows(out, like, dtype):
@@ -504,13 +507,20 @@ def _out_rows(out, like, dtype):
     return out
 
 
+# the current stream's handle, without a torch.cuda.Stream around it where torch offers that (2 us less per call)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
 def _call(dev, f, *args):
     """The library call on dev's current stream, with dev current."""
     if dev.index == torch.cuda.current_device():
-        _check(f(*args, ctypes.c_void_p(torch.cuda.current_stream(dev).cuda_stream)))
+        rc = f(*args, _raw_stream(dev.index))
     else:
         with torch.cuda.device(dev):
-            _check(f(*args, ctypes.c_void_p(torch.cuda.current_stream(dev).cuda_stream)))
+            rc = f(*args, _raw_stream(dev.index))
+    if rc != 0:
+        _check(rc)
 
 
 def shape_logits(rows: torch.Tensor, rows_per_request: int = 1, *, history=None, history_len=None, prompt_len=None,
@@ -572,15 +582,14 @@ def top_logits(rows: torch.Tensor, k_max: int, topk=None, temperature: float = 1
     k = int(k_max)
     if k < 0 or k > K_MAX:
         raise ValueError("k_max must be in [0, K_MAX]")
-    out = {"ids": torch.empty((n, k), dtype=torch.int32, device=dev),
-           "logits": torch.empty((n, k), dtype=torch.float32, device=dev),
-           "len": _i32(n, dev), "lse": torch.empty(n, dtype=torch.float32, device=dev), "status": _i32(n, dev)}
-    nbytes = int(lib.dspark_top_logits_workspace(n, V, k))
+    ids, logits = torch.empty((n, k), dtype=torch.int32, device=dev), torch.empty((n, k), dtype=torch.float32, device=dev)
+    length, lse, st = _i32(n, dev), torch.empty(n, dtype=torch.float32, device=dev), _i32(n, dev)
+    nbytes = lib.dspark_top_logits_workspace(n, V, k)
     ws = torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
-    tk = None if topk is None else ctypes.c_void_p(_arg(topk, "topk", torch.int32, (n,), dev))
-    _call(dev, lib.dspark_top_logits, ctypes.byref(r), tk, k, float(temperature), _p(out["ids"]), _p(out["logits"]),
-          _p(out["len"]), _p(out["lse"]), _p(out["status"]), _p(ws), nbytes)
-    return out
+    _call(dev, lib.dspark_top_logits, ctypes.byref(r), _arg(topk, "topk", torch.int32, (n,), dev), k, float(temperature),
+          ids.data_ptr(), logits.data_ptr(), length.data_ptr(), lse.data_ptr(), st.data_ptr(),
+          ws.data_ptr() if nbytes else None, nbytes)
+    return {"ids": ids, "logits": logits, "len": length, "lse": lse, "status": st}
 
 
 def _teacher(t, n, dev) -> Teacher:
@@ -594,8 +603,7 @@ def _teacher(t, n, dev) -> Teacher:
                    _arg(t.get("lse"), "teacher lse", torch.float32, (n,), dev), k, 0)
 
 
-def _distill_ws(lib, n, V, dev):
-    nbytes = int(lib.dspark_distill_workspace(n, V))
+def _distill_ws(nbytes, dev):
     return (torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None), nbytes
 
 
@@ -611,7 +619,7 @@ def distill(student: torch.Tensor, teacher, temperature: float = 1.0):
     t = _teacher(teacher, n, dev)
     out = {"loss": torch.empty(n, dtype=torch.float32, device=dev),
            "stats": torch.empty((n, DISTILL_STATS), dtype=torch.float64, device=dev), "status": _i32(n, dev)}
-    ws, nbytes = _distill_ws(lib, n, V, dev)
+    ws, nbytes = _distill_ws(lib.dspark_distill_workspace(n, V), dev)
     _call(dev, lib.dspark_distill, ctypes.byref(r), ctypes.byref(t), float(temperature), _p(out["loss"]),
           _p(out["stats"]), _p(out["status"]), _p(ws), nbytes)
     return out
@@ -645,7 +653,7 @@ def distill_step(student: torch.Tensor, teacher, weight: torch.Tensor, temperatu
     g = _out_rows(out, student, student.dtype)
     loss, st = torch.empty(n, dtype=torch.float32, device=dev), _i32(n, dev)
     w = ctypes.c_void_p(_arg(weight, "weight", torch.float32, (n,), dev))
-    ws, nbytes = _distill_ws(lib, n, V, dev)
+    ws, nbytes = _distill_ws(lib.dspark_distill_step_workspace(n, V), dev)
     _call(dev, lib.dspark_distill_step, ctypes.byref(r), ctypes.byref(t), float(temperature), w, _p(loss), _p(g),
           g.stride(0), _p(st), _p(ws), nbytes)
     return {"loss": loss, "grad": g, "status": st}

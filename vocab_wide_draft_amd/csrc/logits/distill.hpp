@@ -60,6 +60,38 @@ constexpr float kLog2e = 1.4426950408889634f;
 
 __device__ __forceinline__ bool finite_row_value(float x) { return (__float_as_uint(x) & 0x7f800000u) != 0x7f800000u; }
 
+// body(t, v) for every vector of a row's ids [start, start + size) that this
+// thread of T owns, t counted from start; kAhead loads are on their way at a
+// time.  BACK: from the end back, streamed (the last use of the row).
+constexpr int kAhead = 4;
+template <int DT, bool BACK, int T, class BODY>
+__device__ __forceinline__ void for_row(const typename El<DT>::T* x, int start, int size, BODY body) {
+  constexpr int N = kVec<DT>, STEP = T * N;
+  const typename El<DT>::T* row = x + start;
+  const int whole = size / (kAhead * STEP) * (kAhead * STEP);
+  const auto rest = [&] {
+    for (int t = whole + (int)threadIdx.x * N; t < size; t += STEP) {
+      float v[N];
+      unpack<DT, N>(raw_vec<DT, N, BACK>(row, t, size), v);
+      body(t, v);
+    }
+  };
+  if (BACK) rest();
+  for (int i = 0; i < whole; i += kAhead * STEP) {
+    const int base = BACK ? whole - kAhead * STEP - i : i;
+    Raw<DT, N> q[kAhead];
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) q[k] = raw_whole<DT, N, BACK>(row, (uint32_t)(base + k * STEP + (int)threadIdx.x * N));
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      float v[N];
+      unpack<DT, N>(q[k], v);
+      body(base + k * STEP + (int)threadIdx.x * N, v);
+    }
+  }
+  if (!BACK) rest();
+}
+
 // The slice's part of a row (see above).  Returns with the whole workgroup.
 template <int DT>
 __device__ void distill_slice(const DistillArgs& a, int64_t r, int s, uint32_t* lds) {
@@ -144,13 +176,11 @@ __device__ void distill_slice(const DistillArgs& a, int64_t r, int s, uint32_t* 
     for (int j = 0; j < kListPer; ++j) s_on += __builtin_amdgcn_exp2f((on_x[j] - m_on) * c);
   }
   __syncthreads();
-  // the row off the list: running maximum and sum; a vector
-  // moves the maximum at most once
+  // the row off the list: running maximum and sum; a vector moves the maximum
+  // at most once
   constexpr int N = kVec<DT>;
   float m = -__builtin_inff(), s_off = 0.0f;
-  for (int t = threadIdx.x * N; t < size; t += kSliceBS * N) {
-    float v[N];
-    load_vec<DT, N, false>(x, start + t, V, v);
+  for_row<DT, false, kSliceBS>(x, start, size, [&](int t, float (&v)[N]) {
     const uint32_t bits = tail ? on.members<N>(t) : 0u;
     if (bits) {
 #pragma unroll
@@ -166,7 +196,7 @@ __device__ void distill_slice(const DistillArgs& a, int64_t r, int s, uint32_t* 
     const float ref = m == -__builtin_inff() ? 0.0f : m;
 #pragma unroll
     for (int l = 0; l < N; ++l) s_off += __builtin_amdgcn_exp2f((v[l] - ref) * c);
-  }
+  });
   // a NaN or +inf shows in the sum or the maximum; which of the two, the thread's own logits tell
   if (s_off != s_off || m == __builtin_inff()) {
     for (int t = threadIdx.x * N; t < size; t += kSliceBS * N) {
@@ -354,9 +384,8 @@ __global__ void __launch_bounds__(kSliceBS) distill_grad_kernel(DistillArgs a) {
   const float M = (float)sh.M, M_off = (float)sh.M_off, inv_s = (float)sh.inv_s;
   const double w = (double)a.weight[r] * a.inv_t;
   const float w_on = (float)w, f_off = (float)(sh.f_off * w);
-  for (int t = threadIdx.x * N; t < size; t += kSliceBS * N) {
-    float v[N];
-    load_vec<DT, N, true>(x, start + t, V, v);
+  XT* const out = g + start;
+  for_row<DT, true, kSliceBS>(x, start, size, [&](int t, float (&v)[N]) {
     const uint32_t bits = on.members<N>(t);
 #pragma unroll
     for (int l = 0; l < N; ++l) {
@@ -365,40 +394,8 @@ __global__ void __launch_bounds__(kSliceBS) distill_grad_kernel(DistillArgs a) {
       v[l] = e * f_off;
       if (listed) v[l] = (e * inv_s - p[on.entry(t + l) & (DSPARK_K_MAX - 1)]) * w_on;
     }
-    store_vec<DT, N>(g, start + t, V, v);
-  }
-}
-
-// body(t, v) for every vector of a row's ids [start, start + size) that this
-// thread of T owns, t counted from start; kAhead loads are on their way at a
-// time.  BACK: from the end back, streamed (the last use of the row).
-constexpr int kAhead = 4;
-template <int DT, bool BACK, int T, class BODY>
-__device__ __forceinline__ void for_row(const typename El<DT>::T* x, int start, int size, BODY body) {
-  constexpr int N = kVec<DT>, STEP = T * N;
-  const typename El<DT>::T* row = x + start;
-  const int whole = size / (kAhead * STEP) * (kAhead * STEP);
-  const auto rest = [&] {
-    for (int t = whole + (int)threadIdx.x * N; t < size; t += STEP) {
-      float v[N];
-      unpack<DT, N>(raw_vec<DT, N, BACK>(row, t, size), v);
-      body(t, v);
-    }
-  };
-  if (BACK) rest();
-  for (int i = 0; i < whole; i += kAhead * STEP) {
-    const int base = BACK ? whole - kAhead * STEP - i : i;
-    Raw<DT, N> q[kAhead];
-#pragma unroll
-    for (int k = 0; k < kAhead; ++k) q[k] = raw_whole<DT, N, BACK>(row, (uint32_t)(base + k * STEP + (int)threadIdx.x * N));
-#pragma unroll
-    for (int k = 0; k < kAhead; ++k) {
-      float v[N];
-      unpack<DT, N>(q[k], v);
-      body(base + k * STEP + (int)threadIdx.x * N, v);
-    }
-  }
-  if (!BACK) rest();
+    store_vec<DT, N>(out, t, size, v);
+  });
 }
 
 // Loss and gradient of one row by one workgroup, where the rows fill the
