@@ -95,6 +95,7 @@ struct TopScratch {
   uint32_t scan[NWV];
   double red[NWV];
   uint32_t bin, above;
+  uint32_t few[64], n_few;  // the keys of a bin that holds few
 };
 
 // The bin where the running count from bin 0 on reaches `need` (which the
@@ -156,6 +157,29 @@ __device__ __forceinline__ TopCut top_cut(const uint32_t (&key)[PER], uint32_t l
     __syncthreads();
     if (held == n) return TopCut{blo - 1u, 0u};  // all keys from blo on (blo >= 1)
     if (shift == 0) return TopCut{bhi, n};
+    if (held <= 64u) {  // one wave ranks them
+      if (threadIdx.x == 0) sh.n_few = 0u;
+      __syncthreads();
+#pragma unroll
+      for (int j = 0; j < PER; ++j)
+        if (key[j] >= blo && key[j] <= bhi) sh.few[atomicAdd(&sh.n_few, 1u)] = key[j];
+      __syncthreads();
+      if (wave_id() == 0) {
+        const uint32_t own = (uint32_t)lane_id() < held ? sh.few[lane_id()] : 0u;
+        uint32_t more = 0, same = 0;
+        for (uint32_t i = 0; i < held; ++i) {
+          const uint32_t o = sh.few[i];
+          more += o > own ? 1u : 0u;
+          same += o == own ? 1u : 0u;
+        }
+        if (own && more < n && n <= more + same) {  // (every lane that holds the key: the same values)
+          sh.bin = own;
+          sh.above = n - more;
+        }
+      }
+      __syncthreads();
+      return TopCut{sh.bin, sh.above};
+    }
     hi = bhi;
     lo = blo;
   }
@@ -391,7 +415,9 @@ __device__ __forceinline__ void push_ge(uint32_t& mask, float x, float t) {
 // maximum, a multiply-add, an exponential of four cycles' issue, an addition
 // and two for the mask per logit), so everything per thread is kept small:
 // each wave has a reference of its own, the order of the candidates comes
-// from one scan of packed counts, and a candidate's logit is read again.
+// from one scan of packed counts.  A candidate's logit is picked from a copy of
+// the slice in LDS (read again from memory it held its wave up: 91 us instead
+// of 71 for 1,280 bf16 rows).
 template <int DT>
 __global__ void __launch_bounds__(kSliceBS) top_slice_kernel(TopSliceArgs q) {
   __shared__ __align__(16) uint32_t sample[kSliceBS];
@@ -408,6 +434,7 @@ __global__ void __launch_bounds__(kSliceBS) top_slice_kernel(TopSliceArgs q) {
   const XT* row = static_cast<const XT*>(q.a.x) + r * q.a.stride;
   const int run = (V / 64) & ~7;  // the sample: 64 runs of 32 logits, four threads each
   float smp[8], x[U][N];
+  __shared__ __align__(16) uint32_t held[kTopSlice * sizeof(XT) / 4];  // the slice as it was loaded
 #pragma unroll
   for (int i = 0; i < 8 / N; ++i) {
     float y[N];
@@ -415,12 +442,13 @@ __global__ void __launch_bounds__(kSliceBS) top_slice_kernel(TopSliceArgs q) {
 #pragma unroll
     for (int l = 0; l < N; ++l) smp[i * N + l] = y[l];
   }
+  Raw<DT, N> raw[U];
   if (start + kTopSlice <= V) {  // (uniform)
 #pragma unroll
-    for (int i = 0; i < U; ++i) load_whole<DT, N, true>(row, start + (i * kSliceBS + tid) * N, x[i]);
+    for (int i = 0; i < U; ++i) raw[i] = raw_whole<DT, N, true>(row + start, (uint32_t)(i * kSliceBS + tid) * N);
   } else {
 #pragma unroll
-    for (int i = 0; i < U; ++i) load_vec<DT, N, true>(row, start + (i * kSliceBS + tid) * N, V, x[i]);
+    for (int i = 0; i < U; ++i) raw[i] = raw_vec<DT, N, true>(row + start, (i * kSliceBS + tid) * N, V - start);
   }
   float top = smp[0];
 #pragma unroll
@@ -443,6 +471,12 @@ __global__ void __launch_bounds__(kSliceBS) top_slice_kernel(TopSliceArgs q) {
     // -inf is no candidate: the threshold is the lowest finite value at least
     const float t = top_key_value<DSPARK_BF16>(T);
     if (lane_id() == 0) thr = t >= -3.4028235e38f ? t : -3.4028235e38f;
+  }
+#pragma unroll
+  for (int i = 0; i < U; ++i) {
+    unpack<DT, N>(raw[i], x[i]);
+    const uint4 w = make_uint4(raw[i].w[0], raw[i].w[1], raw[i].w[2], raw[i].w[3]);
+    *reinterpret_cast<uint4*>(held + (i * kSliceBS + tid) * 4) = w;
   }
   float m = x[0][0];
 #pragma unroll
@@ -514,7 +548,7 @@ __global__ void __launch_bounds__(kSliceBS) top_slice_kernel(TopSliceArgs q) {
       before[w] += 1ull << (16 * i);
       left &= ~((1u << (N - 1)) >> l << (N * i));
       const int place = ((4 * w + i) * kSliceBS + tid) * N + l;
-      if (pos < (uint32_t)q.cap) list[pos] = Cand<DT>::make(El<DT>::get(row, start + place), place);
+      if (pos < (uint32_t)q.cap) list[pos] = Cand<DT>::make(El<DT>::get(reinterpret_cast<const XT*>(held), place), place);
     }
   }
   if (tid == 0) {
@@ -537,11 +571,9 @@ __global__ void __launch_bounds__(64 * NWV) top_select_kernel(TopSliceArgs q) {
   const int64_t r = block_number(a.n);
   if (r < 0) return;
   const TopPart* part = q.part + r * q.slices;
-  if (wave_id() == 0) {
+  if (wave_id() == 1) {  // the sums: one wave's record per lane
     const int l = lane_id();
     constexpr float kNone = -__builtin_inff();
-    const auto either = [](uint32_t u, uint32_t v) { return u | v; };
-    // the sums: one wave's record per lane
     float m = kNone;
     for (int i = l; i < q.slices * kSliceNW; i += 64) m = __builtin_fmaxf(m, part[i / kSliceNW].m[i % kSliceNW]);
     const float M = wave_reduce(m, kNone, [](float u, float v) { return __builtin_fmaxf(u, v); });
@@ -552,7 +584,14 @@ __global__ void __launch_bounds__(64 * NWV) top_select_kernel(TopSliceArgs q) {
       if (mi > kNone) sum += (double)part[i / kSliceNW].sum[i % kSliceNW] * exp(sum_reference(a, mi) - top);
     }
     sum = wave_sum(sum);
-    // the lists: two slices per lane
+    if (l == 0) {
+      row_sum = sum;
+      row_m = M;
+    }
+  }
+  if (wave_id() == 0) {  // the lists: two slices per lane
+    const int l = lane_id();
+    const auto either = [](uint32_t u, uint32_t v) { return u | v; };
     uint32_t n[2] = {0u, 0u}, flags = 0u, over = 0u;
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
@@ -569,8 +608,6 @@ __global__ void __launch_bounds__(64 * NWV) top_select_kernel(TopSliceArgs q) {
     first[2 * l + 1] = inc - n[1];
     if (l == 63) first[kTopSlices] = inc;
     if (l == 0) {
-      row_sum = sum;
-      row_m = M;
       row_flags = flags;
       row_over = over;
     }
