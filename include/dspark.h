@@ -362,7 +362,7 @@ int dspark_sharded_q(const dspark_rows* rows, int32_t n_shards, const dspark_q* 
  *           history[r * history_stride .. + history_len[r]), of which the
  *           first prompt_len[r] are the prompt's and the rest were generated
  *           (prompt_len NULL: all were).  0 <= prompt_len[r] <=
- *           history_len[r] <= history_max <= history_stride.
+ *           history_len[r] <= history_max <= history_stride, history_max <= 2^30.
  *   draft:  the drafted tokens; row i counts draft[r * draft_stride .. + i)
  *           as generated (draft_stride >= rows_per_request - 1).
  *   repetition (> 0), frequency, presence: the request's penalties (finite;

@@ -354,6 +354,21 @@ def test_shape_other_stream_and_graph_replays():
             assert torch.equal(o["logits"].view(torch.int16), eager.view(torch.int16)), rep
 
 
+def test_shape_empty_arguments():
+    x = torch.ones((3, 40), device=dev())
+    two = f32([2.0] * 3)
+    empty = torch.zeros((3, 0), dtype=torch.int32, device=dev())
+    g = B.shape_logits(x, history=empty, history_len=i32([0, 1, 0]), presence=two)
+    assert g["status"].tolist() == [0, L.ST_BAD_HISTORY, 0] and (g["logits"][0] == 1).all()
+    g = B.shape_logits(x, history=empty, presence=two)
+    assert not g["status"].any() and torch.equal(g["logits"], x)
+    off = torch.zeros(4, dtype=torch.int64, device=dev())
+    g = B.shape_logits(x, bias=(off, i32([]), f32([])))
+    assert not g["status"].any() and torch.equal(g["logits"], x)
+    with pytest.raises(ValueError):
+        B.shape_logits(x, mask=torch.zeros((0, 2), dtype=torch.int32, device=dev()), mask_row=i32([0, 0, 0]))
+
+
 def test_shape_no_rows():
     g = B.shape_logits(torch.zeros((0, 64), device=dev()), 6)
     assert g["logits"].shape == (0, 64) and g["status"].shape == (0,)

@@ -41,7 +41,7 @@ def test_shape_refusals():
     assert _shape(r, _how(), st=None) == -1
     assert _shape(r, _how(history=1, history_max=8, history_stride=7)) == -1
     assert _shape(r, _how(history=1, history_max=-1, history_stride=7)) == -1
-    assert _shape(r, _how(history=1, history_max=1 << 31, history_stride=1 << 31)) == -1
+    assert _shape(r, _how(history=1, history_max=(1 << 30) + 1, history_stride=1 << 31)) == -1
     assert _shape(r, _how(history=1, history_max=8, history_stride=8)) == -1  # no history_len
     assert _shape(r, _how(6, draft=1, draft_stride=4)) == -1
     assert _shape(r, _how(bias_offset=1, bias_total=-1)) == -1

@@ -549,12 +549,14 @@ def shape_logits(rows: torch.Tensor, rows_per_request: int = 1, *, history=None,
     h, h_max, h_stride = _matrix(history, "history", torch.int32, R, dev)
     if history is not None and history_len is None:
         history_len = torch.full((R,), h_max, dtype=torch.int32, device=dev)
+    if history is not None and h_max == 0:
+        h = history_len.data_ptr()  # nothing to read, but the lengths are still checked
     d, d_cols, d_stride = _matrix(draft, "draft", torch.int32, R, dev)
     if draft is not None and d_cols < P - 1:
         raise ValueError("draft must have at least rows_per_request - 1 columns")
     m, m_cols, m_stride = (None, 0, 0) if mask is None else _matrix(mask, "mask", torch.int32, mask.shape[0], dev)
-    if mask is not None and m_cols < (V + 31) // 32:
-        raise ValueError("mask must have at least (V + 31) // 32 columns")
+    if mask is not None and (m_cols < (V + 31) // 32 or mask.shape[0] == 0):
+        raise ValueError("mask must have rows of at least (V + 31) // 32 columns")
     offsets, ids, values = bias if bias is not None else (None, None, None)
     total = 0 if ids is None else ids.numel()
     i32, f32 = torch.int32, torch.float32

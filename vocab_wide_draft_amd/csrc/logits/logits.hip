@@ -137,8 +137,8 @@ int dspark_shape_logits(const dspark_rows* rows, const dspark_shaping* how, void
   if (rows->n_rows % how->rows_per_request != 0) return fail(DSPARK_EINVAL, "n_rows is not a multiple of rows_per_request");
   rc = check_out(rows, out, out_dtype, out_stride);
   if (rc) return rc;
-  if (how->history && (how->history_max < 0 || how->history_stride < how->history_max || how->history_max > 0x7fffffff))
-    return fail(DSPARK_EINVAL, "history_max must be in [0, history_stride]");
+  if (how->history && (how->history_max < 0 || how->history_stride < how->history_max || how->history_max > (1 << 30)))
+    return fail(DSPARK_EINVAL, "history_max must be in [0, history_stride], at most 2^30");
   if (how->draft && how->draft_stride < how->rows_per_request - 1)
     return fail(DSPARK_EINVAL, "draft_stride < rows_per_request - 1");
   if (how->bias_offset && how->bias_total < 0) return fail(DSPARK_EINVAL, "bias_total < 0");

@@ -638,9 +638,13 @@ __global__ void __launch_bounds__(64 * NWV) top_select_kernel(TopSliceArgs q) {
     n = total < (uint32_t)k ? (int)total : k;
     // this thread's candidates: neighbours in id order
     const int per = (int)((total + 64 * NWV - 1) / (64 * NWV));
+    const typename Cand<DT>::T* lists = static_cast<const typename Cand<DT>::T*>(q.cand) + r * q.slices * q.cap;
+    uint32_t at[kTopPer];
+    typename Cand<DT>::T e[kTopPer];
 #pragma unroll
-    for (int j = 0; j < kTopPer; ++j) {
+    for (int j = 0; j < kTopPer; ++j) {  // where they lie
       const uint32_t g = threadIdx.x * (uint32_t)per + (uint32_t)j;
+      at[j] = 0xffffffffu;
       if (j < per && g < total) {
         int lo = 0, hi = q.slices - 1;  // the last slice that starts at or before g
         while (lo < hi) {
@@ -648,9 +652,20 @@ __global__ void __launch_bounds__(64 * NWV) top_select_kernel(TopSliceArgs q) {
           if (first[mid] <= g) lo = mid;
           else hi = mid - 1;
         }
-        const typename Cand<DT>::T e = (static_cast<const typename Cand<DT>::T*>(q.cand) + (r * q.slices + lo) * q.cap)[g - first[lo]];
-        v[j] = Cand<DT>::value(e);
-        id[j] = (uint32_t)(lo * kTopSlice + Cand<DT>::place(e));
+        id[j] = (uint32_t)lo;
+        at[j] = (uint32_t)(lo * q.cap) + g - first[lo];
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < kTopPer; ++j) {  // all loads on their way
+      e[j] = typename Cand<DT>::T{};
+      if (at[j] != 0xffffffffu) e[j] = lists[at[j]];
+    }
+#pragma unroll
+    for (int j = 0; j < kTopPer; ++j) {
+      if (at[j] != 0xffffffffu) {
+        v[j] = Cand<DT>::value(e[j]);
+        id[j] = id[j] * (uint32_t)kTopSlice + (uint32_t)Cand<DT>::place(e[j]);
         key[j] = top_key<DT>(v[j]);
       }
     }
