@@ -467,7 +467,7 @@ typedef struct {
  * Q_UNSORTED, Q_NONFINITE (a listed logit or lse that is not finite) for the
  * teacher's list (the smallest), then ROW_NAN, ROW_POSINF or ROW_ZERO_MASS for
  * the student's row; a refused row has loss 0 and gradient 0.
- * ws: dspark_distill_workspace() bytes, 16-byte aligned. */
+ * ws: dspark_distill_workspace() bytes, 16-byte aligned (NULL where it is 0). */
 #define DSPARK_DISTILL_STATS 5
 size_t dspark_distill_workspace(int64_t n_rows, int64_t vocab);
 int dspark_distill(const dspark_rows* student, const dspark_teacher* teacher, float temperature, float* loss,
@@ -484,9 +484,7 @@ int dspark_distill_backward(const dspark_rows* student, const dspark_teacher* te
                             int64_t grad_stride, void* stream);
 
 /* Both in one call, for row weights known beforehand: loss (unweighted) and
- * grad of sum_r weight[r] loss[r], as the two calls above give them.  ws:
- * dspark_distill_step_workspace() bytes, 16-byte aligned (NULL where it is 0). */
-size_t dspark_distill_step_workspace(int64_t n_rows, int64_t vocab);
+ * grad of sum_r weight[r] loss[r], as the two calls above give them. */
 int dspark_distill_step(const dspark_rows* student, const dspark_teacher* teacher, float temperature,
                         const float* weight, float* loss, void* grad, int64_t grad_stride, int32_t* row_status,
                         void* ws, size_t ws_bytes, void* stream);

@@ -74,8 +74,7 @@ def test_distill_refusals():
     V = 65536
     r = B.Rows(0x100000, 1, 0, 6, V, V)  # long enough for a workspace in every entry point
     need = lib.dspark_distill_workspace(6, V)
-    assert lib.dspark_distill_step_workspace(6, V) == need
-    assert lib.dspark_distill_step_workspace(6, 64) == 0 and lib.dspark_distill_step_workspace(4096, V) == 0
+    assert lib.dspark_distill_workspace(6, 64) == 0  # short rows need none
     assert need > 0 and lib.dspark_distill_workspace(0, V) == 0 and lib.dspark_distill_workspace(6, 0) == 0
     t = B.Teacher(0x10000, 0x10000, 0x10000, None, 8, 0)
 

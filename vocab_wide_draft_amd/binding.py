@@ -70,7 +70,6 @@ EXPORTS = ["dspark_propose", "dspark_q_alloc", "dspark_sample", "dspark_verify_g
            "dspark_q_alloc_weights", "dspark_cr_expf", "dspark_q_encode", "dspark_q_validate", "dspark_margin", "dspark_verify_stochastic", "dspark_verify_ratio", "dspark_sharded_propose", "dspark_sharded_propose_noalloc", "dspark_sharded_q", "dspark_sharded_q_workspace", "dspark_workspace_bytes", "dspark_q_semantic_id",
            "dspark_shape_logits", "dspark_top_logits", "dspark_top_logits_workspace", "dspark_distill",
            "dspark_distill_backward", "dspark_distill_step", "dspark_distill_workspace",
-           "dspark_distill_step_workspace",
            "dspark_status_name", "dspark_last_error", "dspark_abi_version"]
 
 
@@ -115,7 +114,6 @@ def load_library():
         "dspark_distill_backward": (ctypes.c_int, [RP, TP, F32, P, P, P, P, I64, P]),
         "dspark_distill_step": (ctypes.c_int, [RP, TP, F32, P, P, P, I64, P, P, SZ, P]),
         "dspark_distill_workspace": (SZ, [I64, I64]),
-        "dspark_distill_step_workspace": (SZ, [I64, I64]),
         "dspark_q_semantic_id": (ctypes.c_char_p, []),
         "dspark_status_name": (ctypes.c_char_p, [I32]),
         "dspark_last_error": (ctypes.c_char_p, []),
@@ -655,7 +653,7 @@ def distill_step(student: torch.Tensor, teacher, weight: torch.Tensor, temperatu
     g = _out_rows(out, student, student.dtype)
     loss, st = torch.empty(n, dtype=torch.float32, device=dev), _i32(n, dev)
     w = ctypes.c_void_p(_arg(weight, "weight", torch.float32, (n,), dev))
-    ws, nbytes = _distill_ws(lib.dspark_distill_step_workspace(n, V), dev)
+    ws, nbytes = _distill_ws(lib.dspark_distill_workspace(n, V), dev)
     _call(dev, lib.dspark_distill_step, ctypes.byref(r), ctypes.byref(t), float(temperature), w, _p(loss), _p(g),
           g.stride(0), _p(st), _p(ws), nbytes)
     return {"loss": loss, "grad": g, "status": st}

@@ -398,25 +398,24 @@ __global__ void __launch_bounds__(kSliceBS) distill_grad_kernel(DistillArgs a) {
   });
 }
 
-// Loss and gradient of one row by one workgroup, where the rows fill the
-// chip: the row is read twice, the second time, from its end back, out of
-// the caches (the rows in work at once are about half of the last-level
-// cache), so that HBM sees one read and one write.
-template <int DT, int NWV>
+// Loss and, with GRAD, gradient of one row by one workgroup, where the rows
+// fill the chip or are short.  For the gradient the row is read again, from
+// its end back, out of the caches (the rows in work at once are about the
+// last-level cache), so that HBM sees little more than one read and one write.
+template <int DT, int NWV, bool GRAD>
 __global__ void __launch_bounds__(64 * NWV, 8) distill_row_kernel(DistillArgs a) {
   constexpr int T = 64 * NWV, N = kVec<DT>, PER = DSPARK_K_MAX / T;
   extern __shared__ uint32_t lds[];
   __shared__ double red[NWV];
   __shared__ float redf[NWV];
   __shared__ uint32_t redu[NWV];
-  __shared__ float p[DSPARK_K_MAX];
+  __shared__ float p[GRAD ? DSPARK_K_MAX : 1];
   __shared__ DistillRow sh;
   typedef typename El<DT>::T XT;
   const int64_t r = block_number(a.n);
   if (r < 0) return;
   const int V = a.V, tid = (int)threadIdx.x, words = (V + 31) / 32;
   const XT* x = static_cast<const XT*>(a.x) + r * a.x_stride;
-  XT* g = static_cast<XT*>(a.grad) + r * a.grad_stride;
   const int32_t* ids = a.ids + r * a.k_max;
   const float* zl = a.logits + r * a.k_max;
   const bool tail = a.lse != nullptr;
@@ -532,9 +531,12 @@ __global__ void __launch_bounds__(64 * NWV, 8) distill_row_kernel(DistillArgs a)
   __syncthreads();
   const bool live = status == DSPARK_ST_OK && len > 0;  // (uniform)
   if (tid == 0) {
-    a.loss[r] = live ? (float)sh.loss : 0.0f;
-    a.row_status[r] = status;
+    if (!live) sh = DistillRow{};
+    sh.status = status;
+    distill_row_out(a, r, sh);
   }
+  if constexpr (!GRAD) return;
+  XT* g = static_cast<XT*>(a.grad) + r * a.grad_stride;
   if (!live) {
     float v[N];
 #pragma unroll

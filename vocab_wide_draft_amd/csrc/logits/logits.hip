@@ -279,17 +279,25 @@ void launch_part(const DistillArgs& a, int dtype, hipStream_t s) {
   if (dtype == DSPARK_BF16) hipLaunchKernelGGL(distill_part_kernel<DSPARK_BF16>, grid, dim3(kSliceBS), distill_lds(a), s, a);
   else hipLaunchKernelGGL(distill_part_kernel<DSPARK_F32>, grid, dim3(kSliceBS), distill_lds(a), s, a);
 }
-// Whether dspark_distill_step gives each row one workgroup: where the rows
-// fill the chip (V = 129,280 in bf16: 256 rows 43 us against 41 in slices,
-// 512 70 / 73, 4,096 476 / 551; 64 38 / 21) or are short (one launch instead
-// of two, and up to 4,096 rows of 20,003 ids 101 / 105).
-bool step_by_rows(int64_t n, int64_t V) { return V <= kRowMost && (n >= 256 || V <= 32768); }
-template <int NWV>
-void launch_rows(const DistillArgs& a, int dtype, hipStream_t s) {
+// Whether each row gets one workgroup.  Short rows: one launch instead of two
+// (4,096 rows of 20,003 ids in bf16, loss and gradient: 101 us against 105 in
+// slices).  Longer ones where they fill the chip and are read twice, for loss
+// and gradient together (V = 129,280 in bf16: 256 rows 43 / 41 us, 512 70 / 73,
+// 4,096 476 / 551; 64 38 / 21); the loss alone is as fast in slices (1,280
+// rows 79 / 75).
+bool short_rows(int64_t V) { return V <= 32768; }
+bool step_by_rows(int64_t n, int64_t V) { return short_rows(V) || (n >= 256 && V <= kRowMost); }
+template <int NWV, bool GRAD>
+void launch_rows_waves(const DistillArgs& a, int dtype, hipStream_t s) {
   const size_t lds = 2u * 4u * (((size_t)a.V + 31) / 32);
   const dim3 grid = grid_of(a.n), block(64 * NWV);
-  if (dtype == DSPARK_BF16) hipLaunchKernelGGL(HIP_KERNEL_NAME(distill_row_kernel<DSPARK_BF16, NWV>), grid, block, lds, s, a);
-  else hipLaunchKernelGGL(HIP_KERNEL_NAME(distill_row_kernel<DSPARK_F32, NWV>), grid, block, lds, s, a);
+  if (dtype == DSPARK_BF16) hipLaunchKernelGGL(HIP_KERNEL_NAME(distill_row_kernel<DSPARK_BF16, NWV, GRAD>), grid, block, lds, s, a);
+  else hipLaunchKernelGGL(HIP_KERNEL_NAME(distill_row_kernel<DSPARK_F32, NWV, GRAD>), grid, block, lds, s, a);
+}
+template <bool GRAD>
+void launch_rows(const DistillArgs& a, int dtype, hipStream_t s) {
+  if (a.V <= 8192) launch_rows_waves<4, GRAD>(a, dtype, s);
+  else launch_rows_waves<8, GRAD>(a, dtype, s);
 }
 template <bool FROM_STATS>
 void launch_grad(const DistillArgs& a, int dtype, hipStream_t s) {
@@ -307,11 +315,8 @@ extern "C" {
 
 size_t dspark_distill_workspace(int64_t n_rows, int64_t vocab) {
   if (n_rows <= 0 || n_rows > (1 << 24) || vocab < 1 || vocab > DSPARK_V_MAX) return 0;
+  if (short_rows(vocab)) return 0;
   return distill_part_bytes(n_rows, vocab) + 4u * (size_t)n_rows;
-}
-
-size_t dspark_distill_step_workspace(int64_t n_rows, int64_t vocab) {
-  return step_by_rows(n_rows, vocab) ? 0 : dspark_distill_workspace(n_rows, vocab);
 }
 
 int dspark_distill(const dspark_rows* student, const dspark_teacher* teacher, float temperature, float* loss,
@@ -327,8 +332,12 @@ int dspark_distill(const dspark_rows* student, const dspark_teacher* teacher, fl
   a.stats = stats;
   a.row_status = row_status;
   hipStream_t s = static_cast<hipStream_t>(stream);
-  launch_part(a, student->dtype, s);
-  hipLaunchKernelGGL(distill_join_kernel, grid_of((a.n + kSliceNW - 1) / kSliceNW), dim3(kSliceBS), 0, s, a);
+  if (short_rows(a.V)) {
+    launch_rows<false>(a, student->dtype, s);
+  } else {
+    launch_part(a, student->dtype, s);
+    hipLaunchKernelGGL(distill_join_kernel, grid_of((a.n + kSliceNW - 1) / kSliceNW), dim3(kSliceBS), 0, s, a);
+  }
   return host_check_launch();
 }
 
@@ -360,7 +369,7 @@ int dspark_distill_step(const dspark_rows* student, const dspark_teacher* teache
   if (rc) return rc;
   if (student->n_rows == 0) return DSPARK_SUCCESS;
   if (!weight || !loss || !row_status) return fail(DSPARK_EINVAL, "NULL weight or output");
-  rc = check_distill_ws(dspark_distill_step_workspace(student->n_rows, student->vocab), ws, ws_bytes);
+  rc = check_distill_ws(dspark_distill_workspace(student->n_rows, student->vocab), ws, ws_bytes);
   if (rc) return rc;
   DistillArgs a = distill_args(student, teacher, temperature, ws);
   a.loss = loss;
@@ -370,8 +379,7 @@ int dspark_distill_step(const dspark_rows* student, const dspark_teacher* teache
   a.grad_stride = grad_stride;
   hipStream_t s = static_cast<hipStream_t>(stream);
   if (step_by_rows(a.n, a.V)) {
-    if (a.V <= 8192) launch_rows<4>(a, student->dtype, s);
-    else launch_rows<8>(a, student->dtype, s);
+    launch_rows<true>(a, student->dtype, s);
   } else {
     launch_part(a, student->dtype, s);
     launch_grad<false>(a, student->dtype, s);
