@@ -659,6 +659,21 @@ def distill_step(student: torch.Tensor, teacher, weight: torch.Tensor, temperatu
     return {"loss": loss, "grad": g, "status": st}
 
 
+def _distill_grad(ctx, grad_loss):
+    # (what forward has checked is not checked again: on torch's backward thread every call costs three times as much)
+    student, ids, logits, length, lse, stats, status = ctx.saved_tensors
+    n, V = student.shape
+    dev = student.device
+    g = _empty_rows(n, V, student.dtype, dev)
+    r = Rows(student.data_ptr(), DTYPE_F32 if student.dtype == torch.float32 else DTYPE_BF16, 0, n, V, student.stride(0))
+    t = Teacher(ids.data_ptr(), logits.data_ptr(), length.data_ptr(), None if lse is None else lse.data_ptr(),
+                ids.shape[1], 0)
+    gl = grad_loss.to(torch.float32).contiguous()
+    _call(dev, _LIB.dspark_distill_backward, ctypes.byref(r), ctypes.byref(t), ctx.temperature, stats.data_ptr(),
+          status.data_ptr(), gl.data_ptr(), g.data_ptr(), g.stride(0))
+    return g, None, None, None, None, None
+
+
 class _Distill(torch.autograd.Function):
     @staticmethod
     def forward(ctx, student, ids, logits, length, lse, temperature):
@@ -668,13 +683,10 @@ class _Distill(torch.autograd.Function):
         return out["loss"]
 
     @staticmethod
-    @torch.autograd.function.once_differentiable
     def backward(ctx, grad_loss):
-        student, ids, logits, length, lse, stats, status = ctx.saved_tensors
-        teacher = {"ids": ids, "logits": logits, "len": length, "lse": lse}
-        g = distill_backward(student, teacher, {"stats": stats, "status": status},
-                             grad_loss.to(torch.float32).contiguous(), ctx.temperature)
-        return g, None, None, None, None, None
+        if torch.is_grad_enabled():  # a graph of the gradient is asked for: its derivative is refused
+            return torch.autograd.function.once_differentiable(_distill_grad)(ctx, grad_loss)
+        return _distill_grad(ctx, grad_loss)
 
 
 def distill_loss(student: torch.Tensor, teacher, temperature: float = 1.0) -> torch.Tensor:
