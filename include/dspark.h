@@ -362,13 +362,14 @@ int dspark_sharded_q(const dspark_rows* rows, int32_t n_shards, const dspark_q* 
  *           history[r * history_stride .. + history_len[r]), of which the
  *           first prompt_len[r] are the prompt's and the rest were generated
  *           (prompt_len NULL: all were).  0 <= prompt_len[r] <=
- *           history_len[r] <= history_max <= history_stride, history_max <= 2^30.
+ *           history_len[r] <= history_max <= history_stride, history_max <= 2^30
+ *           (memory is read up to history_max, whatever the length).
  *   draft:  the drafted tokens; row i counts draft[r * draft_stride .. + i)
  *           as generated (draft_stride >= rows_per_request - 1).
- *   repetition (> 0), frequency, presence: the request's penalties (finite;
- *           NULL = 1, 0, 0).  Where all three are neutral, history and draft
- *           are not read.
- *   temperature: > 0, finite, and with a finite reciprocal (NULL = 1).
+ *   repetition (in [2^-100, 2^100]), frequency, presence (finite): the
+ *           request's penalties (NULL = 1, 0, 0).  Where all three are
+ *           neutral, history and draft have no effect and are not checked.
+ *   temperature: in [2^-100, 2^100] (NULL = 1).
  *   bias_offset (int64[n_requests + 1]), bias_ids, bias_values: request r's
  *           biases are the entries bias_offset[r] .. bias_offset[r + 1) of
  *           ids (strictly ascending) and values (finite, or -inf to ban a
@@ -427,8 +428,8 @@ int dspark_shape_logits(const dspark_rows* rows, const dspark_shaping* how, void
  * [n_rows][k_max], ascending) with logits (float[n_rows][k_max], the row's
  * values), zeros past len[r] (int32[n_rows]).  lse[r] (float, may be NULL) =
  * log sum_v exp(x_v / temperature) over the whole row.  k_max: 0 ..
- * DSPARK_K_MAX (0: ids and logits may be NULL); temperature > 0, finite, with
- * a finite reciprocal.  row_status[r]: OK, ROW_NAN, ROW_POSINF,
+ * DSPARK_K_MAX (0: ids and logits may be NULL); temperature: in [2^-100,
+ * 2^100].  row_status[r]: OK, ROW_NAN, ROW_POSINF,
  * ROW_ZERO_MASS or BAD_TOPK; a refused row has len 0, lse 0 and zeros. */
 int dspark_top_logits(const dspark_rows* rows, const int32_t* topk, int32_t k_max, float temperature, int32_t* ids,
                       float* logits, int32_t* len, float* lse, int32_t* row_status, void* ws, size_t ws_bytes,
@@ -451,7 +452,7 @@ typedef struct {
 } dspark_teacher;
 
 /* Distillation loss of student rows s against a teacher's top logits z, at
- * temperature T: with q = softmax(s / T) over the whole vocabulary and, on
+ * temperature T (in [2^-100, 2^100]): with q = softmax(s / T) over the whole vocabulary and, on
  * the list J, p_j = exp(z_j / T - lse) (lse NULL: softmax of z / T over J),
  *   loss = sum_J p_j (log p_j - log q_j) + P log(P / Q),
  *   P = max(0, 1 - sum_J p_j), Q = sum of q off the list.

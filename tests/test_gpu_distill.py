@@ -156,6 +156,17 @@ def test_distill_whole_vocabulary_on_the_list():
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("V", [300, 40003])
+@pytest.mark.parametrize("temp", [2.0 ** -100, 2.0 ** -10, 2.0 ** 10, 2.0 ** 100])
+def test_distill_extreme_temperatures(dtype, V, temp):
+    rng = np.random.default_rng(V + 1)
+    a = rows_of(rng, 3, V, dtype, 2.0)
+    # a teacher's lse keeps 24 bits, which at the lowest temperatures say nothing of its small probabilities
+    t = lists(rng, f64(a, dtype), 20, temp, temp >= 1.0)
+    run_all(a, dtype, t, temp, np.ones(3, np.float32))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_distill_refused_rows(dtype):
     rng = np.random.default_rng(13)
     V, k, n = 5003, 12, 14

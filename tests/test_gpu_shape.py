@@ -303,6 +303,19 @@ def test_shape_many_rows_of_one_request(dtype):
             check(got[j], w, mag, dtype == "bf16", j)
 
 
+def test_shape_factor_ranges():
+    x = torch.ones((6, 64), device=dev())
+    lo, hi = 2.0 ** -100, 2.0 ** 100
+    hist = i32(np.zeros((6, 1)))
+    r = f32([lo, hi, 2.0 ** -101, 2.0 ** 101, np.inf, -1.0])
+    g = B.shape_logits(x, history=hist, repetition=r)
+    assert g["status"].tolist() == [0, 0] + [L.ST_BAD_PENALTY] * 4
+    assert g["logits"][:2, 0].tolist() == [hi, lo] and (g["logits"][:2, 1:] == 1).all()
+    g = B.shape_logits(x, temperature=r)
+    assert g["status"].tolist() == [0, 0] + [L.ST_BAD_PENALTY] * 4
+    assert (g["logits"][0] == hi).all() and (g["logits"][1] == lo).all() and (g["logits"][2:] == -np.inf).all()
+
+
 def test_shape_mask_per_row_without_index():
     rng = np.random.default_rng(2)
     a = rows_of(rng, 4, 129, "bf16")

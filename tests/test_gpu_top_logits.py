@@ -131,6 +131,15 @@ def test_top_special(dtype, V, k):
         assert torch.equal(h[name].view(40, 14, -1), g[name].view(1, 14, -1).expand(40, 14, -1)), name
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("V", [300, 20003])
+@pytest.mark.parametrize("temp", [2.0 ** -100, 2.0 ** -10, 2.0 ** 10, 2.0 ** 100])
+def test_top_extreme_temperatures(dtype, V, temp):
+    rng = np.random.default_rng(V)
+    a = rows_of(rng, 4, V, dtype)
+    check_rows(a, dtype, [20] * 4, temp, B.top_logits(to_dev(a, dtype), 20, temperature=temp))
+
+
 def test_top_refused_k_and_k0():
     rng = np.random.default_rng(4)
     for dtype in ("bf16", "f32"):

@@ -60,7 +60,7 @@ def test_top_refusals():
     r = B.Rows(0x10000, 1, 0, 6, 64, 64)
     assert _top(r, -1) == -1
     assert _top(r, 1025) == -1
-    for t in (0.0, -1.0, float("inf"), float("nan"), 1e-45):
+    for t in (0.0, -1.0, float("inf"), float("nan"), 1e-45, 2.0 ** -101, 2.0 ** 101):
         assert _top(r, 4, t) == -1, t
     assert _top(r, 4, ids=None) == -1
     assert _top(r, 4, ln=None) == -1

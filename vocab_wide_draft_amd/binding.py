@@ -483,11 +483,15 @@ def _matrix(t, name, dtype, n, dev):
     """(address, columns, row stride) of an [n, columns] argument with unit column stride."""
     if t is None:
         return None, 0, 0
-    if t.dtype != dtype or t.dim() != 2 or t.shape[0] != n or t.device != dev:
+    shape = t.shape
+    if t.dtype != dtype or len(shape) != 2 or shape[0] != n or t.device != dev:
         raise ValueError(f"{name} must be a 2-D {dtype} tensor with {n} rows on {dev}")
-    if (t.shape[1] > 1 and t.stride(1) != 1) or (n > 1 and t.stride(0) < t.shape[1]):
+    cols = shape[1]
+    if t.is_contiguous():
+        return t.data_ptr(), cols, cols
+    if (cols > 1 and t.stride(1) != 1) or (n > 1 and t.stride(0) < cols):
         raise ValueError(f"{name} must have unit column stride and rows that do not overlap")
-    return t.data_ptr(), t.shape[1], max(t.stride(0), t.shape[1])
+    return t.data_ptr(), cols, max(t.stride(0), cols)
 
 
 def _empty_rows(n, V, dtype, dev):

@@ -19,8 +19,7 @@ int fail(int code, const char* msg) { return host_fail(code, msg); }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
-// a temperature whose reciprocal is a finite binary32 above 0
-bool temperature_ok(float t) { return t > 0.0f && std::isfinite(t) && std::isfinite(1.0f / t) && 1.0f / t > 0.0f; }
+bool temperature_ok(float t) { return t >= 0x1p-100f && t <= 0x1p100f; }
 
 // a grid of at least n workgroups in two dimensions (a launch takes fewer
 // than 2^32 threads per dimension)
@@ -178,7 +177,7 @@ int dspark_top_logits(const dspark_rows* rows, const int32_t* topk, int32_t k_ma
   int rc = host_check_rows(rows, "rows NULL");
   if (rc) return rc;
   if (k_max < 0 || k_max > DSPARK_K_MAX) return fail(DSPARK_EINVAL, "k_max must be in [0, DSPARK_K_MAX]");
-  if (!temperature_ok(temperature)) return fail(DSPARK_EINVAL, "temperature must be above 0 with a finite reciprocal");
+  if (!temperature_ok(temperature)) return fail(DSPARK_EINVAL, "temperature must be in [2^-100, 2^100]");
   if (rows->n_rows == 0) return DSPARK_SUCCESS;
   if (!len || !row_status || (k_max > 0 && (!ids || !logits))) return fail(DSPARK_EINVAL, "NULL output");
   const TopPlan plan = top_plan(rows->n_rows, rows->vocab, k_max);
@@ -241,7 +240,7 @@ int check_distill(const dspark_rows* student, const dspark_teacher* t, float tem
   if (rc) return rc;
   if (!t) return fail(DSPARK_EINVAL, "NULL teacher");
   if (t->k_max < 0 || t->k_max > DSPARK_K_MAX) return fail(DSPARK_EINVAL, "k_max must be in [0, DSPARK_K_MAX]");
-  if (!temperature_ok(temperature)) return fail(DSPARK_EINVAL, "temperature must be above 0 with a finite reciprocal");
+  if (!temperature_ok(temperature)) return fail(DSPARK_EINVAL, "temperature must be in [2^-100, 2^100]");
   if (student->n_rows > 0 && (!t->len || (t->k_max > 0 && (!t->ids || !t->logits))))
     return fail(DSPARK_EINVAL, "NULL teacher list");
   return DSPARK_SUCCESS;

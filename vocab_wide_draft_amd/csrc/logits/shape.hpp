@@ -36,6 +36,9 @@ constexpr uint32_t kPrompt = 0x80000000u;
 
 __device__ __forceinline__ bool finite_f32(float x) { return (__float_as_uint(x) & 0x7f800000u) != 0x7f800000u; }
 
+// factors whose reciprocals keep all their bits
+__device__ __forceinline__ bool in_range(float x) { return x >= 0x1p-100f && x <= 0x1p100f; }
+
 // bit l of `bits` set: a, else b (the bit widened to a word that selects)
 __device__ __forceinline__ float pick_bit(uint32_t bits, int l, float a, float b) {
   const uint32_t m = (uint32_t)((int32_t)(bits << (31 - l)) >> 31);
@@ -117,14 +120,15 @@ __global__ void __launch_bounds__(64 * NWV) shape_kernel(ShapeArgs a) {
   const float rep = h.repetition ? h.repetition[r] : 1.0f;
   const float freq = h.frequency ? h.frequency[r] : 0.0f;
   const float pres = h.presence ? h.presence[r] : 0.0f;
-  const float inv_rep = 1.0f / rep, inv_t = 1.0f / (h.temperature ? h.temperature[r] : 1.0f);
+  const float temp = h.temperature ? h.temperature[r] : 1.0f;
+  const float inv_rep = 1.0f / rep, inv_t = 1.0f / temp;
   const bool penal = rep != 1.0f || freq != 0.0f || pres != 0.0f;  // (uniform)
   const bool counted = penal && h.history;
   const bool drafted = penal && h.draft;
   const int64_t b0 = h.bias_offset ? h.bias_offset[r] : 0, b1 = h.bias_offset ? h.bias_offset[r + 1] : 0;
 
   uint32_t wrong = 0;
-  if (!(rep > 0.0f) || !finite_f32(rep) || !finite_f32(freq) || !finite_f32(pres) || !(inv_t > 0.0f) || !finite_f32(inv_t))
+  if (!in_range(rep) || !in_range(temp) || !finite_f32(freq) || !finite_f32(pres))
     wrong |= 1u << (DSPARK_ST_BAD_PENALTY - DSPARK_ST_BAD_HISTORY);
   const bool bias_ok = b0 >= 0 && b0 <= b1 && b1 <= h.bias_total;
   if (!bias_ok) wrong |= 1u << (DSPARK_ST_BAD_BIAS - DSPARK_ST_BAD_HISTORY);
