@@ -229,6 +229,22 @@ def test_shape_masks_and_special_values():
     assert (g[3] == -np.inf).all()  # lowest value times two overflows
 
 
+@pytest.mark.parametrize("dtype,out", [("bf16", "bf16"), ("bf16", "f32"), ("f32", "f32")])
+@pytest.mark.parametrize("R,P,H", [(3, 1, 20000), (3, 6, 20000), (60, 2, 17000), (70, 1, 100), (70, 3, 100)])
+def test_shape_every_kernel_choice(dtype, out, R, P, H):
+    """Few and many requests, short and long histories, few and many rows each (V above one workgroup's slice)."""
+    rng = np.random.default_rng(R + P)
+    V = 70003
+    a = rows_of(rng, R * P, V, dtype)
+    c = case(rng, R, P, V, H, 30, True)
+    g = call(c, to_dev(a, dtype), P, out_dtype=torch.float32 if out == "f32" else None)
+    assert (g["status"] == 0).all()
+    got = g["logits"]
+    for j in sorted({0, P - 1, P, 2 * P - 1, R * P - 1}):
+        w, mag = want(c, {j: f64(a[j], dtype)}, P, j)
+        check(host64(got[j]), w, mag, out == "bf16", j)
+
+
 def test_shape_counts_beyond_16_bits_and_long_history():
     rng = np.random.default_rng(3)
     V, H = 5000, 200_000

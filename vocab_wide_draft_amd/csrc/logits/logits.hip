@@ -63,18 +63,28 @@ int slice_of(int64_t owners, int64_t V, int64_t most, int64_t want) {
   return (int)(std::min<int64_t>(groups, most / kSliceStep) * kSliceStep);
 }
 
-// Vocabularies of at most 2,048 ids take one workgroup of 256 threads per
-// request, longer ones workgroups of 512 (1,024 threads leave two workgroups
-// on a CU instead of three: 6,144 bf16 rows took 726 instead of 686 us).
-template <int TI, int TO, int NWV>
-void launch_shape_waves(ShapeArgs a, hipStream_t s) {
-  a.slices = (a.V + 64 * NWV * 8 - 1) / (64 * NWV * 8);
-  hipLaunchKernelGGL(HIP_KERNEL_NAME(shape_kernel<TI, TO, NWV>), row_slice_grid(a.n_requests, a.slices), dim3(64 * NWV), 0, s, a);
+template <int TI, int TO, int NWV, int G, int DEPTH>
+void launch_shape_as(ShapeArgs a, hipStream_t s) {
+  constexpr int slice = 64 * NWV * 8 * G;
+  a.slices = (a.V + slice - 1) / slice;
+  hipLaunchKernelGGL(HIP_KERNEL_NAME(shape_kernel<TI, TO, NWV, G, DEPTH>), row_slice_grid(a.n_requests, a.slices),
+                     dim3(64 * NWV), 0, s, a);
 }
+// What keeps enough loads on their way: two eights of logits per thread and
+// two rows ahead (V = 129,280, 1,024 requests, bf16: 6 rows each 564 us against
+// 631 with one eight, three rows ahead and 512 threads, 1 row 196 / 266).
+// float32 results need more registers, and with three rows or more the other
+// is as fast or faster (float32, 6 rows: 1,139 / 1,104 us, 1 row 204 / 255).
+// So is it where the requests leave CUs idle and the history is long, which
+// 512 threads scan in half the steps (histories of up to 32,768 tokens, 6
+// bf16 rows each: 16 requests 28.0 / 23.5 us, 4 23.7 / 17.6; 64 63.7 / 68.9).
 template <int TI, int TO>
 void launch_shape(const ShapeArgs& a, hipStream_t s) {
-  if (a.V <= 64 * 4 * 8) launch_shape_waves<TI, TO, 4>(a, s);
-  else launch_shape_waves<TI, TO, 8>(a, s);
+  if (a.V <= 2048) launch_shape_as<TI, TO, 4, 1, 2>(a, s);
+  else if ((TO == DSPARK_F32 && a.how.rows_per_request > 2) ||
+           (a.how.history && a.how.history_max >= 16384 && a.n_requests * a.V < 1 << 22))
+    launch_shape_as<TI, TO, 8, 1, TI == DSPARK_F32 ? 2 : 3>(a, s);
+  else launch_shape_as<TI, TO, 4, 2, 2>(a, s);
 }
 
 // How dspark_top_logits cuts rows longer than kTopSmall (bytes 0: not at
