@@ -75,6 +75,18 @@ def test_top_around_the_sizes_where_the_kernel_changes(dtype, V, k):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("V,k", [(4096, 30), (4097, 30), (8000, 200), (8000, 900), (16384, 1024)])
+def test_top_many_rows_of_middle_length(dtype, V, k):
+    rng = np.random.default_rng(V + 3 * k)
+    a = np.tile(rows_of(rng, 20, V, dtype), (27, 1))
+    a[7] = special_rows(rng, V, dtype)[6]  # ties
+    g = B.top_logits(to_dev(a, dtype), k)
+    check_rows(a, dtype, [k] * 540, 1.0, g, rows=list(range(20)) + [539])
+    for name in g:
+        assert torch.equal(g[name][20:].view(26, 20, -1), g[name][20:40].view(1, 20, -1).expand(26, 20, -1)), name
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_top_where_the_sample_misleads(dtype):
     """The largest logits all inside, or all outside, the sampled runs."""
     rng = np.random.default_rng(77)

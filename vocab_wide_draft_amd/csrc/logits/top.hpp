@@ -1,8 +1,8 @@
 // The top logits of a row with the log-sum-exp of the whole row
 // (dspark_top_logits).
 //
-// Rows of more than kTopSmall ids are cut into slices of 8,192 ids, one
-// workgroup each, which reads its slice once into registers.  A threshold that the k-th
+// Long rows (and many rows of middle length) are cut into slices of 8,192
+// ids, one workgroup each, which reads its slice once into registers.  A threshold that the k-th
 // largest logit lies above with good odds comes from a sample of the row
 // (2,048 logits, the same for every slice of the row), so that one pass
 // yields the slice's maximum, its sum of exponentials and the few logits
@@ -10,7 +10,9 @@
 // selects exactly among those candidates.  A row whose candidates are too
 // few or too many for their list (heavy ties, a sample that misleads) is
 // selected from memory by that kernel's workgroup instead: slower, the same
-// answer.  Shorter rows are held whole in one workgroup's registers.
+// answer.  Other rows are held whole in one workgroup's registers.  1,280 bf16
+// rows of V = 129,280 take 71 + 16 us (4.7 TB/s of their bytes while they are
+// read), 320 float32 rows 36 + 15.
 //
 // Exponentials are exp2(x c - K), one fused multiply-add each, with c the
 // binary32 rounding of log2(e) / T and K = c times a maximum: the reference
