@@ -100,7 +100,9 @@ def test_distill_small(tail, dtype, V, k, n):
 
 @pytest.mark.parametrize("tail", [False, True])
 @pytest.mark.parametrize("dtype,V,n", [("bf16", 129280, 3), ("bf16", 131072, 2), ("bf16", 131073, 2), ("f32", 129280, 2),
-                                       ("bf16", 129280, 300), ("bf16", 129281, 700), ("f32", 129280, 300), ("f32", 1 << 20, 2)])
+                                       ("bf16", 129280, 300), ("bf16", 129281, 700), ("f32", 129280, 300), ("f32", 1 << 20, 2),
+                                       ("bf16", 140001, 260), ("bf16", 8192, 3), ("f32", 8193, 3), ("bf16", 32768, 3),
+                                       ("f32", 32769, 3)])
 def test_distill_long(tail, dtype, V, n):
     """Few rows (split over many workgroups) and many (one or few each)."""
     rng = np.random.default_rng(V + n)
@@ -244,6 +246,74 @@ def test_distill_in_place_padding_and_strides(dtype):
         assert got.data_ptr() == x.data_ptr() and torch.equal(wide[:, V:], behind)
         assert torch.equal(got, ref["grad"]) if how == "step" else True
         check(a[:, :V], dtype, t, 1.0, w.cpu().numpy(), ref["loss"].cpu().numpy(), host64(got))
+
+
+@pytest.mark.parametrize("V", [700, 40001])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("tail", [False, True])
+def test_distill_bad_logits_on_the_list(dtype, tail, V):
+    rng = np.random.default_rng(23)
+    x = (rng.standard_normal((4, V)) * 2).astype(np.float32)
+    ids, zl, ln, lse = lists(rng, x.astype(np.float64), 9, 1.0, tail, ragged=False)
+    x[0, ids[0, 4]] = np.inf
+    x[1, ids[1, 8]] = np.nan
+    x[2, ids[2, 0]] = np.nan
+    x[2, (ids[2, 0] + 1) % V] = np.inf
+    a = x if dtype == "f32" else np.where(np.isnan(x), 0x7FC0, W.f32_to_bf16_bits(np.nan_to_num(x, nan=0.0, posinf=np.inf, neginf=-np.inf))).astype(np.uint16)
+    tt, w = teacher((ids, zl, ln, lse)), torch.ones(4, device=dev())
+    f, s = B.distill(to_dev(a, dtype), tt), B.distill_step(to_dev(a, dtype), tt, w)
+    exp = [L.ST_ROW_POSINF, L.ST_ROW_NAN, L.ST_ROW_NAN, 0]
+    assert f["status"].tolist() == exp and s["status"].tolist() == exp
+    assert not f["loss"][:3].any() and not s["grad"][:3].any()
+    check(a, dtype, (ids, zl, ln, lse), 1.0, np.ones(4), s["loss"].cpu().numpy(), host64(s["grad"]), [3])
+
+
+def test_distill_on_two_streams_at_once():
+    rng = np.random.default_rng(24)
+    n, V = 40, 50001
+    cases = []
+    for k in (30, 70):
+        a = rows_of(rng, n, V, "bf16", 2.0)
+        cases.append((to_dev(a, "bf16"), teacher(lists(rng, f64(a, "bf16"), k, 1.0, True)), f32(rng.random(n))))
+    ref = [B.distill_step(*c) for c in cases]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in cases]
+    outs = []
+    for _ in range(20):
+        for s, c in zip(streams, cases):
+            with torch.cuda.stream(s):
+                outs.append(B.distill_step(*c))
+    torch.cuda.synchronize()
+    for i, o in enumerate(outs):
+        for name in ("loss", "grad", "status"):
+            assert torch.equal(o[name], ref[i % 2][name]), (i, name)
+
+
+def test_distill_autograd_captured():
+    """Forward and backward of one leaf captured together; no eager graph of that leaf is alive."""
+    rng = np.random.default_rng(25)
+    n, V = 6, 4001
+    a = rows_of(rng, n, V, "f32", 2.0)
+    tt, w = teacher(lists(rng, a.astype(np.float64), 20, 1.0, True)), f32(rng.random(n))
+    data = to_dev(a, "f32")
+    ref = B.distill_step(data, tt, w)
+    x = to_dev(a, "f32").requires_grad_()  # (rows that start 16-byte aligned, as data's do)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        loss = B.distill_loss(x, tt)
+        (grad,) = torch.autograd.grad(loss, x, w)
+    for rep in range(3):
+        with torch.no_grad():
+            x.copy_(data if rep % 2 == 0 else data + 1.0)  # a shift leaves the softmax as it is
+        g.replay()
+        torch.cuda.synchronize()
+        if rep % 2 == 0:
+            assert torch.equal(loss, ref["loss"])
+            again = B.distill_backward(data, tt, B.distill(data, tt), w)
+            assert torch.equal(grad, again)
+        else:
+            assert (loss - ref["loss"]).abs().max() < 1e-4 and (grad - ref["grad"]).abs().max() < 1e-5
 
 
 def test_distill_autograd():

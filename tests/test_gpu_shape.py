@@ -383,6 +383,35 @@ def test_shape_other_stream_and_graph_replays():
             assert torch.equal(o["logits"].view(torch.int16), eager.view(torch.int16)), rep
 
 
+def test_shape_arguments_inside_wider_buffers():
+    rng = np.random.default_rng(46)
+    R, P, V = 3, 6, 5000
+    a = rows_of(rng, R * P, V, "bf16")
+    c = case(rng, R, P, V, 70, 12, False)
+    want_ = call(c, to_dev(a, "bf16"), P)["logits"]
+    wide_h, wide_d = i32(np.full((R, 90), -7)), i32(np.full((R, 11), V + 5))
+    wide_h[:, 8:78] = i32(c["hist"])
+    wide_d[:, 3:8] = i32(c["draft"])
+    off = np.cumsum([0] + [len(b) for b in c["bias"]])
+    flat = [e for b in c["bias"] for e in b]
+    g = B.shape_logits(to_dev(a, "bf16"), P, history=wide_h[:, 8:78], history_len=i32(c["len"]), prompt_len=i32(c["plen"]),
+                       draft=wide_d[:, 3:8], repetition=f32(c["rep"]), frequency=f32(c["freq"]), presence=f32(c["pres"]),
+                       temperature=f32(c["temp"]),
+                       bias=(torch.from_numpy(off.astype(np.int64)).to(dev()), i32([e[0] for e in flat]), f32([e[1] for e in flat])))
+    assert not g["status"].any() and torch.equal(g["logits"].view(torch.int16), want_.view(torch.int16))
+
+
+def test_shape_a_bias_for_every_token():
+    rng = np.random.default_rng(47)
+    V = 30001
+    a = rows_of(rng, 2, V, "f32")
+    val = rng.normal(0, 1, 2 * V).astype(np.float32)
+    off = torch.tensor([0, V, 2 * V], device=dev())
+    g = host64(B.shape_logits(to_dev(a, "f32"), bias=(off, i32(np.tile(np.arange(V), 2)), f32(val)))["logits"])
+    w = a.astype(np.float64) + val.reshape(2, V)
+    assert (np.abs(g - w) <= F * np.abs(w) + 2.0 ** -133).all()
+
+
 def test_shape_empty_arguments():
     x = torch.ones((3, 40), device=dev())
     two = f32([2.0] * 3)

@@ -696,7 +696,9 @@ class _Distill(torch.autograd.Function):
 def distill_loss(student: torch.Tensor, teacher, temperature: float = 1.0) -> torch.Tensor:
     """distill's loss (float32 [n]) as a differentiable function of the
     student rows.  The teacher is constant: its logits must not require a
-    gradient.  Rows that the call refuses have loss 0 and gradient 0."""
+    gradient.  Rows that the call refuses have loss 0 and gradient 0.  It may be
+    captured into a graph with its backward pass, while no eager graph of the
+    same leaves is alive."""
     if teacher["logits"].requires_grad or (teacher.get("lse") is not None and teacher["lse"].requires_grad):
         raise ValueError("the teacher is constant: detach its logits and lse")
     return _Distill.apply(student, teacher["ids"], teacher["logits"], teacher["len"], teacher.get("lse"),
