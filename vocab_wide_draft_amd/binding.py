@@ -494,9 +494,14 @@ def _matrix(t, name, dtype, n, dev):
     return t.data_ptr(), cols, max(t.stride(0), cols)
 
 
+def _padded(V, dtype):
+    """The row stride that keeps rows of V values 16-byte aligned."""
+    return -(-V * dtype.itemsize // 16) * 16 // dtype.itemsize
+
+
 def _empty_rows(n, V, dtype, dev):
     """Rows [n, V] that start 16-byte aligned."""
-    wide = -(-V * dtype.itemsize // 16) * 16 // dtype.itemsize
+    wide = _padded(V, dtype)
     rows = torch.empty((n, wide), dtype=dtype, device=dev)
     return rows if wide == V else rows[:, :V]
 
@@ -570,8 +575,8 @@ def shape_logits(rows: torch.Tensor, rows_per_request: int = 1, *, history=None,
                   _arg(values, "bias values", f32, (total,), dev), total,
                   m, m_stride, 0 if mask is None else mask.shape[0], _arg(mask_row, "mask_row", i32, (n,), dev))
     st = _i32(n, dev)
-    _call(dev, lib.dspark_shape_logits, ctypes.byref(r), ctypes.byref(how), _p(o),
-          DTYPE_F32 if o.dtype == torch.float32 else DTYPE_BF16, o.stride(0), _p(st))
+    _call(dev, lib.dspark_shape_logits, ctypes.byref(r), ctypes.byref(how), o.data_ptr(),
+          DTYPE_F32 if o.dtype == torch.float32 else DTYPE_BF16, o.stride(0), st.data_ptr())
     return {"logits": o, "status": st}
 
 
@@ -611,22 +616,28 @@ def _distill_ws(nbytes, dev):
     return (torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None), nbytes
 
 
+def _distill(student, teacher, temperature):
+    """distill's outputs, and its arguments as the library takes them."""
+    lib = load_library()
+    r = _rows(student)
+    n, V, dev = student.shape[0], student.shape[1], student.device
+    t = _teacher(teacher, n, dev)
+    loss, st = torch.empty(n, dtype=torch.float32, device=dev), _i32(n, dev)
+    stats = torch.empty((n, DISTILL_STATS), dtype=torch.float64, device=dev)
+    ws, nbytes = _distill_ws(lib.dspark_distill_workspace(n, V), dev)
+    _call(dev, lib.dspark_distill, ctypes.byref(r), ctypes.byref(t), float(temperature), loss.data_ptr(),
+          stats.data_ptr(), st.data_ptr(), ws.data_ptr() if nbytes else None, nbytes)
+    return loss, stats, st, r, t
+
+
 def distill(student: torch.Tensor, teacher, temperature: float = 1.0):
     """Distillation loss of every student row [n, V] against a teacher's top
     logits (see dspark_distill).  teacher: {"ids", "logits", "len", "lse"} as
     top_logits returns it at the same temperature; without "lse" (or None)
     the teacher is renormalised over its list.  Returns {"loss", "stats",
     "status"}; stats and status go to distill_backward."""
-    lib = load_library()
-    r = _rows(student)
-    n, V, dev = student.shape[0], student.shape[1], student.device
-    t = _teacher(teacher, n, dev)
-    out = {"loss": torch.empty(n, dtype=torch.float32, device=dev),
-           "stats": torch.empty((n, DISTILL_STATS), dtype=torch.float64, device=dev), "status": _i32(n, dev)}
-    ws, nbytes = _distill_ws(lib.dspark_distill_workspace(n, V), dev)
-    _call(dev, lib.dspark_distill, ctypes.byref(r), ctypes.byref(t), float(temperature), _p(out["loss"]),
-          _p(out["stats"]), _p(out["status"]), _p(ws), nbytes)
-    return out
+    loss, stats, st, _, _ = _distill(student, teacher, temperature)
+    return {"loss": loss, "stats": stats, "status": st}
 
 
 def distill_backward(student: torch.Tensor, teacher, forward, grad_loss: torch.Tensor, temperature: float = 1.0,
@@ -639,11 +650,10 @@ def distill_backward(student: torch.Tensor, teacher, forward, grad_loss: torch.T
     n, dev = student.shape[0], student.device
     t = _teacher(teacher, n, dev)
     g = _out_rows(out, student, student.dtype)
-    st = ctypes.c_void_p(_arg(forward["stats"], "stats", torch.float64, (n, DISTILL_STATS), dev))
-    rs = ctypes.c_void_p(_arg(forward["status"], "status", torch.int32, (n,), dev))
-    gl = ctypes.c_void_p(_arg(grad_loss, "grad_loss", torch.float32, (n,), dev))
-    _call(dev, lib.dspark_distill_backward, ctypes.byref(r), ctypes.byref(t), float(temperature), st, rs, gl, _p(g),
-          g.stride(0))
+    _call(dev, lib.dspark_distill_backward, ctypes.byref(r), ctypes.byref(t), float(temperature),
+          _arg(forward["stats"], "stats", torch.float64, (n, DISTILL_STATS), dev),
+          _arg(forward["status"], "status", torch.int32, (n,), dev),
+          _arg(grad_loss, "grad_loss", torch.float32, (n,), dev), g.data_ptr(), g.stride(0))
     return g
 
 
@@ -656,35 +666,37 @@ def distill_step(student: torch.Tensor, teacher, weight: torch.Tensor, temperatu
     t = _teacher(teacher, n, dev)
     g = _out_rows(out, student, student.dtype)
     loss, st = torch.empty(n, dtype=torch.float32, device=dev), _i32(n, dev)
-    w = ctypes.c_void_p(_arg(weight, "weight", torch.float32, (n,), dev))
+    w = _arg(weight, "weight", torch.float32, (n,), dev)
     ws, nbytes = _distill_ws(lib.dspark_distill_workspace(n, V), dev)
-    _call(dev, lib.dspark_distill_step, ctypes.byref(r), ctypes.byref(t), float(temperature), w, _p(loss), _p(g),
-          g.stride(0), _p(st), _p(ws), nbytes)
+    _call(dev, lib.dspark_distill_step, ctypes.byref(r), ctypes.byref(t), float(temperature), w, loss.data_ptr(),
+          g.data_ptr(), g.stride(0), st.data_ptr(), ws.data_ptr() if nbytes else None, nbytes)
     return {"loss": loss, "grad": g, "status": st}
 
 
 def _distill_grad(ctx, grad_loss):
-    # (what forward has checked is not checked again: on torch's backward thread every call costs three times as much)
-    student, ids, logits, length, lse, stats, status = ctx.saved_tensors
-    n, V = student.shape
-    dev = student.device
-    g = _empty_rows(n, V, student.dtype, dev)
-    r = Rows(student.data_ptr(), DTYPE_F32 if student.dtype == torch.float32 else DTYPE_BF16, 0, n, V, student.stride(0))
-    t = Teacher(ids.data_ptr(), logits.data_ptr(), length.data_ptr(), None if lse is None else lse.data_ptr(),
-                ids.shape[1], 0)
-    gl = grad_loss.to(torch.float32).contiguous()
+    # forward has checked the arguments and laid them out: on torch's backward thread Python takes three times as long
+    saved = ctx.saved_tensors  # (and torch has checked that nobody wrote to them since)
+    r, t, stats, status, shape, V, dev = ctx.laid_out
+    if saved[0].data_ptr() != r.data or saved[1].data_ptr() != t.ids:  # they were moved in between
+        student, ids, logits, length, lse = saved
+        r, t = _rows(student), _teacher({"ids": ids, "logits": logits, "len": length, "lse": lse}, shape[0], dev)
+    if grad_loss.dtype is not torch.float32 or not grad_loss.is_contiguous():
+        grad_loss = grad_loss.to(torch.float32).contiguous()
+    g = torch.empty(shape, dtype=saved[0].dtype, device=dev)
     _call(dev, _LIB.dspark_distill_backward, ctypes.byref(r), ctypes.byref(t), ctx.temperature, stats.data_ptr(),
-          status.data_ptr(), gl.data_ptr(), g.data_ptr(), g.stride(0))
-    return g, None, None, None, None, None
+          status.data_ptr(), grad_loss.data_ptr(), g.data_ptr(), shape[1])
+    return g if shape[1] == V else g[:, :V], None, None, None, None, None
 
 
-class _Distill(torch.autograd.Function):
+class _DistillLoss(torch.autograd.Function):
     @staticmethod
     def forward(ctx, student, ids, logits, length, lse, temperature):
-        out = distill(student, {"ids": ids, "logits": logits, "len": length, "lse": lse}, temperature)
-        ctx.save_for_backward(student, ids, logits, length, lse, out["stats"], out["status"])
+        loss, stats, st, r, t = _distill(student, {"ids": ids, "logits": logits, "len": length, "lse": lse}, temperature)
+        ctx.save_for_backward(student, ids, logits, length, lse)
+        n, V = student.shape
+        ctx.laid_out = (r, t, stats, st, (n, _padded(V, student.dtype)), V, student.device)
         ctx.temperature = temperature
-        return out["loss"]
+        return loss
 
     @staticmethod
     def backward(ctx, grad_loss):
@@ -701,5 +713,5 @@ def distill_loss(student: torch.Tensor, teacher, temperature: float = 1.0) -> to
     same leaves is alive."""
     if teacher["logits"].requires_grad or (teacher.get("lse") is not None and teacher["lse"].requires_grad):
         raise ValueError("the teacher is constant: detach its logits and lse")
-    return _Distill.apply(student, teacher["ids"], teacher["logits"], teacher["len"], teacher.get("lse"),
-                          float(temperature))
+    return _DistillLoss.apply(student, teacher["ids"], teacher["logits"], teacher["len"], teacher.get("lse"),
+                              float(temperature))
