@@ -405,8 +405,8 @@ template <int DT, int NWV, bool GRAD>
 __global__ void __launch_bounds__(64 * NWV, NWV == 4 ? 6 : 8) distill_row_kernel(DistillArgs a) {
   constexpr int T = 64 * NWV, N = kVec<DT>, PER = DSPARK_K_MAX / T;
   extern __shared__ uint32_t lds[];
-  __shared__ double red[NWV];
-  __shared__ float redf[NWV];
+  __shared__ double sum_wave[NWV][4];
+  __shared__ float m_wave[2][NWV], redf[NWV];
   __shared__ uint32_t redu[NWV];
   __shared__ float p[GRAD ? DSPARK_K_MAX : 1];
   __shared__ DistillRow sh;
@@ -419,7 +419,6 @@ __global__ void __launch_bounds__(64 * NWV, NWV == 4 ? 6 : 8) distill_row_kernel
   const float* zl = a.logits + r * a.k_max;
   const bool tail = a.lse != nullptr;
   const auto larger = [](float u, float v) { return __builtin_fmaxf(u, v); };
-  const auto plus = [](double u, double v) { return u + v; };
   const auto either = [](uint32_t u, uint32_t v) { return u | v; };
   constexpr float kNone = -__builtin_inff();
 
@@ -509,30 +508,55 @@ __global__ void __launch_bounds__(64 * NWV, NWV == 4 ? 6 : 8) distill_row_kernel
         for (int l = 0; l < N; ++l) flags |= v[l] != v[l] ? 1u : v[l] == __builtin_inff() ? 2u : 0u;
       }
     }
-    const float M_off = group_reduce<NWV>(m, kNone, larger, redf);
-    const float M_on = group_reduce<NWV>(m_on, kNone, larger, redf);
-    flags = group_reduce<NWV>(flags, 0u, either, redu);
+    // two meetings of the waves: the maxima, which all need, then the sums, which one wave joins
+    m_wave[0][wave_id()] = wave_reduce(m, kNone, larger);
+    m_wave[1][wave_id()] = wave_reduce(m_on, kNone, larger);
+    __syncthreads();
+    float M_off = kNone, M_on = kNone;
+#pragma unroll
+    for (int w = 0; w < NWV; ++w) {
+      M_off = __builtin_fmaxf(M_off, m_wave[0][w]);
+      M_on = __builtin_fmaxf(M_on, m_wave[1][w]);
+    }
     const double f = m == kNone ? 0.0 : (double)__builtin_amdgcn_exp2f((m - M_off) * c);
     const double h = m_on == kNone ? 0.0 : (double)__builtin_amdgcn_exp2f((m_on - M_on) * c);
-    const double off = group_reduce<NWV>((double)s_off * f, 0.0, plus, red);
-    const double sum_on = group_reduce<NWV>((double)s_on * h, 0.0, plus, red);
-    b0 = group_reduce<NWV>(b0, 0.0, plus, red);
-    b1 = group_reduce<NWV>(b1, 0.0, plus, red);
-    status = flags & 1u ? DSPARK_ST_ROW_NAN
-             : flags & 2u ? DSPARK_ST_ROW_POSINF
-             : M_off == kNone && M_on == kNone ? DSPARK_ST_ROW_ZERO_MASS : DSPARK_ST_OK;
-    if (tid == 0 && status == DSPARK_ST_OK) {
-      DistillRow o{};
-      distill_finish(a.inv_t, tail, M_off, M_on, off, sum_on, b0, b1, zm, o);
-      sh = o;
+    const double w_off = wave_sum((double)s_off * f), w_on = wave_sum((double)s_on * h);
+    b0 = wave_sum(b0);
+    b1 = wave_sum(b1);
+    flags = wave_reduce(flags, 0u, either);
+    if (lane_id() == 0) {
+      sum_wave[wave_id()][0] = w_off;
+      sum_wave[wave_id()][1] = w_on;
+      sum_wave[wave_id()][2] = b0;
+      sum_wave[wave_id()][3] = b1;
+      redu[wave_id()] = flags;
     }
+    __syncthreads();
+    if (wave_id() == 0) {
+      const bool have = lane_id() < 4 * NWV;  // lane 4 w + i: sum i of wave w
+      double v = have ? sum_wave[lane_id() >> 2][lane_id() & 3] : 0.0;
+#pragma unroll
+      for (int step = 4; step < 4 * NWV; step *= 2) v += __shfl_xor(v, step, 64);
+      const double off = __shfl(v, 0, 64), sum_on = __shfl(v, 1, 64), t0 = __shfl(v, 2, 64), t1 = __shfl(v, 3, 64);
+      flags = wave_reduce(lane_id() < NWV ? redu[lane_id()] : 0u, 0u, either);
+      if (tid == 0) {
+        DistillRow o{};
+        o.status = flags & 1u ? DSPARK_ST_ROW_NAN
+                   : flags & 2u ? DSPARK_ST_ROW_POSINF
+                   : M_off == kNone && M_on == kNone ? DSPARK_ST_ROW_ZERO_MASS : DSPARK_ST_OK;
+        if (o.status == DSPARK_ST_OK) distill_finish(a.inv_t, tail, M_off, M_on, off, sum_on, t0, t1, zm, o);
+        sh = o;
+      }
+    }
+    __syncthreads();
+    status = sh.status;
   }
-  __syncthreads();
   const bool live = status == DSPARK_ST_OK && len > 0;  // (uniform)
   if (tid == 0) {
-    if (!live) sh = DistillRow{};
-    sh.status = status;
-    distill_row_out(a, r, sh);
+    DistillRow o{};
+    if (live) o = sh;
+    o.status = status;
+    distill_row_out(a, r, o);
   }
   if constexpr (!GRAD) return;
   XT* g = static_cast<XT*>(a.grad) + r * a.grad_stride;
