@@ -95,7 +95,7 @@ void launch_shape(const ShapeArgs& a, hipStream_t s) {
 // The sample's rank leaves four standard deviations above the count expected
 // of the top k.
 struct TopPlan {
-  int slices, cap, rank, waves;
+  int slices, cap, rank, most;  // most: candidates that the selection takes
   size_t bytes, part_bytes;
 };
 TopPlan top_plan(int64_t n, int64_t V, int64_t k_max) {
@@ -107,7 +107,11 @@ TopPlan top_plan(int64_t n, int64_t V, int64_t k_max) {
   // logits of the sample above the rank-th of its 256 maxima, and so of a slice and of the row
   const double above = -std::log(1.0 - p.rank / 256.0) * 256.0;
   const double row = above * (double)V / kTopSample;
-  p.waves = row * 2.5 <= kTopPer * 256 ? 4 : row * 2.5 <= kTopPer * 512 ? 8 : 16;
+  // room for more than twice the candidates expected (one row in 1,280 that
+  // has to be selected from memory costs more than the selection of all), in
+  // workgroups as small as that allows (1,280 bf16 rows, k = 256: 12.3 us in
+  // 256 threads of eleven candidates, 15.6 in 512 of eight)
+  p.most = row * 2.2 <= 2048 ? 2048 : row * 2.2 <= 2816 ? 2816 : row * 2.2 <= 5632 ? 5632 : 8192;
   p.slices = (int)((V + kTopSlice - 1) / kTopSlice);
   p.cap = (int)std::min<double>(kTopSlice, std::ceil((3.0 * above * kTopSlice / kTopSample + 64.0) / 64.0) * 64.0);
   p.part_bytes = (size_t)n * (size_t)p.slices * sizeof(TopPart);
@@ -119,9 +123,10 @@ template <int DT>
 void launch_top_slices(const TopSliceArgs& q, const TopPlan& plan, hipStream_t s) {
   hipLaunchKernelGGL(top_slice_kernel<DT>, row_slice_grid(q.a.n, plan.slices), dim3(kSliceBS), 0, s, q);
   const dim3 grid = grid_of(q.a.n);
-  if (plan.waves == 4) hipLaunchKernelGGL(HIP_KERNEL_NAME(top_select_kernel<DT, 4>), grid, dim3(256), 0, s, q);
-  else if (plan.waves == 8) hipLaunchKernelGGL(HIP_KERNEL_NAME(top_select_kernel<DT, 8>), grid, dim3(512), 0, s, q);
-  else hipLaunchKernelGGL(HIP_KERNEL_NAME(top_select_kernel<DT, 16>), grid, dim3(1024), 0, s, q);
+  if (plan.most == 2048) hipLaunchKernelGGL(HIP_KERNEL_NAME(top_select_kernel<DT, 4, 8>), grid, dim3(256), 0, s, q);
+  else if (plan.most == 2816) hipLaunchKernelGGL(HIP_KERNEL_NAME(top_select_kernel<DT, 4, 11>), grid, dim3(256), 0, s, q);
+  else if (plan.most == 5632) hipLaunchKernelGGL(HIP_KERNEL_NAME(top_select_kernel<DT, 8, 11>), grid, dim3(512), 0, s, q);
+  else hipLaunchKernelGGL(HIP_KERNEL_NAME(top_select_kernel<DT, 16, 8>), grid, dim3(1024), 0, s, q);
 }
 
 template <int DT>

@@ -11,8 +11,8 @@
 // few or too many for their list (heavy ties, a sample that misleads) is
 // selected from memory by that kernel's workgroup instead: slower, the same
 // answer.  Other rows are held whole in one workgroup's registers.  1,280 bf16
-// rows of V = 129,280 take 71 + 16 us (4.7 TB/s of their bytes while they are
-// read), 320 float32 rows 36 + 15.
+// rows of V = 129,280 take 71 + 12 us (4.7 TB/s of their bytes while they are
+// read), 320 float32 rows 36 + 11.
 //
 // Exponentials are exp2(x c - K), one fused multiply-add each, with c the
 // binary32 rounding of log2(e) / T and K = c times a maximum: the reference
@@ -371,7 +371,6 @@ __global__ void __launch_bounds__(64 * NWV) top_small_kernel(TopArgs a) {
 constexpr int kTopSlice = 4 * kSliceStep;                  // ids of a slice
 constexpr int kTopSlices = DSPARK_V_MAX / kTopSlice;       // slices of the longest row
 constexpr int kTopSample = kSliceBS * 8;                   // logits sampled of a row: 64 runs of 32
-constexpr int kTopPer = 8;                                 // candidates per thread of the selection, at most
 
 struct TopPart {
   float m[kSliceNW], sum[kSliceNW];  // of each wave: its maximum, the sum of exponentials relative to it
@@ -561,8 +560,9 @@ __global__ void __launch_bounds__(kSliceBS) top_slice_kernel(TopSliceArgs q) {
   }
 }
 
-// One workgroup per row: joins its slices and selects among the candidates.
-template <int DT, int NWV>
+// One workgroup per row: joins its slices and selects among the candidates
+// (at most kTopPer per thread).
+template <int DT, int NWV, int kTopPer>
 __global__ void __launch_bounds__(64 * NWV) top_select_kernel(TopSliceArgs q) {
   __shared__ TopScratch<NWV> sh;
   __shared__ uint32_t first[kTopSlices + 1];  // candidates before each slice
