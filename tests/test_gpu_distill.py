@@ -10,6 +10,7 @@ p_v by F (its rounding) and the products by 3 F each; bf16 adds 2^-8."""
 import numpy as np
 import pytest
 import torch
+import torch.utils.checkpoint
 
 from oracle import logits as L
 from vocab_wide_draft_amd import binding as B
@@ -341,6 +342,48 @@ def test_distill_autograd():
         loss = B.distill_loss(zz, tt, 2.0)
         zz.add_(1.0)
         loss.sum().backward()
+
+
+@pytest.mark.parametrize("how", ["on the host", "float copies", "same place, other stride", "computed again"])
+def test_distill_autograd_saved_tensor_hooks(how):
+    """What a hook gives back for a saved tensor is what the gradient is computed from."""
+    rng = np.random.default_rng(26)
+    n, V, wide = 5, 4001 if how == "on the host" else 4000, 4096
+    a = rows_of(rng, n, V, "f32", 2.0)
+    tt = teacher(lists(rng, a.astype(np.float64), 30, 2.0, True))
+    rows = torch.zeros((n, wide), device=dev())
+    x = rows[:, :V].copy_(to_dev(a, "f32")).requires_grad_()
+    want = B.distill_backward(x.detach(), tt, B.distill(x.detach(), tt, 2.0), torch.ones(n, device=dev()), 2.0)
+    if how == "computed again":
+        first = {"lse": tt["lse"].clone(), "logits": tt["logits"].clone()}
+
+        def f(y):
+            return B.distill_loss(y, dict(tt, lse=first["lse"] * 1.0, logits=first["logits"] * 1.0), 2.0)
+
+        loss = torch.utils.checkpoint.checkpoint(f, x, use_reentrant=False)
+        held = [torch.full((n,), -50.0, device=dev()) for _ in range(64)]  # over what the first pass has freed
+    else:
+        if how == "on the host":
+            hooks = torch.autograd.graph.save_on_cpu()
+        elif how == "float copies":
+            hooks = torch.autograd.graph.saved_tensors_hooks(
+                lambda t: t.clone() if t.dtype == torch.float32 and t.shape != x.shape else t, lambda t: t)
+        else:
+            def unpack(t):
+                if t.shape != x.shape:
+                    return t
+                dense = rows.view(-1)[:n * V].view(n, V)
+                return dense.copy_(t)
+
+            hooks = torch.autograd.graph.saved_tensors_hooks(lambda t: t.detach().clone() if t.shape == x.shape else t, unpack)
+        with hooks:
+            loss = B.distill_loss(x, tt, 2.0)
+        if how == "float copies":
+            tt["logits"].zero_()
+            tt["lse"].zero_()
+    (got,) = torch.autograd.grad(loss.sum(), x)
+    torch.cuda.synchronize()
+    assert torch.equal(got, want)
 
 
 def test_distill_stream_and_graph_replays():

@@ -673,12 +673,19 @@ def distill_step(student: torch.Tensor, teacher, weight: torch.Tensor, temperatu
     return {"loss": loss, "grad": g, "status": st}
 
 
+def _places(student, ids, logits, length, lse):
+    return (student.data_ptr(), student.stride(), ids.data_ptr(), logits.data_ptr(), length.data_ptr(),
+            None if lse is None else lse.data_ptr())
+
+
 def _distill_grad(ctx, grad_loss):
     # forward has checked the arguments and laid them out: on torch's backward thread Python takes three times as long
     saved = ctx.saved_tensors  # (and torch has checked that nobody wrote to them since)
-    r, t, stats, status, shape, V, dev = ctx.laid_out
-    if saved[0].data_ptr() != r.data or saved[1].data_ptr() != t.ids:  # they were moved in between
+    r, t, stats, status, shape, V, dev, at = ctx.laid_out
+    if _places(*saved) != at:  # a hook on saved tensors gave back others
         student, ids, logits, length, lse = saved
+        if student.stride(1) != 1 or (student.data_ptr() | student.stride(0) * student.element_size()) % 16:
+            student = _empty_rows(shape[0], V, student.dtype, dev).copy_(student)
         r, t = _rows(student), _teacher({"ids": ids, "logits": logits, "len": length, "lse": lse}, shape[0], dev)
     if grad_loss.dtype is not torch.float32 or not grad_loss.is_contiguous():
         grad_loss = grad_loss.to(torch.float32).contiguous()
@@ -694,7 +701,8 @@ class _DistillLoss(torch.autograd.Function):
         loss, stats, st, r, t = _distill(student, {"ids": ids, "logits": logits, "len": length, "lse": lse}, temperature)
         ctx.save_for_backward(student, ids, logits, length, lse)
         n, V = student.shape
-        ctx.laid_out = (r, t, stats, st, (n, _padded(V, student.dtype)), V, student.device)
+        ctx.laid_out = (r, t, stats, st, (n, _padded(V, student.dtype)), V, student.device,
+                         _places(student, ids, logits, length, lse))
         ctx.temperature = temperature
         return loss
 
