@@ -427,6 +427,21 @@ def test_shape_empty_arguments():
         B.shape_logits(x, mask=torch.zeros((0, 2), dtype=torch.int32, device=dev()), mask_row=i32([0, 0, 0]))
 
 
+@pytest.mark.parametrize("how", ["bias without offsets", "bias without values", "masks' rows without masks",
+                                 "lengths without a history", "prompts without a history"])
+def test_shape_incomplete_arguments(how):
+    """An argument that its missing partner would leave without effect is refused."""
+    x = torch.ones((3, 40), device=dev())
+    off, three = torch.tensor([0, 1, 1, 1], device=dev()), i32([1, 1, 1])
+    kw = {"bias without offsets": {"bias": (None, i32([4]), f32([1.0]))},
+          "bias without values": {"bias": (off, i32([4]), None)},
+          "masks' rows without masks": {"mask_row": three},
+          "lengths without a history": {"history_len": three},
+          "prompts without a history": {"prompt_len": three}}[how]
+    with pytest.raises(ValueError):
+        B.shape_logits(x, **kw)
+
+
 def test_shape_no_rows():
     g = B.shape_logits(torch.zeros((0, 64), device=dev()), 6)
     assert g["logits"].shape == (0, 64) and g["status"].shape == (0,)

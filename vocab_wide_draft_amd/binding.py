@@ -562,9 +562,15 @@ def shape_logits(rows: torch.Tensor, rows_per_request: int = 1, *, history=None,
     if draft is not None and d_cols < P - 1:
         raise ValueError("draft must have at least rows_per_request - 1 columns")
     m, m_cols, m_stride = (None, 0, 0) if mask is None else _matrix(mask, "mask", torch.int32, mask.shape[0], dev)
+    if mask_row is not None and mask is None:
+        raise ValueError("mask_row needs mask")
+    if history is None and (history_len is not None or prompt_len is not None):
+        raise ValueError("history_len and prompt_len need history")
     if mask is not None and (m_cols < (V + 31) // 32 or mask.shape[0] == 0):
         raise ValueError("mask must have rows of at least (V + 31) // 32 columns")
     offsets, ids, values = bias if bias is not None else (None, None, None)
+    if bias is not None and (offsets is None or ids is None or values is None):
+        raise ValueError("bias must be (offsets, ids, values)")
     total = 0 if ids is None else ids.numel()
     i32, f32 = torch.int32, torch.float32
     how = Shaping(P, 0, h, h_max, h_stride, _arg(history_len, "history_len", i32, (R,), dev),
