@@ -102,7 +102,7 @@ def test_distill_small(tail, dtype, V, k, n):
 @pytest.mark.parametrize("tail", [False, True])
 @pytest.mark.parametrize("dtype,V,n", [("bf16", 129280, 3), ("bf16", 131072, 2), ("bf16", 131073, 2), ("f32", 129280, 2),
                                        ("bf16", 129280, 300), ("bf16", 129281, 700), ("f32", 129280, 300), ("f32", 1 << 20, 2),
-                                       ("bf16", 140001, 260), ("bf16", 8192, 3), ("f32", 8193, 3), ("bf16", 32768, 3),
+                                       ("bf16", 140001, 260), ("bf16", 65536, 260), ("f32", 32768, 800), ("f32", 32768, 600), ("bf16", 8192, 3), ("f32", 8193, 3), ("bf16", 32768, 3),
                                        ("f32", 32769, 3)])
 def test_distill_long(tail, dtype, V, n):
     """Few rows (split over many workgroups) and many (one or few each)."""
@@ -123,7 +123,7 @@ def test_distill_long(tail, dtype, V, n):
         assert all(torch.equal(part[r], part[r % few]) for r in range(few, n))
 
 
-@pytest.mark.parametrize("V", [60, 9000])
+@pytest.mark.parametrize("V", [60, 9000, 32768])
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("tail", [False, True])
 def test_distill_special_student_rows(dtype, tail, V):
@@ -169,10 +169,11 @@ def test_distill_extreme_temperatures(dtype, V, temp):
     run_all(a, dtype, t, temp, np.ones(3, np.float32))
 
 
+@pytest.mark.parametrize("V", [5003, 32768])
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
-def test_distill_refused_rows(dtype):
+def test_distill_refused_rows(dtype, V):
     rng = np.random.default_rng(13)
-    V, k, n = 5003, 12, 14
+    k, n = 12, 14
     x = (rng.standard_normal((n, V)) * 2).astype(np.float32)
     a = W.f32_to_bf16_bits(x) if dtype == "bf16" else x
     t = lists(rng, f64(a, dtype), k, 1.0, True, ragged=False)
@@ -249,7 +250,7 @@ def test_distill_in_place_padding_and_strides(dtype):
         check(a[:, :V], dtype, t, 1.0, w.cpu().numpy(), ref["loss"].cpu().numpy(), host64(got))
 
 
-@pytest.mark.parametrize("V", [700, 40001])
+@pytest.mark.parametrize("V", [700, 32768, 40001])
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("tail", [False, True])
 def test_distill_bad_logits_on_the_list(dtype, tail, V):

@@ -313,9 +313,22 @@ void launch_rows_waves(const DistillArgs& a, int dtype, hipStream_t s) {
   if (dtype == DSPARK_BF16) hipLaunchKernelGGL(HIP_KERNEL_NAME(distill_row_kernel<DSPARK_BF16, NWV, GRAD>), grid, block, lds, s, a);
   else hipLaunchKernelGGL(HIP_KERNEL_NAME(distill_row_kernel<DSPARK_F32, NWV, GRAD>), grid, block, lds, s, a);
 }
+// Rows of 128 KB or more are read for the gradient by 16 waves each: half the
+// rows are in work at a time, and more of them are still in the last-level
+// cache when they are read again (V = 129,280, 8 / 16 waves: 1,280 bf16 rows
+// 177 / 156 us, 5,120 575 / 562, 1,280 float32 345 / 293, 256 64 / 63; 40,000
+// bf16 ids, 80 KB, 5,120 rows 177 / 212).  The chip holds 512 such rows: the
+// second round of somewhat more leaves CUs idle, unless the rows are long
+// enough to keep HBM busy all the same (640 bf16 rows of 129,280 ids 87 / 95
+// us, float32 170 / 163, of 65,536 80 / 81).
+bool rows_by_16(const DistillArgs& a, int dtype) {
+  const int64_t bytes = (int64_t)a.V * (dtype == DSPARK_BF16 ? 2 : 4);
+  return bytes >= 128 << 10 && (a.n <= 512 || a.n > 768 || bytes >= 384 << 10);
+}
 template <bool GRAD>
 void launch_rows(const DistillArgs& a, int dtype, hipStream_t s) {
   if (a.V <= 8192) launch_rows_waves<4, GRAD>(a, dtype, s);
+  else if (GRAD && rows_by_16(a, dtype)) launch_rows_waves<GRAD ? 16 : 8, GRAD>(a, dtype, s);
   else launch_rows_waves<8, GRAD>(a, dtype, s);
 }
 template <bool FROM_STATS>
