@@ -323,6 +323,35 @@ __global__ void __launch_bounds__(kSliceBS) distill_join_kernel(DistillArgs a) {
   if (lane_id() == 0) distill_row_out(a, r, o);
 }
 
+// A vector's gradient from its logits v, ids t .. t + N - 1 of the set's row:
+// off the list for all, then the listed ones one after the other, whose
+// entries follow each other.
+template <int N>
+__device__ __forceinline__ void distill_grad_vec(const IdSet& on, const float* p, int t, float M, float M_off, float c,
+                                                 float inv_s, float w_on, float f_off, float (&v)[N]) {
+  uint32_t left = on.members<N>(t);
+  float x[N];
+#pragma unroll
+  for (int l = 0; l < N; ++l) {
+    x[l] = v[l];
+    v[l] = __builtin_amdgcn_exp2f((v[l] - M_off) * c) * f_off;
+  }
+  if (left) {
+    uint32_t e = on.entry(t);
+    do {
+      const uint32_t low = left & (0u - left);
+      float y = x[0];
+#pragma unroll
+      for (int l = 1; l < N; ++l) y = low == 1u << l ? x[l] : y;
+      const float d = (__builtin_amdgcn_exp2f((y - M) * c) * inv_s - p[e & (DSPARK_K_MAX - 1)]) * w_on;
+#pragma unroll
+      for (int l = 0; l < N; ++l) v[l] = low == 1u << l ? d : v[l];
+      left ^= low;
+      ++e;
+    } while (left);
+  }
+}
+
 // The gradient of one slice of one row; FROM_STATS: the row's numbers come
 // from the forward call, otherwise they are joined here (and slice 0 writes
 // the row's outputs).
@@ -383,14 +412,7 @@ __global__ void __launch_bounds__(kSliceBS) distill_grad_kernel(DistillArgs a) {
   const float w_on = (float)w, f_off = (float)(sh.f_off * w);
   XT* const out = g + start;
   for_row<DT, true, kSliceBS>(x, start, size, [&](int t, float (&v)[N]) {
-    const uint32_t bits = on.members<N>(t);
-#pragma unroll
-    for (int l = 0; l < N; ++l) {
-      const bool listed = (bits >> l) & 1u;
-      const float e = __builtin_amdgcn_exp2f((v[l] - (listed ? M : M_off)) * c);
-      v[l] = e * f_off;
-      if (listed) v[l] = (e * inv_s - p[on.entry(t + l) & (DSPARK_K_MAX - 1)]) * w_on;
-    }
+    distill_grad_vec<N>(on, p, t, M, M_off, c, inv_s, w_on, f_off, v);
     store_vec<DT, N>(out, t, size, v);
   });
 }
@@ -575,14 +597,7 @@ __global__ void __launch_bounds__(64 * NWV, NWV == 4 ? 6 : 8) distill_row_kernel
   const double w = (double)a.weight[r] * a.inv_t;
   const float w_on = (float)w, f_off = (float)(sh.f_off * w);
   for_row<DT, true, T>(x, 0, V, [&](int t, float (&v)[N]) {
-    const uint32_t bits = on.members<N>(t);
-#pragma unroll
-    for (int l = 0; l < N; ++l) {
-      const bool listed = (bits >> l) & 1u;
-      const float e = __builtin_amdgcn_exp2f((v[l] - (listed ? M : M_off)) * c);
-      v[l] = e * f_off;
-      if (listed) v[l] = (e * inv_s - p[on.entry(t + l) & (DSPARK_K_MAX - 1)]) * w_on;
-    }
+    distill_grad_vec<N>(on, p, t, M, M_off, c, inv_s, w_on, f_off, v);
     store_vec<DT, N>(g, t, V, v);
   });
 }
