@@ -445,6 +445,7 @@ __global__ void __launch_bounds__(64 * NWV, NWV == 4 ? 6 : 8) distill_row_kernel
   constexpr float kNone = -__builtin_inff();
 
   int len = a.len[r];
+  double w_list[PER];  // exp(z / T - zm) of this thread's list entries
   uint32_t wrong = 0;
   if (len < 0 || len > a.k_max) {
     wrong = 1u;
@@ -482,6 +483,7 @@ __global__ void __launch_bounds__(64 * NWV, NWV == 4 ? 6 : 8) distill_row_kernel
 #pragma unroll
     for (int j = 0; j < PER; ++j) {
       on_x[j] = kNone;
+      w_list[j] = 0.0;
       if (id[j] >= 0) {
         const float xj = El<DT>::get(x, id[j]);
         on.add(id[j], prev[j], (uint32_t)(j * T + tid));
@@ -491,7 +493,7 @@ __global__ void __launch_bounds__(64 * NWV, NWV == 4 ? 6 : 8) distill_row_kernel
           flags |= xj != xj ? 1u : xj == __builtin_inff() ? 2u : 0u;
         }
         const double lp = (double)z[j] * a.inv_t - zm;
-        const double w = exp(lp);
+        const double w = w_list[j] = exp(lp);
         if (w > 0.0) {
           b0 += w;
           b1 += w * (lp - (double)xj * a.inv_t);
@@ -589,9 +591,16 @@ __global__ void __launch_bounds__(64 * NWV, NWV == 4 ? 6 : 8) distill_row_kernel
     for (int t = tid * N; t < V; t += T * N) store_vec<DT, N>(g, t, V, v);
     return;
   }
+  double norm = 1.0;  // the teacher's probabilities over w_list
+  if (!tail) {
+    double sum = 0.0;
+#pragma unroll
+    for (int w = 0; w < NWV; ++w) sum += sum_wave[w][2];
+    norm = 1.0 / sum;
+  }
 #pragma unroll
   for (int j = 0; j < PER; ++j)
-    if (id[j] >= 0) p[j * T + tid] = (float)exp((double)z[j] * a.inv_t - sh.zm);
+    if (id[j] >= 0) p[j * T + tid] = (float)(w_list[j] * norm);
   __syncthreads();
   const float M = (float)sh.M, M_off = (float)sh.M_off, inv_s = (float)sh.inv_s;
   const double w = (double)a.weight[r] * a.inv_t;
