@@ -412,13 +412,13 @@ __device__ __forceinline__ void push_ge(uint32_t& mask, float x, float t) {
   asm("v_cmp_ge_f32 vcc, %1, %2\n\tv_addc_co_u32 %0, vcc, %0, %0, vcc" : "+v"(mask) : "v"(x), "v"(t) : "vcc");
 }
 
-// What bounds it is the number of instructions (bf16: an unpack, half a
-// maximum, a multiply-add, an exponential of four cycles' issue, an addition
-// and two for the mask per logit), so everything per thread is kept small:
-// each wave has a reference of its own, the order of the candidates comes
-// from one scan of packed counts.  A candidate's logit is picked from a copy of
-// the slice in LDS (read again from memory it held its wave up: 91 us instead
-// of 71 for 1,280 bf16 rows).
+// What bounds it is reading, though it is a quarter above what a copy's rate
+// would give: without the exponentials (five of eleven cycles' issue per bf16
+// logit) 1,280 bf16 rows take 65 us instead of 71, and an eighth fewer vector
+// instructions around them changed nothing.  Each wave has a reference of its
+// own, the order of the candidates comes from one scan of packed counts.  A
+// candidate's logit is picked from a copy of the slice in LDS (read again from
+// memory it held its wave up: 91 us instead of 71).
 template <int DT>
 __global__ void __launch_bounds__(kSliceBS) top_slice_kernel(TopSliceArgs q) {
   __shared__ __align__(16) uint32_t sample[kSliceBS];
