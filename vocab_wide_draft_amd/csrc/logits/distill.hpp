@@ -471,41 +471,16 @@ __global__ void __launch_bounds__(64 * NWV, NWV == 4 ? 6 : 8) distill_row_kernel
       if (!finite_row_value(z[j])) wrong |= 8u;
     }
   }
-  wrong = group_reduce<NWV>(wrong, 0u, either, redu);
+  wrong = group_reduce<NWV>(wrong, 0u, either, redu);  // (and the set is clear)
   int status = wrong ? DSPARK_ST_Q_BAD_LEN + (wrong & 1u ? 0 : wrong & 2u ? 1 : wrong & 4u ? 2 : 3) : DSPARK_ST_OK;
   const float c = (float)(a.inv_t * (double)kLog2e);
   if (status == DSPARK_ST_OK && len > 0) {  // (uniform)
-    const double zm = tail ? (double)a.lse[r] : (double)group_reduce<NWV>(zmax, kNone, larger, redf) * a.inv_t;
-    __syncthreads();  // the set is clear
-    double b0 = 0.0, b1 = 0.0;
-    float m_on = kNone, s_on = 0.0f, on_x[PER];
-    uint32_t flags = 0;
 #pragma unroll
-    for (int j = 0; j < PER; ++j) {
-      on_x[j] = kNone;
-      w_list[j] = 0.0;
-      if (id[j] >= 0) {
-        const float xj = El<DT>::get(x, id[j]);
-        on.add(id[j], prev[j], (uint32_t)(j * T + tid));
-        if (tail) {
-          on_x[j] = xj;
-          m_on = __builtin_fmaxf(m_on, xj);
-          flags |= xj != xj ? 1u : xj == __builtin_inff() ? 2u : 0u;
-        }
-        const double lp = (double)z[j] * a.inv_t - zm;
-        const double w = w_list[j] = exp(lp);
-        if (w > 0.0) {
-          b0 += w;
-          b1 += w * (lp - (double)xj * a.inv_t);
-        }
-      }
-    }
-    if (m_on > kNone) {
-#pragma unroll
-      for (int j = 0; j < PER; ++j) s_on += __builtin_amdgcn_exp2f((on_x[j] - m_on) * c);
-    }
+    for (int j = 0; j < PER; ++j)
+      if (id[j] >= 0) on.add(id[j], prev[j], (uint32_t)(j * T + tid));
     __syncthreads();
     // off the list: running maximum and sum, a vector moves the maximum at most once
+    uint32_t flags = 0;
     float m = kNone, s_off = 0.0f;
     for_row<DT, false, T>(x, 0, V, [&](int t, float (&v)[N]) {
       const uint32_t bits = tail ? on.members<N>(t) : 0u;
@@ -531,6 +506,33 @@ __global__ void __launch_bounds__(64 * NWV, NWV == 4 ? 6 : 8) distill_row_kernel
 #pragma unroll
         for (int l = 0; l < N; ++l) flags |= v[l] != v[l] ? 1u : v[l] == __builtin_inff() ? 2u : 0u;
       }
+    }
+    // the list's side, now that the row is in the caches
+    const double zm = tail ? (double)a.lse[r] : (double)group_reduce<NWV>(zmax, kNone, larger, redf) * a.inv_t;
+    double b0 = 0.0, b1 = 0.0;
+    float m_on = kNone, s_on = 0.0f, on_x[PER];
+#pragma unroll
+    for (int j = 0; j < PER; ++j) {
+      on_x[j] = kNone;
+      w_list[j] = 0.0;
+      if (id[j] >= 0) {
+        const float xj = El<DT>::get(x, id[j]);
+        if (tail) {
+          on_x[j] = xj;
+          m_on = __builtin_fmaxf(m_on, xj);
+          flags |= xj != xj ? 1u : xj == __builtin_inff() ? 2u : 0u;
+        }
+        const double lp = (double)z[j] * a.inv_t - zm;
+        const double w = w_list[j] = exp(lp);
+        if (w > 0.0) {
+          b0 += w;
+          b1 += w * (lp - (double)xj * a.inv_t);
+        }
+      }
+    }
+    if (m_on > kNone) {
+#pragma unroll
+      for (int j = 0; j < PER; ++j) s_on += __builtin_amdgcn_exp2f((on_x[j] - m_on) * c);
     }
     // two meetings of the waves: the maxima, which all need, then the sums, which one wave joins
     m_wave[0][wave_id()] = wave_reduce(m, kNone, larger);
