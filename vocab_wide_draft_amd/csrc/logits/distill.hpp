@@ -145,37 +145,18 @@ __device__ void distill_slice(const DistillArgs& a, int64_t r, int s, uint32_t* 
   }
   __syncthreads();
   const float c = (float)(a.inv_t * (double)kLog2e);
-  double b0 = 0.0, b1 = 0.0;
-  float m_on = -__builtin_inff(), s_on = 0.0f, on_x[kListPer];
-  uint32_t flags = 0;
+  if (tail) {
 #pragma unroll
-  for (int j = 0; j < kListPer; ++j) {
-    const uint32_t t = (uint32_t)(id[j] - start);
-    on_x[j] = -__builtin_inff();
-    if (id[j] >= 0 && t < (uint32_t)size) {
-      const float xj = El<DT>::get(x, id[j]);
-      if (tail) {
-        atomicOr(&on.bits[t >> 5], 1u << (t & 31));
-        on_x[j] = xj;
-        m_on = __builtin_fmaxf(m_on, xj);
-        flags |= xj != xj ? 1u : xj == __builtin_inff() ? 2u : 0u;
-      }
-      const double lp = (double)z[j] * a.inv_t - zm;
-      const double w = exp(lp);
-      if (w > 0.0) {
-        b0 += w;
-        b1 += w * (lp - (double)xj * a.inv_t);
-      }
+    for (int j = 0; j < kListPer; ++j) {
+      const uint32_t t = (uint32_t)(id[j] - start);
+      if (id[j] >= 0 && t < (uint32_t)size) atomicOr(&on.bits[t >> 5], 1u << (t & 31));
     }
-  }
-  if (m_on > -__builtin_inff()) {
-#pragma unroll
-    for (int j = 0; j < kListPer; ++j) s_on += __builtin_amdgcn_exp2f((on_x[j] - m_on) * c);
   }
   __syncthreads();
   // the row off the list: running maximum and sum; a vector moves the maximum
   // at most once
   constexpr int N = kVec<DT>;
+  uint32_t flags = 0;
   float m = -__builtin_inff(), s_off = 0.0f;
   for_row<DT, false, kSliceBS>(x, start, size, [&](int t, float (&v)[N]) {
     const uint32_t bits = tail ? on.members<N>(t) : 0u;
@@ -202,6 +183,32 @@ __device__ void distill_slice(const DistillArgs& a, int64_t r, int s, uint32_t* 
 #pragma unroll
       for (int l = 0; l < N; ++l) flags |= v[l] != v[l] ? 1u : v[l] == __builtin_inff() ? 2u : 0u;
     }
+  }
+  // the list's side, now that the slice is in the caches
+  double b0 = 0.0, b1 = 0.0;
+  float m_on = -__builtin_inff(), s_on = 0.0f, on_x[kListPer];
+#pragma unroll
+  for (int j = 0; j < kListPer; ++j) {
+    const uint32_t t = (uint32_t)(id[j] - start);
+    on_x[j] = -__builtin_inff();
+    if (id[j] >= 0 && t < (uint32_t)size) {
+      const float xj = El<DT>::get(x, id[j]);
+      if (tail) {
+        on_x[j] = xj;
+        m_on = __builtin_fmaxf(m_on, xj);
+        flags |= xj != xj ? 1u : xj == __builtin_inff() ? 2u : 0u;
+      }
+      const double lp = (double)z[j] * a.inv_t - zm;
+      const double w = exp(lp);
+      if (w > 0.0) {
+        b0 += w;
+        b1 += w * (lp - (double)xj * a.inv_t);
+      }
+    }
+  }
+  if (m_on > -__builtin_inff()) {
+#pragma unroll
+    for (int j = 0; j < kListPer; ++j) s_on += __builtin_amdgcn_exp2f((on_x[j] - m_on) * c);
   }
   const auto larger = [](float p, float q) { return __builtin_fmaxf(p, q); };
   const auto plus = [](double p, double q) { return p + q; };
