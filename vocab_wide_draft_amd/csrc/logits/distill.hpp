@@ -82,10 +82,21 @@ __device__ __forceinline__ void for_row(const typename El<DT>::T* x, int start, 
       body(base + k * STEP + (int)threadIdx.x * N, v);
     }
   }
-  for (int t = whole + (int)threadIdx.x * N; t < size; t += STEP) {
-    float v[N];
-    unpack<DT, N>(raw_vec<DT, N, LAST>(row, t, size), v);
-    body(t, v);
+  if (whole == size) return;
+  Raw<DT, N> q[kAhead];
+#pragma unroll
+  for (int k = 0; k < kAhead; ++k) {
+    const int t = whole + k * STEP + (int)threadIdx.x * N;
+    if (t < size) q[k] = raw_vec<DT, N, LAST>(row, t, size);
+  }
+#pragma unroll
+  for (int k = 0; k < kAhead; ++k) {
+    const int t = whole + k * STEP + (int)threadIdx.x * N;
+    if (t < size) {
+      float v[N];
+      unpack<DT, N>(q[k], v);
+      body(t, v);
+    }
   }
 }
 
