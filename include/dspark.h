@@ -434,7 +434,8 @@ int dspark_shape_logits(const dspark_rows* rows, const dspark_shaping* how, void
 int dspark_top_logits(const dspark_rows* rows, const int32_t* topk, int32_t k_max, float temperature, int32_t* ids,
                       float* logits, int32_t* len, float* lse, int32_t* row_status, void* ws, size_t ws_bytes,
                       void* stream);
-/* Workspace of dspark_top_logits (16-byte aligned). */
+/* Workspace of dspark_top_logits (16-byte aligned); one for n rows serves
+ * fewer rows as well. */
 size_t dspark_top_logits_workspace(int64_t n_rows, int64_t vocab, int32_t k_max);
 
 /* A teacher's rows for dspark_distill: row r lists len[r] tokens (0 <= len[r]
@@ -468,7 +469,8 @@ typedef struct {
  * Q_UNSORTED, Q_NONFINITE (a listed logit or lse that is not finite) for the
  * teacher's list (the smallest), then ROW_NAN, ROW_POSINF or ROW_ZERO_MASS for
  * the student's row; a refused row has loss 0 and gradient 0.
- * ws: dspark_distill_workspace() bytes, 16-byte aligned (NULL where it is 0). */
+ * ws: dspark_distill_workspace() bytes, 16-byte aligned (NULL where it is 0);
+ * one for n rows serves fewer rows as well. */
 #define DSPARK_DISTILL_STATS 5
 size_t dspark_distill_workspace(int64_t n_rows, int64_t vocab);
 int dspark_distill(const dspark_rows* student, const dspark_teacher* teacher, float temperature, float* loss,

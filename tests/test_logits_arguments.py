@@ -109,6 +109,18 @@ def test_distill_refusals():
     assert step(r=empty, t=t0, w=None, grad=0, ws=0, n=0) == 0
 
 
+def test_workspaces_grow_with_the_rows():
+    """One workspace for the largest batch serves every smaller one."""
+    lib = B.load_library()
+    ns = list(range(1, 300)) + [511, 512, 513, 1000, 2047, 2048, 2049, 5120, 1 << 20, 1 << 24]
+    for V in (1, 2048, 8000, 16384, 16385, 32768, 32769, 40000, 65536, 65537, 129280, 131072, 131073, 200000, 1 << 20):
+        for k in (0, 1, 64, 1024):
+            sizes = [lib.dspark_top_logits_workspace(n, V, k) for n in ns]
+            assert sizes == sorted(sizes), (V, k)
+        sizes = [lib.dspark_distill_workspace(n, V) for n in ns]
+        assert sizes == sorted(sizes), V
+
+
 def test_binding_refuses_wrong_tensors():
     dev = torch.device("cpu")
     with pytest.raises(ValueError):

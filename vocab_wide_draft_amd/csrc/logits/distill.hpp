@@ -62,9 +62,10 @@ __device__ __forceinline__ bool finite_row_value(float x) { return (__float_as_u
 
 // body(t, v) for every vector of a row's ids [start, start + size) that this
 // thread of T owns, t counted from start; kAhead loads are on their way at a
-// time (5,120 bf16 rows, loss and gradient: 595 us; 2 at a time 602, 8 spill:
-// 844).  LAST: streamed, the row is not read again (a first reading that is
-// streamed too leaves nothing in the caches for the second: 704 us).
+// time (5,120 bf16 rows, loss and gradient: 550 us, as with 2; 6 628 and 8
+// 665: more registers, fewer waves).  LAST: streamed, the row is not read
+// again (a first reading that is streamed too leaves less in the caches for
+// the second: 670 us).
 constexpr int kAhead = 4;
 template <int DT, bool LAST, int T, class BODY>
 __device__ __forceinline__ void for_row(const typename El<DT>::T* x, int start, int size, BODY body) {
@@ -439,8 +440,8 @@ __global__ void __launch_bounds__(kSliceBS) distill_grad_kernel(DistillArgs a) {
 // fill the chip or are short.  For the gradient the row is read again, out of
 // the caches (the rows in work at once are about the last-level cache), so
 // that HBM sees little more than one read and one write: 5,120 bf16 rows take
-// 570 us, 4.6 TB/s of that read and write, where a copy reaches 5.2; in slices,
-// which read HBM twice, 711.
+// 550 us, 4.8 TB/s of that read and write, where a copy reaches 5.2; in slices,
+// which read HBM twice, 675.
 template <int DT, int NWV, bool GRAD>
 __global__ void __launch_bounds__(64 * NWV, NWV == 4 ? 6 : 8) distill_row_kernel(DistillArgs a) {
   constexpr int T = 64 * NWV, N = kVec<DT>, PER = DSPARK_K_MAX / T;

@@ -298,14 +298,21 @@ void launch_part(const DistillArgs& a, int dtype, hipStream_t s) {
   if (dtype == DSPARK_BF16) hipLaunchKernelGGL(distill_part_kernel<DSPARK_BF16>, grid, dim3(kSliceBS), distill_lds(a), s, a);
   else hipLaunchKernelGGL(distill_part_kernel<DSPARK_F32>, grid, dim3(kSliceBS), distill_lds(a), s, a);
 }
-// Whether each row gets one workgroup.  Short rows: one launch instead of two
-// (4,096 rows of 20,003 ids in bf16, loss and gradient: 101 us against 105 in
-// slices).  Longer ones where they fill the chip and are read twice, for loss
-// and gradient together (V = 129,280 in bf16: 256 rows 43 / 41 us, 512 70 / 73,
-// 4,096 476 / 551; 64 38 / 21); the loss alone is as fast in slices (1,280
-// rows 79 / 75).
-bool short_rows(int64_t V) { return V <= 32768; }
-bool step_by_rows(int64_t n, int64_t V) { return short_rows(V) || (n >= 256 && V <= kRowMost); }
+// Whether each row gets one workgroup: short rows (one launch instead of two:
+// 4,096 rows of 20,003 ids in bf16, loss and gradient, 84 us against 97 in
+// slices), and longer ones where they fill half of the chip, or a quarter of
+// it with rows that are not long (V = 129,280 in bf16, loss and gradient: 64
+// rows 26 / 20 us, 128 28 / 26, 192 30 / 35, 512 62 / 72, 4,096 443 / 539;
+// the loss alone 128 rows 18 / 19, 256 19 / 23, 1,280 67 / 70; 65,536 float32,
+// loss and gradient: 64 rows 22 / 25).
+bool by_rows(int64_t n, int64_t V) { return V <= 32768 || (V <= kRowMost && n >= (V <= 65536 ? 64 : 128)); }
+// The same for the loss alone.  Long rows that together are more than the
+// last-level cache stay in slices: of rows that were read side by side the
+// backward call finds less there (V = 129,280, both calls, rows / slices: 640
+// float32 184 / 169 us, 1,280 bf16 177 / 171, 250 bf16 52 / 56).
+bool loss_by_rows(int64_t n, int64_t V, int64_t element) {
+  return by_rows(n, V) && (V <= 65536 || n * V * element <= 256 << 20);
+}
 template <int NWV, bool GRAD>
 void launch_rows_waves(const DistillArgs& a, int dtype, hipStream_t s) {
   const size_t lds = 2u * 4u * (((size_t)a.V + 31) / 32);
@@ -316,11 +323,11 @@ void launch_rows_waves(const DistillArgs& a, int dtype, hipStream_t s) {
 // Rows of 128 KB or more are read for the gradient by 16 waves each: half the
 // rows are in work at a time, and more of them are still in the last-level
 // cache when they are read again (V = 129,280, 8 / 16 waves: 1,280 bf16 rows
-// 177 / 156 us, 5,120 575 / 562, 1,280 float32 345 / 293, 256 64 / 63; 40,000
-// bf16 ids, 80 KB, 5,120 rows 177 / 212).  The chip holds 512 such rows: the
+// 170 / 153 us, 5,120 561 / 550, 1,280 float32 335 / 295, 256 63 / 63; 40,000
+// bf16 ids, 80 KB, 5,120 rows 175 / 200).  The chip holds 512 such rows: the
 // second round of somewhat more leaves CUs idle, unless the rows are long
-// enough to keep HBM busy all the same (640 bf16 rows of 129,280 ids 87 / 95
-// us, float32 170 / 163, of 65,536 80 / 81).
+// enough to keep HBM busy all the same (640 bf16 rows of 129,280 ids 84 / 89
+// us, float32 171 / 161, of 65,536 80 / 79).
 bool rows_by_16(const DistillArgs& a, int dtype) {
   const int64_t bytes = (int64_t)a.V * (dtype == DSPARK_BF16 ? 2 : 4);
   return bytes >= 128 << 10 && (a.n <= 512 || a.n > 768 || bytes >= 384 << 10);
@@ -347,8 +354,12 @@ extern "C" {
 
 size_t dspark_distill_workspace(int64_t n_rows, int64_t vocab) {
   if (n_rows <= 0 || n_rows > (1 << 24) || vocab < 1 || vocab > DSPARK_V_MAX) return 0;
-  if (short_rows(vocab)) return 0;
-  return distill_part_bytes(n_rows, vocab) + 4u * (size_t)n_rows;
+  if (vocab <= 32768) return 0;  // (by rows, however many)
+  // at least distill_part_bytes(m, vocab) + 4 m for every m <= n_rows: a row
+  // has at most 64 slices and at most 2,048 / m, or those of kDistillSliceMost ids
+  const int64_t few = std::min<int64_t>(2048, 64 * n_rows);
+  const int64_t many = n_rows * ((vocab + kDistillSliceMost - 1) / kDistillSliceMost);
+  return (size_t)std::max(few, many) * sizeof(DistillPart) + 4u * (size_t)n_rows;
 }
 
 int dspark_distill(const dspark_rows* student, const dspark_teacher* teacher, float temperature, float* loss,
@@ -364,7 +375,7 @@ int dspark_distill(const dspark_rows* student, const dspark_teacher* teacher, fl
   a.stats = stats;
   a.row_status = row_status;
   hipStream_t s = static_cast<hipStream_t>(stream);
-  if (short_rows(a.V)) {
+  if (loss_by_rows(a.n, a.V, student->dtype == DSPARK_BF16 ? 2 : 4)) {
     launch_rows<false>(a, student->dtype, s);
   } else {
     launch_part(a, student->dtype, s);
@@ -410,7 +421,7 @@ int dspark_distill_step(const dspark_rows* student, const dspark_teacher* teache
   a.grad = grad;
   a.grad_stride = grad_stride;
   hipStream_t s = static_cast<hipStream_t>(stream);
-  if (step_by_rows(a.n, a.V)) {
+  if (by_rows(a.n, a.V)) {
     launch_rows<true>(a, student->dtype, s);
   } else {
     launch_part(a, student->dtype, s);
