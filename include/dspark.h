@@ -427,7 +427,8 @@ int dspark_shape_logits(const dspark_rows* rows, const dspark_shaping* how, void
  * logits by (logit desc, id asc), fewer when it has fewer: ids (int32
  * [n_rows][k_max], ascending) with logits (float[n_rows][k_max], the row's
  * values), zeros past len[r] (int32[n_rows]).  lse[r] (float, may be NULL) =
- * log sum_v exp(x_v / temperature) over the whole row.  k_max: 0 ..
+ * log sum_v exp(x_v / temperature) over the whole row (infinite where it
+ * passes binary32, which dspark_distill refuses).  k_max: 0 ..
  * DSPARK_K_MAX (0: ids and logits may be NULL); temperature: in [2^-100,
  * 2^100].  row_status[r]: OK, ROW_NAN, ROW_POSINF,
  * ROW_ZERO_MASS or BAD_TOPK; a refused row has len 0, lse 0 and zeros. */

@@ -18,7 +18,10 @@
 // binary32 rounding of log2(e) / T and K = c times a maximum: the reference
 // K is exact as it stands (the sum is over 2^(x c) / 2^K), and what the
 // rounding of c does to the row's largest logits is put back in binary64
-// (sum_reference).  Where K would leave binary32 they are exp2((x - m) c).
+// (sum_reference).  The exponent of the maximum itself is then K's own rounding,
+// half its last place: 2 at |K| = 2^26, but hundreds from 2^32 on (logits of 1e9
+// and more, or temperatures below 2^-26), where the exponential overflows or
+// vanishes.  From 2^26 on they are exp2((x - m) c), exactly 1 at the maximum.
 #pragma once
 #include "slices.hpp"
 
@@ -49,8 +52,8 @@ __device__ __forceinline__ int row_k(const TopArgs& a, int64_t r) {
   return k < 0 || k > cap ? -1 : k;
 }
 
-// whether K = m c stays far inside binary32
-__device__ __forceinline__ bool reference_fits(const TopArgs& a, float m) { return __builtin_fabsf(m) * a.c < 1e30f; }
+// whether the rounding of K = m c stays within 2 (see above)
+__device__ __forceinline__ bool reference_fits(const TopArgs& a, float m) { return __builtin_fabsf(m) * a.c < 0x1p26f; }
 // log of what a sum of exponentials relative to the maximum m is to be multiplied by
 __device__ __forceinline__ double sum_reference(const TopArgs& a, float m) {
   if (!reference_fits(a, m)) return (double)m * a.inv_t;
