@@ -461,8 +461,9 @@ typedef struct {
  * The last term is there only with lse, and only where P > 0 and the student
  * has a finite logit off the list.  Its
  * gradient with respect to s, computed by dspark_distill_backward:
- *   (q_v - p_v) / T on the list;  q_v (1 - P / Q) / T off it (q_v / T
- *   without the last term).
+ *   (q_v - p_v) / T on the list;  q_v (1 - P / Q) / T off it;
+ *   without the last term (b q_v - p_v) / T on the list and b q_v / T off it,
+ *   b = sum_J p_j (one where lse is NULL).
  * A row with len[r] = 0 teaches nothing: loss 0, gradient 0, its student row
  * is not read.  A student's -inf at a token with p > 0 gives loss +inf.
  * loss: float[n_rows].  stats: double[n_rows][DSPARK_DISTILL_STATS], what

@@ -95,6 +95,7 @@ def distill_row(x, ids, z, temp=1.0, lse=None):
     p = np.exp(lp)
     with np.errstate(invalid="ignore"):
         loss = float(np.where(p > 0, p * (lp - logq[ids]), 0.0).sum())
+    # the derivative of -p_j log q_j is p_j q_v - p_j [v = j]: the softmax times sum p, which with P is one
     grad = q.copy()
     P = Q = 0.0
     off = np.ones(len(x), bool)
@@ -106,6 +107,7 @@ def distill_row(x, ids, z, temp=1.0, lse=None):
             grad[off] *= 1.0 - P / Q
         else:
             P = 0.0
+            grad *= float(p.sum())
     grad[ids] -= p
     full = np.zeros(len(x))
     full[ids] = p

@@ -14,6 +14,9 @@
 //   with lse:    loss = B1 + B0 lse_u + P (log P - log Q),  P = 1 - B0
 //                off the list dL/du_v = e^(u_v - M_off / T) (e^((M_off - M) / T) / S - P / S_off)
 //   normalised:  loss = B1 / B0 - log B0 + lse_u  (every id counts as off the list in the sums)
+// The softmax stands in the gradient times sum p, which is B0 with lse and one
+// otherwise.  The last term adds P to it, B0 + P = 1; without that term (P <= 0,
+// or nothing off the list) the factor stays, and 1 / S is kept as B0 / S.
 // Every term is a sum over slices of the vocabulary once each slice's
 // maximum is put back, so slices are worked on apart and joined.  Sums over
 // a thread's logits are binary32, everything joined is binary64, as is the
@@ -250,7 +253,7 @@ __device__ void distill_slice(const DistillArgs& a, int64_t r, int s, uint32_t* 
 struct DistillRow {  // what the gradient needs of a row
   int status;
   double M;      // the row's maximum
-  double inv_s;  // 1 / S
+  double inv_s;  // 1 / S, times sum p where the last term is left out
   double M_off;  // the maximum off the list
   double f_off;  // dL/du off the list over e^(u - M_off / T)
   double zm;     // log of the teacher's normaliser
@@ -268,14 +271,15 @@ __device__ __forceinline__ void distill_finish(double inv_t, bool tail, float m_
   const double S = off * e_off + on * e_on;  // (the first underflows where the rest is out of sight)
   const double log_s = log(S), lse_u = (double)m * inv_t + log_s;
   o.M = m;
-  o.inv_s = 1.0 / S;
   o.M_off = m_off == kNone ? 0.0 : m_off;
+  const double P = 1.0 - b0;
+  const bool rest = tail && P > 0.0 && off > 0.0;  // the last term
+  o.inv_s = (tail && !rest ? b0 : 1.0) / S;
   o.f_off = e_off * o.inv_s;
   if (tail) {
     o.zm = zm;
     o.loss = b1 + b0 * lse_u;
-    const double P = 1.0 - b0;
-    if (P > 0.0 && off > 0.0) {
+    if (rest) {
       o.loss += P * (log(P) - (((double)m_off - (double)m) * inv_t + log(off) - log_s));
       o.f_off -= P / off;
     }
