@@ -88,8 +88,8 @@ def distill_row(x, ids, z, temp=1.0, lse=None):
     """(loss, gradient, q, p over the vocabulary, P, Q) of one good row with a nonempty list."""
     x, z = np.asarray(x, np.float64), np.asarray(z, np.float64)
     ids = np.asarray(ids, np.int64)
-    u = x / temp
-    logq = u - logsumexp(u)
+    d = (x - x.max()) / temp  # (from the maximum: a row far from zero keeps its differences)
+    logq = d - np.log(np.exp(d).sum())
     q = np.exp(logq)
     lp = z / temp - (logsumexp(z / temp) if lse is None else float(lse))
     p = np.exp(lp)

@@ -4,21 +4,23 @@
 // Mathematics.  u = s / T.  Off the list, a row needs M_off = max s and S_off =
 // sum exp(u - M_off / T); on the list M_on and S_on, and, with w_j = exp(z_j / T
 // - zm) (zm: the teacher's lse, or the list's maximum when it is
-// renormalised), B0 = sum w_j and B1 = sum w_j (z_j / T - zm - u_j).  The two
-// sides are kept apart, each with its own maximum: S - S_on would cancel
+// renormalised), B0 = sum w_j and B1 = sum w_j (z_j / T - zm - (u_j - M / T)),
+// M the row's maximum: a row far from zero, such as one that a mask has left
+// at its type's lowest value, would lose its loss in the difference of two
+// sums of the logits themselves.  The two sides are kept apart, each with its own maximum: S - S_on would cancel
 // where the list holds nearly all mass, and with one maximum S_off would
 // underflow where the list lies far above the rest, while the loss still
 // holds the logarithm of that mass and the gradient its distribution.  With
 // M = max(M_off, M_on) and S = S_off e^((M_off - M) / T) + S_on e^((M_on - M) / T),
-//   lse_u = M / T + log S,  log Q = M_off / T + log S_off - lse_u
-//   with lse:    loss = B1 + B0 lse_u + P (log P - log Q),  P = 1 - B0
+//   log Q = (M_off - M) / T + log S_off - log S
+//   with lse:    loss = B1 + B0 log S + P (log P - log Q),  P = 1 - B0
 //                off the list dL/du_v = e^(u_v - M_off / T) (e^((M_off - M) / T) / S - P / S_off)
-//   normalised:  loss = B1 / B0 - log B0 + lse_u  (every id counts as off the list in the sums)
+//   normalised:  loss = B1 / B0 - log B0 + log S  (every id counts as off the list in the sums)
 // The softmax stands in the gradient times sum p, which is B0 with lse and one
 // otherwise.  The last term adds P to it, B0 + P = 1; without that term (P <= 0,
 // or nothing off the list) the factor stays, and 1 / S is kept as B0 / S.
 // Every term is a sum over slices of the vocabulary once each slice's
-// maximum is put back, so slices are worked on apart and joined.  Sums over
+// maximum is put back (in B1, too), so slices are worked on apart and joined.  Sums over
 // a thread's logits are binary32, everything joined is binary64, as is the
 // list's side (P = 1 - B0 loses what binary32 would keep of it).  The hardware
 // exponential gives 0 below 2^-126 relative to a maximum.
@@ -200,35 +202,39 @@ __device__ void distill_slice(const DistillArgs& a, int64_t r, int s, uint32_t* 
     }
   }
   // the list's side, now that the slice is in the caches
-  double b0 = 0.0, b1 = 0.0;
-  float m_on = -__builtin_inff(), s_on = 0.0f, on_x[kListPer];
+  double b0 = 0.0, b1 = 0.0, w_list[kListPer];
+  float m_on = -__builtin_inff(), s_on = 0.0f, x_list[kListPer];
 #pragma unroll
   for (int j = 0; j < kListPer; ++j) {
     const uint32_t t = (uint32_t)(id[j] - start);
-    on_x[j] = -__builtin_inff();
+    x_list[j] = -__builtin_inff();
+    w_list[j] = 0.0;
     if (id[j] >= 0 && t < (uint32_t)size) {
-      const float xj = El<DT>::get(x, id[j]);
+      const float xj = x_list[j] = El<DT>::get(x, id[j]);
       if (tail) {
-        on_x[j] = xj;
         m_on = __builtin_fmaxf(m_on, xj);
         flags |= xj != xj ? 1u : xj == __builtin_inff() ? 2u : 0u;
       }
       const double lp = (double)z[j] * a.inv_t - zm;
-      const double w = exp(lp);
+      const double w = w_list[j] = exp(lp);
       if (w > 0.0) {
         b0 += w;
-        b1 += w * (lp - (double)xj * a.inv_t);
+        b1 += w * lp;
       }
     }
   }
   if (m_on > -__builtin_inff()) {
 #pragma unroll
-    for (int j = 0; j < kListPer; ++j) s_on += __builtin_amdgcn_exp2f((on_x[j] - m_on) * c);
+    for (int j = 0; j < kListPer; ++j) s_on += __builtin_amdgcn_exp2f((x_list[j] - m_on) * c);
   }
   const auto larger = [](float p, float q) { return __builtin_fmaxf(p, q); };
   const auto plus = [](double p, double q) { return p + q; };
   const float M_off = group_reduce<kSliceNW>(m, -__builtin_inff(), larger, redf);
   const float M_on = group_reduce<kSliceNW>(m_on, -__builtin_inff(), larger, redf);
+  const double M = (double)__builtin_fmaxf(M_off, M_on);  // (-inf: no listed logit of the slice is finite, b1 is +inf or 0)
+#pragma unroll
+  for (int j = 0; j < kListPer; ++j)
+    if (w_list[j] > 0.0) b1 -= w_list[j] * (x_list[j] == -__builtin_inff() ? -(double)__builtin_inff() : ((double)x_list[j] - M) * a.inv_t);
   flags = group_reduce<kSliceNW>(flags, 0u, [](uint32_t p, uint32_t q) { return p | q; }, redu);
   const double f = m == -__builtin_inff() ? 0.0 : (double)__builtin_amdgcn_exp2f((m - M_off) * c);
   const double g = m_on == -__builtin_inff() ? 0.0 : (double)__builtin_amdgcn_exp2f((m_on - M_on) * c);
@@ -260,7 +266,7 @@ struct DistillRow {  // what the gradient needs of a row
   double loss;
 };
 
-// The loss and the gradient's numbers from a row's sums (a finite maximum, no NaN, no +inf).
+// The loss and the gradient's numbers from a row's sums (a finite maximum, which b1 is relative to, no NaN, no +inf).
 __device__ __forceinline__ void distill_finish(double inv_t, bool tail, float m_off, float m_on, double off, double on,
                                                double b0, double b1, double zm, DistillRow& o) {
   constexpr float kNone = -__builtin_inff();
@@ -269,7 +275,7 @@ __device__ __forceinline__ void distill_finish(double inv_t, bool tail, float m_
   const double e_off = m_off == kNone ? 0.0 : exp(((double)m_off - (double)m) * inv_t);
   const double e_on = m_on == kNone ? 0.0 : exp(((double)m_on - (double)m) * inv_t);
   const double S = off * e_off + on * e_on;  // (the first underflows where the rest is out of sight)
-  const double log_s = log(S), lse_u = (double)m * inv_t + log_s;
+  const double log_s = log(S);
   o.M = m;
   o.M_off = m_off == kNone ? 0.0 : m_off;
   const double P = 1.0 - b0;
@@ -278,7 +284,7 @@ __device__ __forceinline__ void distill_finish(double inv_t, bool tail, float m_
   o.f_off = e_off * o.inv_s;
   if (tail) {
     o.zm = zm;
-    o.loss = b1 + b0 * lse_u;
+    o.loss = b1 + b0 * log_s;
     if (rest) {
       o.loss += P * (log(P) - (((double)m_off - (double)m) * inv_t + log(off) - log_s));
       o.f_off -= P / off;
@@ -286,7 +292,7 @@ __device__ __forceinline__ void distill_finish(double inv_t, bool tail, float m_
   } else {
     const double lz = log(b0);
     o.zm = zm + lz;
-    o.loss = b1 / b0 - lz + lse_u;
+    o.loss = b1 / b0 - lz + log_s;
   }
 }
 
@@ -309,7 +315,10 @@ __device__ __forceinline__ DistillRow distill_join(const DistillArgs& a, int64_t
   // e^((x - y) / T) of two maxima, 0 where x is none
   const auto shift = [&](float x, float y) { return x == kNone ? 0.0 : exp(((double)x - (double)y) * a.inv_t); };
   const double off = wave_sum(p.s_off * shift(p.m_off, m_off)), on = wave_sum(p.s_on * shift(p.m_on, m_on));
-  const double b0 = wave_sum(p.b0), b1 = wave_sum(p.b1);
+  // a slice's maximum put back in b1, to which it adds: no difference of large numbers
+  const float m_own = __builtin_fmaxf(p.m_off, p.m_on);
+  const double lower = m_own == kNone ? 0.0 : ((double)m - (double)m_own) * a.inv_t;
+  const double b0 = wave_sum(p.b0), b1 = wave_sum(p.b1 + p.b0 * lower);
   distill_finish(a.inv_t, a.lse != nullptr, m_off, m_on, off, on, b0, b1, a.part[r * a.slices].zm, o);
   return o;
 }
@@ -533,15 +542,14 @@ __global__ void __launch_bounds__(64 * NWV, NWV == 4 ? 6 : 8) distill_row_kernel
     // the list's side, now that the row is in the caches
     const double zm = tail ? (double)a.lse[r] : (double)group_reduce<NWV>(zmax, kNone, larger, redf) * a.inv_t;
     double b0 = 0.0, b1 = 0.0;
-    float m_on = kNone, s_on = 0.0f, on_x[PER];
+    float m_on = kNone, s_on = 0.0f, x_list[PER];
 #pragma unroll
     for (int j = 0; j < PER; ++j) {
-      on_x[j] = kNone;
+      x_list[j] = kNone;
       w_list[j] = 0.0;
       if (id[j] >= 0) {
-        const float xj = El<DT>::get(x, id[j]);
+        const float xj = x_list[j] = El<DT>::get(x, id[j]);
         if (tail) {
-          on_x[j] = xj;
           m_on = __builtin_fmaxf(m_on, xj);
           flags |= xj != xj ? 1u : xj == __builtin_inff() ? 2u : 0u;
         }
@@ -549,13 +557,13 @@ __global__ void __launch_bounds__(64 * NWV, NWV == 4 ? 6 : 8) distill_row_kernel
         const double w = w_list[j] = exp(lp);
         if (w > 0.0) {
           b0 += w;
-          b1 += w * (lp - (double)xj * a.inv_t);
+          b1 += w * lp;
         }
       }
     }
     if (m_on > kNone) {
 #pragma unroll
-      for (int j = 0; j < PER; ++j) s_on += __builtin_amdgcn_exp2f((on_x[j] - m_on) * c);
+      for (int j = 0; j < PER; ++j) s_on += __builtin_amdgcn_exp2f((x_list[j] - m_on) * c);
     }
     // two meetings of the waves: the maxima, which all need, then the sums, which one wave joins
     m_wave[0][wave_id()] = wave_reduce(m, kNone, larger);
@@ -567,6 +575,10 @@ __global__ void __launch_bounds__(64 * NWV, NWV == 4 ? 6 : 8) distill_row_kernel
       M_off = __builtin_fmaxf(M_off, m_wave[0][w]);
       M_on = __builtin_fmaxf(M_on, m_wave[1][w]);
     }
+    const double M = (double)__builtin_fmaxf(M_off, M_on);
+#pragma unroll
+    for (int j = 0; j < PER; ++j)
+      if (w_list[j] > 0.0) b1 -= w_list[j] * (((double)x_list[j] - M) * a.inv_t);
     const double f = m == kNone ? 0.0 : (double)__builtin_amdgcn_exp2f((m - M_off) * c);
     const double h = m_on == kNone ? 0.0 : (double)__builtin_amdgcn_exp2f((m_on - M_on) * c);
     const double w_off = wave_sum((double)s_off * f), w_on = wave_sum((double)s_on * h);
