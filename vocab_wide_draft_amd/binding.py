@@ -514,6 +514,13 @@ def _out_rows(out, like, dtype):
     return out
 
 
+def _written(out):
+    """Rows of the caller that the library has written count as written in place: torch refuses a backward pass that
+    saved them."""
+    if out is not None:
+        torch.autograd.graph.increment_version(out)
+
+
 # the current stream's handle, without a torch.cuda.Stream around it where torch offers that (2 us less per call)
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
     (lambda index: torch.cuda.current_stream(index).cuda_stream)
@@ -583,6 +590,7 @@ def shape_logits(rows: torch.Tensor, rows_per_request: int = 1, *, history=None,
     st = _i32(n, dev)
     _call(dev, lib.dspark_shape_logits, ctypes.byref(r), ctypes.byref(how), o.data_ptr(),
           DTYPE_F32 if o.dtype == torch.float32 else DTYPE_BF16, o.stride(0), st.data_ptr())
+    _written(out)
     return {"logits": o, "status": st}
 
 
@@ -660,6 +668,7 @@ def distill_backward(student: torch.Tensor, teacher, forward, grad_loss: torch.T
           _arg(forward["stats"], "stats", torch.float64, (n, DISTILL_STATS), dev),
           _arg(forward["status"], "status", torch.int32, (n,), dev),
           _arg(grad_loss, "grad_loss", torch.float32, (n,), dev), g.data_ptr(), g.stride(0))
+    _written(out)
     return g
 
 
@@ -676,6 +685,7 @@ def distill_step(student: torch.Tensor, teacher, weight: torch.Tensor, temperatu
     ws, nbytes = _distill_ws(lib.dspark_distill_workspace(n, V), dev)
     _call(dev, lib.dspark_distill_step, ctypes.byref(r), ctypes.byref(t), float(temperature), w, loss.data_ptr(),
           g.data_ptr(), g.stride(0), st.data_ptr(), ws.data_ptr() if nbytes else None, nbytes)
+    _written(out)
     return {"loss": loss, "grad": g, "status": st}
 
 
