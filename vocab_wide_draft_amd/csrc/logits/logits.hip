@@ -102,7 +102,7 @@ TopPlan top_plan(int64_t n, int64_t V, int64_t k_max) {
   TopPlan p{};
   if (V <= kTopSmall && (n < 512 || V <= 4096)) return p;
   const double mu = (double)std::max<int64_t>(std::min(k_max, V), 1) * kTopSample / (double)V;  // < 128 above kTopSmall
-  p.rank = (int)std::ceil(mu + 4.0 * std::sqrt(mu) + 4.0);                                      // < 178 there
+  p.rank = (int)std::ceil(mu + 4.0 * std::sqrt(mu) + 4.0);                                      // <= 178 there
   if (V <= kTopSmall && p.rank > 200) return p;
   // logits of the sample above the rank-th of its 256 maxima, and so of a slice and of the row
   const double above = -std::log(1.0 - p.rank / 256.0) * 256.0;
@@ -110,7 +110,12 @@ TopPlan top_plan(int64_t n, int64_t V, int64_t k_max) {
   // room for more than twice the candidates expected (one row in 1,280 that
   // has to be selected from memory costs more than the selection of all), in
   // workgroups as small as that allows (1,280 bf16 rows, k = 256: 12.3 us in
-  // 256 threads of eleven candidates, 15.6 in 512 of eight)
+  // 256 threads of eleven candidates, 15.6 in 512 of eight).  Not so for the
+  // longest rows: a sample of 2,048 of 524,288 ids leaves room for 1.9 times as
+  // many at k = 1,024, of 1,048,576 ids for 2.0 times (k = 256) to 1.3 (1,024),
+  // and 0.3, 1 and 13 % of rows of normal logits pass it.  They are selected
+  // from memory (64 rows of 1,048,576 ids, call: bf16 43 us where none is, k =
+  // 64, and 790 where some are, k = 256 to 1,024; float32 1,100 to 1,220).
   p.most = row * 2.2 <= 2048 ? 2048 : row * 2.2 <= 2816 ? 2816 : row * 2.2 <= 5632 ? 5632 : 8192;
   p.slices = (int)((V + kTopSlice - 1) / kTopSlice);
   p.cap = (int)std::min<double>(kTopSlice, std::ceil((3.0 * above * kTopSlice / kTopSample + 64.0) / 64.0) * 64.0);
