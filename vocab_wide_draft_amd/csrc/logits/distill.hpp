@@ -196,7 +196,7 @@ __device__ void distill_slice(const DistillArgs& a, int64_t r, int s, uint32_t* 
   if (s_off != s_off || m == __builtin_inff()) {
     for (int t = threadIdx.x * N; t < size; t += kSliceBS * N) {
       float v[N];
-      load_vec<DT, N, false>(x, start + t, V, v);
+      load_vec<DT, N>(x, start + t, V, v);
 #pragma unroll
       for (int l = 0; l < N; ++l) flags |= v[l] != v[l] ? 1u : v[l] == __builtin_inff() ? 2u : 0u;
     }
@@ -534,7 +534,7 @@ __global__ void __launch_bounds__(64 * NWV, NWV == 4 ? 6 : 8) distill_row_kernel
     if (s_off != s_off || m == __builtin_inff()) {  // a NaN or +inf: which, the logits tell
       for (int t = tid * N; t < V; t += T * N) {
         float v[N];
-        load_vec<DT, N, false>(x, t, V, v);
+        load_vec<DT, N>(x, t, V, v);
 #pragma unroll
         for (int l = 0; l < N; ++l) flags |= v[l] != v[l] ? 1u : v[l] == __builtin_inff() ? 2u : 0u;
       }

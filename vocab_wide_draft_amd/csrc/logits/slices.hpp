@@ -58,41 +58,30 @@ struct El<DSPARK_F32> {
 };
 
 // N neighbouring logits of a row, from id v on (v a multiple of N), as one
-// load of a thread: N = 8 or 4 of bf16, 4 of float32, so that the lanes of a
+// load of a thread: N = 8 of bf16, 4 of float32, so that the lanes of a
 // wave read one unbroken stretch.  (Two loads of 16 bytes at a stride of 32,
 // eight float32 per thread, fetch every line twice when they are streamed.)
-// NT: streamed, not read again soon.
-template <int DT, int N, bool NT>
+template <int DT, int N>
 __device__ __forceinline__ void load_whole(const typename El<DT>::T* row, int v, float (&x)[N]) {
-  static_assert(N == 4 || (N == 8 && DT == DSPARK_BF16), "one load of at most 16 bytes");
+  static_assert(N == (DT == DSPARK_BF16 ? 8 : 4), "one load of 16 bytes");
   if constexpr (DT == DSPARK_F32) {
-    const v4f* p = reinterpret_cast<const v4f*>(row + v);
-    const v4f a = NT ? __builtin_nontemporal_load(p) : *p;
+    const v4f a = *reinterpret_cast<const v4f*>(row + v);
 #pragma unroll
     for (int i = 0; i < 4; ++i) x[i] = a[i];
-  } else if constexpr (N == 8) {
-    const v4u* p = reinterpret_cast<const v4u*>(row + v);
-    const v4u u = NT ? __builtin_nontemporal_load(p) : *p;
+  } else {
+    const v4u u = *reinterpret_cast<const v4u*>(row + v);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      x[2 * i] = bf16_lo(u[i]);
-      x[2 * i + 1] = bf16_hi(u[i]);
-    }
-  } else {
-    const v2u* p = reinterpret_cast<const v2u*>(row + v);
-    const v2u u = NT ? __builtin_nontemporal_load(p) : *p;
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
       x[2 * i] = bf16_lo(u[i]);
       x[2 * i + 1] = bf16_hi(u[i]);
     }
   }
 }
 // the same at the end of a row: ids past V read as -inf and touch no memory
-template <int DT, int N, bool NT>
+template <int DT, int N>
 __device__ __forceinline__ void load_vec(const typename El<DT>::T* row, int v, int V, float (&x)[N]) {
   if (v + N <= V) {
-    load_whole<DT, N, NT>(row, v, x);
+    load_whole<DT, N>(row, v, x);
   } else {
 #pragma unroll
     for (int l = 0; l < N; ++l) x[l] = v + l < V ? El<DT>::get(row, v + l) : -__builtin_inff();
@@ -101,18 +90,15 @@ __device__ __forceinline__ void load_vec(const typename El<DT>::T* row, int v, i
 
 template <int DT, int N>
 __device__ __forceinline__ void store_vec(typename El<DT>::T* row, int v, int V, const float (&x)[N]) {
-  static_assert(N == 4 || (N == 8 && DT == DSPARK_BF16), "one store of at most 16 bytes");
+  static_assert(N == (DT == DSPARK_BF16 ? 8 : 4), "one store of 16 bytes");
   char* at = reinterpret_cast<char*>(row) + (uint32_t)v * (uint32_t)sizeof(*row);
   if (v + N <= V) {
     if constexpr (DT == DSPARK_F32) {
       const v4f a = {x[0], x[1], x[2], x[3]};
       __builtin_nontemporal_store(a, reinterpret_cast<v4f*>(at));
-    } else if constexpr (N == 8) {
+    } else {
       const v4u u = {bf16_pair(x[0], x[1]), bf16_pair(x[2], x[3]), bf16_pair(x[4], x[5]), bf16_pair(x[6], x[7])};
       __builtin_nontemporal_store(u, reinterpret_cast<v4u*>(at));
-    } else {
-      const v2u u = {bf16_pair(x[0], x[1]), bf16_pair(x[2], x[3])};
-      __builtin_nontemporal_store(u, reinterpret_cast<v2u*>(at));
     }
   } else {
 #pragma unroll
@@ -121,8 +107,9 @@ __device__ __forceinline__ void store_vec(typename El<DT>::T* row, int v, int V,
   }
 }
 
-// A vector as it is loaded, to be unpacked where it is used: a load that is
-// to stay in flight must not be touched before.
+// A vector as it is loaded (4 of bf16, too), to be unpacked where it is used:
+// a load that is to stay in flight must not be touched before.  NT: streamed,
+// not read again soon.
 template <int DT, int N>
 struct Raw {
   uint32_t w[DT == DSPARK_F32 ? N : N / 2];

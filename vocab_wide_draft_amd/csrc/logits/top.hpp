@@ -245,7 +245,7 @@ __device__ __forceinline__ int top_from_memory(const TopArgs& a, int64_t r, int 
     __syncthreads();
     for (int v = (int)threadIdx.x * N; v < V; v += kStep) {
       float x[N];
-      load_vec<DT, N, false>(row, v, V, x);
+      load_vec<DT, N>(row, v, V, x);
 #pragma unroll
       for (int l = 0; l < N; ++l) {
         const uint32_t key = top_key<DT>(x[l]);
@@ -281,7 +281,7 @@ __device__ __forceinline__ int top_from_memory(const TopArgs& a, int64_t r, int 
   for (int base = 0; base < V; base += kStep) {
     const int v = base + (int)threadIdx.x * N;
     float x[N];
-    if (v < V) load_vec<DT, N, false>(row, v, V, x);
+    if (v < V) load_vec<DT, N>(row, v, V, x);
     uint32_t cnt = 0, total;
 #pragma unroll
     for (int l = 0; l < N; ++l) {
@@ -332,7 +332,7 @@ __global__ void __launch_bounds__(64 * NWV) top_small_kernel(TopArgs a) {
 #pragma unroll
   for (int g = 0; g < 8 * G / N; ++g) {
     float y[N];
-    load_vec<DT, N, false>(row, v0 + N * g, a.V, y);
+    load_vec<DT, N>(row, v0 + N * g, a.V, y);
 #pragma unroll
     for (int l = 0; l < N; ++l) {
       x[N * g + l] = y[l];
@@ -442,7 +442,7 @@ __global__ void __launch_bounds__(kSliceBS) top_slice_kernel(TopSliceArgs q) {
 #pragma unroll
   for (int i = 0; i < 8 / N; ++i) {
     float y[N];
-    load_whole<DT, N, false>(row, (tid >> 2) * run + (i * 4 + (tid & 3)) * N, y);
+    load_whole<DT, N>(row, (tid >> 2) * run + (i * 4 + (tid & 3)) * N, y);
 #pragma unroll
     for (int l = 0; l < N; ++l) smp[i * N + l] = y[l];
   }
