@@ -126,7 +126,7 @@ __device__ void distill_slice(const DistillArgs& a, int64_t r, int s, uint32_t* 
     len = 0;
   }
   const bool tail = a.lse != nullptr;
-  IdSet on{lds, lds + words};
+  IdSet on{lds, nullptr};  // (members alone are asked for)
   if (len > 0 && tail) on.clear(words);
   // the list: which entries are ours, and (slice 0) whether it may be used
   int32_t id[kListPer];

@@ -296,12 +296,14 @@ DistillArgs distill_args(const dspark_rows* student, const dspark_teacher* t, fl
   return a;
 }
 
-size_t distill_lds(const DistillArgs& a) { return 2u * 4u * ((size_t)a.slice / 32); }
+// A slice's set of ids: its bits, and for the gradient the words' first entries.
+size_t distill_lds(const DistillArgs& a, bool entries) { return (entries ? 2u : 1u) * 4u * ((size_t)a.slice / 32); }
 
 void launch_part(const DistillArgs& a, int dtype, hipStream_t s) {
   const dim3 grid = row_slice_grid(a.n, a.slices);
-  if (dtype == DSPARK_BF16) hipLaunchKernelGGL(distill_part_kernel<DSPARK_BF16>, grid, dim3(kSliceBS), distill_lds(a), s, a);
-  else hipLaunchKernelGGL(distill_part_kernel<DSPARK_F32>, grid, dim3(kSliceBS), distill_lds(a), s, a);
+  const size_t lds = distill_lds(a, false);
+  if (dtype == DSPARK_BF16) hipLaunchKernelGGL(distill_part_kernel<DSPARK_BF16>, grid, dim3(kSliceBS), lds, s, a);
+  else hipLaunchKernelGGL(distill_part_kernel<DSPARK_F32>, grid, dim3(kSliceBS), lds, s, a);
 }
 // Whether each row gets one workgroup: short rows (one launch instead of two:
 // 4,096 rows of 20,003 ids in bf16, loss and gradient, 84 us against 97 in
@@ -346,10 +348,11 @@ void launch_rows(const DistillArgs& a, int dtype, hipStream_t s) {
 template <bool FROM_STATS>
 void launch_grad(const DistillArgs& a, int dtype, hipStream_t s) {
   const dim3 grid = row_slice_grid(a.n, a.slices);
+  const size_t lds = distill_lds(a, true);
   if (dtype == DSPARK_BF16)
-    hipLaunchKernelGGL(HIP_KERNEL_NAME(distill_grad_kernel<DSPARK_BF16, FROM_STATS>), grid, dim3(kSliceBS), distill_lds(a), s, a);
+    hipLaunchKernelGGL(HIP_KERNEL_NAME(distill_grad_kernel<DSPARK_BF16, FROM_STATS>), grid, dim3(kSliceBS), lds, s, a);
   else
-    hipLaunchKernelGGL(HIP_KERNEL_NAME(distill_grad_kernel<DSPARK_F32, FROM_STATS>), grid, dim3(kSliceBS), distill_lds(a), s, a);
+    hipLaunchKernelGGL(HIP_KERNEL_NAME(distill_grad_kernel<DSPARK_F32, FROM_STATS>), grid, dim3(kSliceBS), lds, s, a);
 }
 
 }  // namespace
