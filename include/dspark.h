@@ -409,7 +409,9 @@ typedef struct {
  *   z = z - frequency c_v - presence [c_v > 0];
  *   z = (z + bias_v) / temperature;
  *   z = -inf where the row's mask does not allow v, whatever x is.
- * Computed in binary32 and rounded once to out_dtype (the rows' own type, or
+ * Computed in binary32, both quotients as products with the reciprocal of the
+ * factor (rounded once itself, so each may be off by a rounding more than a
+ * quotient is), and rounded once to out_dtype (the rows' own type, or
  * DSPARK_F32 for bf16 rows).  out: rows of vocab values, out_stride elements
  * apart, 16-byte aligned like the input rows; either the input itself (same
  * type and stride: in place) or memory apart from it.  What lies between
@@ -443,7 +445,12 @@ size_t dspark_top_logits_workspace(int64_t n_rows, int64_t vocab, int32_t k_max)
  * <= k_max <= DSPARK_K_MAX) by strictly ascending id with finite logits, as
  * dspark_top_logits writes them.  lse: log sum_v exp(z_v / temperature) of
  * the teacher's whole row at the loss's temperature, or NULL to renormalise
- * the teacher over the list. */
+ * the teacher over the list.  As lse is binary32, the listed probabilities are
+ * off by up to |lse| 2^-24 of themselves, and what they leave of one by as much:
+ * a tail below that (1e-6 at lse = 17; anything at temperatures that take lse
+ * past 2^24) is rounding, and so are the last term of the loss and its gradient
+ * off the list where the student's tail is as small.  Such teachers are better
+ * renormalised. */
 typedef struct {
   const int32_t* ids;
   const float* logits;

@@ -467,6 +467,10 @@ def sharded_q(rows: torch.Tensor, n_shards: int, topk=None, k_max: int = 0, draw
 
 # ---- operators on logit rows: shaping, a teacher's top logits, distillation.
 # Their work runs on the rows' device and on that device's current stream.
+# Rows that they read or write start 16-byte aligned, as everywhere in the
+# library: a contiguous [n, V] tensor has such rows where V is a multiple of 8
+# (bf16) or 4 (float32); for other V, rows are the first V columns of a wider
+# tensor, and unaligned ones are refused (DsparkError).
 
 
 def _arg(t, name, dtype, shape, dev):
@@ -731,7 +735,9 @@ class _DistillLoss(torch.autograd.Function):
 
 def distill_loss(student: torch.Tensor, teacher, temperature: float = 1.0) -> torch.Tensor:
     """distill's loss (float32 [n]) as a differentiable function of the
-    student rows.  The teacher is constant: its logits must not require a
+    student rows, which start 16-byte aligned (other V than multiples of 8 in
+    bf16, 4 in float32: the first V columns of a wider tensor).  The teacher is
+    constant: its logits must not require a
     gradient.  Rows that the call refuses have loss 0 and gradient 0.  It may be
     captured into a graph with its backward pass, while no eager graph of the
     same leaves is alive."""
