@@ -475,7 +475,8 @@ typedef struct {
  * is not read.  A student's -inf at a token with p > 0 gives loss +inf.
  * loss: float[n_rows].  stats: double[n_rows][DSPARK_DISTILL_STATS], what
  * the backward call takes (opaque).  row_status[r]: OK, Q_BAD_LEN, Q_BAD_ID,
- * Q_UNSORTED, Q_NONFINITE (a listed logit or lse that is not finite) for the
+ * Q_UNSORTED, Q_NONFINITE (a listed logit or lse that is not finite, or, with
+ * lse, listed probabilities whose sum passes binary32) for the
  * teacher's list (the smallest), then ROW_NAN, ROW_POSINF or ROW_ZERO_MASS for
  * the student's row; a refused row has loss 0 and gradient 0.
  * ws: dspark_distill_workspace() bytes, 16-byte aligned (NULL where it is 0);

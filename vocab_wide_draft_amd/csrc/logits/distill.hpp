@@ -266,6 +266,16 @@ struct DistillRow {  // what the gradient needs of a row
   double loss;
 };
 
+// Status of a good list's row from its sums and flags.  With lse, listed
+// probabilities that sum to more than binary32 holds are the list's fault: lse
+// far too small, as its 24 bits may make it at low temperatures.
+__device__ __forceinline__ int distill_status(bool tail, double b0, uint32_t flags, float m) {
+  return tail && !(b0 <= (double)3.40282347e38f) ? DSPARK_ST_Q_NONFINITE
+         : flags & 1u ? DSPARK_ST_ROW_NAN
+         : flags & 2u ? DSPARK_ST_ROW_POSINF
+         : m == -__builtin_inff() ? DSPARK_ST_ROW_ZERO_MASS : DSPARK_ST_OK;
+}
+
 // The loss and the gradient's numbers from a row's sums (a finite maximum, which b1 is relative to, no NaN, no +inf).
 __device__ __forceinline__ void distill_finish(double inv_t, bool tail, float m_off, float m_on, double off, double on,
                                                double b0, double b1, double zm, DistillRow& o) {
@@ -308,9 +318,8 @@ __device__ __forceinline__ DistillRow distill_join(const DistillArgs& a, int64_t
   const uint32_t flags = wave_reduce((uint32_t)p.flags, 0u, [](uint32_t x, uint32_t y) { return x | y; });
   const float m_off = wave_reduce(p.m_off, kNone, larger), m_on = wave_reduce(p.m_on, kNone, larger);
   const float m = __builtin_fmaxf(m_off, m_on);
-  if (flags & 1u) o.status = DSPARK_ST_ROW_NAN;
-  else if (flags & 2u) o.status = DSPARK_ST_ROW_POSINF;
-  else if (m == kNone) o.status = DSPARK_ST_ROW_ZERO_MASS;
+  const double b0 = wave_sum(p.b0);
+  o.status = distill_status(a.lse != nullptr, b0, flags, m);
   if (o.status != DSPARK_ST_OK) return o;
   // e^((x - y) / T) of two maxima, 0 where x is none
   const auto shift = [&](float x, float y) { return x == kNone ? 0.0 : exp(((double)x - (double)y) * a.inv_t); };
@@ -318,7 +327,7 @@ __device__ __forceinline__ DistillRow distill_join(const DistillArgs& a, int64_t
   // a slice's maximum put back in b1, to which it adds: no difference of large numbers
   const float m_own = __builtin_fmaxf(p.m_off, p.m_on);
   const double lower = m_own == kNone ? 0.0 : ((double)m - (double)m_own) * a.inv_t;
-  const double b0 = wave_sum(p.b0), b1 = wave_sum(p.b1 + p.b0 * lower);
+  const double b1 = wave_sum(p.b1 + p.b0 * lower);
   distill_finish(a.inv_t, a.lse != nullptr, m_off, m_on, off, on, b0, b1, a.part[r * a.slices].zm, o);
   return o;
 }
@@ -602,9 +611,7 @@ __global__ void __launch_bounds__(64 * NWV, NWV == 4 ? 6 : 8) distill_row_kernel
       flags = wave_reduce(lane_id() < NWV ? redu[lane_id()] : 0u, 0u, either);
       if (tid == 0) {
         DistillRow o{};
-        o.status = flags & 1u ? DSPARK_ST_ROW_NAN
-                   : flags & 2u ? DSPARK_ST_ROW_POSINF
-                   : M_off == kNone && M_on == kNone ? DSPARK_ST_ROW_ZERO_MASS : DSPARK_ST_OK;
+        o.status = distill_status(tail, t0, flags, __builtin_fmaxf(M_off, M_on));
         if (o.status == DSPARK_ST_OK) distill_finish(a.inv_t, tail, M_off, M_on, off, sum_on, t0, t1, zm, o);
         sh = o;
       }
