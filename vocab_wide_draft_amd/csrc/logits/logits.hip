@@ -77,7 +77,10 @@ void launch_shape_as(ShapeArgs a, hipStream_t s) {
 // is as fast or faster (float32, 6 rows: 1,139 / 1,104 us, 1 row 204 / 255).
 // So is it where the requests leave CUs idle and the history is long, which
 // 512 threads scan in half the steps (histories of up to 32,768 tokens, 6
-// bf16 rows each: 16 requests 28.0 / 23.5 us, 4 23.7 / 17.6; 64 63.7 / 68.9).
+// bf16 rows each: 16 requests 28.0 / 23.5 us, 4 23.7 / 17.6; 64 63.7 / 68.9;
+// 24 32.5 / 31.3, where the rounds fit 48 55 / 52 as well and 32 36 / 42).
+// bf16 rows with float32 results: 1,024 requests of 6 rows 876 / 868, 64 of 6
+// 63.5 / 62.5, but 1,024 of 3 431 / 453, of 2 302 / 345, of 1 217 / 266.
 template <int TI, int TO>
 void launch_shape(const ShapeArgs& a, hipStream_t s) {
   if (a.V <= 2048) launch_shape_as<TI, TO, 4, 1, 2>(a, s);
@@ -333,8 +336,11 @@ void launch_rows_waves(const DistillArgs& a, int dtype, hipStream_t s) {
 // 170 / 153 us, 5,120 561 / 550, 1,280 float32 335 / 295, 256 63 / 63; 40,000
 // bf16 ids, 80 KB, 5,120 rows 175 / 200).  The chip holds 512 such rows: the
 // second round of somewhat more leaves CUs idle, unless the rows are long
-// enough to keep HBM busy all the same (640 bf16 rows of 129,280 ids 84 / 89
-// us, float32 171 / 161, of 65,536 80 / 79).
+// enough to keep HBM busy all the same (V = 129,280, 8 / 16 waves: bf16 512
+// rows 65 / 63 us, 520 76 / 79, 576 79 / 85, 640 84 / 90, 704 89 / 90, 768 96 /
+// 95, 800 113 / 103; float32 520 151 / 144, 640 167 / 162, 768 197 / 183; 65,536
+// float32 ids 640 79 / 82, 768 95 / 90, 800 105 / 98).  A third round does not
+// turn it again: 1,030 bf16 rows 141 / 126, 1,100 149 / 136.
 bool rows_by_16(const DistillArgs& a, int dtype) {
   const int64_t bytes = (int64_t)a.V * (dtype == DSPARK_BF16 ? 2 : 4);
   return bytes >= 128 << 10 && (a.n <= 512 || a.n > 768 || bytes >= 384 << 10);
