@@ -202,27 +202,35 @@ __device__ void distill_slice(const DistillArgs& a, int64_t r, int s, uint32_t* 
     }
   }
   // the list's side, now that the slice is in the caches
-  double b0 = 0.0, b1 = 0.0, w_list[kListPer];
-  float m_on = -__builtin_inff(), s_on = 0.0f, x_list[kListPer];
+  double b0 = 0.0, b1 = 0.0;
+  float m_own = -__builtin_inff(), s_on = 0.0f, x_list[kListPer];
 #pragma unroll
   for (int j = 0; j < kListPer; ++j) {
     const uint32_t t = (uint32_t)(id[j] - start);
     x_list[j] = -__builtin_inff();
-    w_list[j] = 0.0;
     if (id[j] >= 0 && t < (uint32_t)size) {
       const float xj = x_list[j] = El<DT>::get(x, id[j]);
-      if (tail) {
-        m_on = __builtin_fmaxf(m_on, xj);
-        flags |= xj != xj ? 1u : xj == __builtin_inff() ? 2u : 0u;
-      }
+      m_own = __builtin_fmaxf(m_own, xj);
+      if (tail) flags |= xj != xj ? 1u : xj == __builtin_inff() ? 2u : 0u;
+    } else {
+      id[j] = -1;
+    }
+  }
+  // b1 from this thread's largest listed logit first: once the slice's maximum
+  // is known, one addition puts it back
+  const double ref = m_own == -__builtin_inff() ? 0.0 : (double)m_own;
+#pragma unroll
+  for (int j = 0; j < kListPer; ++j) {
+    if (id[j] >= 0) {
       const double lp = (double)z[j] * a.inv_t - zm;
-      const double w = w_list[j] = exp(lp);
+      const double w = exp(lp);
       if (w > 0.0) {
         b0 += w;
-        b1 += w * lp;
+        b1 += w * (lp - ((double)x_list[j] - ref) * a.inv_t);
       }
     }
   }
+  const float m_on = tail ? m_own : -__builtin_inff();
   if (m_on > -__builtin_inff()) {
 #pragma unroll
     for (int j = 0; j < kListPer; ++j) s_on += __builtin_amdgcn_exp2f((x_list[j] - m_on) * c);
@@ -231,10 +239,8 @@ __device__ void distill_slice(const DistillArgs& a, int64_t r, int s, uint32_t* 
   const auto plus = [](double p, double q) { return p + q; };
   const float M_off = group_reduce<kSliceNW>(m, -__builtin_inff(), larger, redf);
   const float M_on = group_reduce<kSliceNW>(m_on, -__builtin_inff(), larger, redf);
-  const double M = (double)__builtin_fmaxf(M_off, M_on);  // (-inf: no listed logit of the slice is finite, b1 is +inf or 0)
-#pragma unroll
-  for (int j = 0; j < kListPer; ++j)
-    if (w_list[j] > 0.0) b1 -= w_list[j] * (x_list[j] == -__builtin_inff() ? -(double)__builtin_inff() : ((double)x_list[j] - M) * a.inv_t);
+  const float M = __builtin_fmaxf(M_off, M_on);
+  if (b0 > 0.0 && M > -__builtin_inff()) b1 += b0 * (((double)M - ref) * a.inv_t);  // (without a finite logit b1 is +inf)
   flags = group_reduce<kSliceNW>(flags, 0u, [](uint32_t p, uint32_t q) { return p | q; }, redu);
   const double f = m == -__builtin_inff() ? 0.0 : (double)__builtin_amdgcn_exp2f((m - M_off) * c);
   const double g = m_on == -__builtin_inff() ? 0.0 : (double)__builtin_amdgcn_exp2f((m_on - M_on) * c);
@@ -551,25 +557,30 @@ __global__ void __launch_bounds__(64 * NWV, NWV == 4 ? 6 : 8) distill_row_kernel
     // the list's side, now that the row is in the caches
     const double zm = tail ? (double)a.lse[r] : (double)group_reduce<NWV>(zmax, kNone, larger, redf) * a.inv_t;
     double b0 = 0.0, b1 = 0.0;
-    float m_on = kNone, s_on = 0.0f, x_list[PER];
+    float m_own = kNone, s_on = 0.0f, x_list[PER];
 #pragma unroll
     for (int j = 0; j < PER; ++j) {
       x_list[j] = kNone;
-      w_list[j] = 0.0;
       if (id[j] >= 0) {
         const float xj = x_list[j] = El<DT>::get(x, id[j]);
-        if (tail) {
-          m_on = __builtin_fmaxf(m_on, xj);
-          flags |= xj != xj ? 1u : xj == __builtin_inff() ? 2u : 0u;
-        }
+        m_own = __builtin_fmaxf(m_own, xj);
+        if (tail) flags |= xj != xj ? 1u : xj == __builtin_inff() ? 2u : 0u;
+      }
+    }
+    const double ref = m_own == kNone ? 0.0 : (double)m_own;  // (as in a slice)
+#pragma unroll
+    for (int j = 0; j < PER; ++j) {
+      w_list[j] = 0.0;
+      if (id[j] >= 0) {
         const double lp = (double)z[j] * a.inv_t - zm;
         const double w = w_list[j] = exp(lp);
         if (w > 0.0) {
           b0 += w;
-          b1 += w * lp;
+          b1 += w * (lp - ((double)x_list[j] - ref) * a.inv_t);
         }
       }
     }
+    const float m_on = tail ? m_own : kNone;
     if (m_on > kNone) {
 #pragma unroll
       for (int j = 0; j < PER; ++j) s_on += __builtin_amdgcn_exp2f((x_list[j] - m_on) * c);
@@ -584,10 +595,7 @@ __global__ void __launch_bounds__(64 * NWV, NWV == 4 ? 6 : 8) distill_row_kernel
       M_off = __builtin_fmaxf(M_off, m_wave[0][w]);
       M_on = __builtin_fmaxf(M_on, m_wave[1][w]);
     }
-    const double M = (double)__builtin_fmaxf(M_off, M_on);
-#pragma unroll
-    for (int j = 0; j < PER; ++j)
-      if (w_list[j] > 0.0) b1 -= w_list[j] * (((double)x_list[j] - M) * a.inv_t);
+    if (b0 > 0.0) b1 += b0 * (((double)__builtin_fmaxf(M_off, M_on) - ref) * a.inv_t);
     const double f = m == kNone ? 0.0 : (double)__builtin_amdgcn_exp2f((m - M_off) * c);
     const double h = m_on == kNone ? 0.0 : (double)__builtin_amdgcn_exp2f((m_on - M_on) * c);
     const double w_off = wave_sum((double)s_off * f), w_on = wave_sum((double)s_on * h);
