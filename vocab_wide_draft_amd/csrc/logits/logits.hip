@@ -71,7 +71,7 @@ void launch_shape_as(ShapeArgs a, hipStream_t s) {
                      dim3(64 * NWV), 0, s, a);
 }
 // What keeps enough loads on their way: two eights of logits per thread and
-// two rows ahead (V = 129,280, 1,024 requests, bf16: 6 rows each 564 us against
+// two rows ahead (side by side, V = 129,280, 1,024 requests, bf16: 6 rows each 564 us against
 // 631 with one eight, three rows ahead and 512 threads, 1 row 196 / 266).
 // float32 results need more registers, and with three rows or more the other
 // is as fast or faster (float32, 6 rows: 1,139 / 1,104 us, 1 row 204 / 255).

@@ -14,7 +14,7 @@
 // owner's registers between rows.  Every slice scans the whole history, so
 // slices are not narrow (4,096 ids), and what is read from memory is asked
 // for early: up to three rows ahead, the first rows and the first of the
-// history before anything else.  6,144 bf16 rows with everything take 573 us
+// history before anything else.  6,144 bf16 rows with everything take 576 us
 // (5.6 TB/s of what they read and write), their temperature alone 530.
 #pragma once
 #include "slices.hpp"
