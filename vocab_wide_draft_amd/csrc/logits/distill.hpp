@@ -7,11 +7,12 @@
 // renormalised), B0 = sum w_j and B1 = sum w_j (z_j / T - zm - (u_j - M / T)),
 // M the row's maximum: a row far from zero, such as one that a mask has left
 // at its type's lowest value, would lose its loss in the difference of two
-// sums of the logits themselves.  The two sides are kept apart, each with its own maximum: S - S_on would cancel
-// where the list holds nearly all mass, and with one maximum S_off would
-// underflow where the list lies far above the rest, while the loss still
-// holds the logarithm of that mass and the gradient its distribution.  With
-// M = max(M_off, M_on) and S = S_off e^((M_off - M) / T) + S_on e^((M_on - M) / T),
+// sums of the logits themselves.  The two sides are kept apart, each with its
+// own maximum: S - S_on would cancel where the list holds nearly all mass, and
+// with one maximum S_off would underflow where the list lies far above the
+// rest, while the loss still holds the logarithm of that mass and the gradient
+// its distribution.  With M = max(M_off, M_on) and
+// S = S_off e^((M_off - M) / T) + S_on e^((M_on - M) / T),
 //   log Q = (M_off - M) / T + log S_off - log S
 //   with lse:    loss = B1 + B0 log S + P (log P - log Q),  P = 1 - B0
 //                off the list dL/du_v = e^(u_v - M_off / T) (e^((M_off - M) / T) / S - P / S_off)
@@ -19,9 +20,9 @@
 // The softmax stands in the gradient times sum p, which is B0 with lse and one
 // otherwise.  The last term adds P to it, B0 + P = 1; without that term (P <= 0,
 // or nothing off the list) the factor stays, and 1 / S is kept as B0 / S.
-// Every term is a sum over slices of the vocabulary once each slice's
-// maximum is put back (in B1, too), so slices are worked on apart and joined.  Sums over
-// a thread's logits are binary32, everything joined is binary64, as is the
+// Every term is a sum over slices of the vocabulary once each slice's maximum
+// is put back (in B1, too), so slices are worked on apart and joined.  Sums
+// over a thread's logits are binary32, everything joined is binary64, as is the
 // list's side (P = 1 - B0 loses what binary32 would keep of it).  The hardware
 // exponential gives 0 below 2^-126 relative to a maximum.
 #pragma once
