@@ -91,6 +91,10 @@ extern "C" {
 #define DSPARK_ST_BAD_PENALTY 20       /* a penalty or temperature outside its range */
 #define DSPARK_ST_BAD_BIAS 21          /* bias offsets out of order, ids not strictly ascending in [0, V), or a NaN / +inf value */
 #define DSPARK_ST_BAD_MASK 22          /* a mask row index outside [-1, n_masks) */
+/* refusals of dspark_beam_select and dspark_beam_reorder */
+#define DSPARK_ST_BAD_SCORE 23         /* a beam's score that is NaN or +inf */
+#define DSPARK_ST_BAD_PARENT 24        /* a parent outside [-1, beams) */
+#define DSPARK_ST_BAD_LENGTH 25        /* a length outside [0, positions] */
 
 typedef enum { DSPARK_F32 = 0, DSPARK_BF16 = 1 } dspark_dtype;
 typedef enum { DSPARK_GREEDY = 0, DSPARK_SAMPLED = 1 } dspark_mode;
@@ -500,6 +504,65 @@ int dspark_distill_backward(const dspark_rows* student, const dspark_teacher* te
  * grad of sum_r weight[r] loss[r], as the two calls above give them. */
 int dspark_distill_step(const dspark_rows* student, const dspark_teacher* teacher, float temperature,
                         const float* weight, float* loss, void* grad, int64_t grad_stride, int32_t* row_status,
+                        void* ws, size_t ws_bytes, void* stream);
+
+/* A matrix in 8-bit floating point (e4m3: 4 significant bits, at most 448, no
+ * infinity) with a scale for each block of 128 columns of one row (block_rows
+ * 1: hidden states, gradients) or of 128 rows (block_rows 128: weights); what
+ * it stands for is value * scale.
+ *   values: n_rows rows of cols bytes, row_stride bytes apart; cols and
+ *           row_stride are multiples of 16, the first row is 16-byte aligned.
+ *           Matrices of other widths are filled up with zero columns.
+ *   scales: (n_rows + block_rows - 1) / block_rows rows of (cols + 127) / 128
+ *           scales, scale_stride scales apart: float (DSPARK_SCALE_F32) or the
+ *           exponent byte of a power of two, 2^(byte - 127), 255 a NaN
+ *           (DSPARK_SCALE_E8M0).  0 <= n_rows <= 2^24, 16 <= cols <= 2^20. */
+typedef enum { DSPARK_SCALE_F32 = 0, DSPARK_SCALE_E8M0 = 1 } dspark_scale;
+typedef struct {
+  void* values;
+  void* scales;
+  int32_t scale_dtype;
+  int32_t block_rows;
+  int64_t n_rows;
+  int64_t cols;
+  int64_t row_stride;
+  int64_t scale_stride;
+} dspark_fp8;
+
+/* Quantises rows x (float32 or bf16) into out: out->n_rows is the rows' number
+ * and out->cols their width rounded up to a multiple of 16 (the columns past
+ * the width become zeros).  With a = the largest |x| of a block:
+ *   float scales: s = RN32(a / 448);
+ *   powers of two: the least s = 2^e with 448 s >= a;
+ * (s = 1 where a = 0, and at least 2^-126), and each value is x / s rounded to
+ * binary32, cut off at +-448 and rounded to the nearest even e4m3.  A block
+ * that holds a NaN or an infinity has a NaN scale and NaN values. */
+int dspark_quantize_blocks(const dspark_rows* x, const dspark_fp8* out, void* stream);
+
+/* Logits of quantised rows: out[m][n] = sum_k x[m][k] w[n][k] over what the
+ * matrices stand for, summed in binary32 and rounded once to out_dtype.
+ * For bf16 results the products of eight neighbouring columns are cut to 2^-13
+ * of the largest of them before they are added (the 8-bit matrix instruction);
+ * float32 results keep them whole.
+ * x: block_rows 1; w: block_rows 128, the vocabulary head (a row for each
+ * token) or, for the gradient of the hidden states, its transpose; both of
+ * the same cols and scale_dtype.  out: x->n_rows rows of w->n_rows values,
+ * out_stride elements apart, 16-byte aligned; what lies between rows is not
+ * written.  A row of x with a NaN gives NaN throughout, which every later
+ * step refuses.  ws: dspark_block_product_workspace() bytes, 16-byte aligned
+ * (NULL where it is 0); it is free again when the call's work is done. */
+size_t dspark_block_product_workspace(int64_t x_rows, int64_t w_rows, int64_t cols);
+int dspark_block_product(const dspark_fp8* x, const dspark_fp8* w, void* out, int32_t out_dtype, int64_t out_stride,
+                         void* ws, size_t ws_bytes, void* stream);
+
+/* The same from rows in float32 or bf16 (x->vocab wide, w->cols that width
+ * rounded up to a multiple of 16): they are quantised as by
+ * dspark_quantize_blocks, with scales of w's type, and multiplied.  Of the
+ * hidden states and the head: logits; of the logits' gradient and the
+ * transposed head: the hidden states' gradient (the derivative of the product
+ * by its quantised left operand, with the gradient quantised as it comes). */
+size_t dspark_block_linear_workspace(int64_t x_rows, int64_t w_rows, int64_t cols);
+int dspark_block_linear(const dspark_rows* x, const dspark_fp8* w, void* out, int32_t out_dtype, int64_t out_stride,
                         void* ws, size_t ws_bytes, void* stream);
 
 /* Test entry: the dense allocation steps of dspark_q_alloc applied to

@@ -22,7 +22,8 @@ STATUS_NAMES = {0: "OK", 1: "ROW_NAN", 2: "ROW_POSINF", 3: "ROW_ZERO_MASS", 4: "
                 5: "ALLOC_INCONSISTENT", 6: "TARGET_INVALID", 7: "DRAFT_INVALID", 8: "BAD_WEIGHT",
                 9: "BAD_TOPK", 10: "Q_BAD_LEN", 11: "Q_BAD_ID", 12: "Q_UNSORTED", 13: "Q_NONFINITE",
                 14: "Q_NEGATIVE", 15: "Q_NOT_DYADIC", 16: "Q_PADDING", 17: "Q_MASS", 18: "Q_TOKEN",
-                19: "BAD_HISTORY", 20: "BAD_PENALTY", 21: "BAD_BIAS", 22: "BAD_MASK"}
+                19: "BAD_HISTORY", 20: "BAD_PENALTY", 21: "BAD_BIAS", 22: "BAD_MASK",
+                23: "BAD_SCORE", 24: "BAD_PARENT", 25: "BAD_LENGTH"}
 
 
 class DsparkError(RuntimeError):
@@ -64,12 +65,22 @@ class Teacher(ctypes.Structure):
                 ("lse", ctypes.c_void_p), ("k_max", ctypes.c_int32), ("reserved", ctypes.c_int32)]
 
 
+class Fp8(ctypes.Structure):
+    _fields_ = [("values", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("scale_dtype", ctypes.c_int32),
+                ("block_rows", ctypes.c_int32), ("n_rows", ctypes.c_int64), ("cols", ctypes.c_int64),
+                ("row_stride", ctypes.c_int64), ("scale_stride", ctypes.c_int64)]
+
+
 DISTILL_STATS = 5
+SCALE_F32 = 0
+SCALE_E8M0 = 1
 
 EXPORTS = ["dspark_propose", "dspark_q_alloc", "dspark_sample", "dspark_verify_greedy", "dspark_fused",
            "dspark_q_alloc_weights", "dspark_cr_expf", "dspark_q_encode", "dspark_q_validate", "dspark_margin", "dspark_verify_stochastic", "dspark_verify_ratio", "dspark_sharded_propose", "dspark_sharded_propose_noalloc", "dspark_sharded_q", "dspark_sharded_q_workspace", "dspark_workspace_bytes", "dspark_q_semantic_id",
            "dspark_shape_logits", "dspark_top_logits", "dspark_top_logits_workspace", "dspark_distill",
            "dspark_distill_backward", "dspark_distill_step", "dspark_distill_workspace",
+           "dspark_quantize_blocks", "dspark_block_product", "dspark_block_product_workspace",
+           "dspark_block_linear", "dspark_block_linear_workspace",
            "dspark_status_name", "dspark_last_error", "dspark_abi_version"]
 
 
@@ -89,6 +100,7 @@ def load_library():
     P, I32, I64, SZ = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
     RP, QP = ctypes.POINTER(Rows), ctypes.POINTER(Q)
     TP, F32 = ctypes.POINTER(Teacher), ctypes.c_float
+    FP = ctypes.POINTER(Fp8)
     sig = {
         "dspark_propose": (ctypes.c_int, [RP, P, P, P, P, SZ, P]),
         "dspark_q_alloc": (ctypes.c_int, [RP, QP, P, P, SZ, P]),
@@ -114,6 +126,11 @@ def load_library():
         "dspark_distill_backward": (ctypes.c_int, [RP, TP, F32, P, P, P, P, I64, P]),
         "dspark_distill_step": (ctypes.c_int, [RP, TP, F32, P, P, P, I64, P, P, SZ, P]),
         "dspark_distill_workspace": (SZ, [I64, I64]),
+        "dspark_quantize_blocks": (ctypes.c_int, [RP, FP, P]),
+        "dspark_block_product": (ctypes.c_int, [FP, FP, P, I32, I64, P, SZ, P]),
+        "dspark_block_product_workspace": (SZ, [I64, I64, I64]),
+        "dspark_block_linear": (ctypes.c_int, [RP, FP, P, I32, I64, P, SZ, P]),
+        "dspark_block_linear_workspace": (SZ, [I64, I64, I64]),
         "dspark_q_semantic_id": (ctypes.c_char_p, []),
         "dspark_status_name": (ctypes.c_char_p, [I32]),
         "dspark_last_error": (ctypes.c_char_p, []),
@@ -745,3 +762,149 @@ def distill_loss(student: torch.Tensor, teacher, temperature: float = 1.0) -> to
         raise ValueError("the teacher is constant: detach its logits and lse")
     return _DistillLoss.apply(student, teacher["ids"], teacher["logits"], teacher["len"], teacher.get("lse"),
                               float(temperature))
+
+
+# ---- the vocabulary head in 8-bit floating point: quantisation in blocks of
+# 128, the product that makes logit rows, and its gradient.  A quantised
+# matrix is {"values": float8_e4m3fn [rows, cols], "scales"}: cols a multiple
+# of 16, the last ones zeros where the matrix is narrower; scales float32 or
+# float8_e8m0fnu, one for each 128 columns of a row (hidden states, gradients)
+# or of 128 rows (weights).
+
+
+def _fp8(q, name, block_rows, dev) -> Fp8:
+    values, scales = q["values"], q["scales"]
+    if values.dtype != torch.float8_e4m3fn or values.dim() != 2 or values.device != dev:
+        raise ValueError(f"{name} values must be a 2-D float8_e4m3fn tensor on {dev}")
+    n, cols = values.shape
+    blocks = (-(-n // block_rows), -(-cols // 128))
+    if scales.dtype not in (torch.float32, torch.float8_e8m0fnu) or scales.shape != blocks or scales.device != dev:
+        raise ValueError(f"{name} scales must be a float32 or float8_e8m0fnu tensor of shape {blocks} on {dev}")
+    if cols % 16 or cols == 0:
+        raise ValueError(f"{name} must have a multiple of 16 columns (fill up with zeros)")
+    if values.stride(1) != 1 or (n > 1 and values.stride(0) < cols):
+        raise ValueError(f"{name} values must have unit column stride and rows that do not overlap")
+    if (blocks[1] > 1 and scales.stride(1) != 1) or (blocks[0] > 1 and scales.stride(0) < blocks[1]):
+        raise ValueError(f"{name} scales must have unit column stride and rows that do not overlap")
+    return Fp8(values.data_ptr(), scales.data_ptr(), SCALE_F32 if scales.dtype == torch.float32 else SCALE_E8M0,
+               block_rows, n, cols, values.stride(0) if n > 1 else cols, scales.stride(0) if blocks[0] > 1 else blocks[1])
+
+
+def quantize_blocks(x: torch.Tensor, block_rows: int = 1, scale_dtype=torch.float32):
+    """Rows x [n, width] in e4m3 with a scale for each 128 columns of
+    block_rows (1 or 128) rows (see dspark_quantize_blocks): {"values"
+    float8_e4m3fn [n, width rounded up to a multiple of 16], "scales"}.
+    scale_dtype: float32, or float8_e8m0fnu for powers of two."""
+    lib = load_library()
+    r = _rows(x)
+    if block_rows not in (1, 128):
+        raise ValueError("block_rows must be 1 or 128")
+    if scale_dtype not in (torch.float32, torch.float8_e8m0fnu):
+        raise ValueError("scale_dtype must be float32 or float8_e8m0fnu")
+    n, dev = x.shape[0], x.device
+    cols = -(-x.shape[1] // 16) * 16
+    q = {"values": torch.empty((n, cols), dtype=torch.float8_e4m3fn, device=dev),
+         "scales": torch.empty((-(-n // block_rows), -(-cols // 128)), dtype=scale_dtype, device=dev)}
+    _call(dev, lib.dspark_quantize_blocks, ctypes.byref(r), ctypes.byref(_fp8(q, "out", block_rows, dev)))
+    return q
+
+
+def transpose_blocks(w, cols: int):
+    """The transpose of a quantised weight matrix whose first `cols` columns
+    are its own (the rest fill up): what head_logits needs for the gradient.
+    It is laid out once, with torch."""
+    values, scales = w["values"], w["scales"]
+    n = values.shape[0]
+    if not 0 < cols <= values.shape[1]:
+        raise ValueError("cols must be in [1, the matrix's columns]")
+    t = torch.zeros((cols, -(-n // 16) * 16), dtype=torch.uint8, device=values.device)
+    t[:, :n] = values.view(torch.uint8)[:, :cols].t()
+    return {"values": t.view(torch.float8_e4m3fn), "scales": scales[:, :-(-cols // 128)].t().contiguous()}
+
+
+def _product_out(n, V, out, out_dtype, dev):
+    if out is None:
+        out = _empty_rows(n, V, out_dtype, dev)
+    elif out.shape != (n, V) or out.dtype != out_dtype or out.device != dev or out.stride(1) != 1 or (n > 1 and out.stride(0) < V):
+        raise ValueError(f"out must be a {out_dtype} tensor of shape {(n, V)} with unit column stride on {dev}")
+    if out_dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError("out_dtype must be float32 or bfloat16")
+    return out, DTYPE_F32 if out_dtype == torch.float32 else DTYPE_BF16, out.stride(0) if n > 1 else max(out.stride(0), V)
+
+
+def block_product(x, w, out_dtype=torch.bfloat16, out=None) -> torch.Tensor:
+    """Logit rows [n, V] of quantised rows x (a scale for each row's blocks)
+    and a quantised matrix w of V rows (a scale for blocks of 128 rows), both
+    with scales of one type (see dspark_block_product).  out: rows to write."""
+    lib = load_library()
+    dev = x["values"].device
+    fx, fw = _fp8(x, "x", 1, dev), _fp8(w, "w", 128, dev)
+    o, dt, stride = _product_out(fx.n_rows, fw.n_rows, out, out_dtype, dev)
+    nbytes = lib.dspark_block_product_workspace(fx.n_rows, fw.n_rows, fx.cols)
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
+    _call(dev, lib.dspark_block_product, ctypes.byref(fx), ctypes.byref(fw), o.data_ptr(), dt, stride,
+          ws.data_ptr() if nbytes else None, nbytes)
+    _written(out)
+    return o
+
+
+def block_linear(x: torch.Tensor, w, out_dtype=None, out=None) -> torch.Tensor:
+    """The same from rows x [n, width] in float32 or bf16, quantised on the
+    way (see dspark_block_linear); out_dtype: x's type by default."""
+    lib = load_library()
+    r = _rows(x)
+    n, dev = x.shape[0], x.device
+    fw = _fp8(w, "w", 128, dev)
+    o, dt, stride = _product_out(n, fw.n_rows, out, out_dtype or (x.dtype if out is None else out.dtype), dev)
+    nbytes = lib.dspark_block_linear_workspace(n, fw.n_rows, x.shape[1])
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
+    _call(dev, lib.dspark_block_linear, ctypes.byref(r), ctypes.byref(fw), o.data_ptr(), dt, stride,
+          ws.data_ptr() if nbytes else None, nbytes)
+    _written(out)
+    return o
+
+
+def _aligned_rows(x):
+    """x itself, or a copy whose rows start 16-byte aligned."""
+    if x.stride(1) == 1 and x.stride(0) >= x.shape[1] and (x.data_ptr() | x.stride(0) * x.element_size()) % 16 == 0:
+        return x
+    return _empty_rows(x.shape[0], x.shape[1], x.dtype, x.device).copy_(x)
+
+
+def _head_grad(ctx, grad):
+    values, scales = ctx.saved_tensors
+    return block_linear(_aligned_rows(grad), {"values": values, "scales": scales}, ctx.dtype), None, None
+
+
+class _HeadLogits(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, head, out_dtype):
+        t = head["transposed"]
+        ctx.save_for_backward(t["values"], t["scales"])
+        ctx.dtype = x.dtype
+        return block_linear(x, head["weight"], out_dtype)
+
+    @staticmethod
+    def backward(ctx, grad):
+        if torch.is_grad_enabled():  # a graph of the gradient is asked for: its derivative is refused
+            return torch.autograd.function.once_differentiable(_head_grad)(ctx, grad)
+        return _head_grad(ctx, grad)
+
+
+def head_logits(x: torch.Tensor, head, out_dtype=None) -> torch.Tensor:
+    """Logits [n, V] of hidden states x [n, width] (float32 or bf16, rows
+    16-byte aligned) and a head {"weight": a quantised matrix [V, width],
+    "transposed": transpose_blocks(weight, width)}, a differentiable function
+    of x: the logits' gradient is quantised in blocks of 128 tokens, as x is in
+    blocks of 128 channels, and multiplied with the transposed head.  The head
+    is constant; without a gradient "transposed" is not needed."""
+    if x.requires_grad and torch.is_grad_enabled():
+        t = head.get("transposed")
+        if t is None:
+            raise ValueError('the gradient needs head["transposed"] (see transpose_blocks)')
+        if t["values"].shape[0] != x.shape[1]:
+            raise ValueError('head["transposed"] must have a row for each channel of x')
+        if any(q[k].requires_grad for q in (head["weight"], t) for k in ("values", "scales")):
+            raise ValueError("the head is constant: detach it")
+        return _HeadLogits.apply(x, head, out_dtype)
+    return block_linear(x, head["weight"], out_dtype)

@@ -11,7 +11,7 @@ import tempfile
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
-SOURCES = [os.path.join(HERE, "csrc", "dspark.hip"), os.path.join(HERE, "csrc", "logits", "logits.hip")]
+SOURCES = [os.path.join(HERE, "csrc", *at) for at in (("dspark.hip",), ("logits", "logits.hip"), ("head", "head.hip"))]
 OUT = os.path.join(HERE, "libdspark.so")
 
 FLAGS = [

@@ -891,11 +891,6 @@ void launch_sharded_q(ShardQArgs a, bool sparse, void* stream) {
 namespace {
 thread_local char g_err[512];
 
-int fail(int code, const char* msg) {
-  std::snprintf(g_err, sizeof g_err, "%s", msg);
-  return code;
-}
-
 int check_launch() {
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) {
@@ -905,8 +900,6 @@ int check_launch() {
   g_err[0] = 0;
   return DSPARK_SUCCESS;
 }
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 // Device address of `scratch` on the current device, looked up once per
 // device (with that device current) and kept.
@@ -1085,7 +1078,10 @@ void set_q(RowsArgs& a, const dspark_q* q) {
 }  // namespace
 
 // the same checks and error message for the entry points of the other source files
-int dspark::host_fail(int code, const char* msg) { return fail(code, msg); }
+int dspark::host_fail(int code, const char* msg) {
+  std::snprintf(g_err, sizeof g_err, "%s", msg);
+  return code;
+}
 int dspark::host_check_launch() { return check_launch(); }
 int dspark::host_check_rows(const dspark_rows* r, const char* what) { return check_rows(r, what); }
 
@@ -1120,6 +1116,9 @@ const char* dspark_status_name(int32_t code) {
     case DSPARK_ST_BAD_PENALTY: return "BAD_PENALTY";
     case DSPARK_ST_BAD_BIAS: return "BAD_BIAS";
     case DSPARK_ST_BAD_MASK: return "BAD_MASK";
+    case DSPARK_ST_BAD_SCORE: return "BAD_SCORE";
+    case DSPARK_ST_BAD_PARENT: return "BAD_PARENT";
+    case DSPARK_ST_BAD_LENGTH: return "BAD_LENGTH";
     default: return "UNKNOWN";
   }
 }

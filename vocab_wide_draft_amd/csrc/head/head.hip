@@ -1,0 +1,250 @@
+// The vocabulary head in 8-bit floating point: quantisation in blocks, and
+// the product that makes logit rows, or sends their gradient back (the entry
+// points declared in include/dspark.h).
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+
+#include "../host_checks.hpp"
+#include "dspark.h"
+#include "product.hpp"
+#include "quantize.hpp"
+
+namespace dspark {
+namespace {
+
+constexpr int64_t kFp8Rows = 1 << 24, kFp8Cols = 1 << 20, kFp8Stride = 1 << 22;
+
+int check_fp8(const dspark_fp8* q, const char* what) {
+  if (!q) return fail(DSPARK_EINVAL, what);
+  if (q->scale_dtype != DSPARK_SCALE_F32 && q->scale_dtype != DSPARK_SCALE_E8M0)
+    return fail(DSPARK_EINVAL, "scale_dtype must be F32 or E8M0");
+  if (q->block_rows != 1 && q->block_rows != kBlock) return fail(DSPARK_EINVAL, "block_rows must be 1 or 128");
+  if (q->n_rows < 0 || q->n_rows > kFp8Rows) return fail(DSPARK_EINVAL, "fp8 rows out of range");
+  if (q->cols < 16 || q->cols > kFp8Cols || q->cols % 16 != 0)
+    return fail(DSPARK_EINVAL, "fp8 cols must be a multiple of 16 in [16, 2^20]");
+  if (q->row_stride < q->cols || q->row_stride > kFp8Stride) return fail(DSPARK_EINVAL, "fp8 row_stride must be in [cols, 2^22]");
+  if (q->scale_stride < (q->cols + kBlock - 1) / kBlock) return fail(DSPARK_EINVAL, "scale_stride is shorter than a row's scales");
+  if (!aligned16(q->values) || q->row_stride % 16 != 0)
+    return fail(DSPARK_EALIGN, "fp8 rows must start 16-byte aligned (values and row_stride)");
+  if (q->scale_dtype == DSPARK_SCALE_F32 && (reinterpret_cast<uintptr_t>(q->scales) & 3u) != 0)
+    return fail(DSPARK_EALIGN, "float scales must be 4-byte aligned");
+  if (q->n_rows > 0 && (!q->values || !q->scales)) return fail(DSPARK_EINVAL, "NULL fp8 values or scales");
+  return DSPARK_SUCCESS;
+}
+
+template <int DT, int ST>
+void launch_quantize(QuantArgs a, int block_rows, hipStream_t s) {
+  if (block_rows == kBlock) {
+    hipLaunchKernelGGL(HIP_KERNEL_NAME(quantize_tiles_kernel<DT, ST>), grid_of((a.n + kBlock - 1) / kBlock * a.blocks),
+                       dim3(kSliceBS), 0, s, a);
+    return;
+  }
+  constexpr int step = kSliceBS * kVec<DT>;
+  const int all = (a.cols + step - 1) / step;
+  if (a.n * all >= 4096) {
+    a.chunks = (all + 3) / 4;
+    hipLaunchKernelGGL(HIP_KERNEL_NAME(quantize_rows_kernel<DT, ST, 4>), grid_of(a.n * a.chunks), dim3(kSliceBS), 0, s, a);
+  } else {
+    a.chunks = all;
+    hipLaunchKernelGGL(HIP_KERNEL_NAME(quantize_rows_kernel<DT, ST, 1>), grid_of(a.n * a.chunks), dim3(kSliceBS), 0, s, a);
+  }
+}
+
+void quantize(const dspark_rows* x, const dspark_fp8* out, hipStream_t s) {
+  QuantArgs a{};
+  a.x = x->data;
+  a.stride = x->row_stride;
+  a.n = x->n_rows;
+  a.width = (int)x->vocab;
+  a.cols = (int)out->cols;
+  a.blocks = (a.cols + kBlock - 1) / kBlock;
+  a.v = static_cast<uint8_t*>(out->values);
+  a.v_stride = out->row_stride;
+  a.s = out->scales;
+  a.s_stride = out->scale_stride;
+  if (x->dtype == DSPARK_F32) {
+    if (out->scale_dtype == DSPARK_SCALE_F32) launch_quantize<DSPARK_F32, DSPARK_SCALE_F32>(a, out->block_rows, s);
+    else launch_quantize<DSPARK_F32, DSPARK_SCALE_E8M0>(a, out->block_rows, s);
+  } else {
+    if (out->scale_dtype == DSPARK_SCALE_F32) launch_quantize<DSPARK_BF16, DSPARK_SCALE_F32>(a, out->block_rows, s);
+    else launch_quantize<DSPARK_BF16, DSPARK_SCALE_E8M0>(a, out->block_rows, s);
+  }
+}
+
+int64_t up(int64_t n, int64_t to) { return (n + to - 1) / to * to; }
+
+int check_product_out(int64_t M, int64_t N, const void* out, int32_t dtype, int64_t stride) {
+  if (dtype != DSPARK_F32 && dtype != DSPARK_BF16) return fail(DSPARK_EINVAL, "out_dtype must be F32 or BF16");
+  if (stride < N) return fail(DSPARK_EINVAL, "output stride is shorter than a row");
+  if (!aligned16(out) || ((stride * (dtype == DSPARK_BF16 ? 2 : 4)) & 15) != 0)
+    return fail(DSPARK_EALIGN, "output rows must start 16-byte aligned (data and stride * element size)");
+  if (M > 0 && N > 0 && !out) return fail(DSPARK_EINVAL, "NULL output rows");
+  return DSPARK_SUCCESS;
+}
+
+struct ProductPlan {
+  int tile_m, tile_n, splits, split_steps;
+  size_t bytes;
+};
+ProductPlan product_plan(int64_t M, int64_t N, int64_t K) {
+  ProductPlan p{};
+  p.tile_m = M <= 16 ? 16 : M <= 64 ? 64 : 128;
+  p.tile_n = M <= 64 ? 256 : 128;
+  const int64_t tiles = ((M + p.tile_m - 1) / p.tile_m) * ((N + p.tile_n - 1) / p.tile_n);
+  const int64_t steps = (K + kBlock - 1) / kBlock;
+  const int64_t want = std::max<int64_t>(1, std::min<int64_t>(512 / std::max<int64_t>(tiles, 1), steps / 4));
+  p.split_steps = (int)((steps + want - 1) / want);
+  p.splits = (int)((steps + p.split_steps - 1) / p.split_steps);
+  p.bytes = p.splits > 1 ? (size_t)p.splits * (size_t)M * (size_t)up(N, 4) * 4u : 0;
+  return p;
+}
+
+template <int ST, bool WIDE, int OUT>
+void launch_tiles(const ProductPlan& p, ProductArgs a, hipStream_t s) {
+  const dim3 grid = grid_of(a.tiles_m * a.tiles_n * a.splits);
+  if (p.tile_m == 16) hipLaunchKernelGGL(HIP_KERNEL_NAME(product_kernel<1, 4, 1, ST, WIDE, OUT>), grid, dim3(256), 0, s, a);
+  else if (p.tile_m == 64) hipLaunchKernelGGL(HIP_KERNEL_NAME(product_kernel<4, 4, 1, ST, WIDE, OUT>), grid, dim3(256), 0, s, a);
+  else hipLaunchKernelGGL(HIP_KERNEL_NAME(product_kernel<4, 2, 2, ST, WIDE, OUT>), grid, dim3(256), 0, s, a);
+}
+
+void product(const dspark_fp8* x, const dspark_fp8* w, void* out, int32_t out_dtype, int64_t out_stride, void* ws, hipStream_t s) {
+  const ProductPlan p = product_plan(x->n_rows, w->n_rows, x->cols);
+  ProductArgs a{};
+  a.x = static_cast<const uint8_t*>(x->values);
+  a.w = static_cast<const uint8_t*>(w->values);
+  a.x_stride = x->row_stride;
+  a.w_stride = w->row_stride;
+  a.xs = x->scales;
+  a.ws = w->scales;
+  a.xs_stride = x->scale_stride;
+  a.ws_stride = w->scale_stride;
+  a.M = x->n_rows;
+  a.N = w->n_rows;
+  a.K = (int)x->cols;
+  a.steps = (a.K + kBlock - 1) / kBlock;
+  a.splits = p.splits;
+  a.split_steps = p.split_steps;
+  a.tiles_m = (a.M + p.tile_m - 1) / p.tile_m;
+  a.tiles_n = (a.N + p.tile_n - 1) / p.tile_n;
+  a.out = p.splits > 1 ? ws : out;
+  a.out_stride = p.splits > 1 ? up(a.N, 4) : out_stride;
+  const bool wide = out_dtype == DSPARK_F32, bf16 = p.splits == 1 && !wide;
+  if (x->scale_dtype == DSPARK_SCALE_F32) {
+    if (wide) launch_tiles<DSPARK_SCALE_F32, true, DSPARK_F32>(p, a, s);
+    else if (bf16) launch_tiles<DSPARK_SCALE_F32, false, DSPARK_BF16>(p, a, s);
+    else launch_tiles<DSPARK_SCALE_F32, false, DSPARK_F32>(p, a, s);
+  } else {
+    if (wide) launch_tiles<DSPARK_SCALE_E8M0, true, DSPARK_F32>(p, a, s);
+    else if (bf16) launch_tiles<DSPARK_SCALE_E8M0, false, DSPARK_BF16>(p, a, s);
+    else launch_tiles<DSPARK_SCALE_E8M0, false, DSPARK_F32>(p, a, s);
+  }
+  if (p.splits > 1) {
+    ProductJoinArgs j{};
+    j.part = static_cast<const float*>(ws);
+    j.splits = p.splits;
+    j.vectors = (int)(a.out_stride / 4);
+    j.M = a.M;
+    j.N = a.N;
+    j.out = out;
+    j.out_stride = out_stride;
+    const dim3 grid = grid_of((j.M * j.vectors + kSliceBS - 1) / kSliceBS);
+    if (out_dtype == DSPARK_F32) hipLaunchKernelGGL(product_join_kernel<DSPARK_F32>, grid, dim3(kSliceBS), 0, s, j);
+    else hipLaunchKernelGGL(product_join_kernel<DSPARK_BF16>, grid, dim3(kSliceBS), 0, s, j);
+  }
+}
+
+bool product_sizes(int64_t M, int64_t N, int64_t cols) {
+  return M > 0 && M <= kFp8Rows && N > 0 && N <= kFp8Rows && cols >= 1 && cols <= kFp8Cols;
+}
+
+// The quantised rows of a linear call in its workspace: values, scales, and
+// behind them the product's.
+struct LinearPlan {
+  int64_t cols, blocks;
+  size_t scales_at, ws_at, bytes;
+};
+LinearPlan linear_plan(int64_t M, int64_t N, int64_t width) {
+  LinearPlan p{};
+  p.cols = up(width, 16);
+  p.blocks = (p.cols + kBlock - 1) / kBlock;
+  p.scales_at = (size_t)(M * p.cols);
+  p.ws_at = p.scales_at + (size_t)up(M * p.blocks * 4, 256);
+  p.bytes = p.ws_at + product_plan(M, N, p.cols).bytes;
+  return p;
+}
+
+int check_ws(size_t need, const void* ws, size_t ws_bytes) {
+  if (!aligned16(ws)) return fail(DSPARK_EALIGN, "workspace must be 16-byte aligned");
+  if (need > 0 && (!ws || ws_bytes < need)) return fail(DSPARK_EWORKSPACE, "workspace too small");
+  return DSPARK_SUCCESS;
+}
+
+}  // namespace
+}  // namespace dspark
+
+using namespace dspark;
+
+extern "C" {
+
+int dspark_quantize_blocks(const dspark_rows* x, const dspark_fp8* out, void* stream) {
+  int rc = host_check_rows(x, "rows NULL");
+  if (rc) return rc;
+  rc = check_fp8(out, "NULL fp8 matrix");
+  if (rc) return rc;
+  if (out->n_rows != x->n_rows) return fail(DSPARK_EINVAL, "the fp8 matrix has another number of rows");
+  if (out->cols != up(x->vocab, 16)) return fail(DSPARK_EINVAL, "fp8 cols must be the rows' width rounded up to a multiple of 16");
+  if (x->n_rows == 0) return DSPARK_SUCCESS;
+  quantize(x, out, static_cast<hipStream_t>(stream));
+  return host_check_launch();
+}
+
+size_t dspark_block_product_workspace(int64_t x_rows, int64_t w_rows, int64_t cols) {
+  return product_sizes(x_rows, w_rows, cols) ? product_plan(x_rows, w_rows, up(cols, 16)).bytes : 0;
+}
+
+int dspark_block_product(const dspark_fp8* x, const dspark_fp8* w, void* out, int32_t out_dtype, int64_t out_stride,
+                         void* ws, size_t ws_bytes, void* stream) {
+  int rc = check_fp8(x, "NULL left matrix");
+  if (rc) return rc;
+  rc = check_fp8(w, "NULL right matrix");
+  if (rc) return rc;
+  if (x->block_rows != 1 || w->block_rows != kBlock) return fail(DSPARK_EINVAL, "block_rows must be 1 on the left and 128 on the right");
+  if (x->cols != w->cols) return fail(DSPARK_EINVAL, "the matrices' cols differ");
+  if (x->scale_dtype != w->scale_dtype) return fail(DSPARK_EINVAL, "the matrices' scale_dtype differs");
+  rc = check_product_out(x->n_rows, w->n_rows, out, out_dtype, out_stride);
+  if (rc) return rc;
+  if (x->n_rows == 0 || w->n_rows == 0) return DSPARK_SUCCESS;
+  rc = check_ws(product_plan(x->n_rows, w->n_rows, x->cols).bytes, ws, ws_bytes);
+  if (rc) return rc;
+  product(x, w, out, out_dtype, out_stride, ws, static_cast<hipStream_t>(stream));
+  return host_check_launch();
+}
+
+size_t dspark_block_linear_workspace(int64_t x_rows, int64_t w_rows, int64_t cols) {
+  return product_sizes(x_rows, w_rows, cols) ? linear_plan(x_rows, w_rows, cols).bytes : 0;
+}
+
+int dspark_block_linear(const dspark_rows* x, const dspark_fp8* w, void* out, int32_t out_dtype, int64_t out_stride,
+                        void* ws, size_t ws_bytes, void* stream) {
+  int rc = host_check_rows(x, "rows NULL");
+  if (rc) return rc;
+  rc = check_fp8(w, "NULL right matrix");
+  if (rc) return rc;
+  if (w->block_rows != kBlock) return fail(DSPARK_EINVAL, "block_rows must be 128 on the right");
+  if (w->cols != up(x->vocab, 16)) return fail(DSPARK_EINVAL, "w->cols must be the rows' width rounded up to a multiple of 16");
+  rc = check_product_out(x->n_rows, w->n_rows, out, out_dtype, out_stride);
+  if (rc) return rc;
+  if (x->n_rows == 0 || w->n_rows == 0) return DSPARK_SUCCESS;
+  const LinearPlan p = linear_plan(x->n_rows, w->n_rows, x->vocab);
+  rc = check_ws(p.bytes, ws, ws_bytes);
+  if (rc) return rc;
+  char* at = static_cast<char*>(ws);
+  dspark_fp8 q{at, at + p.scales_at, w->scale_dtype, 1, x->n_rows, p.cols, p.cols, p.blocks};
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  quantize(x, &q, s);
+  product(&q, w, out, out_dtype, out_stride, p.bytes > p.ws_at ? at + p.ws_at : nullptr, s);
+  return host_check_launch();
+}
+
+}  // extern "C"

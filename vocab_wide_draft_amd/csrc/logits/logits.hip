@@ -15,24 +15,7 @@
 namespace dspark {
 namespace {
 
-int fail(int code, const char* msg) { return host_fail(code, msg); }
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
 bool temperature_ok(float t) { return t >= 0x1p-100f && t <= 0x1p100f; }
-
-// a grid of at least n workgroups in two dimensions (a launch takes fewer
-// than 2^32 threads per dimension)
-dim3 grid_of(int64_t n) {
-  const int64_t x = std::min<int64_t>(n, 1 << 20);
-  return dim3((unsigned)x, (unsigned)((n + x - 1) / x));
-}
-
-// a grid of `slices` workgroups for each of n rows (see row_slice)
-dim3 row_slice_grid(int64_t n, int slices) {
-  const int64_t line = std::min<int64_t>((n + 7) & ~int64_t(7), kRowsPerY);
-  return dim3((unsigned)(line * slices), (unsigned)((n + kRowsPerY - 1) / kRowsPerY));
-}
 
 // Output rows beside input rows: the same memory (same type and stride) or
 // memory apart.

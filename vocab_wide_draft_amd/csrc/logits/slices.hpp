@@ -18,8 +18,7 @@ __device__ __forceinline__ int64_t block_number(int64_t total) {
   return b < total ? b : -1;
 }
 
-// The row and slice of a workgroup of a grid laid out by row_slice_grid (host
-// side): the slices of one row go to workgroups eight apart, which run on one
+// The row and slice of a workgroup of a grid laid out by row_slice_grid: the slices of one row go to workgroups eight apart, which run on one
 // of the eight XCDs, so that what they all read of the row stays in its L2.
 // False past the last row (uniform).
 __device__ __forceinline__ bool row_slice(int64_t n, int slices, int64_t& r, int& s) {
@@ -27,6 +26,12 @@ __device__ __forceinline__ bool row_slice(int64_t n, int slices, int64_t& r, int
   s = (int)(x - rows * (uint32_t)slices);
   r = (int64_t)blockIdx.y * kRowsPerY + (int64_t)rows * 8 + (blockIdx.x & 7u);
   return r < n;
+}
+
+// a grid of `slices` workgroups for each of n rows (see row_slice; host side)
+inline dim3 row_slice_grid(int64_t n, int slices) {
+  const int64_t all = (n + 7) & ~int64_t(7), line = all < kRowsPerY ? all : kRowsPerY;
+  return dim3((unsigned)(line * slices), (unsigned)((n + kRowsPerY - 1) / kRowsPerY));
 }
 
 typedef unsigned int v2u __attribute__((ext_vector_type(2)));
