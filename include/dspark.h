@@ -565,6 +565,62 @@ size_t dspark_block_linear_workspace(int64_t x_rows, int64_t w_rows, int64_t col
 int dspark_block_linear(const dspark_rows* x, const dspark_fp8* w, void* out, int32_t out_dtype, int64_t out_stride,
                         void* ws, size_t ws_bytes, void* stream);
 
+/* One step of beam search: the n_out best continuations of each request's
+ * beams.  rows: final logits, request r's beams b = 0 .. beams - 1 in rows
+ * r * beams + b; scores (float[n_rows]): the beams' log-probabilities so far;
+ * finished (int32[n_rows], may be NULL): nonzero where a beam has ended.
+ * Candidates:
+ *   of a beam with a finite score that has not ended, every token v with
+ *     logit x_v > -inf, with score + x_v - log sum_u exp(x_u);
+ *   of one that has ended, end_token with its score as it is (its row is not
+ *     read);
+ *   of a beam with score -inf, none: the slot is empty, its row is not read.
+ * They are ordered by score (desc), beam (asc), logit (desc), token (asc),
+ * scores compared in binary64 with the log-sum-exp exact to binary64's
+ * rounding wherever it decides.  parent, token, score, out_finished ([n_out]
+ * a request): the candidate's beam in the request, its token, its score
+ * rounded to binary32, and whether it comes from an ended beam or its token is
+ * end_token; len[r] of them, behind which stand empty slots (parent -1, token
+ * 0, score -inf, finished 0).  beams in [1, DSPARK_BEAM_MAX], n_out in [1,
+ * DSPARK_BEAM_OUT_MAX], beams * n_out <= 4096, end_token in [-1, vocab) (-1:
+ * none; finished must then be NULL).  req_status[r]: OK, ROW_NAN or
+ * ROW_POSINF for a row that is read, or BAD_SCORE; a refused request has len 0
+ * and empty slots.  ws: dspark_beam_select_workspace() bytes, 16-byte aligned;
+ * one for n rows serves fewer rows as well. */
+#define DSPARK_BEAM_MAX 64
+#define DSPARK_BEAM_OUT_MAX 128
+size_t dspark_beam_select_workspace(int64_t n_rows, int64_t vocab, int32_t n_out);
+int dspark_beam_select(const dspark_rows* rows, const float* scores, const int32_t* finished, int32_t beams,
+                       int32_t n_out, int32_t end_token, int32_t* parent, int32_t* token, float* score,
+                       int32_t* out_finished, int32_t* len, int32_t* req_status, void* ws, size_t ws_bytes,
+                       void* stream);
+
+/* A state of every beam (one layer's cache, say): the part of beam b of
+ * request r lies at in + r * in_request + b * in_beam and consists, for each of
+ * `outer` parts in_outer apart, of `rows` positions of row_bytes bytes, in_row
+ * apart (all strides in bytes).  rows 0: the state has no positions and is one
+ * row of row_bytes.  out: the same layout with strides of its own; out == in
+ * (with the same strides) reorders in place, other memory must lie apart.
+ * Parts of different beams, and different states, do not overlap. */
+typedef struct {
+  const void* in;
+  void* out;
+  int64_t in_request, in_beam, in_outer, in_row;
+  int64_t out_request, out_beam, out_outer, out_row;
+  int64_t outer, rows, row_bytes;
+} dspark_state;
+
+/* Reorders the states after a step of beam search: slot b of request r takes
+ * the state that slot parent[r * beams + b] had before (-1: the slot is left as
+ * it is).  length (int32[requests], may be NULL): only the first length[r]
+ * positions are taken, what lies behind them is not read or written.
+ * 1 <= beams <= DSPARK_BEAM_MAX; all states are in place, or none.
+ * req_status[r]: OK, BAD_PARENT (outside [-1, beams)) or BAD_LENGTH (outside
+ * [0, the least `rows` of the states that have positions]); the states of a
+ * refused request are left as they are. */
+int dspark_beam_reorder(const dspark_state* states, int32_t n_states, int64_t requests, int32_t beams,
+                        const int32_t* parent, const int32_t* length, int32_t* req_status, void* stream);
+
 /* Test entry: the dense allocation steps of dspark_q_alloc applied to
  * caller-given float32 weights (normalised weights in [0, 1]), so that the
  * consistency assertions can be reached with constructed inputs.

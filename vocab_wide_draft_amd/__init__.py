@@ -10,4 +10,5 @@ from .binding import (  # noqa: F401
     load_library, propose, q_alloc, q_alloc_weights, q_semantic_id, sample, status_name,
     verify_greedy, cr_expf, workspace_bytes, shape_logits, top_logits, distill, distill_backward,
     distill_loss, distill_step, quantize_blocks, transpose_blocks, block_product, block_linear, head_logits,
+    beam_select, beam_reorder,
 )

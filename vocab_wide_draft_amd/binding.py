@@ -71,6 +71,15 @@ class Fp8(ctypes.Structure):
                 ("row_stride", ctypes.c_int64), ("scale_stride", ctypes.c_int64)]
 
 
+class State(ctypes.Structure):
+    _fields_ = [("in_", ctypes.c_void_p), ("out", ctypes.c_void_p),
+                ("in_request", ctypes.c_int64), ("in_beam", ctypes.c_int64), ("in_outer", ctypes.c_int64), ("in_row", ctypes.c_int64),
+                ("out_request", ctypes.c_int64), ("out_beam", ctypes.c_int64), ("out_outer", ctypes.c_int64), ("out_row", ctypes.c_int64),
+                ("outer", ctypes.c_int64), ("rows", ctypes.c_int64), ("row_bytes", ctypes.c_int64)]
+
+
+BEAM_MAX = 64
+BEAM_OUT_MAX = 128
 DISTILL_STATS = 5
 SCALE_F32 = 0
 SCALE_E8M0 = 1
@@ -81,6 +90,7 @@ EXPORTS = ["dspark_propose", "dspark_q_alloc", "dspark_sample", "dspark_verify_g
            "dspark_distill_backward", "dspark_distill_step", "dspark_distill_workspace",
            "dspark_quantize_blocks", "dspark_block_product", "dspark_block_product_workspace",
            "dspark_block_linear", "dspark_block_linear_workspace",
+           "dspark_beam_select", "dspark_beam_select_workspace", "dspark_beam_reorder",
            "dspark_status_name", "dspark_last_error", "dspark_abi_version"]
 
 
@@ -131,6 +141,9 @@ def load_library():
         "dspark_block_product_workspace": (SZ, [I64, I64, I64]),
         "dspark_block_linear": (ctypes.c_int, [RP, FP, P, I32, I64, P, SZ, P]),
         "dspark_block_linear_workspace": (SZ, [I64, I64, I64]),
+        "dspark_beam_select": (ctypes.c_int, [RP, P, P, I32, I32, I32, P, P, P, P, P, P, P, SZ, P]),
+        "dspark_beam_select_workspace": (SZ, [I64, I64, I32]),
+        "dspark_beam_reorder": (ctypes.c_int, [ctypes.POINTER(State), I32, I64, I32, P, P, P, P]),
         "dspark_q_semantic_id": (ctypes.c_char_p, []),
         "dspark_status_name": (ctypes.c_char_p, [I32]),
         "dspark_last_error": (ctypes.c_char_p, []),
@@ -908,3 +921,100 @@ def head_logits(x: torch.Tensor, head, out_dtype=None) -> torch.Tensor:
             raise ValueError("the head is constant: detach it")
         return _HeadLogits.apply(x, head, out_dtype)
     return block_linear(x, head["weight"], out_dtype)
+
+
+# ---- beam search on logit rows.
+
+
+def beam_select(rows: torch.Tensor, scores: torch.Tensor, n_out: int | None = None, *, finished=None, end_token: int = -1):
+    """The n_out (default: twice the beams, at most BEAM_OUT_MAX) best
+    continuations of each request's beams (see dspark_beam_select).  rows
+    [requests * beams, V]; scores float32 [requests, beams], -inf for an empty
+    slot; finished int32 [requests, beams], nonzero for an ended beam, which
+    continues with end_token at its score.  Returns {"parent", "token",
+    "score", "finished"} ([requests, n_out]), "len" and "status" ([requests])."""
+    lib = load_library()
+    r = _rows(rows)
+    n, V, dev = rows.shape[0], rows.shape[1], rows.device
+    if scores.dim() != 2 or scores.numel() != n:
+        raise ValueError("scores must be [requests, beams] with a row of logits for each")
+    R, beams = scores.shape
+    k = min(2 * beams, BEAM_OUT_MAX) if n_out is None else int(n_out)
+    i32 = torch.int32
+    s, f = _arg(scores, "scores", torch.float32, (R, beams), dev), _arg(finished, "finished", i32, (R, beams), dev)
+    parent, token, ended = (torch.empty((R, max(k, 0)), dtype=i32, device=dev) for _ in range(3))
+    score = torch.empty((R, max(k, 0)), dtype=torch.float32, device=dev)
+    length, st = _i32(R, dev), _i32(R, dev)
+    nbytes = lib.dspark_beam_select_workspace(n, V, k)
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
+    _call(dev, lib.dspark_beam_select, ctypes.byref(r), s, f, beams, k, int(end_token), parent.data_ptr(), token.data_ptr(),
+          score.data_ptr(), ended.data_ptr(), length.data_ptr(), st.data_ptr(), ws.data_ptr() if nbytes else None, nbytes)
+    return {"parent": parent, "token": token, "score": score, "finished": ended, "len": length, "status": st}
+
+
+def _layout(x, axis):
+    """(strides of requests, beams, outer, positions; outer, positions, bytes of a position) of a state, strides in bytes."""
+    es, size, stride = x.element_size(), x.shape, x.stride()
+    inner, reach = 1, 1
+    for d in range(x.dim() - 1, min(axis, x.dim() - 1), -1):
+        if size[d] > 1 and stride[d] != reach:
+            raise ValueError("a state's dimensions after its positions must be contiguous")
+        inner, reach = inner * size[d], reach * size[d]
+    if x.dim() <= axis:  # no positions: everything after the beams is one row
+        for d in range(x.dim() - 1, 1, -1):
+            if size[d] > 1 and stride[d] != inner:
+                raise ValueError("a state without positions must be contiguous after its beams")
+            inner *= size[d]
+        return stride[0] * es, stride[1] * es, 0, 0, 1, 0, inner * es
+    outer, step = 1, 0
+    for d in range(axis - 1, 1, -1):  # the dimensions between beams and positions, as one
+        if size[d] == 1:
+            continue
+        if outer > 1 and stride[d] != step * outer:
+            raise ValueError("a state's dimensions between its beams and positions must lie evenly")
+        if outer == 1:
+            step = stride[d]
+        outer *= size[d]
+    return stride[0] * es, stride[1] * es, step * es, stride[axis] * es, outer, size[axis], inner * es
+
+
+def beam_reorder(states, parent: torch.Tensor, length=None, *, axis: int = 2, out=None):
+    """Gives every slot the state of its parent (see dspark_beam_reorder).
+    states: a sequence of tensors [requests, beams, ...] (every layer's caches,
+    say), reordered in place, or into `out`, tensors of the same shapes and
+    types; parent int32 [requests, beams].  length int32 [requests]: only the
+    first length[r] positions, which dimension `axis` counts; states of fewer
+    dimensions are taken whole.  Returns {"states", "status"}."""
+    lib = load_library()
+    states = list(states)
+    if not states:
+        raise ValueError("no states")
+    into = states if out is None else list(out)
+    if parent.dim() != 2:
+        raise ValueError("parent must be [requests, beams]")
+    R, beams = parent.shape
+    dev = parent.device
+    if not parent.is_cuda:
+        raise ValueError("parent must be on the GPU")
+    if axis < 2:
+        raise ValueError("axis counts from the dimensions after requests and beams: 2 or more")
+    if len(into) != len(states):
+        raise ValueError("out must be as many tensors as states")
+    laid = (State * len(states))()
+    for at, x, y in zip(laid, states, into):
+        if x.dim() < 2 or x.shape[:2] != (R, beams) or x.device != dev:
+            raise ValueError(f"a state must be a tensor [{R}, {beams}, ...] on {dev}")
+        if y.shape != x.shape or y.dtype != x.dtype or y.device != dev:
+            raise ValueError("out must be tensors of the states' shapes, types and device")
+    live = [i for i, x in enumerate(states) if x.numel()]
+    for k, i in enumerate(live):
+        a, b = _layout(states[i], axis), _layout(into[i], axis)
+        laid[k] = State(states[i].data_ptr(), into[i].data_ptr(), *a[:4], *b[:4], *a[4:])
+    st = _i32(R, dev)
+    if not live:
+        return {"states": into, "status": st.zero_()}
+    _call(dev, lib.dspark_beam_reorder, laid, len(live), R, beams, _arg(parent, "parent", torch.int32, (R, beams), dev),
+          _arg(length, "length", torch.int32, (R,), dev), st.data_ptr())
+    for y in into:
+        _written(y)
+    return {"states": into, "status": st}

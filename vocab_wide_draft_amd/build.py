@@ -11,7 +11,8 @@ import tempfile
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
-SOURCES = [os.path.join(HERE, "csrc", *at) for at in (("dspark.hip",), ("logits", "logits.hip"), ("head", "head.hip"))]
+SOURCES = [os.path.join(HERE, "csrc", *at) for at in
+           (("dspark.hip",), ("logits", "logits.hip"), ("head", "head.hip"), ("beam", "beam.hip"))]
 OUT = os.path.join(HERE, "libdspark.so")
 
 FLAGS = [

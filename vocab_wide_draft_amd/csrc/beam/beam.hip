@@ -1,0 +1,223 @@
+// Beam search on logit rows: the selection over beams and vocabulary, and the
+// reordering of the beams' states (the entry points declared in
+// include/dspark.h).
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+
+#include "../host_checks.hpp"
+#include "dspark.h"
+#include "reorder.hpp"
+#include "select.hpp"
+
+namespace dspark {
+namespace {
+
+static_assert(kBeams == DSPARK_BEAM_MAX && kBeamOut == DSPARK_BEAM_OUT_MAX, "limits of the interface");
+
+struct BeamPlan {
+  int slice, slices, cap;
+  size_t part_at, bytes;
+};
+BeamPlan beam_plan_of(int64_t n, int64_t V, int n_out, int slice) {
+  BeamPlan p{};
+  p.slice = slice;
+  p.slices = (int)((V + slice - 1) / slice);
+  p.cap = 2 * n_out + 64;
+  p.part_at = (size_t)n * (size_t)p.slices * (size_t)p.cap * sizeof(uint64_t);
+  p.bytes = p.part_at + (size_t)n * (size_t)p.slices * sizeof(BeamPart);
+  return p;
+}
+constexpr int kBeamLong = 8192, kBeamShort = 2048;  // logits of a slice
+bool beam_short(int64_t n, int64_t V) { return n * ((V + kBeamLong - 1) / kBeamLong) < 512 && V <= kBeamShort * kBeamSlices; }
+BeamPlan beam_plan(int64_t n, int64_t V, int n_out) {
+  return beam_plan_of(n, V, n_out, beam_short(n, V) ? kBeamShort : kBeamLong);
+}
+
+template <int DT>
+void launch_select(const BeamArgs& a, int slice, hipStream_t s) {
+  constexpr int step = kSliceBS * kVec<DT>;
+  const dim3 grid = row_slice_grid(a.x.n, a.slices);
+  if (slice == kBeamShort) hipLaunchKernelGGL(HIP_KERNEL_NAME(beam_slice_kernel<DT, kBeamShort / step>), grid, dim3(kSliceBS), 0, s, a);
+  else hipLaunchKernelGGL(HIP_KERNEL_NAME(beam_slice_kernel<DT, kBeamLong / step>), grid, dim3(kSliceBS), 0, s, a);
+  hipLaunchKernelGGL(HIP_KERNEL_NAME(beam_join_kernel<DT, 8>), grid_of(a.requests), dim3(512),
+                     (size_t)a.beams * (size_t)a.n_out * sizeof(uint64_t), s, a);
+}
+
+// the bytes that a state's layout spans; -1 where parts overlap
+int64_t span(const int64_t (&size)[4], const int64_t (&stride)[4], int64_t row_bytes, bool apart) {
+  int order[4] = {0, 1, 2, 3};
+  std::sort(order, order + 4, [&](int a, int b) { return stride[a] < stride[b]; });
+  int64_t reach = row_bytes;
+  for (int i : order) {
+    if (size[i] <= 1) continue;
+    if (stride[i] < 0 || (apart && stride[i] < reach)) return -1;
+    reach += stride[i] * (size[i] - 1);
+  }
+  return reach;
+}
+
+template <int BYTES>
+void launch_reorder_as(const ReorderArgs& a, hipStream_t s) {
+  const dim3 grid = grid_of(a.first[a.n_states]), block(kSliceBS);
+  if constexpr (BYTES >= 8) {
+    if (a.beams <= 8) {
+      hipLaunchKernelGGL(HIP_KERNEL_NAME(reorder_kernel<BYTES, 8>), grid, block, 0, s, a);
+      return;
+    }
+    if (a.beams <= 16) {
+      hipLaunchKernelGGL(HIP_KERNEL_NAME(reorder_kernel<BYTES, 16>), grid, block, 0, s, a);
+      return;
+    }
+  }
+  if constexpr (BYTES == 8) {
+    hipLaunchKernelGGL(HIP_KERNEL_NAME(reorder_kernel<BYTES, 32>), grid, block, 0, s, a);
+  } else if constexpr (BYTES < 8) {
+    if (a.beams <= 16) hipLaunchKernelGGL(HIP_KERNEL_NAME(reorder_kernel<BYTES, 16>), grid, block, 0, s, a);
+    else hipLaunchKernelGGL(HIP_KERNEL_NAME(reorder_kernel<BYTES, 64>), grid, block, 0, s, a);
+  }
+}
+
+}  // namespace
+}  // namespace dspark
+
+using namespace dspark;
+
+extern "C" {
+
+size_t dspark_beam_select_workspace(int64_t n_rows, int64_t vocab, int32_t n_out) {
+  if (n_rows <= 0 || n_rows > (1 << 24) || vocab < 1 || vocab > DSPARK_V_MAX || n_out < 1 || n_out > DSPARK_BEAM_OUT_MAX) return 0;
+  size_t bytes = beam_plan(n_rows, vocab, n_out).bytes;
+  if (!beam_short(n_rows, vocab) && beam_short(1, vocab)) {  // fewer rows have more slices: the most rows that do
+    const int64_t most = 511 / ((vocab + kBeamLong - 1) / kBeamLong);
+    bytes = std::max(bytes, beam_plan(std::min(n_rows, most), vocab, n_out).bytes);
+  }
+  return bytes;
+}
+
+int dspark_beam_select(const dspark_rows* rows, const float* scores, const int32_t* finished, int32_t beams,
+                       int32_t n_out, int32_t end_token, int32_t* parent, int32_t* token, float* score,
+                       int32_t* out_finished, int32_t* len, int32_t* req_status, void* ws, size_t ws_bytes,
+                       void* stream) {
+  int rc = host_check_rows(rows, "rows NULL");
+  if (rc) return rc;
+  if (beams < 1 || beams > DSPARK_BEAM_MAX) return fail(DSPARK_EINVAL, "beams must be in [1, DSPARK_BEAM_MAX]");
+  if (n_out < 1 || n_out > DSPARK_BEAM_OUT_MAX) return fail(DSPARK_EINVAL, "n_out must be in [1, DSPARK_BEAM_OUT_MAX]");
+  if (beams * n_out > 4096) return fail(DSPARK_EINVAL, "beams * n_out must be at most 4096");
+  if (rows->n_rows % beams != 0) return fail(DSPARK_EINVAL, "n_rows is not a multiple of beams");
+  if (end_token < -1 || end_token >= rows->vocab) return fail(DSPARK_EINVAL, "end_token must be in [-1, vocab)");
+  if (finished && end_token < 0) return fail(DSPARK_EINVAL, "finished needs an end_token");
+  if (rows->n_rows == 0) return DSPARK_SUCCESS;
+  if (!scores || !parent || !token || !score || !out_finished || !len || !req_status) return fail(DSPARK_EINVAL, "NULL scores or output");
+  const BeamPlan p = beam_plan(rows->n_rows, rows->vocab, n_out);
+  if (!aligned16(ws)) return fail(DSPARK_EALIGN, "workspace must be 16-byte aligned");
+  if (!ws || ws_bytes < p.bytes) return fail(DSPARK_EWORKSPACE, "workspace smaller than dspark_beam_select_workspace()");
+  BeamArgs a{};
+  a.x.n = rows->n_rows;
+  a.x.x = rows->data;
+  a.x.stride = rows->row_stride;
+  a.x.V = (int)rows->vocab;
+  a.x.inv_t = 1.0;
+  a.x.c = (float)1.4426950408889634;
+  a.scores = scores;
+  a.finished = finished;
+  a.beams = beams;
+  a.n_out = n_out;
+  a.end_token = end_token;
+  a.requests = rows->n_rows / beams;
+  a.parent = parent;
+  a.token = token;
+  a.score = score;
+  a.out_finished = out_finished;
+  a.len = len;
+  a.status = req_status;
+  a.slices = p.slices;
+  a.cap = p.cap;
+  a.cand = static_cast<uint64_t*>(ws);
+  a.part = reinterpret_cast<BeamPart*>(static_cast<char*>(ws) + p.part_at);
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  if (rows->dtype == DSPARK_F32) launch_select<DSPARK_F32>(a, p.slice, s);
+  else launch_select<DSPARK_BF16>(a, p.slice, s);
+  return host_check_launch();
+}
+
+int dspark_beam_reorder(const dspark_state* states, int32_t n_states, int64_t requests, int32_t beams,
+                        const int32_t* parent, const int32_t* length, int32_t* req_status, void* stream) {
+  if (n_states < 1 || !states) return fail(DSPARK_EINVAL, "no states");
+  if (requests < 0 || requests > (1 << 24)) return fail(DSPARK_EINVAL, "requests out of range");
+  if (beams < 1 || beams > DSPARK_BEAM_MAX) return fail(DSPARK_EINVAL, "beams must be in [1, DSPARK_BEAM_MAX]");
+  const bool in_place = states[0].in == states[0].out;
+  uint64_t bits = 0;
+  int64_t least = INT64_MAX;
+  for (int i = 0; i < n_states; ++i) {
+    const dspark_state& t = states[i];
+    if (t.outer < 1 || t.rows < 0 || t.row_bytes < 1 || t.row_bytes > INT32_MAX || t.outer > (1 << 24) || t.rows > INT32_MAX ||
+        t.rows * t.row_bytes >= (int64_t(1) << 39))
+      return fail(DSPARK_EINVAL, "a state's outer, rows or row_bytes is out of range");
+    const int64_t size[4] = {requests, beams, t.outer, std::max<int64_t>(t.rows, 1)};
+    const int64_t in[4] = {t.in_request, t.in_beam, t.in_outer, t.in_row}, out[4] = {t.out_request, t.out_beam, t.out_outer, t.out_row};
+    const int64_t in_span = span(size, in, t.row_bytes, false), out_span = span(size, out, t.row_bytes, true);
+    if (in_span < 0 || out_span < 0) return fail(DSPARK_EINVAL, "a state's strides make its parts overlap");
+    if (requests > 0 && (!t.in || !t.out)) return fail(DSPARK_EINVAL, "NULL state");
+    if ((t.in == t.out) != in_place) return fail(DSPARK_EINVAL, "all states must be in place, or none");
+    for (int d = 0; d < 4; ++d) {
+      if (size[d] <= 1) continue;
+      if (in_place && in[d] != out[d]) return fail(DSPARK_EINVAL, "in place needs the same strides");
+      bits |= (uint64_t)in[d] | (uint64_t)out[d];
+    }
+    if (!in_place) {
+      const char *x = static_cast<const char*>(t.in), *y = static_cast<const char*>(t.out);
+      if (x < y + out_span && y < x + in_span) return fail(DSPARK_EINVAL, "a state's output overlaps its input");
+    }
+    for (int j = 0; j < i; ++j)
+      if (requests > 0 && states[j].out == t.out) return fail(DSPARK_EINVAL, "a state is listed twice");
+    bits |= (uint64_t)t.row_bytes | (uint64_t)reinterpret_cast<uintptr_t>(t.in) | (uint64_t)reinterpret_cast<uintptr_t>(t.out);
+    if (t.rows > 0) least = std::min(least, t.rows);
+  }
+  if (requests == 0) return DSPARK_SUCCESS;
+  if (!parent || !req_status) return fail(DSPARK_EINVAL, "NULL parent or req_status");
+  // vectors of what divides every address, and of which a thread can hold one of every beam
+  int bytes = 16;
+  while (bits % (uint64_t)bytes != 0) bytes /= 2;
+  if (beams > 16) bytes = std::min(bytes, beams > 32 ? 4 : 8);
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  for (int at = 0; at < n_states; at += kStates) {
+    ReorderArgs a{};
+    a.n_states = std::min(kStates, n_states - at);
+    a.beams = beams;
+    a.requests = requests;
+    a.parent = parent;
+    a.length = length;
+    a.status = at == 0 ? req_status : nullptr;
+    a.least_rows = least == INT64_MAX ? INT32_MAX : least;
+    a.in_place = in_place;
+    for (int i = 0; i < a.n_states; ++i) {
+      const dspark_state& t = states[at + i];
+      ReorderState& u = a.state[i];
+      u.in = static_cast<const char*>(t.in);
+      u.out = static_cast<char*>(t.out);
+      u.in_request = t.in_request;
+      u.in_beam = t.in_beam;
+      u.in_outer = t.in_outer;
+      u.in_row = t.in_row;
+      u.out_request = t.out_request;
+      u.out_beam = t.out_beam;
+      u.out_outer = t.out_outer;
+      u.out_row = t.out_row;
+      u.rows = t.rows;
+      u.outer = t.outer;
+      u.vectors = (uint32_t)(t.row_bytes / bytes);
+      u.flat = t.rows <= 1 || (t.in_row == t.row_bytes && t.out_row == t.row_bytes);
+      u.chunks = (uint32_t)((std::max<int64_t>(t.rows, 1) * (int64_t)u.vectors + kSliceBS - 1) / kSliceBS);
+      a.first[i + 1] = a.first[i] + requests * t.outer * (int64_t)u.chunks;
+    }
+    if (bytes == 16) launch_reorder_as<16>(a, s);
+    else if (bytes == 8) launch_reorder_as<8>(a, s);
+    else if (bytes == 4) launch_reorder_as<4>(a, s);
+    else if (bytes == 2) launch_reorder_as<2>(a, s);
+    else launch_reorder_as<1>(a, s);
+  }
+  return host_check_launch();
+}
+
+}  // extern "C"
