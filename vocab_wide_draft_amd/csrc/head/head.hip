@@ -87,10 +87,10 @@ struct ProductPlan {
   int tile_m, tile_n, splits, split_steps;
   size_t bytes;
 };
-ProductPlan product_plan(int64_t M, int64_t N, int64_t K) {
+ProductPlan product_plan(int64_t M, int64_t N, int64_t K, bool wide) {
   ProductPlan p{};
-  p.tile_m = M <= 16 ? 16 : M <= 64 ? 64 : 128;
-  p.tile_n = M <= 64 ? 256 : 128;
+  p.tile_m = M <= 16 ? 16 : M <= 64 ? 64 : M <= 128 || wide ? 128 : 256;
+  p.tile_n = p.tile_m == 128 ? 128 : 256;
   const int64_t tiles = ((M + p.tile_m - 1) / p.tile_m) * ((N + p.tile_n - 1) / p.tile_n);
   const int64_t steps = (K + kBlock - 1) / kBlock;
   const int64_t want = std::max<int64_t>(1, std::min<int64_t>(512 / std::max<int64_t>(tiles, 1), steps / 4));
@@ -100,16 +100,22 @@ ProductPlan product_plan(int64_t M, int64_t N, int64_t K) {
   return p;
 }
 
+// whichever type the results have
+size_t product_bytes(int64_t M, int64_t N, int64_t K) {
+  return std::max(product_plan(M, N, K, false).bytes, product_plan(M, N, K, true).bytes);
+}
+
 template <int ST, bool WIDE, int OUT>
 void launch_tiles(const ProductPlan& p, ProductArgs a, hipStream_t s) {
   const dim3 grid = grid_of(a.tiles_m * a.tiles_n * a.splits);
   if (p.tile_m == 16) hipLaunchKernelGGL(HIP_KERNEL_NAME(product_kernel<1, 4, 1, ST, WIDE, OUT>), grid, dim3(256), 0, s, a);
   else if (p.tile_m == 64) hipLaunchKernelGGL(HIP_KERNEL_NAME(product_kernel<4, 4, 1, ST, WIDE, OUT>), grid, dim3(256), 0, s, a);
-  else hipLaunchKernelGGL(HIP_KERNEL_NAME(product_kernel<4, 2, 2, ST, WIDE, OUT>), grid, dim3(256), 0, s, a);
+  else if (p.tile_m == 128) hipLaunchKernelGGL(HIP_KERNEL_NAME(product_kernel<4, 2, 2, ST, WIDE, OUT>), grid, dim3(256), 0, s, a);
+  else if constexpr (!WIDE) hipLaunchKernelGGL(HIP_KERNEL_NAME(product_tile_kernel<4, ST, OUT>), grid, dim3(512), 0, s, a);
 }
 
 void product(const dspark_fp8* x, const dspark_fp8* w, void* out, int32_t out_dtype, int64_t out_stride, void* ws, hipStream_t s) {
-  const ProductPlan p = product_plan(x->n_rows, w->n_rows, x->cols);
+  const ProductPlan p = product_plan(x->n_rows, w->n_rows, x->cols, out_dtype == DSPARK_F32);
   ProductArgs a{};
   a.x = static_cast<const uint8_t*>(x->values);
   a.w = static_cast<const uint8_t*>(w->values);
@@ -170,7 +176,7 @@ LinearPlan linear_plan(int64_t M, int64_t N, int64_t width) {
   p.blocks = (p.cols + kBlock - 1) / kBlock;
   p.scales_at = (size_t)(M * p.cols);
   p.ws_at = p.scales_at + (size_t)up(M * p.blocks * 4, 256);
-  p.bytes = p.ws_at + product_plan(M, N, p.cols).bytes;
+  p.bytes = p.ws_at + product_bytes(M, N, p.cols);
   return p;
 }
 
@@ -200,7 +206,7 @@ int dspark_quantize_blocks(const dspark_rows* x, const dspark_fp8* out, void* st
 }
 
 size_t dspark_block_product_workspace(int64_t x_rows, int64_t w_rows, int64_t cols) {
-  return product_sizes(x_rows, w_rows, cols) ? product_plan(x_rows, w_rows, up(cols, 16)).bytes : 0;
+  return product_sizes(x_rows, w_rows, cols) ? product_bytes(x_rows, w_rows, up(cols, 16)) : 0;
 }
 
 int dspark_block_product(const dspark_fp8* x, const dspark_fp8* w, void* out, int32_t out_dtype, int64_t out_stride,
@@ -215,7 +221,7 @@ int dspark_block_product(const dspark_fp8* x, const dspark_fp8* w, void* out, in
   rc = check_product_out(x->n_rows, w->n_rows, out, out_dtype, out_stride);
   if (rc) return rc;
   if (x->n_rows == 0 || w->n_rows == 0) return DSPARK_SUCCESS;
-  rc = check_ws(product_plan(x->n_rows, w->n_rows, x->cols).bytes, ws, ws_bytes);
+  rc = check_ws(product_bytes(x->n_rows, w->n_rows, x->cols), ws, ws_bytes);
   if (rc) return rc;
   product(x, w, out, out_dtype, out_stride, ws, static_cast<hipStream_t>(stream));
   return host_check_launch();

@@ -61,6 +61,22 @@ __device__ __forceinline__ v8b widen(int lo, int hi) {
   return v8b{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
 }
 
+// The same, not waited for by what reads LDS afterwards (the compiler waits
+// for every load into an array before any read of it): loads_arrived() does.
+__device__ __forceinline__ void load_lds_ahead(v4i from, uint32_t to, int offset) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(to), "v"(offset), "s"(from) : "memory", "m0");
+}
+__device__ __forceinline__ void loads_arrived() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+// the buffer's four words, as buffer_of makes them
+__device__ __forceinline__ v4i buffer_words(const void* p, int64_t bytes) {
+  const uint64_t at = reinterpret_cast<uint64_t>(p);
+  return v4i{__builtin_amdgcn_readfirstlane((int)(uint32_t)at), __builtin_amdgcn_readfirstlane((int)(uint32_t)(at >> 32)),
+             __builtin_amdgcn_readfirstlane(bytes < 0 ? 0 : (int)bytes), 0x00020000};
+}
+__device__ __forceinline__ uint32_t lds_address(const void* p) {
+  return (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) const char*)p));
+}
+
 // 16 neighbouring values of a row
 template <int OUT>
 __device__ __forceinline__ void put_row16(void* row, int64_t n, int64_t N, const float (&v)[16]) {
@@ -88,8 +104,15 @@ template <int UM, int WN, int WM, int ST, bool WIDE, int OUT>
 __global__ void __launch_bounds__(64 * WN * WM) product_kernel(ProductArgs a) {
   constexpr int TN = 64 * WN, TM = 16 * UM * WM, NWV = WN * WM, GROUPS = (TN + TM) / 8, PER = (GROUPS + NWV - 1) / NWV;
   __shared__ __align__(16) uint8_t lds[2][(TN + TM) * kBlock];
-  const int64_t b = block_number(a.tiles_m * a.tiles_n * a.splits);
+  const int64_t total = a.tiles_m * a.tiles_n * a.splits;
+  int64_t b = block_number(total);
   if (b < 0) return;
+  // Workgroups go to the eight XCDs in turn: each takes a stretch of tiles, m
+  // first, so that those in work at a time share rows of both matrices in its L2.
+  if (total >= 64) {
+    const int64_t each = total / 8, more = total % 8, xcd = b & 7;
+    b = xcd * each + (xcd < more ? xcd : more) + (b >> 3);
+  }
   const int64_t tm = b % a.tiles_m, rest = b / a.tiles_m;
   const int64_t tn = rest % a.tiles_n;
   const int split = (int)(rest / a.tiles_n);
@@ -202,6 +225,180 @@ __global__ void __launch_bounds__(64 * WN * WM) product_kernel(ProductArgs a) {
       for (int i = 0; i < 4; ++i) v[4 * t + i] = acc[t][u][i];
     }
     put_row16<OUT>(out + m * a.out_stride * (int64_t)sizeof(typename El<OUT>::T), n0 + wn * 64 + 16 * g, a.N, v);
+  }
+}
+
+struct Yes { static constexpr bool value = true; };
+struct No { static constexpr bool value = false; };
+
+// Tiles of 256 rows of w by 64 U rows of x for many rows: eight waves, two by
+// four, of 128 by 16 U each.  One barrier a step: it stands before the last
+// quarter of a step's matrix instructions, when the wave has read all that it
+// needs of the step's buffer and the next step's has arrived, so that the
+// fetch after next goes into the former and the first reads of the latter
+// run under that quarter.
+template <int U, int ST, int OUT>
+__global__ void __launch_bounds__(512, 2) product_tile_kernel(ProductArgs a) {
+  constexpr int TN = 256, TM = 64 * U, T = 8, ROWS = TN + TM, BUF = ROWS * kBlock;
+  __shared__ __align__(16) uint8_t lds[2][BUF];
+  __shared__ uint32_t scales[2][TM + 2];
+  const int64_t total = a.tiles_m * a.tiles_n * a.splits;
+  int64_t b = block_number(total);
+  if (b < 0) return;
+  if (total >= 64) {  // (as in product_kernel)
+    const int64_t each = total / 8, more = total % 8, xcd = b & 7;
+    b = xcd * each + (xcd < more ? xcd : more) + (b >> 3);
+  }
+  const int64_t tm = b % a.tiles_m, rest = b / a.tiles_m;
+  const int64_t tn = rest % a.tiles_n;
+  const int split = (int)(rest / a.tiles_n);
+  const int64_t m0 = tm * TM, n0 = tn * TN;
+  const int first = split * a.split_steps, last = first + a.split_steps < a.steps ? first + a.split_steps : a.steps;
+  const int rows_w = a.N - n0 < TN ? (int)(a.N - n0) : TN, rows_x = a.M - m0 < TM ? (int)(a.M - m0) : TM;
+  const int tid = (int)threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wm = wave & 3, wn = wave >> 2, r = lane & 15, g = lane >> 4;
+
+  // fetches: the first four waves 64 rows of w each, the others 16 U rows of x
+  // each.  The eight chunks of 16 bytes of a row lie in LDS in an order of its
+  // own (key), so that lanes that read one chunk of neighbouring rows hit
+  // different banks.
+  const bool of_w = wave < 4;
+  const int64_t stride = of_w ? a.w_stride : a.x_stride;
+  const int row0 = of_w ? wave * 64 : (wave - 4) * 16 * U;
+  const uint8_t* from = (of_w ? a.w + n0 * a.w_stride : a.x + m0 * a.x_stride);
+  const int64_t bytes = (of_w ? rows_w : rows_x) * stride;
+  const int sub = lane >> 3;
+  // key of a row: w's 0-3 by its last two bits and the bit of 32, x's by its last three
+  const int col_a = ((lane & 7) ^ (of_w ? sub & 3 : sub)) * 16, col_b = of_w ? col_a ^ 64 : col_a;
+  const int base = (row0 + sub) * (int)stride;
+  const uint32_t to0 = lds_address(&lds[0][(of_w ? row0 : TN + row0) * kBlock]);
+  const auto fetch = [&](int step, int buf) {
+    const int64_t at = (int64_t)step * kBlock;
+    const v4i f = buffer_words(from + at, bytes - at);
+    const int left = a.K - (int)at;
+    const int oa = col_a < left ? base + col_a : kPastEnd, ob = col_b < left ? base + col_b : kPastEnd;
+    const uint32_t to = to0 + (uint32_t)(buf * BUF);
+    if (of_w) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) load_lds_ahead(f, to + j * 1024, (j < 4 ? oa : ob) + j * 8 * (int)stride);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 2 * U; ++j) load_lds_ahead(f, to + j * 1024, oa + j * 8 * (int)stride);
+    }
+  };
+  // a thread's scale: of a row of x, or of one of w's two blocks
+  const bool has_scale = tid < TM + 2;
+  const int64_t scale_at = tid < TM ? (m0 + tid < a.M ? m0 + tid : a.M - 1) * a.xs_stride
+                                    : ((n0 + (tid - TM) * 128 < a.N ? n0 + (tid - TM) * 128 : a.N - 1) / kBlock) * a.ws_stride;
+  const void* scale_of = tid < TM ? a.xs : a.ws;
+  const auto fetch_scale = [&](int step) -> uint32_t {
+    if (!has_scale) return 0u;
+    if constexpr (ST == DSPARK_SCALE_E8M0) return static_cast<const uint8_t*>(scale_of)[scale_at + step];
+    else return static_cast<const uint32_t*>(scale_of)[scale_at + step];
+  };
+
+  v4f acc[T][U];
+#pragma unroll
+  for (int t = 0; t < T; ++t) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) acc[t][u] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+  }
+  const int at_w = (wn * 128 + 32 * (r >> 2) + (r & 3)) * kBlock + ((g ^ (r & 7)) * 16);
+  const int at_x = (TN + wm * 16 * U + r) * kBlock + ((g ^ (r & 7)) * 16);
+  const auto frag = [&](int buf, int at) {
+    const v4i lo = *reinterpret_cast<const v4i*>(&lds[0][buf * BUF + at]), hi = *reinterpret_cast<const v4i*>(&lds[0][buf * BUF + (at ^ 64)]);
+    return v8i{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+  };
+
+  v8i fx[U], fw[2][2];
+  uint32_t sx[U], sw, next_scale = 0;
+  const auto read_scales = [&](int buf) {
+    sw = scales[buf][TM + wn];
+#pragma unroll
+    for (int u = 0; u < U; ++u) sx[u] = scales[buf][wm * 16 * U + 16 * u + r];
+    if constexpr (ST == DSPARK_SCALE_F32) {
+#pragma unroll
+      for (int u = 0; u < U; ++u) sx[u] = __float_as_uint(__uint_as_float(sw) * __uint_as_float(sx[u]));
+    }
+  };
+  const auto multiply = [&](int t, int u, const v8i& w) {
+    if constexpr (ST == DSPARK_SCALE_E8M0) {
+      acc[t][u] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w, fx[u], acc[t][u], 0, 0, 0, (int)sw, 0, (int)sx[u]);
+    } else {
+      const v4f p = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w, fx[u], v4f{0.0f, 0.0f, 0.0f, 0.0f}, 0, 0, 0, 127, 0, 127);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[t][u][i] = __builtin_fmaf(p[i], __uint_as_float(sx[u]), acc[t][u][i]);
+    }
+  };
+
+  if (first < last) {
+    next_scale = fetch_scale(first);
+    fetch(first, 0);
+    if (has_scale) scales[0][tid] = next_scale;
+    if (first + 1 < last) next_scale = fetch_scale(first + 1);
+    loads_arrived();
+    __syncthreads();
+    if (first + 1 < last) fetch(first + 1, 1);
+    read_scales(0);
+#pragma unroll
+    for (int u = 0; u < U; ++u) fx[u] = frag(0, at_x + u * 16 * kBlock);
+    fw[0][0] = frag(0, at_w);
+    fw[0][1] = frag(0, at_w + 512);
+  }
+  // one step; MORE: another one follows
+  const auto run = [&](int step, int buf, auto more) {
+    constexpr bool MORE = decltype(more)::value;
+#pragma unroll
+    for (int c = 0; c < T / 2; ++c) {
+      if (c < T / 2 - 1) {
+        fw[(c + 1) & 1][0] = frag(buf, at_w + (2 * c + 2) * 512);
+        fw[(c + 1) & 1][1] = frag(buf, at_w + (2 * c + 3) * 512);
+      } else if constexpr (MORE) {
+        if (has_scale) scales[buf ^ 1][tid] = next_scale;
+        loads_arrived();
+        __syncthreads();  // the next step's buffer has arrived, this one has been read
+        if (step + 2 < last) {
+          next_scale = fetch_scale(step + 2);
+          fetch(step + 2, buf);
+        }
+        fw[(c + 1) & 1][0] = frag(buf ^ 1, at_w);
+        fw[(c + 1) & 1][1] = frag(buf ^ 1, at_w + 512);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        multiply(2 * c, u, fw[c & 1][0]);
+        multiply(2 * c + 1, u, fw[c & 1][1]);
+        if constexpr (MORE) {
+          if (c == T / 2 - 1) {
+            __builtin_amdgcn_sched_barrier(0);
+            fx[u] = frag(buf ^ 1, at_x + u * 16 * kBlock);
+          }
+        }
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    if constexpr (MORE) read_scales(buf ^ 1);
+  };
+  for (int step = first; step + 1 < last; ++step) run(step, (step - first) & 1, Yes{});
+  if (first < last) run(last - 1, (last - 1 - first) & 1, No{});
+
+  char* out = static_cast<char*>(a.out);
+  if (a.splits > 1) out += (int64_t)split * a.M * a.out_stride * (int64_t)sizeof(typename El<OUT>::T);
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const int64_t m = m0 + wm * 16 * U + 16 * u + r;
+    if (m >= a.M) continue;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      float v[16];
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[4 * t + i] = acc[4 * h + t][u][i];
+      }
+      put_row16<OUT>(out + m * a.out_stride * (int64_t)sizeof(typename El<OUT>::T), n0 + wn * 128 + 32 * g + 16 * h, a.N, v);
+    }
   }
 }
 
