@@ -4,6 +4,7 @@
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
+#include <cmath>
 
 #include "../host_checks.hpp"
 #include "dspark.h"
@@ -24,7 +25,8 @@ int check_fp8(const dspark_fp8* q, const char* what) {
   if (q->cols < 16 || q->cols > kFp8Cols || q->cols % 16 != 0)
     return fail(DSPARK_EINVAL, "fp8 cols must be a multiple of 16 in [16, 2^20]");
   if (q->row_stride < q->cols || q->row_stride > kFp8Stride) return fail(DSPARK_EINVAL, "fp8 row_stride must be in [cols, 2^22]");
-  if (q->scale_stride < (q->cols + kBlock - 1) / kBlock) return fail(DSPARK_EINVAL, "scale_stride is shorter than a row's scales");
+  if (q->scale_stride < (q->cols + kBlock - 1) / kBlock || q->scale_stride > kFp8Cols)
+    return fail(DSPARK_EINVAL, "scale_stride must be in [a row's scales, 2^20]");
   if (!aligned16(q->values) || q->row_stride % 16 != 0)
     return fail(DSPARK_EALIGN, "fp8 rows must start 16-byte aligned (values and row_stride)");
   if (q->scale_dtype == DSPARK_SCALE_F32 && (reinterpret_cast<uintptr_t>(q->scales) & 3u) != 0)
@@ -51,7 +53,8 @@ void launch_quantize(QuantArgs a, int block_rows, hipStream_t s) {
   }
 }
 
-void quantize(const dspark_rows* x, const dspark_fp8* out, hipStream_t s) {
+// s_step: scales between the blocks of a row
+void quantize(const dspark_rows* x, const dspark_fp8* out, int64_t s_step, hipStream_t s) {
   QuantArgs a{};
   a.x = x->data;
   a.stride = x->row_stride;
@@ -63,6 +66,7 @@ void quantize(const dspark_rows* x, const dspark_fp8* out, hipStream_t s) {
   a.v_stride = out->row_stride;
   a.s = out->scales;
   a.s_stride = out->scale_stride;
+  a.s_step = s_step;
   if (x->dtype == DSPARK_F32) {
     if (out->scale_dtype == DSPARK_SCALE_F32) launch_quantize<DSPARK_F32, DSPARK_SCALE_F32>(a, out->block_rows, s);
     else launch_quantize<DSPARK_F32, DSPARK_SCALE_E8M0>(a, out->block_rows, s);
@@ -88,13 +92,33 @@ struct ProductPlan {
   size_t bytes;
 };
 ProductPlan product_plan(int64_t M, int64_t N, int64_t K, bool wide) {
-  ProductPlan p{};
-  p.tile_m = M <= 16 ? 16 : M <= 64 ? 64 : M <= 128 || wide ? 128 : 256;
-  p.tile_n = p.tile_m == 128 ? 128 : 256;
-  const int64_t tiles = ((M + p.tile_m - 1) / p.tile_m) * ((N + p.tile_n - 1) / p.tile_n);
   const int64_t steps = (K + kBlock - 1) / kBlock;
-  const int64_t want = std::max<int64_t>(1, std::min<int64_t>(512 / std::max<int64_t>(tiles, 1), steps / 4));
-  p.split_steps = (int)((steps + want - 1) / want);
+  ProductPlan p{};
+  p.tile_n = 256;
+  const int64_t tiles_n = (N + 255) / 256;
+  if (M <= 64) {
+    p.tile_m = M <= 16 ? 16 : 64;
+    const int64_t want = std::max<int64_t>(1, std::min<int64_t>(512 / std::max<int64_t>(tiles_n, 1), steps / 4));
+    p.split_steps = (int)((steps + want - 1) / want);
+  } else {
+    // the width and the number of parts that should take least: rounds of 256
+    // tiles (parts of a long product fill the last one), us for a step of a tile of
+    // 64 u rows, three steps for its beginning and end, the parts' way through memory
+    double best = 0.0;
+    for (int u = wide ? 2 : 4; u >= 1; --u) {
+      const int64_t tiles = (M + 64 * u - 1) / (64 * u) * tiles_n;
+      for (int64_t s = 1; s <= 16 && (s == 1 || (steps / s >= 8 && tiles * (s - 1) < 1024)); ++s) {
+        const double rounds = (double)(tiles * s) / 256.0;
+        const double time = (rounds < 8.0 ? std::ceil(rounds) : rounds) * (double)((steps + s - 1) / s + 3) * (0.70 + 0.25 * u) +
+                            (s > 1 ? 2e-6 * 4.0 * (double)s * (double)M * (double)N / 4.0 : 0.0);
+        if (best == 0.0 || time < best) {
+          best = time;
+          p.tile_m = 64 * u;
+          p.split_steps = (int)((steps + s - 1) / s);
+        }
+      }
+    }
+  }
   p.splits = (int)((steps + p.split_steps - 1) / p.split_steps);
   p.bytes = p.splits > 1 ? (size_t)p.splits * (size_t)M * (size_t)up(N, 4) * 4u : 0;
   return p;
@@ -105,16 +129,28 @@ size_t product_bytes(int64_t M, int64_t N, int64_t K) {
   return std::max(product_plan(M, N, K, false).bytes, product_plan(M, N, K, true).bytes);
 }
 
+template <int ST, bool WIDE, int OUT, int U>
+void launch_tile(const ProductArgs& a, hipStream_t s) {
+  hipLaunchKernelGGL(HIP_KERNEL_NAME(product_tile_kernel<4, U, ST, WIDE, OUT>), grid_of(a.tiles_m * a.tiles_n * a.splits),
+                     dim3(512), 0, s, a);
+}
 template <int ST, bool WIDE, int OUT>
-void launch_tiles(const ProductPlan& p, ProductArgs a, hipStream_t s) {
+void launch_tiles(const ProductPlan& p, ProductArgs a, bool few, hipStream_t s) {
   const dim3 grid = grid_of(a.tiles_m * a.tiles_n * a.splits);
-  if (p.tile_m == 16) hipLaunchKernelGGL(HIP_KERNEL_NAME(product_kernel<1, 4, 1, ST, WIDE, OUT>), grid, dim3(256), 0, s, a);
-  else if (p.tile_m == 64) hipLaunchKernelGGL(HIP_KERNEL_NAME(product_kernel<4, 4, 1, ST, WIDE, OUT>), grid, dim3(256), 0, s, a);
-  else if (p.tile_m == 128) hipLaunchKernelGGL(HIP_KERNEL_NAME(product_kernel<4, 2, 2, ST, WIDE, OUT>), grid, dim3(256), 0, s, a);
-  else if constexpr (!WIDE) hipLaunchKernelGGL(HIP_KERNEL_NAME(product_tile_kernel<4, ST, OUT>), grid, dim3(512), 0, s, a);
+  if (few) {
+    if (p.tile_m == 16) hipLaunchKernelGGL(HIP_KERNEL_NAME(product_kernel<1, 4, 1, ST, WIDE, OUT>), grid, dim3(256), 0, s, a);
+    else hipLaunchKernelGGL(HIP_KERNEL_NAME(product_kernel<4, 4, 1, ST, WIDE, OUT>), grid, dim3(256), 0, s, a);
+    return;
+  }
+  if (p.tile_m == 64) launch_tile<ST, WIDE, OUT, 1>(a, s);
+  else if (p.tile_m == 128) launch_tile<ST, WIDE, OUT, 2>(a, s);
+  if constexpr (!WIDE) {
+    if (p.tile_m == 192) launch_tile<ST, WIDE, OUT, 3>(a, s);
+    else if (p.tile_m == 256) launch_tile<ST, WIDE, OUT, 4>(a, s);
+  }
 }
 
-void product(const dspark_fp8* x, const dspark_fp8* w, void* out, int32_t out_dtype, int64_t out_stride, void* ws, hipStream_t s) {
+void product(const dspark_fp8* x, int64_t xs_step, const dspark_fp8* w, void* out, int32_t out_dtype, int64_t out_stride, void* ws, hipStream_t s) {
   const ProductPlan p = product_plan(x->n_rows, w->n_rows, x->cols, out_dtype == DSPARK_F32);
   ProductArgs a{};
   a.x = static_cast<const uint8_t*>(x->values);
@@ -124,6 +160,7 @@ void product(const dspark_fp8* x, const dspark_fp8* w, void* out, int32_t out_dt
   a.xs = x->scales;
   a.ws = w->scales;
   a.xs_stride = x->scale_stride;
+  a.xs_step = xs_step;
   a.ws_stride = w->scale_stride;
   a.M = x->n_rows;
   a.N = w->n_rows;
@@ -137,13 +174,13 @@ void product(const dspark_fp8* x, const dspark_fp8* w, void* out, int32_t out_dt
   a.out_stride = p.splits > 1 ? up(a.N, 4) : out_stride;
   const bool wide = out_dtype == DSPARK_F32, bf16 = p.splits == 1 && !wide;
   if (x->scale_dtype == DSPARK_SCALE_F32) {
-    if (wide) launch_tiles<DSPARK_SCALE_F32, true, DSPARK_F32>(p, a, s);
-    else if (bf16) launch_tiles<DSPARK_SCALE_F32, false, DSPARK_BF16>(p, a, s);
-    else launch_tiles<DSPARK_SCALE_F32, false, DSPARK_F32>(p, a, s);
+    if (wide) launch_tiles<DSPARK_SCALE_F32, true, DSPARK_F32>(p, a, a.M <= 64, s);
+    else if (bf16) launch_tiles<DSPARK_SCALE_F32, false, DSPARK_BF16>(p, a, a.M <= 64, s);
+    else launch_tiles<DSPARK_SCALE_F32, false, DSPARK_F32>(p, a, a.M <= 64, s);
   } else {
-    if (wide) launch_tiles<DSPARK_SCALE_E8M0, true, DSPARK_F32>(p, a, s);
-    else if (bf16) launch_tiles<DSPARK_SCALE_E8M0, false, DSPARK_BF16>(p, a, s);
-    else launch_tiles<DSPARK_SCALE_E8M0, false, DSPARK_F32>(p, a, s);
+    if (wide) launch_tiles<DSPARK_SCALE_E8M0, true, DSPARK_F32>(p, a, a.M <= 64, s);
+    else if (bf16) launch_tiles<DSPARK_SCALE_E8M0, false, DSPARK_BF16>(p, a, a.M <= 64, s);
+    else launch_tiles<DSPARK_SCALE_E8M0, false, DSPARK_F32>(p, a, a.M <= 64, s);
   }
   if (p.splits > 1) {
     ProductJoinArgs j{};
@@ -201,7 +238,7 @@ int dspark_quantize_blocks(const dspark_rows* x, const dspark_fp8* out, void* st
   if (out->n_rows != x->n_rows) return fail(DSPARK_EINVAL, "the fp8 matrix has another number of rows");
   if (out->cols != up(x->vocab, 16)) return fail(DSPARK_EINVAL, "fp8 cols must be the rows' width rounded up to a multiple of 16");
   if (x->n_rows == 0) return DSPARK_SUCCESS;
-  quantize(x, out, static_cast<hipStream_t>(stream));
+  quantize(x, out, 1, static_cast<hipStream_t>(stream));
   return host_check_launch();
 }
 
@@ -223,7 +260,7 @@ int dspark_block_product(const dspark_fp8* x, const dspark_fp8* w, void* out, in
   if (x->n_rows == 0 || w->n_rows == 0) return DSPARK_SUCCESS;
   rc = check_ws(product_bytes(x->n_rows, w->n_rows, x->cols), ws, ws_bytes);
   if (rc) return rc;
-  product(x, w, out, out_dtype, out_stride, ws, static_cast<hipStream_t>(stream));
+  product(x, 1, w, out, out_dtype, out_stride, ws, static_cast<hipStream_t>(stream));
   return host_check_launch();
 }
 
@@ -246,10 +283,11 @@ int dspark_block_linear(const dspark_rows* x, const dspark_fp8* w, void* out, in
   rc = check_ws(p.bytes, ws, ws_bytes);
   if (rc) return rc;
   char* at = static_cast<char*>(ws);
-  dspark_fp8 q{at, at + p.scales_at, w->scale_dtype, 1, x->n_rows, p.cols, p.cols, p.blocks};
+  // (its scales by blocks: a tile's rows lie next to each other)
+  dspark_fp8 q{at, at + p.scales_at, w->scale_dtype, 1, x->n_rows, p.cols, p.cols, 1};
   hipStream_t s = static_cast<hipStream_t>(stream);
-  quantize(x, &q, s);
-  product(&q, w, out, out_dtype, out_stride, p.bytes > p.ws_at ? at + p.ws_at : nullptr, s);
+  quantize(x, &q, x->n_rows, s);
+  product(&q, x->n_rows, w, out, out_dtype, out_stride, p.bytes > p.ws_at ? at + p.ws_at : nullptr, s);
   return host_check_launch();
 }
 

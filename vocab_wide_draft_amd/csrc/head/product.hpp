@@ -21,7 +21,7 @@ struct ProductArgs {
   const uint8_t *x, *w;
   int64_t x_stride, w_stride;
   const void *xs, *ws;
-  int64_t xs_stride, ws_stride;
+  int64_t xs_stride, xs_step, ws_stride;  // scales of x: between rows, between blocks of 128 columns
   int64_t M, N;
   int K, steps;             // columns, blocks of 128 of them
   int splits, split_steps;  // parts of the columns, blocks of one part
@@ -42,14 +42,11 @@ __device__ __forceinline__ void load_lds(__amdgpu_buffer_rsrc_t from, uint8_t* t
 }
 
 // The value of a scale.
+__device__ __forceinline__ float e8m0_value(uint32_t e) { return __uint_as_float(e == 0u ? 0x00400000u : e == 255u ? 0x7fc00000u : e << 23); }
 template <int ST>
 __device__ __forceinline__ float scale_value(const void* s, int64_t i) {
-  if constexpr (ST == DSPARK_SCALE_F32) {
-    return static_cast<const float*>(s)[i];
-  } else {
-    const uint32_t e = static_cast<const uint8_t*>(s)[i];
-    return __uint_as_float(e == 0u ? 0x00400000u : e == 255u ? 0x7fc00000u : e << 23);
-  }
+  if constexpr (ST == DSPARK_SCALE_F32) return static_cast<const float*>(s)[i];
+  else return e8m0_value(static_cast<const uint8_t*>(s)[i]);
 }
 
 typedef __bf16 v2b __attribute__((ext_vector_type(2)));
@@ -75,6 +72,24 @@ __device__ __forceinline__ v4i buffer_words(const void* p, int64_t bytes) {
 }
 __device__ __forceinline__ uint32_t lds_address(const void* p) {
   return (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) const char*)p));
+}
+
+// eight neighbouring values of a row
+template <int OUT>
+__device__ __forceinline__ void put_row8(void* row, int64_t n, int64_t N, const float (&v)[8]) {
+  typename El<OUT>::T* p = static_cast<typename El<OUT>::T*>(row) + n;
+  if (n + 8 <= N) {
+    if constexpr (OUT == DSPARK_F32) {
+      *reinterpret_cast<v4f*>(p) = v4f{v[0], v[1], v[2], v[3]};
+      *reinterpret_cast<v4f*>(p + 4) = v4f{v[4], v[5], v[6], v[7]};
+    } else {
+      *reinterpret_cast<v4u*>(p) = v4u{bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3]), bf16_pair(v[4], v[5]), bf16_pair(v[6], v[7])};
+    }
+  } else {
+#pragma unroll
+    for (int l = 0; l < 8; ++l)
+      if (n + l < N) El<OUT>::put(p, l, v[l]);
+  }
 }
 
 // 16 neighbouring values of a row
@@ -179,7 +194,7 @@ __global__ void __launch_bounds__(64 * WN * WM) product_kernel(ProductArgs a) {
       const int sw = static_cast<const uint8_t*>(a.ws)[sn * a.ws_stride + step];
       int sx[UM];
 #pragma unroll
-      for (int u = 0; u < UM; ++u) sx[u] = static_cast<const uint8_t*>(a.xs)[sm[u] + step];
+      for (int u = 0; u < UM; ++u) sx[u] = static_cast<const uint8_t*>(a.xs)[sm[u] + step * a.xs_step];
 #pragma unroll
       for (int t = 0; t < 4; ++t) {
         const v8i fw = frag(at_w + t * 4 * kBlock);
@@ -191,7 +206,7 @@ __global__ void __launch_bounds__(64 * WN * WM) product_kernel(ProductArgs a) {
       const float sw = scale_value<ST>(a.ws, sn * a.ws_stride + step);
       float s[UM];
 #pragma unroll
-      for (int u = 0; u < UM; ++u) s[u] = sw * scale_value<ST>(a.xs, sm[u] + step);
+      for (int u = 0; u < UM; ++u) s[u] = sw * scale_value<ST>(a.xs, sm[u] + step * a.xs_step);
 #pragma unroll
       for (int t = 0; t < 4; ++t) {
         const v8i fw = frag(at_w + t * 4 * kBlock);
@@ -228,74 +243,84 @@ __global__ void __launch_bounds__(64 * WN * WM) product_kernel(ProductArgs a) {
   }
 }
 
-struct Yes { static constexpr bool value = true; };
-struct No { static constexpr bool value = false; };
+template <int ST>
+struct ScaleWord { typedef uint32_t W; };
+template <>
+struct ScaleWord<DSPARK_SCALE_E8M0> { typedef uint8_t W; };
 
-// Tiles of 256 rows of w by 64 U rows of x for many rows: eight waves, two by
-// four, of 128 by 16 U each.  One barrier a step: it stands before the last
-// quarter of a step's matrix instructions, when the wave has read all that it
-// needs of the step's buffer and the next step's has arrived, so that the
-// fetch after next goes into the former and the first reads of the latter
-// run under that quarter.
-template <int U, int ST, int OUT>
-__global__ void __launch_bounds__(512, 2) product_tile_kernel(ProductArgs a) {
-  constexpr int TN = 256, TM = 64 * U, T = 8, ROWS = TN + TM, BUF = ROWS * kBlock;
+// Tiles of 256 rows of w by 16 U WM rows of x for many rows: 2 x WM waves of
+// 128 by 16 U each.  One barrier a step: it stands before the last part of a
+// step's matrix instructions, when the wave has read all that it needs of the
+// step's buffer and the next step's has arrived, so that the fetch after next
+// goes into the former and the first reads of the latter run under that part.
+// A step is one block without branches (past the last one the fetch reads a
+// buffer of no bytes): otherwise the compiler moves the instructions past the
+// barrier.
+template <int WM, int U, int ST, bool WIDE, int OUT>
+__global__ void __launch_bounds__(128 * WM, WM / 2) product_tile_kernel(ProductArgs a) {
+  constexpr int TN = 256, TM = 16 * U * WM, T = 8, NWV = 2 * WM, BUF = (TN + TM) * kBlock, GW = TN / 8 / NWV, GX = TM / 8 / NWV;
+  constexpr int AT_ONCE = WM == 4 ? 2 : 1, PARTS = T / AT_ONCE;  // rows of 16 of w between two reads
+  static_assert(GW == 4 || GW == 8, "a wave's rows of w");
   __shared__ __align__(16) uint8_t lds[2][BUF];
-  __shared__ uint32_t scales[2][TM + 2];
+  typedef typename ScaleWord<ST>::W SW;
+  __shared__ SW scales[2][64 * NWV + 2];  // of w from 64 NWV on
   const int64_t total = a.tiles_m * a.tiles_n * a.splits;
   int64_t b = block_number(total);
   if (b < 0) return;
-  if (total >= 64) {  // (as in product_kernel)
+  // Workgroups go to the eight XCDs in turn: each takes a stretch of tiles,
+  // in groups of kTogether by all of m, so that those in work at a time share
+  // rows of both matrices in its L2.
+  if (total >= 64) {
     const int64_t each = total / 8, more = total % 8, xcd = b & 7;
     b = xcd * each + (xcd < more ? xcd : more) + (b >> 3);
   }
-  const int64_t tm = b % a.tiles_m, rest = b / a.tiles_m;
-  const int64_t tn = rest % a.tiles_n;
-  const int split = (int)(rest / a.tiles_n);
-  const int64_t m0 = tm * TM, n0 = tn * TN;
+  constexpr int kTogether = 4;
+  const int64_t plane = a.tiles_m * a.tiles_n;
+  const int split = (int)(b / plane);
+  b -= split * plane;
+  const int64_t group = b / (a.tiles_m * kTogether), in = b - group * a.tiles_m * kTogether;
+  const int64_t across = a.tiles_n - group * kTogether < kTogether ? a.tiles_n - group * kTogether : kTogether;
+  const int64_t m0 = in / across * TM, n0 = (group * kTogether + in % across) * TN;
   const int first = split * a.split_steps, last = first + a.split_steps < a.steps ? first + a.split_steps : a.steps;
   const int rows_w = a.N - n0 < TN ? (int)(a.N - n0) : TN, rows_x = a.M - m0 < TM ? (int)(a.M - m0) : TM;
   const int tid = (int)threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int wm = wave & 3, wn = wave >> 2, r = lane & 15, g = lane >> 4;
+  const int wm = wave % WM, wn = wave / WM, r = lane & 15, g = lane >> 4;
 
-  // fetches: the first four waves 64 rows of w each, the others 16 U rows of x
-  // each.  The eight chunks of 16 bytes of a row lie in LDS in an order of its
-  // own (key), so that lanes that read one chunk of neighbouring rows hit
-  // different banks.
-  const bool of_w = wave < 4;
-  const int64_t stride = of_w ? a.w_stride : a.x_stride;
-  const int row0 = of_w ? wave * 64 : (wave - 4) * 16 * U;
-  const uint8_t* from = (of_w ? a.w + n0 * a.w_stride : a.x + m0 * a.x_stride);
-  const int64_t bytes = (of_w ? rows_w : rows_x) * stride;
-  const int sub = lane >> 3;
-  // key of a row: w's 0-3 by its last two bits and the bit of 32, x's by its last three
-  const int col_a = ((lane & 7) ^ (of_w ? sub & 3 : sub)) * 16, col_b = of_w ? col_a ^ 64 : col_a;
-  const int base = (row0 + sub) * (int)stride;
-  const uint32_t to0 = lds_address(&lds[0][(of_w ? row0 : TN + row0) * kBlock]);
-  const auto fetch = [&](int step, int buf) {
+  // fetches: 8 GW rows of w and 8 GX rows of x for every wave.  The eight
+  // chunks of 16 bytes of a row lie in LDS in an order of its own, so that
+  // lanes that read one chunk of neighbouring rows hit different banks: the
+  // key is a row's last three bits, for w its last two and the bit of 8.
+  const int sub = lane >> 3, w_row = wave * 8 * GW + sub, x_row = wave * 8 * GX + sub;
+  const uint8_t *from_w = a.w + n0 * a.w_stride, *from_x = a.x + m0 * a.x_stride;
+  const int64_t bytes_w = rows_w * a.w_stride, bytes_x = rows_x * a.x_stride;
+  const int col_x = ((lane & 7) ^ sub) * 16, col_w = ((lane & 7) ^ (sub & 3)) * 16;
+  const int base_w = w_row * (int)a.w_stride, base_x = x_row * (int)a.x_stride;
+  const uint32_t to_w = lds_address(&lds[0][wave * 8 * GW * kBlock]), to_x = lds_address(&lds[0][(TN + wave * 8 * GX) * kBlock]);
+  // the j-th of a wave's GW + GX fetches of a step
+  const auto fetch = [&](int step, int buf, int j) {
     const int64_t at = (int64_t)step * kBlock;
-    const v4i f = buffer_words(from + at, bytes - at);
-    const int left = a.K - (int)at;
-    const int oa = col_a < left ? base + col_a : kPastEnd, ob = col_b < left ? base + col_b : kPastEnd;
-    const uint32_t to = to0 + (uint32_t)(buf * BUF);
-    if (of_w) {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) load_lds_ahead(f, to + j * 1024, (j < 4 ? oa : ob) + j * 8 * (int)stride);
+    const int left = step < last ? a.K - (int)at : 0;
+    if (j < GW) {
+      const int col = col_w ^ (j & 1 ? 64 : 0);
+      load_lds_ahead(buffer_words(from_w + at, left > 0 ? bytes_w - at : 0), to_w + (uint32_t)(buf * BUF + j * 1024),
+                     (col < left ? base_w + col : kPastEnd) + j * 8 * (int)a.w_stride);
     } else {
-#pragma unroll
-      for (int j = 0; j < 2 * U; ++j) load_lds_ahead(f, to + j * 1024, oa + j * 8 * (int)stride);
+      j -= GW;
+      load_lds_ahead(buffer_words(from_x + at, left > 0 ? bytes_x - at : 0), to_x + (uint32_t)(buf * BUF + j * 1024),
+                     (col_x < left ? base_x + col_x : kPastEnd) + j * 8 * (int)a.x_stride);
     }
   };
-  // a thread's scale: of a row of x, or of one of w's two blocks
-  const bool has_scale = tid < TM + 2;
-  const int64_t scale_at = tid < TM ? (m0 + tid < a.M ? m0 + tid : a.M - 1) * a.xs_stride
-                                    : ((n0 + (tid - TM) * 128 < a.N ? n0 + (tid - TM) * 128 : a.N - 1) / kBlock) * a.ws_stride;
-  const void* scale_of = tid < TM ? a.xs : a.ws;
-  const auto fetch_scale = [&](int step) -> uint32_t {
-    if (!has_scale) return 0u;
-    if constexpr (ST == DSPARK_SCALE_E8M0) return static_cast<const uint8_t*>(scale_of)[scale_at + step];
-    else return static_cast<const uint32_t*>(scale_of)[scale_at + step];
+  constexpr int FETCHES = GW + GX, EARLY = (FETCHES + 1) / 2;
+  // a part's share of the fetches from `lo` to `hi`, after its u-th group of instructions
+  const auto share = [&](int step, int buf, int lo, int hi, int u) {
+#pragma unroll
+    for (int j = 0; j < FETCHES; ++j)
+      if (j >= lo + (hi - lo) * u / U && j < lo + (hi - lo) * (u + 1) / U) fetch(step, buf, j);
   };
+  // scales, through LDS: a row of x for each of the first threads (the others read past the end), the wave's block of w
+  const int at_sx = tid < rows_x ? tid * (int)a.xs_stride * (int)sizeof(SW) : kPastEnd;
+  const SW *of_sx = static_cast<const SW*>(a.xs) + m0 * a.xs_stride;
+  const SW* of_sw = static_cast<const SW*>(a.ws) + ((n0 + wn * 128 < a.N ? n0 + wn * 128 : a.N - 1) / kBlock) * a.ws_stride;
 
   v4f acc[T][U];
 #pragma unroll
@@ -303,85 +328,161 @@ __global__ void __launch_bounds__(512, 2) product_tile_kernel(ProductArgs a) {
 #pragma unroll
     for (int u = 0; u < U; ++u) acc[t][u] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
   }
-  const int at_w = (wn * 128 + 32 * (r >> 2) + (r & 3)) * kBlock + ((g ^ (r & 7)) * 16);
+  const int at_w = (wn * 128 + 8 * (r >> 2) + (r & 3)) * kBlock + ((g ^ (r & 7)) * 16);
   const int at_x = (TN + wm * 16 * U + r) * kBlock + ((g ^ (r & 7)) * 16);
+  // the matrix instruction's row 4 g + i of its t-th 16 is row 32 (t / 2) + 8 g
+  // + 4 (t % 2) + i, so that a lane holds eight neighbours of an output row and
+  // four lanes 64 or 128 bytes of it
+  const auto row_of = [](int t) { return 32 * (t >> 1) + 4 * (t & 1); };
   const auto frag = [&](int buf, int at) {
     const v4i lo = *reinterpret_cast<const v4i*>(&lds[0][buf * BUF + at]), hi = *reinterpret_cast<const v4i*>(&lds[0][buf * BUF + (at ^ 64)]);
     return v8i{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
   };
 
-  v8i fx[U], fw[2][2];
-  uint32_t sx[U], sw, next_scale = 0;
+  v8i fx[U], fw[2][AT_ONCE];
+  v8b wx[WIDE ? U : 1][4];  // a step's rows of x in bf16
+  uint32_t sx[U], sw;
+  SW next_sx, next_sw;  // (not touched before they have arrived: that would wait for the fetches behind them)
+  const auto put_scales = [&](int buf) {
+    scales[buf][tid] = next_sx;
+    scales[buf][64 * NWV + wn] = next_sw;
+  };
+  const auto fetch_scales = [&](int step) {
+    const __amdgpu_buffer_rsrc_t f = buffer_of(of_sx + (int64_t)step * a.xs_step, ((rows_x - 1) * a.xs_stride + 1) * (int64_t)sizeof(SW));
+    if constexpr (ST == DSPARK_SCALE_E8M0) next_sx = (SW)__builtin_amdgcn_raw_buffer_load_b8(f, at_sx, 0, 0);
+    else next_sx = __builtin_amdgcn_raw_buffer_load_b32(f, at_sx, 0, 0);
+    next_sw = of_sw[step];
+  };
   const auto read_scales = [&](int buf) {
-    sw = scales[buf][TM + wn];
+    sw = scales[buf][64 * NWV + wn];
 #pragma unroll
     for (int u = 0; u < U; ++u) sx[u] = scales[buf][wm * 16 * U + 16 * u + r];
-    if constexpr (ST == DSPARK_SCALE_F32) {
+    if constexpr (WIDE && ST == DSPARK_SCALE_E8M0) {
+      const float w = e8m0_value(sw);
+#pragma unroll
+      for (int u = 0; u < U; ++u) sx[u] = __float_as_uint(w * e8m0_value(sx[u]));
+    } else if constexpr (ST == DSPARK_SCALE_F32) {
 #pragma unroll
       for (int u = 0; u < U; ++u) sx[u] = __float_as_uint(__uint_as_float(sw) * __uint_as_float(sx[u]));
     }
   };
-  const auto multiply = [&](int t, int u, const v8i& w) {
-    if constexpr (ST == DSPARK_SCALE_E8M0) {
-      acc[t][u] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w, fx[u], acc[t][u], 0, 0, 0, (int)sw, 0, (int)sx[u]);
-    } else {
-      const v4f p = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w, fx[u], v4f{0.0f, 0.0f, 0.0f, 0.0f}, 0, 0, 0, 127, 0, 127);
+  // Products with scales of their own are added to the sums one group of
+  // instructions later, while the next ones run.
+  constexpr bool LATER = ST == DSPARK_SCALE_F32 || WIDE;
+  v4f late[AT_ONCE];
+  const auto add_late = [&](int t, int u) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) acc[t][u][i] = __builtin_fmaf(p[i], __uint_as_float(sx[u]), acc[t][u][i]);
+    for (int k = 0; k < AT_ONCE; ++k) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[t + k][u][i] = __builtin_fmaf(late[k][i], __uint_as_float(sx[u]), acc[t + k][u][i]);
     }
   };
+  // rows t .. t + AT_ONCE - 1 of w by u of x; before them, those of last_t and last_u (-1: none)
+  const auto multiply = [&](int t, int u, const v8i (&w)[AT_ONCE], int last_t, int last_u) {
+    if constexpr (!LATER) {
+#pragma unroll
+      for (int k = 0; k < AT_ONCE; ++k)
+        acc[t + k][u] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w[k], fx[u], acc[t + k][u], 0, 0, 0, (int)sw, 0, (int)sx[u]);
+    } else {
+      v4f now[AT_ONCE];
+#pragma unroll
+      for (int k = 0; k < AT_ONCE; ++k) {
+        now[k] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+        if constexpr (WIDE) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            now[k] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(widen(w[k][2 * j], w[k][2 * j + 1]), wx[u][j], now[k], 0, 0, 0);
+        } else {
+          now[k] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w[k], fx[u], now[k], 0, 0, 0, 127, 0, 127);
+        }
+      }
+      if (last_t >= 0) add_late(last_t, last_u);
+#pragma unroll
+      for (int k = 0; k < AT_ONCE; ++k) late[k] = now[k];
+    }
+  };
+  const auto widen_x = [&]() {
+    if constexpr (WIDE) {
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) wx[u][j] = widen(fx[u][2 * j], fx[u][2 * j + 1]);
+      }
+    }
+  };
+  const auto read_w = [&](int buf, int part, int to) {
+#pragma unroll
+    for (int i = 0; i < AT_ONCE; ++i) fw[to][i] = frag(buf, at_w + row_of(part * AT_ONCE + i) * kBlock);
+  };
+  const auto part = [&](int p, auto between) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      multiply(p * AT_ONCE, u, fw[p & 1], u > 0 ? p * AT_ONCE : (p - 1) * AT_ONCE, u > 0 ? u - 1 : U - 1);
+      between(u);
+    }
+  };
+  const auto nothing = [](int) {};
 
   if (first < last) {
-    next_scale = fetch_scale(first);
-    fetch(first, 0);
-    if (has_scale) scales[0][tid] = next_scale;
-    if (first + 1 < last) next_scale = fetch_scale(first + 1);
+    const int second = first + 1 < last ? first + 1 : first;
+    fetch_scales(first);
+#pragma unroll
+    for (int j = 0; j < FETCHES; ++j) fetch(first, 0, j);
     loads_arrived();
+    put_scales(0);
     __syncthreads();
-    if (first + 1 < last) fetch(first + 1, 1);
+    fetch_scales(second);
+#pragma unroll
+    for (int j = 0; j < EARLY; ++j) fetch(first + 1, 1, j);
     read_scales(0);
 #pragma unroll
     for (int u = 0; u < U; ++u) fx[u] = frag(0, at_x + u * 16 * kBlock);
-    fw[0][0] = frag(0, at_w);
-    fw[0][1] = frag(0, at_w + 512);
-  }
-  // one step; MORE: another one follows
-  const auto run = [&](int step, int buf, auto more) {
-    constexpr bool MORE = decltype(more)::value;
+    read_w(0, 0, 0);
+    for (int step = first; step + 1 < last; ++step) {
+      const int buf = (step - first) & 1;
+      widen_x();
 #pragma unroll
-    for (int c = 0; c < T / 2; ++c) {
-      if (c < T / 2 - 1) {
-        fw[(c + 1) & 1][0] = frag(buf, at_w + (2 * c + 2) * 512);
-        fw[(c + 1) & 1][1] = frag(buf, at_w + (2 * c + 3) * 512);
-      } else if constexpr (MORE) {
-        if (has_scale) scales[buf ^ 1][tid] = next_scale;
-        loads_arrived();
-        __syncthreads();  // the next step's buffer has arrived, this one has been read
-        if (step + 2 < last) {
-          next_scale = fetch_scale(step + 2);
-          fetch(step + 2, buf);
-        }
-        fw[(c + 1) & 1][0] = frag(buf ^ 1, at_w);
-        fw[(c + 1) & 1][1] = frag(buf ^ 1, at_w + 512);
-      }
-      __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        multiply(2 * c, u, fw[c & 1][0]);
-        multiply(2 * c + 1, u, fw[c & 1][1]);
-        if constexpr (MORE) {
-          if (c == T / 2 - 1) {
+      for (int p = 0; p < PARTS - 1; ++p) {
+        read_w(buf, p + 1, (p + 1) & 1);
+        __builtin_amdgcn_sched_barrier(0);
+        if (p == 0) {
+          part(p, [&](int u) {
             __builtin_amdgcn_sched_barrier(0);
-            fx[u] = frag(buf ^ 1, at_x + u * 16 * kBlock);
-          }
+            share(step + 1, buf ^ 1, EARLY, FETCHES, u);
+            __builtin_amdgcn_sched_barrier(0);
+          });
+        } else {
+          part(p, nothing);
         }
+        __builtin_amdgcn_sched_barrier(0);
       }
+      loads_arrived();
+      put_scales(buf ^ 1);
+      __syncthreads();  // the next step's buffer has arrived, this one has been read
+      read_w(buf ^ 1, 0, PARTS & 1);
+      const int ahead = step + 2 < last ? step + 2 : step;
+      fetch_scales(ahead);
       __builtin_amdgcn_sched_barrier(0);
+      part(PARTS - 1, [&](int u) {
+        __builtin_amdgcn_sched_barrier(0);
+        fx[u] = frag(buf ^ 1, at_x + u * 16 * kBlock);
+        share(step + 2, buf, 0, EARLY, u);
+        __builtin_amdgcn_sched_barrier(0);
+      });
+      if constexpr (LATER) add_late(T - AT_ONCE, U - 1);
+      __builtin_amdgcn_sched_barrier(0);
+      read_scales(buf ^ 1);
     }
-    if constexpr (MORE) read_scales(buf ^ 1);
-  };
-  for (int step = first; step + 1 < last; ++step) run(step, (step - first) & 1, Yes{});
-  if (first < last) run(last - 1, (last - 1 - first) & 1, No{});
+    const int buf = (last - 1 - first) & 1;
+    widen_x();
+#pragma unroll
+    for (int p = 0; p < PARTS; ++p) {
+      if (p + 1 < PARTS) read_w(buf, p + 1, (p + 1) & 1);
+      part(p, nothing);
+    }
+    if constexpr (LATER) add_late(T - AT_ONCE, U - 1);
+    loads_arrived();  // (the fetches past the last step write to LDS, too)
+  }
 
   char* out = static_cast<char*>(a.out);
   if (a.splits > 1) out += (int64_t)split * a.M * a.out_stride * (int64_t)sizeof(typename El<OUT>::T);
@@ -389,15 +490,12 @@ __global__ void __launch_bounds__(512, 2) product_tile_kernel(ProductArgs a) {
   for (int u = 0; u < U; ++u) {
     const int64_t m = m0 + wm * 16 * U + 16 * u + r;
     if (m >= a.M) continue;
+    char* row = out + m * a.out_stride * (int64_t)sizeof(typename El<OUT>::T);
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      float v[16];
-#pragma unroll
-      for (int t = 0; t < 4; ++t) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) v[4 * t + i] = acc[4 * h + t][u][i];
-      }
-      put_row16<OUT>(out + m * a.out_stride * (int64_t)sizeof(typename El<OUT>::T), n0 + wn * 128 + 32 * g + 16 * h, a.N, v);
+    for (int t = 0; t < T; t += 2) {
+      const v4f lo = acc[t][u], hi = acc[t + 1][u];
+      const float v[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+      put_row8<OUT>(row, n0 + wn * 128 + row_of(t) + 8 * g, a.N, v);
     }
   }
 }

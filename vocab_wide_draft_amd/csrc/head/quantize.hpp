@@ -12,7 +12,7 @@ struct QuantArgs {
   uint8_t* v;
   int64_t v_stride;
   void* s;
-  int64_t s_stride;
+  int64_t s_stride, s_step;  // scales: between rows, between blocks of 128 columns
   int chunks;  // workgroups of a row
 };
 
@@ -122,7 +122,7 @@ __global__ void __launch_bounds__(kSliceBS) quantize_rows_kernel(QuantArgs a) {
     const int c = c0 + (u * kSliceBS + (int)threadIdx.x) * N;
     const BlockScale<ST> s(most_lanes<LANES>(most_of<DT, N>(q[u])));
     if (c < a.cols) put_values<DT, N, ST>(a.v + r * a.v_stride + c, q[u], s);
-    if (c % kBlock == 0 && c / kBlock < a.blocks) s.put(a.s, r * a.s_stride + c / kBlock);
+    if (c % kBlock == 0 && c / kBlock < a.blocks) s.put(a.s, r * a.s_stride + c / kBlock * a.s_step);
   }
 }
 
@@ -154,7 +154,7 @@ __global__ void __launch_bounds__(kSliceBS) quantize_tiles_kernel(QuantArgs a) {
     const int64_t r = r0 + u * ROWS;
     if (r < a.n && c < a.cols) put_values<DT, N, ST>(a.v + r * a.v_stride + c, q[u], s);
   }
-  if (threadIdx.x == 0) s.put(a.s, rb * a.s_stride + cb);
+  if (threadIdx.x == 0) s.put(a.s, rb * a.s_stride + cb * a.s_step);
 }
 
 }  // namespace dspark
