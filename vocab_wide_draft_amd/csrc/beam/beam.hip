@@ -57,25 +57,11 @@ int64_t span(const int64_t (&size)[4], const int64_t (&stride)[4], int64_t row_b
   return reach;
 }
 
-template <int BYTES>
-void launch_reorder_as(const ReorderArgs& a, hipStream_t s) {
-  const dim3 grid = grid_of(a.first[a.n_states]), block(kSliceBS);
-  if constexpr (BYTES >= 8) {
-    if (a.beams <= 8) {
-      hipLaunchKernelGGL(HIP_KERNEL_NAME(reorder_kernel<BYTES, 8>), grid, block, 0, s, a);
-      return;
-    }
-    if (a.beams <= 16) {
-      hipLaunchKernelGGL(HIP_KERNEL_NAME(reorder_kernel<BYTES, 16>), grid, block, 0, s, a);
-      return;
-    }
-  }
-  if constexpr (BYTES == 8) {
-    hipLaunchKernelGGL(HIP_KERNEL_NAME(reorder_kernel<BYTES, 32>), grid, block, 0, s, a);
-  } else if constexpr (BYTES < 8) {
-    if (a.beams <= 16) hipLaunchKernelGGL(HIP_KERNEL_NAME(reorder_kernel<BYTES, 16>), grid, block, 0, s, a);
-    else hipLaunchKernelGGL(HIP_KERNEL_NAME(reorder_kernel<BYTES, 64>), grid, block, 0, s, a);
-  }
+template <int BYTES, int NB>
+void launch_reorder(const ReorderArgs& a, int per, hipStream_t s) {
+  const dim3 grid = grid_of(a.first[a.n_states]);
+  if (per == 2) hipLaunchKernelGGL(HIP_KERNEL_NAME(reorder_kernel<BYTES, NB, 2>), grid, dim3(kSliceBS), 0, s, a);
+  else hipLaunchKernelGGL(HIP_KERNEL_NAME(reorder_kernel<BYTES, NB, 1>), grid, dim3(kSliceBS), 0, s, a);
 }
 
 }  // namespace
@@ -147,7 +133,6 @@ int dspark_beam_reorder(const dspark_state* states, int32_t n_states, int64_t re
   if (requests < 0 || requests > (1 << 24)) return fail(DSPARK_EINVAL, "requests out of range");
   if (beams < 1 || beams > DSPARK_BEAM_MAX) return fail(DSPARK_EINVAL, "beams must be in [1, DSPARK_BEAM_MAX]");
   const bool in_place = states[0].in == states[0].out;
-  uint64_t bits = 0;
   int64_t least = INT64_MAX;
   for (int i = 0; i < n_states; ++i) {
     const dspark_state& t = states[i];
@@ -163,7 +148,6 @@ int dspark_beam_reorder(const dspark_state* states, int32_t n_states, int64_t re
     for (int d = 0; d < 4; ++d) {
       if (size[d] <= 1) continue;
       if (in_place && in[d] != out[d]) return fail(DSPARK_EINVAL, "in place needs the same strides");
-      bits |= (uint64_t)in[d] | (uint64_t)out[d];
     }
     if (!in_place) {
       const char *x = static_cast<const char*>(t.in), *y = static_cast<const char*>(t.out);
@@ -171,15 +155,12 @@ int dspark_beam_reorder(const dspark_state* states, int32_t n_states, int64_t re
     }
     for (int j = 0; j < i; ++j)
       if (requests > 0 && states[j].out == t.out) return fail(DSPARK_EINVAL, "a state is listed twice");
-    bits |= (uint64_t)t.row_bytes | (uint64_t)reinterpret_cast<uintptr_t>(t.in) | (uint64_t)reinterpret_cast<uintptr_t>(t.out);
     if (t.rows > 0) least = std::min(least, t.rows);
   }
   if (requests == 0) return DSPARK_SUCCESS;
   if (!parent || !req_status) return fail(DSPARK_EINVAL, "NULL parent or req_status");
-  // vectors of what divides every address, and of which a thread can hold one of every beam
-  int bytes = 16;
-  while (bits % (uint64_t)bytes != 0) bytes /= 2;
-  if (beams > 16) bytes = std::min(bytes, beams > 32 ? 4 : 8);
+  // 16 bytes of every beam to a thread, fewer where that would be too many registers
+  const int bytes = beams <= 16 ? 16 : beams <= 32 ? 8 : 4;
   hipStream_t s = static_cast<hipStream_t>(stream);
   for (int at = 0; at < n_states; at += kStates) {
     ReorderArgs a{};
@@ -191,6 +172,8 @@ int dspark_beam_reorder(const dspark_state* states, int32_t n_states, int64_t re
     a.status = at == 0 ? req_status : nullptr;
     a.least_rows = least == INT64_MAX ? INT32_MAX : least;
     a.in_place = in_place;
+    bool flat = true;
+    int64_t vectors = 0;
     for (int i = 0; i < a.n_states; ++i) {
       const dspark_state& t = states[at + i];
       ReorderState& u = a.state[i];
@@ -204,18 +187,29 @@ int dspark_beam_reorder(const dspark_state* states, int32_t n_states, int64_t re
       u.out_beam = t.out_beam;
       u.out_outer = t.out_outer;
       u.out_row = t.out_row;
+      u.row_bytes = t.row_bytes;
       u.rows = t.rows;
       u.outer = t.outer;
-      u.vectors = (uint32_t)(t.row_bytes / bytes);
       u.flat = t.rows <= 1 || (t.in_row == t.row_bytes && t.out_row == t.row_bytes);
-      u.chunks = (uint32_t)((std::max<int64_t>(t.rows, 1) * (int64_t)u.vectors + kSliceBS - 1) / kSliceBS);
-      a.first[i + 1] = a.first[i] + requests * t.outer * (int64_t)u.chunks;
+      u.vectors = (uint32_t)((t.row_bytes + bytes - 1) / bytes);
+      flat = flat && (u.flat || t.row_bytes % bytes == 0);
+      vectors += requests * t.outer * std::max<int64_t>(t.rows, 1) * (int64_t)u.vectors;
     }
-    if (bytes == 16) launch_reorder_as<16>(a, s);
-    else if (bytes == 8) launch_reorder_as<8>(a, s);
-    else if (bytes == 4) launch_reorder_as<4>(a, s);
-    else if (bytes == 2) launch_reorder_as<2>(a, s);
-    else launch_reorder_as<1>(a, s);
+    // two vectors of every beam on their way to a thread, where the states are large and their rows hold whole vectors
+    const int per = !flat || vectors < (1 << 20) ? 1 : 2;
+    for (int i = 0; i < a.n_states; ++i) {
+      ReorderState& u = a.state[i];
+      const int64_t rows = std::max<int64_t>(u.rows, 1);
+      // (a flat stretch has one vector more for what is left behind the whole ones)
+      const int64_t all = u.flat ? rows * u.row_bytes / bytes + 1 : rows * (int64_t)u.vectors;
+      u.chunks = (uint32_t)((all + kSliceBS * per - 1) / (kSliceBS * per));
+      a.first[i + 1] = a.first[i] + requests * u.outer * (int64_t)u.chunks;
+    }
+    if (beams <= 4) launch_reorder<16, 4>(a, per, s);
+    else if (beams <= 8) launch_reorder<16, 8>(a, per, s);
+    else if (beams <= 16) launch_reorder<16, 16>(a, per, s);
+    else if (beams <= 32) launch_reorder<8, 32>(a, per, s);
+    else launch_reorder<4, 64>(a, per, s);
   }
   return host_check_launch();
 }
