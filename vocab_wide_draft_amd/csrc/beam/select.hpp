@@ -15,7 +15,7 @@
 // the weights' mean |t| below 18 for 2^20 logits, 2^-24 (0.7 * 18 + 2 + 8) =
 // 1.4e-6).  Where two neighbours in the merged order of different beams lie
 // closer than twice that, their beams' log-sum-exps are computed again in
-// binary64, and the lists are merged again.
+// binary64, and what decides is compared again.
 #pragma once
 #include "../logits/slices.hpp"
 #include "../logits/top.hpp"
@@ -27,9 +27,11 @@ constexpr int kBeamOut = 128;   // candidates selected
 constexpr double kLseOff = 2e-6;
 
 struct BeamPart {
-  float m[kSliceNW], sum[kSliceNW];  // of each wave: its maximum, the sum of exponentials relative to it
-  int32_t flags;                     // 1: a NaN, 2: a +inf
-  int32_t count;                     // candidates in the slice's list
+  float m;              // the slice's maximum
+  float sum[kSliceNW];  // of each wave: the sum of exponentials relative to it
+  int32_t flags;        // 1: a NaN, 2: a +inf
+  int32_t count;        // candidates in the slice's list
+  int32_t reserved;
 };
 
 struct BeamArgs {
@@ -58,11 +60,34 @@ __device__ __forceinline__ uint64_t beam_key(float x, int id) { return ((uint64_
 __device__ __forceinline__ int beam_id(uint64_t k) { return (int)~(uint32_t)k; }
 __device__ __forceinline__ float beam_logit(uint64_t k) { return top_key_value<DSPARK_F32>((uint32_t)(k >> 32)); }
 
+// The largest 16-bit key that at least n of 64 groups' maxima (a lane's v)
+// reach, or for n > 32 of the 256 values themselves: n values do, too.
+__device__ __forceinline__ uint32_t reached_by(uint4 v, int n) {
+  uint32_t T = 0;
+  if (n <= 32) {
+    const uint32_t a = v.x > v.y ? v.x : v.y, b = v.z > v.w ? v.z : v.w, m = a > b ? a : b;
+#pragma unroll
+    for (int bit = 15; bit >= 0; --bit) {
+      const uint32_t up = T | (1u << bit);
+      if (__builtin_popcountll(__ballot(m >= up)) >= n) T = up;
+    }
+  } else {
+#pragma unroll
+    for (int bit = 15; bit >= 0; --bit) {
+      const uint32_t up = T | (1u << bit);
+      const int reach = __builtin_popcountll(__ballot(v.x >= up)) + __builtin_popcountll(__ballot(v.y >= up)) +
+                        __builtin_popcountll(__ballot(v.z >= up)) + __builtin_popcountll(__ballot(v.w >= up));
+      if (reach >= n) T = up;
+    }
+  }
+  return T;
+}
+
 template <int DT, int U>
 __global__ void __launch_bounds__(kSliceBS) beam_slice_kernel(BeamArgs a) {
-  constexpr int N = kVec<DT>, SLICE = U * kSliceBS * N;
+  constexpr int N = kVec<DT>, SLICE = U * kSliceBS * N, WORDS = (U * N + 31) / 32;
   __shared__ __align__(16) uint32_t most[kSliceBS];
-  __shared__ float thr;
+  __shared__ float wave_m[kSliceNW];
   __shared__ uint32_t any_flags, held, counts[kSliceNW];
   typedef typename El<DT>::T XT;
   int64_t r;
@@ -94,27 +119,32 @@ __global__ void __launch_bounds__(kSliceBS) beam_slice_kernel(BeamArgs a) {
     for (int l = 0; l < N; ++l) m = __builtin_fmaxf(m, x[i][l]);
   }
   most[tid] = m != m || m == -__builtin_inff() ? 0u : key32(m) >> 16;
+  const float own_m = wave_reduce(m, -__builtin_inff(), [](float u, float v) { return __builtin_fmaxf(u, v); });
+  if (lane_id() == 0) wave_m[wave_id()] = own_m;
   __syncthreads();
-  if (wave_id() == 0) {
-    // the largest 16-bit key that at least n_out of the threads' maxima reach: n_out logits of the slice do, too
-    const uint4 o = *reinterpret_cast<const uint4*>(most + 4 * lane_id());
-    uint32_t T = 0;
+  float M = wave_m[0];
 #pragma unroll
-    for (int bit = 15; bit >= 0; --bit) {
-      const uint32_t up = T | (1u << bit);
-      const int reach = __builtin_popcountll(__ballot(o.x >= up)) + __builtin_popcountll(__ballot(o.y >= up)) +
-                        __builtin_popcountll(__ballot(o.z >= up)) + __builtin_popcountll(__ballot(o.w >= up));
-      if (reach >= a.n_out) T = up;
-    }
-    const float t = top_key_value<DSPARK_BF16>(T);  // (-inf is no candidate)
-    if (lane_id() == 0) thr = t >= -3.4028235e38f ? t : -3.4028235e38f;
+  for (int w = 1; w < kSliceNW; ++w) M = __builtin_fmaxf(M, wave_m[w]);
+  // the threshold, by every wave for itself: -inf is no candidate
+  float t = top_key_value<DSPARK_BF16>(reached_by(*reinterpret_cast<const uint4*>(most + 4 * lane_id()), a.n_out));
+  t = t >= -3.4028235e38f ? t : -3.4028235e38f;
+  uint32_t mask[WORDS];  // element l of vector i at bit N i + N - 1 - l
+#pragma unroll
+  for (int w = 0; w < WORDS; ++w) mask[w] = 0u;
+#pragma unroll
+  for (int i = U - 1; i >= 0; --i) {
+#pragma unroll
+    for (int l = 0; l < N; ++l) push_ge(mask[i * N / 32], x[i][l], t);
   }
-  const float M = wave_reduce(m, -__builtin_inff(), [](float u, float v) { return __builtin_fmaxf(u, v); });
+  uint32_t mine = 0;
+#pragma unroll
+  for (int w = 0; w < WORDS; ++w) mine += (uint32_t)__builtin_popcount(mask[w]);
+  const uint32_t at = mine ? atomicAdd(&held, mine) : 0u;  // in any order: the keys have one
   const float ref = M == -__builtin_inff() ? 0.0f : M;
   double sum = 0.0;
 #pragma unroll
   for (int i = 0; i < U; ++i) sum += (double)exp_sum(a.x, ref, x[i]);
-  if (sum != sum || M == __builtin_inff()) {  // a NaN or a +inf in this thread, or the wave's
+  if (sum != sum || M == __builtin_inff()) {  // a NaN or a +inf in this thread, or the slice's
     uint32_t flags = 0;
 #pragma unroll
     for (int i = 0; i < U; ++i) {
@@ -124,69 +154,67 @@ __global__ void __launch_bounds__(kSliceBS) beam_slice_kernel(BeamArgs a) {
     if (flags) atomicOr(&any_flags, flags);
   }
   const double wsum = wave_sum(sum);
-  if (lane_id() == 63) {
-    p.m[wave_id()] = M;
-    p.sum[wave_id()] = (float)wsum;
-  }
+  if (lane_id() == 63) p.sum[wave_id()] = (float)wsum;
   __syncthreads();
-  const float t = thr;
-  uint32_t mine = 0;
-#pragma unroll
-  for (int i = 0; i < U; ++i) {
-#pragma unroll
-    for (int l = 0; l < N; ++l) mine += x[i][l] >= t ? 1u : 0u;
-  }
-  const uint32_t of_wave = wave_sum(mine);
-  if (lane_id() == 0) counts[wave_id()] = of_wave;
-  __syncthreads();
-  uint32_t total = 0;
-#pragma unroll
-  for (int w = 0; w < kSliceNW; ++w) total += counts[w];
-  uint64_t least = (uint64_t)key32(t) << 32;
-  if (total > (uint32_t)a.cap) {
-    // too many (equal logits): the key that exactly n_out of them reach, by
-    // halving (uniform; a sum over the workgroup each time)
-    uint64_t lo = least, hi = ~0ull;  // reached by more than n_out, by fewer
-    for (;;) {
-      const uint64_t mid = lo + ((hi - lo) >> 1);
-      mine = 0;
-#pragma unroll
-      for (int i = 0; i < U; ++i) {
-#pragma unroll
-        for (int l = 0; l < N; ++l)
-          mine += x[i][l] >= t && beam_key(x[i][l], start + (i * kSliceBS + tid) * N + l) >= mid ? 1u : 0u;
-      }
-      const uint32_t w = wave_sum(mine);
-      __syncthreads();
-      if (lane_id() == 0) counts[wave_id()] = w;
-      __syncthreads();
-      total = 0;
-#pragma unroll
-      for (int v = 0; v < kSliceNW; ++v) total += counts[v];
-      least = mid;
-      if (total == (uint32_t)a.n_out || hi - lo <= 1) break;  // (no two keys are alike: the former comes)
-      if (total > (uint32_t)a.n_out) lo = mid;
-      else hi = mid;
-    }
-  }
   uint64_t* list = a.cand + (r * a.slices + s) * a.cap;
+  const uint32_t total = held;
+  if (tid == 0) {
+    p.m = M;
+    p.flags = (int32_t)any_flags;
+    p.count = total <= (uint32_t)a.cap ? (int)total : a.n_out;
+  }
+  if (total <= (uint32_t)a.cap) {  // (uniform)
+    uint32_t pos = at;
+#pragma unroll
+    for (int w = 0; w < WORDS; ++w) {
+      for (uint32_t left = mask[w]; left; left &= left - 1) {
+        const int bit = __builtin_ctz(left), e = w * 32 + (bit & ~(N - 1)) + (N - 1 - (bit & (N - 1)));  // vector and element
+        float v = x[0][0];
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+#pragma unroll
+          for (int l = 0; l < N; ++l) v = e == i * N + l ? x[i][l] : v;
+        }
+        list[pos++] = beam_key(v, start + (e / N * kSliceBS + tid) * N + e % N);
+      }
+    }
+    return;
+  }
+  // too many (equal logits): the key that exactly n_out of them reach, by
+  // halving (uniform; a sum over the workgroup each time)
+  uint64_t lo = (uint64_t)key32(t) << 32, hi = ~0ull, least;  // reached by more than n_out, by fewer
+  for (;;) {
+    least = lo + ((hi - lo) >> 1);
+    mine = 0;
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+#pragma unroll
+      for (int l = 0; l < N; ++l)
+        mine += x[i][l] >= t && beam_key(x[i][l], start + (i * kSliceBS + tid) * N + l) >= least ? 1u : 0u;
+    }
+    const uint32_t w = wave_sum(mine);
+    __syncthreads();
+    if (lane_id() == 0) counts[wave_id()] = w;
+    __syncthreads();
+    uint32_t reach = 0;
+#pragma unroll
+    for (int v = 0; v < kSliceNW; ++v) reach += counts[v];
+    if (reach == (uint32_t)a.n_out || hi - lo <= 1) break;  // (no two keys are alike: the former comes)
+    if (reach > (uint32_t)a.n_out) lo = least;
+    else hi = least;
+  }
+  if (tid == 0) held = 0u;
+  __syncthreads();
 #pragma unroll
   for (int i = 0; i < U; ++i) {
 #pragma unroll
     for (int l = 0; l < N; ++l) {
-      if (x[i][l] >= t) {
-        const uint64_t k = beam_key(x[i][l], start + (i * kSliceBS + tid) * N + l);
-        if (k >= least) {
-          const uint32_t at = atomicAdd(&held, 1u);  // in any order: the keys have one
-          if (at < (uint32_t)a.cap) list[at] = k;
-        }
+      const uint64_t k = beam_key(x[i][l], start + (i * kSliceBS + tid) * N + l);
+      if (x[i][l] >= t && k >= least) {
+        const uint32_t to = atomicAdd(&held, 1u);
+        if (to < (uint32_t)a.cap) list[to] = k;
       }
     }
-  }
-  __syncthreads();
-  if (tid == 0) {
-    p.flags = (int32_t)any_flags;
-    p.count = held < (uint32_t)a.cap ? (int)held : a.cap;
   }
 }
 
@@ -246,83 +274,85 @@ __device__ double beam_exact_lse(const BeamArgs& a, int64_t r, float M, double* 
   return (double)M + log(sum);
 }
 
-// One workgroup per request.
+// The join's LDS: what a request's beams came to, and behind it either the
+// candidates that may be among the best, or the beams' sorted lists.
+constexpr int kBeamNear = 1024;  // candidates held
+struct BeamScratch {
+  double lse[kBeams];
+  float m[kBeams], score[kBeams];
+  int32_t n_list[kBeams], flags[kBeams];
+  bool ended[kBeams];
+  double red[16];
+  uint32_t most[512];
+  uint16_t count[kBeams * kBeamSlices];  // of every slice's list
+  uint32_t unsure[2], near;
+};
+struct BeamNear {
+  uint64_t key[kBeamNear];
+  double score[kBeamNear];
+  uint16_t order[kBeamNear];
+  uint8_t beam[kBeamNear];
+};
+constexpr size_t beam_lists_bytes(int beams, int n_out, int waves) {
+  return (size_t)beams * (size_t)n_out * 8 + (size_t)waves * (kBeamOut * 8 + (kBeamSlices + 2) * 4);
+}
+constexpr size_t beam_join_bytes(int beams, int n_out, int waves) {
+  return sizeof(BeamNear) > beam_lists_bytes(beams, n_out, waves) ? sizeof(BeamNear) : beam_lists_bytes(beams, n_out, waves);
+}
+
+__device__ __forceinline__ double beam_off(const BeamScratch& sh, int b) {
+  return kLseOff + 1e-15 * (__builtin_fabs((double)sh.score[b]) + __builtin_fabs(sh.lse[b]));
+}
+__device__ __forceinline__ void beam_put(const BeamArgs& a, int64_t at, int beam, uint64_t key, double score, bool ended) {
+  a.parent[at] = beam;
+  a.token[at] = beam_id(key);
+  a.score[at] = (float)score;
+  a.out_finished[at] = ended || beam_id(key) == a.end_token ? 1 : 0;
+}
+__device__ __forceinline__ void beam_put_empty(const BeamArgs& a, int64_t at) {
+  a.parent[at] = -1;
+  a.token[at] = 0;
+  a.score[at] = -__builtin_inff();
+  a.out_finished[at] = 0;
+}
+
+// The log-sum-exps of the beams in `todo` again in binary64.
 template <int DT, int NWV>
-__global__ void __launch_bounds__(64 * NWV) beam_join_kernel(BeamArgs a) {
-  extern __shared__ __align__(16) uint64_t lists[];  // [beams][n_out], sorted
-  __shared__ uint32_t first[NWV][kBeamSlices + 1];
-  __shared__ uint64_t kept[NWV][kBeamOut];
-  __shared__ double lse[kBeams], scratch[NWV];
-  __shared__ float row_m[kBeams];
-  __shared__ int32_t n_list[kBeams], flags[kBeams];
-  __shared__ uint64_t again;
-  const int64_t q = block_number(a.requests);
-  if (q < 0) return;
+__device__ void beam_exact(const BeamArgs& a, int64_t q, uint64_t todo, BeamScratch& sh) {
+  for (int b = 0; b < a.beams; ++b) {
+    if (!(todo >> b & 1ull)) continue;
+    const double exact = beam_exact_lse<DT, NWV>(a, q * a.beams + b, sh.m[b], sh.red);
+    if (threadIdx.x == 0) sh.lse[b] = exact;
+  }
+  __syncthreads();
+}
+
+// The general way: each beam's best in a sorted list, by its wave, then one
+// wave merges the lists, a beam to a lane.
+template <int DT, int NWV>
+__device__ void beam_join_lists(const BeamArgs& a, int64_t q, BeamScratch& sh, uint64_t* lists) {
   const int lane = lane_id(), wave = wave_id(), n = a.n_out;
+  uint64_t* kept = lists + a.beams * n + wave * kBeamOut;
+  uint32_t* first = reinterpret_cast<uint32_t*>(lists + a.beams * n + NWV * kBeamOut) + wave * (kBeamSlices + 2);
   for (int b = wave; b < a.beams; b += NWV) {  // (uniform in the wave)
-    const int64_t r = q * a.beams + b;
-    const float s = a.scores[r];
-    const bool ended = a.finished && a.finished[r] != 0;
-    if (!beam_live(a, r)) {
-      if (lane == 0) {
-        const bool bad = s != s || s == __builtin_inff();
-        flags[b] = bad ? 4 : 0;
-        n_list[b] = ended && !bad && s > -__builtin_inff() ? 1 : 0;
-        lists[b * n] = beam_key(0.0f, a.end_token);  // a score of its own: s + 0 - 0
-        lse[b] = 0.0;
-        row_m[b] = 0.0f;
-      }
+    if (sh.ended[b]) {
+      if (lane == 0) lists[b * n] = beam_key(0.0f, a.end_token);  // a score of its own: s + (0 - 0)
       continue;
     }
-    const BeamPart* part = a.part + r * a.slices;
-    // the slices' lists and sums: two slices to a lane
-    constexpr float kNone = -__builtin_inff();
-    uint32_t c[2] = {0u, 0u}, f = 0u;
-    float m[2][kSliceNW], sum[2][kSliceNW], mine = kNone;
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-#pragma unroll
-      for (int w = 0; w < kSliceNW; ++w) {
-        m[j][w] = kNone;
-        sum[j][w] = 0.0f;
-      }
-      if (2 * lane + j < a.slices) {
-        const BeamPart& p = part[2 * lane + j];
-        c[j] = (uint32_t)p.count;
-        f |= (uint32_t)p.flags;
-#pragma unroll
-        for (int w = 0; w < kSliceNW; ++w) {
-          m[j][w] = p.m[w];
-          sum[j][w] = p.sum[w];
-          mine = __builtin_fmaxf(mine, m[j][w]);
-        }
-      }
-    }
-    f = wave_reduce(f, 0u, [](uint32_t u, uint32_t v) { return u | v; });
-    const float M = wave_reduce(mine, kNone, [](float u, float v) { return __builtin_fmaxf(u, v); });
-    const uint32_t inc = wave_incl_scan(c[0] + c[1]);
-    first[wave][2 * lane] = inc - c[0] - c[1];
-    first[wave][2 * lane + 1] = inc - c[1];
-    if (lane == 63) first[wave][kBeamSlices] = inc;
-    double total = 0.0, at = 0.0;
-    if (!f && M > kNone) {  // (uniform)
-      const double top = sum_reference(a.x, M);
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-#pragma unroll
-        for (int w = 0; w < kSliceNW; ++w)
-          if (m[j][w] > kNone) total += (double)sum[j][w] * exp(sum_reference(a.x, m[j][w]) - top);
-      }
-      total = wave_sum(total);
-      at = top + log(total);
-    }
+    const int64_t r = q * a.beams + b;
+    const uint32_t c0 = 2 * lane < a.slices ? sh.count[b * a.slices + 2 * lane] : 0u;
+    const uint32_t c1 = 2 * lane + 1 < a.slices ? sh.count[b * a.slices + 2 * lane + 1] : 0u;
+    const uint32_t inc = wave_incl_scan(c0 + c1);
+    first[2 * lane] = inc - c0 - c1;
+    first[2 * lane + 1] = inc - c1;
+    if (lane == 63) first[kBeamSlices] = inc;
     wave_sync();
-    const int count = f || !(M > kNone) ? 0 : (int)first[wave][kBeamSlices];
+    const int count = sh.n_list[b] ? (int)first[kBeamSlices] : 0;
     int held = 0;
     for (int g0 = 0; g0 < count; g0 += (kBeamPer - 2) * 64) {
       uint64_t key[kBeamPer];
 #pragma unroll
-      for (int j = 0; j < 2; ++j) key[j] = j * 64 + lane < held ? kept[wave][j * 64 + lane] : 0ull;  // the best so far
+      for (int j = 0; j < 2; ++j) key[j] = j * 64 + lane < held ? kept[j * 64 + lane] : 0ull;  // the best so far
 #pragma unroll
       for (int j = 2; j < kBeamPer; ++j) {
         const int g = g0 + (j - 2) * 64 + lane;
@@ -331,10 +361,10 @@ __global__ void __launch_bounds__(64 * NWV) beam_join_kernel(BeamArgs a) {
           int lo = 0, hi = a.slices - 1;  // the last slice that starts at or before g
           while (lo < hi) {
             const int mid = (lo + hi + 1) >> 1;
-            if (first[wave][mid] <= (uint32_t)g) lo = mid;
+            if (first[mid] <= (uint32_t)g) lo = mid;
             else hi = mid - 1;
           }
-          key[j] = a.cand[(r * a.slices + lo) * a.cap + g - first[wave][lo]];
+          key[j] = a.cand[(r * a.slices + lo) * a.cap + g - first[lo]];
         }
       }
       const uint64_t least = beam_cut(key, n, &held);
@@ -343,7 +373,7 @@ __global__ void __launch_bounds__(64 * NWV) beam_join_kernel(BeamArgs a) {
 #pragma unroll
       for (int j = 0; j < kBeamPer; ++j) {
         const uint64_t in = __ballot(key[j] >= least);
-        if (key[j] >= least) kept[wave][before + __builtin_popcountll(in & ((1ull << lane) - 1ull))] = key[j];
+        if (key[j] >= least) kept[before + __builtin_popcountll(in & ((1ull << lane) - 1ull))] = key[j];
         before += __builtin_popcountll(in);
       }
       wave_sync();
@@ -353,34 +383,23 @@ __global__ void __launch_bounds__(64 * NWV) beam_join_kernel(BeamArgs a) {
     for (int j = 0; j < kBeamOut / 64; ++j) {
       const int e = j * 64 + lane;
       if (j * 64 < held) {  // (uniform)
-        const uint64_t own = e < held ? kept[wave][e] : 0ull;
+        const uint64_t own = e < held ? kept[e] : 0ull;
         int larger = 0;
-        for (int i = 0; i < held; ++i) larger += kept[wave][i] > own ? 1 : 0;
+        for (int i = 0; i < held; ++i) larger += kept[i] > own ? 1 : 0;
         if (e < held) lists[b * n + larger] = own;
       }
     }
-    if (lane == 0) {
-      flags[b] = (int)f;
-      n_list[b] = held;
-      lse[b] = at;
-      row_m[b] = M;
-    }
+    if (lane == 0) sh.n_list[b] = held;
   }
-  if (threadIdx.x == 0) again = 0ull;
   __syncthreads();
 
-  // the merge: a beam to a lane of the first wave
   const int64_t at_out = q * n;
-  const bool here = lane < a.beams;
-  const float s = here ? a.scores[q * a.beams + lane] : 0.0f;
-  const bool ended = here && a.finished && a.finished[q * a.beams + lane] != 0;
-  const uint32_t bad = wave_reduce(here ? (uint32_t)flags[lane] : 0u, 0u, [](uint32_t u, uint32_t v) { return u | v; });
-  const int status = bad & 1u ? DSPARK_ST_ROW_NAN : bad & 2u ? DSPARK_ST_ROW_POSINF : bad & 4u ? DSPARK_ST_BAD_SCORE : DSPARK_ST_OK;
   const auto merge = [&]() {  // by the first wave; the beams whose order is not certain
     constexpr double kNone = -__builtin_inf();
-    const int mine = here && status == DSPARK_ST_OK ? n_list[lane] : 0;
-    const double base = here ? (double)s : 0.0, minus = here ? lse[lane] : 0.0;
-    const double off = 2.0 * kLseOff + 1e-15 * (__builtin_fabs(base) + __builtin_fabs(minus));
+    const bool here = lane < a.beams;
+    const int mine = here ? sh.n_list[lane] : 0;
+    const double base = here ? (double)sh.score[lane] : 0.0, minus = here ? sh.lse[lane] : 0.0;
+    const double off = here ? beam_off(sh, lane) : 0.0;
     int at = 0;
     uint64_t key = mine > 0 ? lists[lane * n] : 0ull, unsure = 0ull;
     double head = mine > 0 ? base + ((double)beam_logit(key) - minus) : kNone, last = kNone;
@@ -390,14 +409,11 @@ __global__ void __launch_bounds__(64 * NWV) beam_join_kernel(BeamArgs a) {
       if (!(best > kNone)) break;
       const int beam = __builtin_ctzll(__ballot(head == best));
       // every head of another beam than the last one's, so near to it that either may come first
-      const uint64_t near = from < 0 ? 0ull : __ballot(lane != from && head > kNone && last - head <= off);
-      if (near) unsure |= near | 1ull << from;
+      const uint64_t close = from < 0 ? 0ull : __ballot(lane != from && head > kNone && last - head <= off + beam_off(sh, from));
+      if (close) unsure |= close | 1ull << from;
       if (i == n) break;
       if (lane == beam) {
-        a.parent[at_out + i] = lane;
-        a.token[at_out + i] = beam_id(key);
-        a.score[at_out + i] = (float)head;
-        a.out_finished[at_out + i] = ended || beam_id(key) == a.end_token ? 1 : 0;
+        beam_put(a, at_out + i, lane, key, head, sh.ended[lane]);
         ++at;
         key = at < mine ? lists[lane * n + at] : 0ull;
         head = at < mine ? base + ((double)beam_logit(key) - minus) : kNone;
@@ -406,34 +422,218 @@ __global__ void __launch_bounds__(64 * NWV) beam_join_kernel(BeamArgs a) {
       from = beam;
       written = i + 1;
     }
-    for (int i = written + lane; i < n; i += 64) {
-      a.parent[at_out + i] = -1;
-      a.token[at_out + i] = 0;
-      a.score[at_out + i] = -__builtin_inff();
-      a.out_finished[at_out + i] = 0;
-    }
-    if (lane == 0) {
-      a.len[q] = written;
-      a.status[q] = status;
-    }
-    return unsure;
+    for (int i = written + lane; i < n; i += 64) beam_put_empty(a, at_out + i);
+    if (lane == 0) a.len[q] = written;
+    return unsure & ~__ballot(here && sh.ended[lane]);  // (a finished beam's score is exact)
   };
   if (wave == 0) {
-    uint64_t unsure = merge();
-    unsure &= ~__ballot(ended);  // (a finished beam's score is exact)
-    if (lane == 0) again = unsure;
+    const uint64_t unsure = merge();
+    if (lane == 0) {
+      sh.unsure[0] = (uint32_t)unsure;
+      sh.unsure[1] = (uint32_t)(unsure >> 32);
+    }
   }
   __syncthreads();
-  const uint64_t todo = again;
+  const uint64_t todo = (uint64_t)sh.unsure[1] << 32 | sh.unsure[0];
   if (todo) {  // (uniform)
-    for (int b = 0; b < a.beams; ++b) {
-      if (!(todo >> b & 1ull)) continue;
-      const double exact = beam_exact_lse<DT, NWV>(a, q * a.beams + b, row_m[b], scratch);
-      if (threadIdx.x == 0) lse[b] = exact;
-    }
-    __syncthreads();
+    beam_exact<DT, NWV>(a, q, todo, sh);
     if (wave == 0) (void)merge();
   }
+}
+
+// One workgroup per request.  The candidates of all its beams are looked at
+// twice: for the largest score of every thread, of which the n_out-th gives a
+// threshold, and for those that reach it; they are few, and sorted by
+// counting.  Where they are not few (many equal scores, or few threads with
+// candidates), the beams' lists are merged instead.
+template <int DT, int NWV>
+__global__ void __launch_bounds__(64 * NWV) beam_join_kernel(BeamArgs a) {
+  extern __shared__ __align__(16) uint64_t lists[];
+  __shared__ BeamScratch sh;
+  BeamNear& near = *reinterpret_cast<BeamNear*>(lists);
+  const int64_t q = block_number(a.requests);
+  if (q < 0) return;
+  const int lane = lane_id(), wave = wave_id(), tid = (int)threadIdx.x, n = a.n_out;
+  for (int b = wave; b < a.beams; b += NWV) {  // (uniform in the wave)
+    const int64_t r = q * a.beams + b;
+    const float s = a.scores[r];
+    if (!beam_live(a, r)) {
+      const bool bad = s != s || s == __builtin_inff(), ended = a.finished && a.finished[r] != 0 && !bad && s > -__builtin_inff();
+      if (lane == 0) {
+        sh.flags[b] = bad ? 4 : 0;
+        sh.n_list[b] = ended ? 1 : 0;
+        sh.ended[b] = ended;
+        sh.score[b] = s;
+        sh.lse[b] = 0.0;
+        sh.m[b] = 0.0f;
+      }
+      for (int i = lane; i < a.slices; i += 64) sh.count[b * a.slices + i] = 0;
+      continue;
+    }
+    const BeamPart* part = a.part + r * a.slices;
+    constexpr float kNone = -__builtin_inff();
+    uint32_t f = 0u;
+    float m[2] = {kNone, kNone};
+    double sum[2] = {0.0, 0.0};
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {  // two slices to a lane
+      const int i = j * 64 + lane;
+      if (i < a.slices) {
+        const BeamPart p = part[i];
+        sh.count[b * a.slices + i] = (uint16_t)p.count;
+        f |= (uint32_t)p.flags;
+        m[j] = p.m;
+#pragma unroll
+        for (int w = 0; w < kSliceNW; ++w) sum[j] += (double)p.sum[w];
+      }
+    }
+    f = wave_reduce(f, 0u, [](uint32_t u, uint32_t v) { return u | v; });
+    const float M = wave_reduce(__builtin_fmaxf(m[0], m[1]), kNone, [](float u, float v) { return __builtin_fmaxf(u, v); });
+    double lse = 0.0;
+    if (!f && M > kNone) {  // (uniform)
+      const double top = sum_reference(a.x, M);
+      double total = m[0] > kNone ? sum[0] * exp(sum_reference(a.x, m[0]) - top) : 0.0;
+      if (a.slices > 64 && m[1] > kNone) total += sum[1] * exp(sum_reference(a.x, m[1]) - top);
+      lse = top + log(wave_sum(total));
+    }
+    if (lane == 0) {
+      sh.flags[b] = (int)f;
+      sh.n_list[b] = M > kNone ? 1 : 0;
+      sh.ended[b] = false;
+      sh.score[b] = s;
+      sh.lse[b] = lse;
+      sh.m[b] = M;
+    }
+  }
+  if (tid == 0) {
+    sh.unsure[0] = sh.unsure[1] = 0u;
+    sh.near = 0u;
+  }
+  __syncthreads();
+  const uint32_t bad = wave_reduce(lane < a.beams ? (uint32_t)sh.flags[lane] : 0u, 0u, [](uint32_t u, uint32_t v) { return u | v; });
+  const int64_t at_out = q * n;
+  if (tid == 0)
+    a.status[q] = bad & 1u ? DSPARK_ST_ROW_NAN : bad & 2u ? DSPARK_ST_ROW_POSINF : bad & 4u ? DSPARK_ST_BAD_SCORE : DSPARK_ST_OK;
+  if (bad) {  // (uniform)
+    for (int i = tid; i < n; i += 64 * NWV) beam_put_empty(a, at_out + i);
+    if (tid == 0) a.len[q] = 0;
+    return;
+  }
+
+  // every candidate, 16 threads to a list
+  const int n_lists = a.beams * a.slices;
+  const auto score_of = [&](int b, uint64_t key) { return (double)sh.score[b] + ((double)beam_logit(key) - sh.lse[b]); };
+  const auto each = [&](auto take) {
+    for (int L0 = tid >> 4; L0 < n_lists; L0 += 4 * NWV * 4) {
+      uint64_t key[4];
+      int c[4], b[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {  // four lists' loads on their way
+        const int L = L0 + i * NWV * 4;
+        c[i] = L < n_lists ? sh.count[L] : 0;
+        b[i] = (int)((uint32_t)L / (uint32_t)a.slices);
+        key[i] = (tid & 15) < c[i] ? a.cand[(q * n_lists + L) * a.cap + (tid & 15)] : 0ull;
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        for (int e = tid & 15; e < c[i];) {
+          take(b[i], key[i]);
+          e += 16;
+          if (e < c[i]) key[i] = a.cand[(q * n_lists + L0 + i * NWV * 4) * a.cap + e];
+        }
+      }
+    }
+    if (tid < a.beams && sh.ended[tid]) take(tid, beam_key(0.0f, a.end_token));
+  };
+  float top = -__builtin_inff();
+  each([&](int b, uint64_t key) { top = __builtin_fmaxf(top, (float)score_of(b, key)); });
+  static_assert(NWV == 8, "eight maxima to a lane");
+  sh.most[tid] = top == -__builtin_inff() ? 0u : key32(top) >> 16;
+  __syncthreads();
+  uint32_t T = 0;
+  {
+    uint32_t v[NWV], m = 0;
+#pragma unroll
+    for (int i = 0; i < NWV; ++i) {
+      v[i] = sh.most[i * 64 + lane];
+      m = v[i] > m ? v[i] : m;
+    }
+#pragma unroll
+    for (int bit = 15; bit >= 0; --bit) {
+      const uint32_t up = T | (1u << bit);
+      int reach = 0;
+      if (n <= 32) {  // (uniform: 64 groups' maxima, or all 512)
+        reach = __builtin_popcountll(__ballot(m >= up));
+      } else {
+#pragma unroll
+        for (int i = 0; i < NWV; ++i) reach += __builtin_popcountll(__ballot(v[i] >= up));
+      }
+      if (reach >= n) T = up;
+    }
+  }
+  // n candidates' scores reach it as they were computed: those of the best do
+  // so but for what the log-sum-exps are off, and a rounding
+  float t = top_key_value<DSPARK_BF16>(T);
+  t = T ? t - (1e-5f + __builtin_fabsf(t) * 0x1p-20f) : -__builtin_inff();
+  each([&](int b, uint64_t key) {
+    if ((float)score_of(b, key) >= t) {
+      const uint32_t at = atomicAdd(&sh.near, 1u);
+      if (at < (uint32_t)kBeamNear) {
+        near.key[at] = key;
+        near.beam[at] = (uint8_t)b;
+      }
+    }
+  });
+  __syncthreads();
+  const int count = (int)sh.near;
+  if (count > kBeamNear) {  // (uniform)
+    __syncthreads();
+    beam_join_lists<DT, NWV>(a, q, sh, lists);
+    return;
+  }
+  const int out = count < n ? count : n;
+  const auto sort = [&]() {  // a place is the number of better ones: score, then beam, then logit and id
+    for (int i = tid; i < count; i += 64 * NWV) near.score[i] = score_of(near.beam[i], near.key[i]);
+    __syncthreads();
+    for (int i = tid; i < count; i += 64 * NWV) {
+      const double own = near.score[i];
+      const int beam = near.beam[i];
+      const uint64_t key = near.key[i];
+      int better = 0;
+      for (int j = 0; j < count; ++j) {
+        const double o = near.score[j];
+        const int ob = near.beam[j];
+        better += o > own || (o == own && (ob < beam || (ob == beam && near.key[j] > key))) ? 1 : 0;
+      }
+      near.order[better] = (uint16_t)i;
+    }
+    __syncthreads();
+  };
+  sort();
+  // neighbours of two beams, so near to each other that either may come first
+  for (int i = tid; i + 1 < count; i += 64 * NWV) {
+    const int x = near.order[i], y = near.order[i + 1], bx = near.beam[x], by = near.beam[y];
+    const double off = beam_off(sh, bx) + beam_off(sh, by);
+    if (bx != by && near.score[x] - near.score[y] <= off && (i < n || near.score[near.order[n - 1]] - near.score[x] <= off)) {
+      if (!sh.ended[bx]) atomicOr(&sh.unsure[bx >> 5], 1u << (bx & 31));
+      if (!sh.ended[by]) atomicOr(&sh.unsure[by >> 5], 1u << (by & 31));
+    }
+  }
+  __syncthreads();
+  const uint64_t todo = (uint64_t)sh.unsure[1] << 32 | sh.unsure[0];
+  if (todo) {  // (uniform)
+    beam_exact<DT, NWV>(a, q, todo, sh);
+    sort();
+  }
+  for (int i = tid; i < n; i += 64 * NWV) {
+    if (i < out) {
+      const int x = near.order[i];
+      beam_put(a, at_out + i, near.beam[x], near.key[x], near.score[x], sh.ended[near.beam[x]]);
+    } else {
+      beam_put_empty(a, at_out + i);
+    }
+  }
+  if (tid == 0) a.len[q] = out;
 }
 
 }  // namespace dspark
