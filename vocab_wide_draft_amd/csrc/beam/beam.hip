@@ -41,7 +41,7 @@ void launch_select(const BeamArgs& a, int slice, hipStream_t s) {
   if (slice == kBeamShort) hipLaunchKernelGGL(HIP_KERNEL_NAME(beam_slice_kernel<DT, kBeamShort / step>), grid, dim3(kSliceBS), 0, s, a);
   else hipLaunchKernelGGL(HIP_KERNEL_NAME(beam_slice_kernel<DT, kBeamLong / step>), grid, dim3(kSliceBS), 0, s, a);
   hipLaunchKernelGGL(HIP_KERNEL_NAME(beam_join_kernel<DT, 8>), grid_of(a.requests), dim3(512),
-                     beam_join_bytes(a.beams, a.n_out, 8), s, a);
+                     beam_join_bytes(a.beams, a.slices, a.n_out, 8), s, a);
 }
 
 // the bytes that a state's layout spans; -1 where parts overlap

@@ -283,21 +283,24 @@ struct BeamScratch {
   int32_t n_list[kBeams], flags[kBeams];
   bool ended[kBeams];
   double red[16];
-  uint32_t most[512];
   uint16_t count[kBeams * kBeamSlices];  // of every slice's list
-  uint32_t unsure[2], near;
+  uint32_t unsure[2], near, n_worth;
 };
 struct BeamNear {
   uint64_t key[kBeamNear];
-  double score[kBeamNear];
+  union {
+    double score[kBeamNear];
+    uint16_t worth[4 * kBeamNear];  // before the scores: the lists worth looking at
+  };
   uint16_t order[kBeamNear];
   uint8_t beam[kBeamNear];
-};
+};  // behind it, the order key of every slice's best score (its upper half)
 constexpr size_t beam_lists_bytes(int beams, int n_out, int waves) {
   return (size_t)beams * (size_t)n_out * 8 + (size_t)waves * (kBeamOut * 8 + (kBeamSlices + 2) * 4);
 }
-constexpr size_t beam_join_bytes(int beams, int n_out, int waves) {
-  return sizeof(BeamNear) > beam_lists_bytes(beams, n_out, waves) ? sizeof(BeamNear) : beam_lists_bytes(beams, n_out, waves);
+inline size_t beam_join_bytes(int beams, int slices, int n_out, int waves) {
+  const size_t near = sizeof(BeamNear) + (size_t)beams * (size_t)slices * 2, lists = beam_lists_bytes(beams, n_out, waves);
+  return near > lists ? near : lists;
 }
 
 __device__ __forceinline__ double beam_off(const BeamScratch& sh, int b) {
@@ -441,24 +444,31 @@ __device__ void beam_join_lists(const BeamArgs& a, int64_t q, BeamScratch& sh, u
   }
 }
 
-// One workgroup per request.  The candidates of all its beams are looked at
-// twice: for the largest score of every thread, of which the n_out-th gives a
-// threshold, and for those that reach it; they are few, and sorted by
-// counting.  Where they are not few (many equal scores, or few threads with
-// candidates), the beams' lists are merged instead.
+// One workgroup per request.  Every slice's best logit is a candidate, so the
+// n_out-th largest of their scores is a threshold (of few slices, the
+// n_out-th largest of the threads' best candidates): the lists whose best reach
+// it are few, and so are the candidates on them that do, which are sorted by
+// counting.  Where they are not few (many equal scores), the beams' lists are
+// merged instead.
 template <int DT, int NWV>
 __global__ void __launch_bounds__(64 * NWV) beam_join_kernel(BeamArgs a) {
   extern __shared__ __align__(16) uint64_t lists[];
   __shared__ BeamScratch sh;
   BeamNear& near = *reinterpret_cast<BeamNear*>(lists);
+  uint16_t* best = reinterpret_cast<uint16_t*>(&near + 1);  // (0: none)
+  const auto half = [](float x) -> uint16_t { return (uint16_t)(key32(x) >> 16); };
   const int64_t q = block_number(a.requests);
   if (q < 0) return;
   const int lane = lane_id(), wave = wave_id(), tid = (int)threadIdx.x, n = a.n_out;
   for (int b = wave; b < a.beams; b += NWV) {  // (uniform in the wave)
     const int64_t r = q * a.beams + b;
+    // everything on its way at once (the records of a beam that takes no part hold nothing, and are not used)
+    const BeamPart* part = a.part + r * a.slices;
     const float s = a.scores[r];
-    if (!beam_live(a, r)) {
-      const bool bad = s != s || s == __builtin_inff(), ended = a.finished && a.finished[r] != 0 && !bad && s > -__builtin_inff();
+    const int32_t fin = a.finished ? a.finished[r] : 0;
+    const BeamPart p0 = part[lane < a.slices ? lane : 0], p1 = part[64 + lane < a.slices ? 64 + lane : 0];
+    if (!(__builtin_fabsf(s) < __builtin_inff()) || fin != 0) {
+      const bool bad = s != s || s == __builtin_inff(), ended = fin != 0 && !bad && s > -__builtin_inff();
       if (lane == 0) {
         sh.flags[b] = bad ? 4 : 0;
         sh.n_list[b] = ended ? 1 : 0;
@@ -467,10 +477,12 @@ __global__ void __launch_bounds__(64 * NWV) beam_join_kernel(BeamArgs a) {
         sh.lse[b] = 0.0;
         sh.m[b] = 0.0f;
       }
-      for (int i = lane; i < a.slices; i += 64) sh.count[b * a.slices + i] = 0;
+      for (int i = lane; i < a.slices; i += 64) {
+        sh.count[b * a.slices + i] = 0;
+        best[b * a.slices + i] = ended && i == 0 ? half(s) : 0;
+      }
       continue;
     }
-    const BeamPart* part = a.part + r * a.slices;
     constexpr float kNone = -__builtin_inff();
     uint32_t f = 0u;
     float m[2] = {kNone, kNone};
@@ -478,8 +490,8 @@ __global__ void __launch_bounds__(64 * NWV) beam_join_kernel(BeamArgs a) {
 #pragma unroll
     for (int j = 0; j < 2; ++j) {  // two slices to a lane
       const int i = j * 64 + lane;
+      const BeamPart& p = j ? p1 : p0;
       if (i < a.slices) {
-        const BeamPart p = part[i];
         sh.count[b * a.slices + i] = (uint16_t)p.count;
         f |= (uint32_t)p.flags;
         m[j] = p.m;
@@ -496,6 +508,9 @@ __global__ void __launch_bounds__(64 * NWV) beam_join_kernel(BeamArgs a) {
       if (a.slices > 64 && m[1] > kNone) total += sum[1] * exp(sum_reference(a.x, m[1]) - top);
       lse = top + log(wave_sum(total));
     }
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+      if (j * 64 + lane < a.slices) best[b * a.slices + j * 64 + lane] = m[j] > kNone ? half((float)((double)s + ((double)m[j] - lse))) : 0;
     if (lane == 0) {
       sh.flags[b] = (int)f;
       sh.n_list[b] = M > kNone ? 1 : 0;
@@ -507,7 +522,7 @@ __global__ void __launch_bounds__(64 * NWV) beam_join_kernel(BeamArgs a) {
   }
   if (tid == 0) {
     sh.unsure[0] = sh.unsure[1] = 0u;
-    sh.near = 0u;
+    sh.near = sh.n_worth = 0u;
   }
   __syncthreads();
   const uint32_t bad = wave_reduce(lane < a.beams ? (uint32_t)sh.flags[lane] : 0u, 0u, [](uint32_t u, uint32_t v) { return u | v; });
@@ -520,54 +535,62 @@ __global__ void __launch_bounds__(64 * NWV) beam_join_kernel(BeamArgs a) {
     return;
   }
 
-  // every candidate, 16 threads to a list
-  const int n_lists = a.beams * a.slices;
+  // candidates of `total` lists, the w-th of them list_of(w): 16, 32 or 64
+  // threads to a list, two keys to a thread, two lists at a time
+  const int n_lists = a.beams * a.slices, shift = n <= 12 ? 4 : n <= 28 ? 5 : 6, width = 1 << shift, groups = 64 * NWV >> shift;
+  const int e0 = tid & (width - 1);
   const auto score_of = [&](int b, uint64_t key) { return (double)sh.score[b] + ((double)beam_logit(key) - sh.lse[b]); };
-  const auto each = [&](auto take) {
-    for (int L0 = tid >> 4; L0 < n_lists; L0 += 4 * NWV * 4) {
-      uint64_t key[4];
-      int c[4], b[4];
+  const auto each = [&](int total, auto list_of, auto take) {
+    for (int w0 = tid >> shift; w0 < total; w0 += 2 * groups) {
+      uint64_t key[2][2];
+      int L[2];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {  // four lists' loads on their way
-        const int L = L0 + i * NWV * 4;
-        c[i] = L < n_lists ? sh.count[L] : 0;
-        b[i] = (int)((uint32_t)L / (uint32_t)a.slices);
-        key[i] = (tid & 15) < c[i] ? a.cand[(q * n_lists + L) * a.cap + (tid & 15)] : 0ull;
+      for (int i = 0; i < 2; ++i) {
+        L[i] = w0 + i * groups < total ? list_of(w0 + i * groups) : -1;
+        const int c = L[i] >= 0 ? sh.count[L[i]] : 0;
+        const uint64_t* list = a.cand + (q * n_lists + L[i]) * a.cap;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) key[i][j] = e0 + j * width < c ? list[e0 + j * width] : 0ull;
       }
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        for (int e = tid & 15; e < c[i];) {
-          take(b[i], key[i]);
-          e += 16;
-          if (e < c[i]) key[i] = a.cand[(q * n_lists + L0 + i * NWV * 4) * a.cap + e];
-        }
+      for (int i = 0; i < 2; ++i) {
+        if (!key[i][0]) continue;
+        const int b = (int)((uint32_t)L[i] / (uint32_t)a.slices), c = sh.count[L[i]];
+        take(b, key[i][0]);
+        if (key[i][1]) take(b, key[i][1]);
+        for (int e = e0 + 2 * width; e < c; e += width) take(b, a.cand[(q * n_lists + L[i]) * a.cap + e]);
       }
     }
     if (tid < a.beams && sh.ended[tid]) take(tid, beam_key(0.0f, a.end_token));
   };
-  float top = -__builtin_inff();
-  each([&](int b, uint64_t key) { top = __builtin_fmaxf(top, (float)score_of(b, key)); });
-  static_assert(NWV == 8, "eight maxima to a lane");
-  sh.most[tid] = top == -__builtin_inff() ? 0u : key32(top) >> 16;
-  __syncthreads();
+
+  // the threshold: the largest half key that n of the lists' best reach (512
+  // of them, or groups of lists); where there are few lists, that n threads'
+  // best do
+  static_assert(NWV == 8, "eight groups of lists to a lane");
   uint32_t T = 0;
   {
-    uint32_t v[NWV], m = 0;
+    uint32_t v[NWV];
+    if (n_lists >= 4 * n) {  // (uniform)
 #pragma unroll
-    for (int i = 0; i < NWV; ++i) {
-      v[i] = sh.most[i * 64 + lane];
-      m = v[i] > m ? v[i] : m;
+      for (int i = 0; i < NWV; ++i) {
+        v[i] = 0u;
+        for (int L = i * 64 + lane; L < n_lists; L += 64 * NWV) v[i] = best[L] > v[i] ? best[L] : v[i];
+      }
+    } else {
+      float top = -__builtin_inff();
+      each(n_lists, [](int w) { return w; }, [&](int b, uint64_t key) { top = __builtin_fmaxf(top, (float)score_of(b, key)); });
+      near.order[tid] = top > -__builtin_inff() ? half(top) : 0;
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < NWV; ++i) v[i] = near.order[i * 64 + lane];
     }
 #pragma unroll
     for (int bit = 15; bit >= 0; --bit) {
       const uint32_t up = T | (1u << bit);
       int reach = 0;
-      if (n <= 32) {  // (uniform: 64 groups' maxima, or all 512)
-        reach = __builtin_popcountll(__ballot(m >= up));
-      } else {
 #pragma unroll
-        for (int i = 0; i < NWV; ++i) reach += __builtin_popcountll(__ballot(v[i] >= up));
-      }
+      for (int i = 0; i < NWV; ++i) reach += __builtin_popcountll(__ballot(v[i] >= up));
       if (reach >= n) T = up;
     }
   }
@@ -575,18 +598,27 @@ __global__ void __launch_bounds__(64 * NWV) beam_join_kernel(BeamArgs a) {
   // so but for what the log-sum-exps are off, and a rounding
   float t = top_key_value<DSPARK_BF16>(T);
   t = T ? t - (1e-5f + __builtin_fabsf(t) * 0x1p-20f) : -__builtin_inff();
-  each([&](int b, uint64_t key) {
-    if ((float)score_of(b, key) >= t) {
-      const uint32_t at = atomicAdd(&sh.near, 1u);
-      if (at < (uint32_t)kBeamNear) {
-        near.key[at] = key;
-        near.beam[at] = (uint8_t)b;
-      }
+  const uint32_t least = T ? half(t) : 1u;
+  for (int L = tid; L < n_lists; L += 64 * NWV) {
+    if (best[L] >= least && sh.count[L] != 0) {
+      const uint32_t at = atomicAdd(&sh.n_worth, 1u);
+      if (at < 4u * kBeamNear) near.worth[at] = (uint16_t)L;
     }
-  });
+  }
+  __syncthreads();
+  const int n_worth = (int)sh.n_worth;
+  const auto take = [&](int b, uint64_t key) {
+    if (!((float)score_of(b, key) >= t)) return;
+    const uint32_t at = atomicAdd(&sh.near, 1u);
+    if (at < (uint32_t)kBeamNear) {
+      near.key[at] = key;
+      near.beam[at] = (uint8_t)b;
+    }
+  };
+  if (n_worth <= 4 * kBeamNear) each(n_worth, [&](int w) { return (int)near.worth[w]; }, take);
   __syncthreads();
   const int count = (int)sh.near;
-  if (count > kBeamNear) {  // (uniform)
+  if (count > kBeamNear || n_worth > 4 * kBeamNear) {  // (uniform)
     __syncthreads();
     beam_join_lists<DT, NWV>(a, q, sh, lists);
     return;
@@ -595,17 +627,19 @@ __global__ void __launch_bounds__(64 * NWV) beam_join_kernel(BeamArgs a) {
   const auto sort = [&]() {  // a place is the number of better ones: score, then beam, then logit and id
     for (int i = tid; i < count; i += 64 * NWV) near.score[i] = score_of(near.beam[i], near.key[i]);
     __syncthreads();
-    for (int i = tid; i < count; i += 64 * NWV) {
+    for (int i = tid >> 2; i < count; i += 16 * NWV) {  // four threads to a candidate
       const double own = near.score[i];
       const int beam = near.beam[i];
       const uint64_t key = near.key[i];
-      int better = 0;
-      for (int j = 0; j < count; ++j) {
+      uint32_t better = 0;
+      for (int j = tid & 3; j < count; j += 4) {
         const double o = near.score[j];
         const int ob = near.beam[j];
-        better += o > own || (o == own && (ob < beam || (ob == beam && near.key[j] > key))) ? 1 : 0;
+        better += o > own || (o == own && (ob < beam || (ob == beam && near.key[j] > key))) ? 1u : 0u;
       }
-      near.order[better] = (uint16_t)i;
+      better += dpp_u32<0xb1, 0xf, 0xf>(better, better);  // quad_perm 1,0,3,2
+      better += dpp_u32<0x4e, 0xf, 0xf>(better, better);  // quad_perm 2,3,0,1
+      if ((tid & 3) == 0) near.order[better] = (uint16_t)i;
     }
     __syncthreads();
   };
