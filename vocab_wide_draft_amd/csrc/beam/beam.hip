@@ -28,18 +28,23 @@ BeamPlan beam_plan_of(int64_t n, int64_t V, int n_out, int slice) {
   p.bytes = p.part_at + (size_t)n * (size_t)p.slices * sizeof(BeamPart);
   return p;
 }
-constexpr int kBeamLong = 8192, kBeamShort = 2048;  // logits of a slice
-bool beam_short(int64_t n, int64_t V) { return n * ((V + kBeamLong - 1) / kBeamLong) < 512 && V <= kBeamShort * kBeamSlices; }
-BeamPlan beam_plan(int64_t n, int64_t V, int n_out) {
-  return beam_plan_of(n, V, n_out, beam_short(n, V) ? kBeamShort : kBeamLong);
+// The most logits of a slice: 8,192, or fewer where those leave CUs idle and
+// the join takes as many slices.
+constexpr int64_t kBeamWant = 512;
+int beam_slice(int64_t n, int64_t V) {
+  int slice = 8192;
+  while (slice > 2048 && n * ((V + slice - 1) / slice) < kBeamWant && V <= (int64_t)slice / 2 * kBeamSlices) slice /= 2;
+  return slice;
 }
+BeamPlan beam_plan(int64_t n, int64_t V, int n_out) { return beam_plan_of(n, V, n_out, beam_slice(n, V)); }
 
 template <int DT>
 void launch_select(const BeamArgs& a, int slice, hipStream_t s) {
   constexpr int step = kSliceBS * kVec<DT>;
   const dim3 grid = row_slice_grid(a.x.n, a.slices);
-  if (slice == kBeamShort) hipLaunchKernelGGL(HIP_KERNEL_NAME(beam_slice_kernel<DT, kBeamShort / step>), grid, dim3(kSliceBS), 0, s, a);
-  else hipLaunchKernelGGL(HIP_KERNEL_NAME(beam_slice_kernel<DT, kBeamLong / step>), grid, dim3(kSliceBS), 0, s, a);
+  if (slice == 2048) hipLaunchKernelGGL(HIP_KERNEL_NAME(beam_slice_kernel<DT, 2048 / step>), grid, dim3(kSliceBS), 0, s, a);
+  else if (slice == 4096) hipLaunchKernelGGL(HIP_KERNEL_NAME(beam_slice_kernel<DT, 4096 / step>), grid, dim3(kSliceBS), 0, s, a);
+  else hipLaunchKernelGGL(HIP_KERNEL_NAME(beam_slice_kernel<DT, 8192 / step>), grid, dim3(kSliceBS), 0, s, a);
   hipLaunchKernelGGL(HIP_KERNEL_NAME(beam_join_kernel<DT, 8>), grid_of(a.requests), dim3(512),
                      beam_join_bytes(a.beams, a.slices, a.n_out, 8), s, a);
 }
@@ -73,10 +78,11 @@ extern "C" {
 
 size_t dspark_beam_select_workspace(int64_t n_rows, int64_t vocab, int32_t n_out) {
   if (n_rows <= 0 || n_rows > (1 << 24) || vocab < 1 || vocab > DSPARK_V_MAX || n_out < 1 || n_out > DSPARK_BEAM_OUT_MAX) return 0;
+  // fewer rows may have more slices: the most rows that have slices of each length
   size_t bytes = beam_plan(n_rows, vocab, n_out).bytes;
-  if (!beam_short(n_rows, vocab) && beam_short(1, vocab)) {  // fewer rows have more slices: the most rows that do
-    const int64_t most = 511 / ((vocab + kBeamLong - 1) / kBeamLong);
-    bytes = std::max(bytes, beam_plan(std::min(n_rows, most), vocab, n_out).bytes);
+  for (int64_t slice = 4096; slice <= 8192; slice *= 2) {
+    const int64_t rows = std::min<int64_t>(n_rows, (kBeamWant - 1) / ((vocab + slice - 1) / slice));
+    if (rows > 0) bytes = std::max(bytes, beam_plan(rows, vocab, n_out).bytes);
   }
   return bytes;
 }
@@ -118,6 +124,7 @@ int dspark_beam_select(const dspark_rows* rows, const float* scores, const int32
   a.len = len;
   a.status = req_status;
   a.slices = p.slices;
+  a.length = (int)((rows->vocab + p.slices * 8 - 1) / (p.slices * 8) * 8);
   a.cap = p.cap;
   a.cand = static_cast<uint64_t*>(ws);
   a.part = reinterpret_cast<BeamPart*>(static_cast<char*>(ws) + p.part_at);

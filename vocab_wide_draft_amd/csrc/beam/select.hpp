@@ -42,7 +42,7 @@ struct BeamArgs {
   int64_t requests;
   int32_t *parent, *token, *out_finished, *len, *status;
   float* score;
-  int slices, cap;  // of a row; candidates of a slice's list
+  int slices, length, cap;  // of a row, of nearly equal length; candidates of a slice's list
   BeamPart* part;   // [rows][slices]
   uint64_t* cand;   // [rows][slices][cap]
 };
@@ -61,11 +61,12 @@ __device__ __forceinline__ int beam_id(uint64_t k) { return (int)~(uint32_t)k; }
 __device__ __forceinline__ float beam_logit(uint64_t k) { return top_key_value<DSPARK_F32>((uint32_t)(k >> 32)); }
 
 // The largest 16-bit key that at least n of 64 groups' maxima (a lane's v)
-// reach, or for n > 32 of the 256 values themselves: n values do, too.
+// reach, or where n is much for them, of the 256 values themselves: n values
+// do, too.  0 where there are fewer than n.
 __device__ __forceinline__ uint32_t reached_by(uint4 v, int n) {
   uint32_t T = 0;
-  if (n <= 32) {
-    const uint32_t a = v.x > v.y ? v.x : v.y, b = v.z > v.w ? v.z : v.w, m = a > b ? a : b;
+  const uint32_t a = v.x > v.y ? v.x : v.y, b = v.z > v.w ? v.z : v.w, m = a > b ? a : b;
+  if (2 * n <= __builtin_popcountll(__ballot(m != 0u))) {  // (uniform)
 #pragma unroll
     for (int bit = 15; bit >= 0; --bit) {
       const uint32_t up = T | (1u << bit);
@@ -85,7 +86,7 @@ __device__ __forceinline__ uint32_t reached_by(uint4 v, int n) {
 
 template <int DT, int U>
 __global__ void __launch_bounds__(kSliceBS) beam_slice_kernel(BeamArgs a) {
-  constexpr int N = kVec<DT>, SLICE = U * kSliceBS * N, WORDS = (U * N + 31) / 32;
+  constexpr int N = kVec<DT>, WORDS = (U * N + 31) / 32;
   __shared__ __align__(16) uint32_t most[kSliceBS];
   __shared__ float wave_m[kSliceNW];
   __shared__ uint32_t any_flags, held, counts[kSliceNW];
@@ -94,16 +95,19 @@ __global__ void __launch_bounds__(kSliceBS) beam_slice_kernel(BeamArgs a) {
   int s;
   if (!row_slice(a.x.n, a.slices, r, s)) return;
   BeamPart& p = a.part[r * a.slices + s];
-  const int start = s * SLICE, V = a.x.V, tid = (int)threadIdx.x;
+  const int start = s * a.length, end = a.x.V - start < a.length ? a.x.V - start : a.length, tid = (int)threadIdx.x;
   if (!beam_live(a, r)) return;  // (uniform; the join does not read its record)
   const XT* row = static_cast<const XT*>(a.x.x) + r * a.x.stride;
   Raw<DT, N> raw[U];
-  if (start + SLICE <= V) {  // (uniform)
 #pragma unroll
-    for (int i = 0; i < U; ++i) raw[i] = raw_whole<DT, N, true>(row + start, (uint32_t)(i * kSliceBS + tid) * N);
-  } else {
+  for (int i = 0; i < U; ++i) {
+    const int v = (i * kSliceBS + tid) * N;
+    if (v < end) {
+      raw[i] = raw_vec<DT, N, true>(row + start, v, end);
+    } else {
 #pragma unroll
-    for (int i = 0; i < U; ++i) raw[i] = raw_vec<DT, N, true>(row + start, (i * kSliceBS + tid) * N, V - start);
+      for (int w = 0; w < 4; ++w) raw[i].w[w] = DT == DSPARK_F32 ? 0xff800000u : 0xff80ff80u;
+    }
   }
   if (tid == 0) {
     any_flags = 0u;
