@@ -5,7 +5,9 @@ current torch stream."""
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
+import struct
 
 import torch
 
@@ -143,7 +145,7 @@ def load_library():
         "dspark_block_linear_workspace": (SZ, [I64, I64, I64]),
         "dspark_beam_select": (ctypes.c_int, [RP, P, P, I32, I32, I32, P, P, P, P, P, P, P, SZ, P]),
         "dspark_beam_select_workspace": (SZ, [I64, I64, I32]),
-        "dspark_beam_reorder": (ctypes.c_int, [ctypes.POINTER(State), I32, I64, I32, P, P, P, P]),
+        "dspark_beam_reorder": (ctypes.c_int, [P, I32, I64, I32, P, P, P, P]),
         "dspark_q_semantic_id": (ctypes.c_char_p, []),
         "dspark_status_name": (ctypes.c_char_p, [I32]),
         "dspark_last_error": (ctypes.c_char_p, []),
@@ -814,12 +816,13 @@ def quantize_blocks(x: torch.Tensor, block_rows: int = 1, scale_dtype=torch.floa
         raise ValueError("block_rows must be 1 or 128")
     if scale_dtype not in (torch.float32, torch.float8_e8m0fnu):
         raise ValueError("scale_dtype must be float32 or float8_e8m0fnu")
-    n, dev = x.shape[0], x.device
-    cols = -(-x.shape[1] // 16) * 16
-    q = {"values": torch.empty((n, cols), dtype=torch.float8_e4m3fn, device=dev),
-         "scales": torch.empty((-(-n // block_rows), -(-cols // 128)), dtype=scale_dtype, device=dev)}
-    _call(dev, lib.dspark_quantize_blocks, ctypes.byref(r), ctypes.byref(_fp8(q, "out", block_rows, dev)))
-    return q
+    n, width = x.shape
+    dev, cols, blocks = x.device, -(-width // 16) * 16, -(-width // 128)
+    values = torch.empty((n, cols), dtype=torch.float8_e4m3fn, device=dev)
+    scales = torch.empty((-(-n // block_rows), blocks), dtype=scale_dtype, device=dev)
+    f = Fp8(values.data_ptr(), scales.data_ptr(), SCALE_F32 if scale_dtype is torch.float32 else SCALE_E8M0, block_rows, n, cols, cols, blocks)
+    _call(dev, lib.dspark_quantize_blocks, ctypes.byref(r), ctypes.byref(f))
+    return {"values": values, "scales": scales}
 
 
 def transpose_blocks(w, cols: int):
@@ -942,9 +945,10 @@ def beam_select(rows: torch.Tensor, scores: torch.Tensor, n_out: int | None = No
     k = min(2 * beams, BEAM_OUT_MAX) if n_out is None else int(n_out)
     i32 = torch.int32
     s, f = _arg(scores, "scores", torch.float32, (R, beams), dev), _arg(finished, "finished", i32, (R, beams), dev)
-    parent, token, ended = (torch.empty((R, max(k, 0)), dtype=i32, device=dev) for _ in range(3))
+    # (few allocations: each costs the host as much as a tenth of a small call)
+    parent, token, ended = torch.empty((3, R, max(k, 0)), dtype=i32, device=dev).unbind()
     score = torch.empty((R, max(k, 0)), dtype=torch.float32, device=dev)
-    length, st = _i32(R, dev), _i32(R, dev)
+    length, st = torch.empty((2, R), dtype=i32, device=dev).unbind()
     nbytes = lib.dspark_beam_select_workspace(n, V, k)
     ws = torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
     _call(dev, lib.dspark_beam_select, ctypes.byref(r), s, f, beams, k, int(end_token), parent.data_ptr(), token.data_ptr(),
@@ -952,20 +956,20 @@ def beam_select(rows: torch.Tensor, scores: torch.Tensor, n_out: int | None = No
     return {"parent": parent, "token": token, "score": score, "finished": ended, "len": length, "status": st}
 
 
-def _layout(x, axis):
-    """(strides of requests, beams, outer, positions; outer, positions, bytes of a position) of a state, strides in bytes."""
-    es, size, stride = x.element_size(), x.shape, x.stride()
+@functools.lru_cache(maxsize=1024)
+def _layout(size, stride, es, axis):
+    """(strides of requests, beams, outer, positions in bytes), (outer, positions, bytes of a position) of a state."""
     inner, reach = 1, 1
-    for d in range(x.dim() - 1, min(axis, x.dim() - 1), -1):
+    for d in range(len(size) - 1, min(axis, len(size) - 1), -1):
         if size[d] > 1 and stride[d] != reach:
             raise ValueError("a state's dimensions after its positions must be contiguous")
         inner, reach = inner * size[d], reach * size[d]
-    if x.dim() <= axis:  # no positions: everything after the beams is one row
-        for d in range(x.dim() - 1, 1, -1):
+    if len(size) <= axis:  # no positions: everything after the beams is one row
+        for d in range(len(size) - 1, 1, -1):
             if size[d] > 1 and stride[d] != inner:
                 raise ValueError("a state without positions must be contiguous after its beams")
             inner *= size[d]
-        return stride[0] * es, stride[1] * es, 0, 0, 1, 0, inner * es
+        return (stride[0] * es, stride[1] * es, 0, 0), (1, 0, inner * es)
     outer, step = 1, 0
     for d in range(axis - 1, 1, -1):  # the dimensions between beams and positions, as one
         if size[d] == 1:
@@ -975,7 +979,7 @@ def _layout(x, axis):
         if outer == 1:
             step = stride[d]
         outer *= size[d]
-    return stride[0] * es, stride[1] * es, step * es, stride[axis] * es, outer, size[axis], inner * es
+    return (stride[0] * es, stride[1] * es, step * es, stride[axis] * es), (outer, size[axis], inner * es)
 
 
 def beam_reorder(states, parent: torch.Tensor, length=None, *, axis: int = 2, out=None):
@@ -1000,21 +1004,25 @@ def beam_reorder(states, parent: torch.Tensor, length=None, *, axis: int = 2, ou
         raise ValueError("axis counts from the dimensions after requests and beams: 2 or more")
     if len(into) != len(states):
         raise ValueError("out must be as many tensors as states")
-    laid = (State * len(states))()
-    for at, x, y in zip(laid, states, into):
-        if x.dim() < 2 or x.shape[:2] != (R, beams) or x.device != dev:
+    laid = []  # State records, field by field
+    for x, y in zip(states, into):
+        size = x.shape
+        if len(size) < 2 or size[0] != R or size[1] != beams or x.device != dev:
             raise ValueError(f"a state must be a tensor [{R}, {beams}, ...] on {dev}")
-        if y.shape != x.shape or y.dtype != x.dtype or y.device != dev:
-            raise ValueError("out must be tensors of the states' shapes, types and device")
-    live = [i for i, x in enumerate(states) if x.numel()]
-    for k, i in enumerate(live):
-        a, b = _layout(states[i], axis), _layout(into[i], axis)
-        laid[k] = State(states[i].data_ptr(), into[i].data_ptr(), *a[:4], *b[:4], *a[4:])
+        es = x.element_size()
+        strides, counts = _layout(size, x.stride(), es, axis)
+        if y is x:
+            to = strides
+        else:
+            if y.shape != size or y.dtype != x.dtype or y.device != dev:
+                raise ValueError("out must be tensors of the states' shapes, types and device")
+            to = _layout(size, y.stride(), es, axis)[0]
+        if x.numel():
+            laid += (x.data_ptr(), y.data_ptr(), *strides, *to, *counts)
     st = _i32(R, dev)
-    if not live:
+    if not laid:
         return {"states": into, "status": st.zero_()}
-    _call(dev, lib.dspark_beam_reorder, laid, len(live), R, beams, _arg(parent, "parent", torch.int32, (R, beams), dev),
-          _arg(length, "length", torch.int32, (R,), dev), st.data_ptr())
-    for y in into:
-        _written(y)
+    _call(dev, lib.dspark_beam_reorder, struct.pack(f"{len(laid)}q", *laid), len(laid) // 13, R, beams,
+          _arg(parent, "parent", torch.int32, (R, beams), dev), _arg(length, "length", torch.int32, (R,), dev), st.data_ptr())
+    torch.autograd.graph.increment_version(into)  # (as _written does)
     return {"states": into, "status": st}
