@@ -87,7 +87,9 @@ int check_product_out(int64_t M, int64_t N, const void* out, int32_t dtype, int6
   return DSPARK_SUCCESS;
 }
 
+enum ProductWay { kDirect, kStaged, kTiles };
 struct ProductPlan {
+  ProductWay way;
   int tile_m, tile_n, splits, split_steps;
   size_t bytes;
 };
@@ -97,13 +99,22 @@ ProductPlan product_plan(int64_t M, int64_t N, int64_t K, bool wide) {
   p.tile_n = 256;
   const int64_t tiles_n = (N + 255) / 256;
   if (M <= 64) {
-    p.tile_m = M <= 16 ? 16 : 64;
-    const int64_t want = std::max<int64_t>(1, std::min<int64_t>(512 / std::max<int64_t>(tiles_n, 1), steps / 4));
+    // Straight from memory while that is short, through LDS (whole lines of w
+    // at a time, and x once for 256 rows of w) where bandwidth counts; direct /
+    // staged, float scales, bf16 results, w out of the caches, us: 20 MB of w, 1
+    // row 8.7 / 11.8, 24 rows 11 / 17, 64 rows 17 / 22; 60 MB 16 / 20, 21 / 26,
+    // 30 / 36; 102 MB 25 / 25, 30 / 32, 44 / 42; 205 MB 56 / 50, 65 / 51, 100 / 63.
+    p.way = N * K <= (M <= 32 ? 112 << 20 : 64 << 20) ? kDirect : kStaged;
+    p.tile_m = M <= 16 ? 16 : M <= 32 ? 32 : 64;
+    if (p.way == kDirect) p.tile_n = 64;
+    const int64_t tiles = (N + p.tile_n - 1) / p.tile_n;
+    const int64_t want = std::max<int64_t>(1, std::min<int64_t>(512 / std::max<int64_t>(tiles, 1), steps / 4));
     p.split_steps = (int)((steps + want - 1) / want);
   } else {
     // the width and the number of parts that should take least: rounds of 256
     // tiles (parts of a long product fill the last one), us for a step of a tile of
     // 64 u rows, three steps for its beginning and end, the parts' way through memory
+    p.way = kTiles;
     double best = 0.0;
     for (int u = wide ? 2 : 4; u >= 1; --u) {
       const int64_t tiles = (M + 64 * u - 1) / (64 * u) * tiles_n;
@@ -135,10 +146,17 @@ void launch_tile(const ProductArgs& a, hipStream_t s) {
                      dim3(512), 0, s, a);
 }
 template <int ST, bool WIDE, int OUT>
-void launch_tiles(const ProductPlan& p, ProductArgs a, bool few, hipStream_t s) {
+void launch_tiles(const ProductPlan& p, ProductArgs a, hipStream_t s) {
   const dim3 grid = grid_of(a.tiles_m * a.tiles_n * a.splits);
-  if (few) {
+  if (p.way == kDirect) {
+    if (p.tile_m == 16) hipLaunchKernelGGL(HIP_KERNEL_NAME(product_few_kernel<1, ST, WIDE, OUT>), grid, dim3(256), 0, s, a);
+    else if (p.tile_m == 32) hipLaunchKernelGGL(HIP_KERNEL_NAME(product_few_kernel<2, ST, WIDE, OUT>), grid, dim3(256), 0, s, a);
+    else hipLaunchKernelGGL(HIP_KERNEL_NAME(product_few_kernel<4, ST, WIDE, OUT>), grid, dim3(256), 0, s, a);
+    return;
+  }
+  if (p.way == kStaged) {
     if (p.tile_m == 16) hipLaunchKernelGGL(HIP_KERNEL_NAME(product_kernel<1, 4, 1, ST, WIDE, OUT>), grid, dim3(256), 0, s, a);
+    else if (p.tile_m == 32) hipLaunchKernelGGL(HIP_KERNEL_NAME(product_kernel<2, 4, 1, ST, WIDE, OUT>), grid, dim3(256), 0, s, a);
     else hipLaunchKernelGGL(HIP_KERNEL_NAME(product_kernel<4, 4, 1, ST, WIDE, OUT>), grid, dim3(256), 0, s, a);
     return;
   }
@@ -174,13 +192,13 @@ void product(const dspark_fp8* x, int64_t xs_step, const dspark_fp8* w, void* ou
   a.out_stride = p.splits > 1 ? up(a.N, 4) : out_stride;
   const bool wide = out_dtype == DSPARK_F32, bf16 = p.splits == 1 && !wide;
   if (x->scale_dtype == DSPARK_SCALE_F32) {
-    if (wide) launch_tiles<DSPARK_SCALE_F32, true, DSPARK_F32>(p, a, a.M <= 64, s);
-    else if (bf16) launch_tiles<DSPARK_SCALE_F32, false, DSPARK_BF16>(p, a, a.M <= 64, s);
-    else launch_tiles<DSPARK_SCALE_F32, false, DSPARK_F32>(p, a, a.M <= 64, s);
+    if (wide) launch_tiles<DSPARK_SCALE_F32, true, DSPARK_F32>(p, a, s);
+    else if (bf16) launch_tiles<DSPARK_SCALE_F32, false, DSPARK_BF16>(p, a, s);
+    else launch_tiles<DSPARK_SCALE_F32, false, DSPARK_F32>(p, a, s);
   } else {
-    if (wide) launch_tiles<DSPARK_SCALE_E8M0, true, DSPARK_F32>(p, a, a.M <= 64, s);
-    else if (bf16) launch_tiles<DSPARK_SCALE_E8M0, false, DSPARK_BF16>(p, a, a.M <= 64, s);
-    else launch_tiles<DSPARK_SCALE_E8M0, false, DSPARK_F32>(p, a, a.M <= 64, s);
+    if (wide) launch_tiles<DSPARK_SCALE_E8M0, true, DSPARK_F32>(p, a, s);
+    else if (bf16) launch_tiles<DSPARK_SCALE_E8M0, false, DSPARK_BF16>(p, a, s);
+    else launch_tiles<DSPARK_SCALE_E8M0, false, DSPARK_F32>(p, a, s);
   }
   if (p.splits > 1) {
     ProductJoinArgs j{};

@@ -243,6 +243,139 @@ __global__ void __launch_bounds__(64 * WN * WM) product_kernel(ProductArgs a) {
   }
 }
 
+// Few rows of x (16 UM at most): what bounds them is the reading of w.  A
+// workgroup takes 64 rows of w, each of its four waves every fourth block of
+// 128 columns, straight from memory into registers one block ahead, without a
+// barrier; the waves' sums meet in LDS at the end.
+template <int UM, int ST, bool WIDE, int OUT>
+__global__ void __launch_bounds__(256) product_few_kernel(ProductArgs a) {
+  constexpr int TM = 16 * UM, PITCH = 68;  // (a row's 64 sums, and room that spreads rows over the banks)
+  __shared__ __align__(16) float part[4][TM * PITCH];
+  const int64_t b = block_number(a.tiles_m * a.tiles_n * a.splits);
+  if (b < 0) return;
+  const int64_t n0 = b % a.tiles_n * 64;
+  const int split = (int)(b / a.tiles_n);
+  const int first = split * a.split_steps, last = first + a.split_steps < a.steps ? first + a.split_steps : a.steps;
+  const int lane = lane_id(), wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6), r = lane & 15, g = lane >> 4;
+  const int rows_w = a.N - n0 < 64 ? (int)(a.N - n0) : 64, rows_x = (int)a.M;
+  const __amdgpu_buffer_rsrc_t fw = buffer_of(a.w + n0 * a.w_stride, (rows_w - 1) * a.w_stride + a.K),
+                               fx = buffer_of(a.x, (rows_x - 1) * a.x_stride + a.K);
+  // the matrix instruction's row 4 g + i of its t-th 16 is row 32 (t / 2) + 8 g + 4 (t % 2) + i
+  const auto row_of = [](int t) { return 32 * (t >> 1) + 4 * (t & 1); };
+  const int at_w = (8 * (r >> 2) + (r & 3)) * (int)a.w_stride + g * 16, at_x = r * (int)a.x_stride + g * 16;
+  const int64_t sn = n0 / kBlock * a.ws_stride;
+
+  struct Held {
+    v4i w[4][2], x[UM][2];
+    float sw, sx[UM];
+    int ew, ex[UM];
+  };
+  const auto load = [&](int step, Held& h) {
+    const int k = step * kBlock;
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      const bool in = k + g * 16 + c * 64 < a.K && step < last;
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        const int row = row_of(t) + 8 * (r >> 2) + (r & 3);
+        h.w[t][c] = __builtin_amdgcn_raw_buffer_load_b128(fw, in && row < rows_w ? at_w + row_of(t) * (int)a.w_stride + k + c * 64 : kPastEnd, 0, 0);
+      }
+#pragma unroll
+      for (int u = 0; u < UM; ++u)
+        h.x[u][c] = __builtin_amdgcn_raw_buffer_load_b128(fx, in && 16 * u + r < rows_x ? at_x + 16 * u * (int)a.x_stride + k + c * 64 : kPastEnd, 0, 0);
+    }
+    const int at = step < last ? step : last - 1;
+    if constexpr (ST == DSPARK_SCALE_E8M0 && !WIDE) h.ew = static_cast<const uint8_t*>(a.ws)[sn + at];
+    else h.sw = scale_value<ST>(a.ws, sn + at);
+#pragma unroll
+    for (int u = 0; u < UM; ++u) {
+      const int64_t s = (16 * u + r < rows_x ? 16 * u + r : rows_x - 1) * a.xs_stride + at * a.xs_step;
+      if constexpr (ST == DSPARK_SCALE_E8M0 && !WIDE) h.ex[u] = static_cast<const uint8_t*>(a.xs)[s];
+      else h.sx[u] = scale_value<ST>(a.xs, s);
+    }
+  };
+  v4f acc[4][UM];
+#pragma unroll
+  for (int t = 0; t < 4; ++t) {
+#pragma unroll
+    for (int u = 0; u < UM; ++u) acc[t][u] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+  }
+  const auto multiply = [&](const Held& h) {
+    const auto whole = [](const v4i (&v)[2]) { return v8i{v[0][0], v[0][1], v[0][2], v[0][3], v[1][0], v[1][1], v[1][2], v[1][3]}; };
+    v8i x[UM];
+    v8b wx[WIDE ? UM : 1][4];
+#pragma unroll
+    for (int u = 0; u < UM; ++u) {
+      x[u] = whole(h.x[u]);
+      if constexpr (WIDE) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) wx[u][j] = widen(x[u][2 * j], x[u][2 * j + 1]);
+      }
+    }
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+      const v8i w = whole(h.w[t]);
+      v8b ww[4];
+      if constexpr (WIDE) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) ww[j] = widen(w[2 * j], w[2 * j + 1]);
+      }
+#pragma unroll
+      for (int u = 0; u < UM; ++u) {
+        if constexpr (ST == DSPARK_SCALE_E8M0 && !WIDE) {
+          acc[t][u] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w, x[u], acc[t][u], 0, 0, 0, h.ew, 0, h.ex[u]);
+        } else {
+          v4f p = {0.0f, 0.0f, 0.0f, 0.0f};
+          if constexpr (WIDE) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) p = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ww[j], wx[u][j], p, 0, 0, 0);
+          } else {
+            p = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w, x[u], p, 0, 0, 0, 127, 0, 127);
+          }
+          const float s = h.sw * h.sx[u];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) acc[t][u][i] = __builtin_fmaf(p[i], s, acc[t][u][i]);
+        }
+      }
+    }
+  };
+  Held even, odd;
+  int step = first + wave;
+  load(step, even);
+  while (step < last) {  // (past the last block: zeros with the last block's scales)
+    load(step + 4, odd);
+    multiply(even);
+    step += 4;
+    if (step >= last) break;
+    load(step + 4, even);
+    multiply(odd);
+    step += 4;
+  }
+#pragma unroll
+  for (int u = 0; u < UM; ++u) {
+#pragma unroll
+    for (int t = 0; t < 4; ++t) *reinterpret_cast<v4f*>(&part[wave][(16 * u + r) * PITCH + row_of(t) + 8 * g]) = acc[t][u];
+  }
+  __syncthreads();
+  char* out = static_cast<char*>(a.out);
+  if (a.splits > 1) out += (int64_t)split * a.M * a.out_stride * (int64_t)sizeof(typename El<OUT>::T);
+#pragma unroll
+  for (int m = (int)threadIdx.x >> 3; m < TM; m += 32) {
+    if (m >= rows_x) break;
+    const int n = ((int)threadIdx.x & 7) * 8;
+    float v[8];
+#pragma unroll
+    for (int l = 0; l < 8; l += 4) {
+      v4f s = *reinterpret_cast<const v4f*>(&part[0][m * PITCH + n + l]);
+#pragma unroll
+      for (int w = 1; w < 4; ++w) s += *reinterpret_cast<const v4f*>(&part[w][m * PITCH + n + l]);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[l + i] = s[i];
+    }
+    put_row8<OUT>(out + m * a.out_stride * (int64_t)sizeof(typename El<OUT>::T), n0 + n, a.N, v);
+  }
+}
+
 template <int ST>
 struct ScaleWord { typedef uint32_t W; };
 template <>
