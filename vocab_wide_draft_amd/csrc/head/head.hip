@@ -111,16 +111,22 @@ ProductPlan product_plan(int64_t M, int64_t N, int64_t K, bool wide) {
     const int64_t want = std::max<int64_t>(1, std::min<int64_t>(512 / std::max<int64_t>(tiles, 1), steps / 4));
     p.split_steps = (int)((steps + want - 1) / want);
   } else {
-    // the width and the number of parts that should take least: rounds of 256
-    // tiles (parts of a long product fill the last one), us for a step of a tile of
-    // 64 u rows, three steps for its beginning and end, the parts' way through memory
+    // The width and the number of parts that should take least: rounds of 256
+    // tiles (parts of a long product fill the last one); for a step of a tile of
+    // 64 u rows 0.38 + 0.28 u us, and 0.86 us for its columns of w out of memory
+    // shared by the tiles that read them; three steps for a tile's beginning and
+    // end; the parts' way through memory.  (129,280 x 5,120, powers of two, us for
+    // u = 1, 2, 3, 4: 64 rows 133, 138, 162, 168; 128: 195, 152, 172, 176; 256:
+    // 308, 230, 276, 206; 384: 405, 308, 294, 304; 768: 741, 538, 509, 439; 5,120:
+    // 4,500, 3,190, 2,870, 2,560.)
     p.way = kTiles;
     double best = 0.0;
     for (int u = wide ? 2 : 4; u >= 1; --u) {
-      const int64_t tiles = (M + 64 * u - 1) / (64 * u) * tiles_n;
+      const int64_t tiles_m = (M + 64 * u - 1) / (64 * u), tiles = tiles_m * tiles_n;
       for (int64_t s = 1; s <= 16 && (s == 1 || (steps / s >= 8 && tiles * (s - 1) < 1024)); ++s) {
         const double rounds = (double)(tiles * s) / 256.0;
-        const double time = (rounds < 8.0 ? std::ceil(rounds) : rounds) * (double)((steps + s - 1) / s + 3) * (0.70 + 0.25 * u) +
+        const double time = (rounds < 8.0 ? std::ceil(rounds) : rounds) * (double)((steps + s - 1) / s + 3) *
+                                (0.38 + 0.28 * u + 0.86 / (double)tiles_m) +
                             (s > 1 ? 2e-6 * 4.0 * (double)s * (double)M * (double)N / 4.0 : 0.0);
         if (best == 0.0 || time < best) {
           best = time;
@@ -142,7 +148,7 @@ size_t product_bytes(int64_t M, int64_t N, int64_t K) {
 
 template <int ST, bool WIDE, int OUT, int U>
 void launch_tile(const ProductArgs& a, hipStream_t s) {
-  hipLaunchKernelGGL(HIP_KERNEL_NAME(product_tile_kernel<4, U, ST, WIDE, OUT>), grid_of(a.tiles_m * a.tiles_n * a.splits),
+  hipLaunchKernelGGL(HIP_KERNEL_NAME(product_tile_kernel<U, ST, WIDE, OUT>), grid_of(a.tiles_m * a.tiles_n * a.splits),
                      dim3(512), 0, s, a);
 }
 template <int ST, bool WIDE, int OUT>

@@ -59,11 +59,25 @@ __device__ __forceinline__ v8b widen(int lo, int hi) {
 }
 
 // The same, not waited for by what reads LDS afterwards (the compiler waits
-// for every load into an array before any read of it): loads_arrived() does.
+// for every load into an array before any read of it): loads_but() does.
+template <int BYTES>
 __device__ __forceinline__ void load_lds_ahead(v4i from, uint32_t to, int offset) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(to), "v"(offset), "s"(from) : "memory", "m0");
+  static_assert(BYTES == 16 || BYTES == 4 || BYTES == 1, "of a lane (a byte becomes a word)");
+  if constexpr (BYTES == 16)
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(to), "v"(offset), "s"(from) : "memory", "m0");
+  else if constexpr (BYTES == 4)
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds" ::"s"(to), "v"(offset), "s"(from) : "memory", "m0");
+  else
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_ubyte %1, %2, 0 offen lds" ::"s"(to), "v"(offset), "s"(from) : "memory", "m0");
 }
-__device__ __forceinline__ void loads_arrived() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+// waits for all but the wave's last N loads (N < 16)
+template <int N>
+__device__ __forceinline__ void loads_but() {
+  static_assert(N < 16, "of four bits");
+  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+}
+// a barrier that waits for the wave's own reads of LDS, but for no load
+__device__ __forceinline__ void group_barrier() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
 // the buffer's four words, as buffer_of makes them
 __device__ __forceinline__ v4i buffer_words(const void* p, int64_t bytes) {
   const uint64_t at = reinterpret_cast<uint64_t>(p);
@@ -376,27 +390,32 @@ __global__ void __launch_bounds__(256) product_few_kernel(ProductArgs a) {
   }
 }
 
-template <int ST>
-struct ScaleWord { typedef uint32_t W; };
-template <>
-struct ScaleWord<DSPARK_SCALE_E8M0> { typedef uint8_t W; };
-
-// Tiles of 256 rows of w by 16 U WM rows of x for many rows: 2 x WM waves of
-// 128 by 16 U each.  One barrier a step: it stands before the last part of a
-// step's matrix instructions, when the wave has read all that it needs of the
-// step's buffer and the next step's has arrived, so that the fetch after next
-// goes into the former and the first reads of the latter run under that part.
-// A step is one block without branches (past the last one the fetch reads a
-// buffer of no bytes): otherwise the compiler moves the instructions past the
-// barrier.
-template <int WM, int U, int ST, bool WIDE, int OUT>
-__global__ void __launch_bounds__(128 * WM, WM / 2) product_tile_kernel(ProductArgs a) {
-  constexpr int TN = 256, TM = 16 * U * WM, T = 8, NWV = 2 * WM, BUF = (TN + TM) * kBlock, GW = TN / 8 / NWV, GX = TM / 8 / NWV;
-  constexpr int AT_ONCE = WM == 4 ? 2 : 1, PARTS = T / AT_ONCE;  // rows of 16 of w between two reads
-  static_assert(GW == 4 || GW == 8, "a wave's rows of w");
-  __shared__ __align__(16) uint8_t lds[2][BUF];
-  typedef typename ScaleWord<ST>::W SW;
-  __shared__ SW scales[2][64 * NWV + 2];  // of w from 64 NWV on
+// Tiles of 256 rows of w by 64 U rows of x for many rows: eight waves, two by
+// four, of 128 by 16 U each.  One barrier a step: it stands before the last
+// part of a step's matrix instructions, when the wave has read all that it
+// needs of the step's buffer and the next step's has arrived, so that a later
+// step's fetches go into the former and the first reads of the latter run
+// under that part.  The fetches are spread between the instructions of that
+// part and the next step's first: all at once they hold the waves up (5,120
+// rows x 129,280 x 5,120, powers of two: 3,000 us against 2,660).  A step is
+// one block without branches (past the last one the fetches read a buffer of no
+// bytes): otherwise the compiler moves the instructions past the barrier; and
+// no load in it is the compiler's own, which would wait for all those before it.
+//
+// Where U leaves room for three buffers a fetch has two steps to arrive (128
+// rows 172 -> 152 us, 64 rows 154 -> 133: what bounds those is the reading of
+// w).  The largest tiles are bound by power: with 65 % of the matrix cores'
+// cycles in use the clock falls from 2.4 to 1.9 GHz (2.56 ms, 2,645 TFLOP/s;
+// 2.22 ms at 2.2 GHz without the fetches).  A second barrier a step, which
+// gives a fetch more time, costs more than it gives there (2,867 us).
+template <int U, int ST, bool WIDE, int OUT>
+__global__ void __launch_bounds__(512, 2) product_tile_kernel(ProductArgs a) {
+  constexpr int TN = 256, TM = 64 * U, T = 8, BUF = (TN + TM) * kBlock, GW = 4, GX = U, FETCHES = GW + GX, EARLY = (FETCHES + 1) / 2;
+  constexpr int STAGES = U <= 2 ? 3 : 2;  // buffers that LDS has room for
+  constexpr int AT_ONCE = 2, PARTS = T / AT_ONCE;  // rows of 16 of w between two reads
+  constexpr int SE = ST == DSPARK_SCALE_F32 ? 4 : 1;
+  __shared__ __align__(16) uint8_t lds[STAGES][BUF];
+  __shared__ uint32_t scales[STAGES][TM + 128];  // of x's rows, of w's two blocks, and room that nobody reads
   const int64_t total = a.tiles_m * a.tiles_n * a.splits;
   int64_t b = block_number(total);
   if (b < 0) return;
@@ -417,9 +436,9 @@ __global__ void __launch_bounds__(128 * WM, WM / 2) product_tile_kernel(ProductA
   const int first = split * a.split_steps, last = first + a.split_steps < a.steps ? first + a.split_steps : a.steps;
   const int rows_w = a.N - n0 < TN ? (int)(a.N - n0) : TN, rows_x = a.M - m0 < TM ? (int)(a.M - m0) : TM;
   const int tid = (int)threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int wm = wave % WM, wn = wave / WM, r = lane & 15, g = lane >> 4;
+  const int wm = wave & 3, wn = wave >> 2, r = lane & 15, g = lane >> 4;
 
-  // fetches: 8 GW rows of w and 8 GX rows of x for every wave.  The eight
+  // Fetches: 8 GW rows of w and 8 GX rows of x for every wave.  The eight
   // chunks of 16 bytes of a row lie in LDS in an order of its own, so that
   // lanes that read one chunk of neighbouring rows hit different banks: the
   // key is a row's last three bits, for w its last two and the bit of 8.
@@ -435,25 +454,34 @@ __global__ void __launch_bounds__(128 * WM, WM / 2) product_tile_kernel(ProductA
     const int left = step < last ? a.K - (int)at : 0;
     if (j < GW) {
       const int col = col_w ^ (j & 1 ? 64 : 0);
-      load_lds_ahead(buffer_words(from_w + at, left > 0 ? bytes_w - at : 0), to_w + (uint32_t)(buf * BUF + j * 1024),
+      load_lds_ahead<16>(buffer_words(from_w + at, left > 0 ? bytes_w - at : 0), to_w + (uint32_t)(buf * BUF + j * 1024),
                      (col < left ? base_w + col : kPastEnd) + j * 8 * (int)a.w_stride);
     } else {
       j -= GW;
-      load_lds_ahead(buffer_words(from_x + at, left > 0 ? bytes_x - at : 0), to_x + (uint32_t)(buf * BUF + j * 1024),
+      load_lds_ahead<16>(buffer_words(from_x + at, left > 0 ? bytes_x - at : 0), to_x + (uint32_t)(buf * BUF + j * 1024),
                      (col_x < left ? base_x + col_x : kPastEnd) + j * 8 * (int)a.x_stride);
     }
   };
-  constexpr int FETCHES = GW + GX, EARLY = (FETCHES + 1) / 2;
   // a part's share of the fetches from `lo` to `hi`, after its u-th group of instructions
   const auto share = [&](int step, int buf, int lo, int hi, int u) {
 #pragma unroll
     for (int j = 0; j < FETCHES; ++j)
       if (j >= lo + (hi - lo) * u / U && j < lo + (hi - lo) * (u + 1) / U) fetch(step, buf, j);
   };
-  // scales, through LDS: a row of x for each of the first threads (the others read past the end), the wave's block of w
-  const int at_sx = tid < rows_x ? tid * (int)a.xs_stride * (int)sizeof(SW) : kPastEnd;
-  const SW *of_sx = static_cast<const SW*>(a.xs) + m0 * a.xs_stride;
-  const SW* of_sw = static_cast<const SW*>(a.ws) + ((n0 + wn * 128 < a.N ? n0 + wn * 128 : a.N - 1) / kBlock) * a.ws_stride;
+  // Scales: the first U waves' lanes a row of x each, the next wave's first two
+  // lanes a block of w each (the rest fetch nothing, into room for it).
+  const bool of_x = wave < U, of_w = wave == U;
+  const int64_t block_w = n0 / kBlock, last_w = (a.N - 1) / kBlock;
+  const char* scale_from = of_x ? static_cast<const char*>(a.xs) + (m0 + wave * 64) * a.xs_stride * SE
+                                : static_cast<const char*>(a.ws) + block_w * a.ws_stride * SE;
+  const int64_t scale_step = (of_x ? a.xs_step : 1) * SE;
+  const int scale_at = of_x ? (wave * 64 + lane < rows_x ? lane * (int)a.xs_stride * SE : kPastEnd)
+                            : of_w && lane < 2 && block_w + lane <= last_w ? lane * (int)a.ws_stride * SE : kPastEnd;
+  const uint32_t scale_to = lds_address(&scales[0][of_x ? wave * 64 : of_w ? TM : TM + 64]);
+  const auto fetch_scales = [&](int step, int buf) {
+    load_lds_ahead<SE>(buffer_words(scale_from + step * scale_step, step < last ? 0x40000000 : 0),
+                       scale_to + (uint32_t)(buf * (int)sizeof(scales[0])), scale_at);
+  };
 
   v4f acc[T][U];
 #pragma unroll
@@ -475,19 +503,8 @@ __global__ void __launch_bounds__(128 * WM, WM / 2) product_tile_kernel(ProductA
   v8i fx[U], fw[2][AT_ONCE];
   v8b wx[WIDE ? U : 1][4];  // a step's rows of x in bf16
   uint32_t sx[U], sw;
-  SW next_sx, next_sw;  // (not touched before they have arrived: that would wait for the fetches behind them)
-  const auto put_scales = [&](int buf) {
-    scales[buf][tid] = next_sx;
-    scales[buf][64 * NWV + wn] = next_sw;
-  };
-  const auto fetch_scales = [&](int step) {
-    const __amdgpu_buffer_rsrc_t f = buffer_of(of_sx + (int64_t)step * a.xs_step, ((rows_x - 1) * a.xs_stride + 1) * (int64_t)sizeof(SW));
-    if constexpr (ST == DSPARK_SCALE_E8M0) next_sx = (SW)__builtin_amdgcn_raw_buffer_load_b8(f, at_sx, 0, 0);
-    else next_sx = __builtin_amdgcn_raw_buffer_load_b32(f, at_sx, 0, 0);
-    next_sw = of_sw[step];
-  };
   const auto read_scales = [&](int buf) {
-    sw = scales[buf][64 * NWV + wn];
+    sw = scales[buf][TM + wn];
 #pragma unroll
     for (int u = 0; u < U; ++u) sx[u] = scales[buf][wm * 16 * U + 16 * u + r];
     if constexpr (WIDE && ST == DSPARK_SCALE_E8M0) {
@@ -557,22 +574,21 @@ __global__ void __launch_bounds__(128 * WM, WM / 2) product_tile_kernel(ProductA
   const auto nothing = [](int) {};
 
   if (first < last) {
-    const int second = first + 1 < last ? first + 1 : first;
-    fetch_scales(first);
 #pragma unroll
-    for (int j = 0; j < FETCHES; ++j) fetch(first, 0, j);
-    loads_arrived();
-    put_scales(0);
-    __syncthreads();
-    fetch_scales(second);
+    for (int s = 0; s < STAGES; ++s) {
+      fetch_scales(first + s, s);
 #pragma unroll
-    for (int j = 0; j < EARLY; ++j) fetch(first + 1, 1, j);
+      for (int j = 0; j < (s < STAGES - 1 ? FETCHES : EARLY); ++j) fetch(first + s, s, j);
+    }
+    loads_but<(STAGES - 2) * (FETCHES + 1) + 1 + EARLY>();
+    group_barrier();
     read_scales(0);
 #pragma unroll
     for (int u = 0; u < U; ++u) fx[u] = frag(0, at_x + u * 16 * kBlock);
     read_w(0, 0, 0);
+    int buf = 0;
     for (int step = first; step + 1 < last; ++step) {
-      const int buf = (step - first) & 1;
+      const int next = buf + 1 < STAGES ? buf + 1 : 0, before = buf > 0 ? buf - 1 : STAGES - 1;
       widen_x();
 #pragma unroll
       for (int p = 0; p < PARTS - 1; ++p) {
@@ -581,7 +597,7 @@ __global__ void __launch_bounds__(128 * WM, WM / 2) product_tile_kernel(ProductA
         if (p == 0) {
           part(p, [&](int u) {
             __builtin_amdgcn_sched_barrier(0);
-            share(step + 1, buf ^ 1, EARLY, FETCHES, u);
+            share(step + STAGES - 1, before, EARLY, FETCHES, u);
             __builtin_amdgcn_sched_barrier(0);
           });
         } else {
@@ -589,24 +605,22 @@ __global__ void __launch_bounds__(128 * WM, WM / 2) product_tile_kernel(ProductA
         }
         __builtin_amdgcn_sched_barrier(0);
       }
-      loads_arrived();
-      put_scales(buf ^ 1);
-      __syncthreads();  // the next step's buffer has arrived, this one has been read
-      read_w(buf ^ 1, 0, PARTS & 1);
-      const int ahead = step + 2 < last ? step + 2 : step;
-      fetch_scales(ahead);
+      loads_but<(STAGES - 2) * (FETCHES + 1)>();
+      group_barrier();  // the next step's buffer has arrived, this one has been read
+      read_w(next, 0, PARTS & 1);
+      fetch_scales(step + STAGES, buf);
       __builtin_amdgcn_sched_barrier(0);
       part(PARTS - 1, [&](int u) {
         __builtin_amdgcn_sched_barrier(0);
-        fx[u] = frag(buf ^ 1, at_x + u * 16 * kBlock);
-        share(step + 2, buf, 0, EARLY, u);
+        fx[u] = frag(next, at_x + u * 16 * kBlock);
+        share(step + STAGES, buf, 0, EARLY, u);
         __builtin_amdgcn_sched_barrier(0);
       });
       if constexpr (LATER) add_late(T - AT_ONCE, U - 1);
       __builtin_amdgcn_sched_barrier(0);
-      read_scales(buf ^ 1);
+      read_scales(next);
+      buf = next;
     }
-    const int buf = (last - 1 - first) & 1;
     widen_x();
 #pragma unroll
     for (int p = 0; p < PARTS; ++p) {
@@ -614,7 +628,7 @@ __global__ void __launch_bounds__(128 * WM, WM / 2) product_tile_kernel(ProductA
       part(p, nothing);
     }
     if constexpr (LATER) add_late(T - AT_ONCE, U - 1);
-    loads_arrived();  // (the fetches past the last step write to LDS, too)
+    loads_but<0>();  // (the fetches past the last step write to LDS, too)
   }
 
   char* out = static_cast<char*>(a.out);
