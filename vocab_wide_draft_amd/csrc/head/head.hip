@@ -98,15 +98,19 @@ ProductPlan product_plan(int64_t M, int64_t N, int64_t K, bool wide) {
   ProductPlan p{};
   p.tile_n = 256;
   const int64_t tiles_n = (N + 255) / 256;
-  if (M <= 64) {
-    // Straight from memory while that is short, through LDS (whole lines of w
-    // at a time, and x once for 256 rows of w) where bandwidth counts; direct /
-    // staged, float scales, bf16 results, w out of the caches, us: 20 MB of w, 1
-    // row 8.7 / 11.8, 24 rows 11 / 17, 64 rows 17 / 22; 60 MB 16 / 20, 21 / 26,
-    // 30 / 36; 102 MB 25 / 25, 30 / 32, 44 / 42; 205 MB 56 / 50, 65 / 51, 100 / 63.
-    p.way = N * K <= (M <= 32 ? 112 << 20 : 64 << 20) ? kDirect : kStaged;
-    p.tile_m = M <= 16 ? 16 : M <= 32 ? 32 : 64;
-    if (p.way == kDirect) p.tile_n = 64;
+  // Few rows go straight from memory while w is short, and through LDS (whole
+  // lines of w at a time) where bandwidth counts, unless tiles do as well;
+  // direct / staged / tiles, float scales, bf16 results, w out of the caches, us:
+  // 20 MB of w, 1 row 8.7 / 11.8, 32 rows 11.9 / 18 / 14, 48 rows 16.3 / 20 / 14;
+  // 60 MB 16.4 / 19.5, 22 / 28 / 24, 28 / 32 / 24; 102 MB 25 / 25, 31 / 33 / 27;
+  // 131 MB 33 / 32, 40 / 38 / 32; 205 MB 56 / 50, 70 / 51 / 51; 662 MB 129 / 115,
+  // 186 / 121 / 124.  float32 results, 662 MB, 32 rows: staged 130, tiles 165.
+  const int64_t bytes = N * K;
+  const bool direct = M <= 32 && bytes <= 112 << 20;
+  if (direct || M <= 16 || (M <= 32 && (wide || bytes > 300 << 20))) {
+    p.way = direct ? kDirect : kStaged;
+    p.tile_m = M <= 16 ? 16 : 32;
+    if (direct) p.tile_n = 64;
     const int64_t tiles = (N + p.tile_n - 1) / p.tile_n;
     const int64_t want = std::max<int64_t>(1, std::min<int64_t>(512 / std::max<int64_t>(tiles, 1), steps / 4));
     p.split_steps = (int)((steps + want - 1) / want);
@@ -155,15 +159,13 @@ template <int ST, bool WIDE, int OUT>
 void launch_tiles(const ProductPlan& p, ProductArgs a, hipStream_t s) {
   const dim3 grid = grid_of(a.tiles_m * a.tiles_n * a.splits);
   if (p.way == kDirect) {
-    if (p.tile_m == 16) hipLaunchKernelGGL(HIP_KERNEL_NAME(product_few_kernel<1, ST, WIDE, OUT>), grid, dim3(256), 0, s, a);
-    else if (p.tile_m == 32) hipLaunchKernelGGL(HIP_KERNEL_NAME(product_few_kernel<2, ST, WIDE, OUT>), grid, dim3(256), 0, s, a);
-    else hipLaunchKernelGGL(HIP_KERNEL_NAME(product_few_kernel<4, ST, WIDE, OUT>), grid, dim3(256), 0, s, a);
+    if (p.tile_m == 16) hipLaunchKernelGGL(HIP_KERNEL_NAME(product_direct_kernel<1, ST, WIDE, OUT>), grid, dim3(256), 0, s, a);
+    else hipLaunchKernelGGL(HIP_KERNEL_NAME(product_direct_kernel<2, ST, WIDE, OUT>), grid, dim3(256), 0, s, a);
     return;
   }
   if (p.way == kStaged) {
-    if (p.tile_m == 16) hipLaunchKernelGGL(HIP_KERNEL_NAME(product_kernel<1, 4, 1, ST, WIDE, OUT>), grid, dim3(256), 0, s, a);
-    else if (p.tile_m == 32) hipLaunchKernelGGL(HIP_KERNEL_NAME(product_kernel<2, 4, 1, ST, WIDE, OUT>), grid, dim3(256), 0, s, a);
-    else hipLaunchKernelGGL(HIP_KERNEL_NAME(product_kernel<4, 4, 1, ST, WIDE, OUT>), grid, dim3(256), 0, s, a);
+    if (p.tile_m == 16) hipLaunchKernelGGL(HIP_KERNEL_NAME(product_staged_kernel<1, ST, WIDE, OUT>), grid, dim3(256), 0, s, a);
+    else hipLaunchKernelGGL(HIP_KERNEL_NAME(product_staged_kernel<2, ST, WIDE, OUT>), grid, dim3(256), 0, s, a);
     return;
   }
   if (p.tile_m == 64) launch_tile<ST, WIDE, OUT, 1>(a, s);

@@ -126,30 +126,29 @@ __device__ __forceinline__ void put_row16(void* row, int64_t n, int64_t N, const
   }
 }
 
-// Tiles of 64 WN rows of w by 16 UM WM rows of x, WN x WM waves.  The rows of
-// w are the matrix instruction's rows, in an order that gives each lane 16
-// neighbouring values of one output row.
-template <int UM, int WN, int WM, int ST, bool WIDE, int OUT>
-__global__ void __launch_bounds__(64 * WN * WM) product_kernel(ProductArgs a) {
-  constexpr int TN = 64 * WN, TM = 16 * UM * WM, NWV = WN * WM, GROUPS = (TN + TM) / 8, PER = (GROUPS + NWV - 1) / NWV;
+// Few rows of x (16 UM at most) and a long w, whose reading bounds them: tiles
+// of 256 rows of w, four waves of 64 each, whole lines of w at a time into LDS,
+// one step ahead (one row x 129,280 x 5,120: 115 us, 5.7 TB/s; 16 rows 118).  The
+// rows of w are the matrix instruction's rows, in an order that gives each lane
+// 16 neighbouring values of one output row.
+template <int UM, int ST, bool WIDE, int OUT>
+__global__ void __launch_bounds__(256) product_staged_kernel(ProductArgs a) {
+  constexpr int TN = 256, TM = 16 * UM, NWV = 4, GROUPS = (TN + TM) / 8, PER = (GROUPS + NWV - 1) / NWV;
   __shared__ __align__(16) uint8_t lds[2][(TN + TM) * kBlock];
-  const int64_t total = a.tiles_m * a.tiles_n * a.splits;
+  const int64_t total = a.tiles_n * a.splits;
   int64_t b = block_number(total);
   if (b < 0) return;
-  // Workgroups go to the eight XCDs in turn: each takes a stretch of tiles, m
-  // first, so that those in work at a time share rows of both matrices in its L2.
+  // Workgroups go to the eight XCDs in turn: each takes a stretch of tiles.
   if (total >= 64) {
     const int64_t each = total / 8, more = total % 8, xcd = b & 7;
     b = xcd * each + (xcd < more ? xcd : more) + (b >> 3);
   }
-  const int64_t tm = b % a.tiles_m, rest = b / a.tiles_m;
-  const int64_t tn = rest % a.tiles_n;
-  const int split = (int)(rest / a.tiles_n);
-  const int64_t m0 = tm * TM, n0 = tn * TN;
+  const int64_t n0 = b % a.tiles_n * TN;
+  const int split = (int)(b / a.tiles_n);
   const int first = split * a.split_steps, last = first + a.split_steps < a.steps ? first + a.split_steps : a.steps;
-  const int rows_w = a.N - n0 < TN ? (int)(a.N - n0) : TN, rows_x = a.M - m0 < TM ? (int)(a.M - m0) : TM;
-  const uint8_t *w0 = a.w + n0 * a.w_stride, *x0 = a.x + m0 * a.x_stride;
-  const int lane = lane_id(), wave = wave_id(), wn = wave % WN, wm = wave / WN, r = lane & 15, g = lane >> 4;
+  const int rows_w = a.N - n0 < TN ? (int)(a.N - n0) : TN, rows_x = (int)a.M;
+  const uint8_t *w0 = a.w + n0 * a.w_stride;
+  const int lane = lane_id(), wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6), r = lane & 15, g = lane >> 4;
 
   // A row's eight chunks of 16 bytes lie in LDS in an order of its own, so
   // that 16 lanes that read the same chunk of 16 rows hit different banks.
@@ -165,7 +164,7 @@ __global__ void __launch_bounds__(64 * WN * WM) product_kernel(ProductArgs a) {
   }
   const auto fetch = [&](int step, int buf) {
     const int64_t at = (int64_t)step * kBlock;
-    const __amdgpu_buffer_rsrc_t fw = buffer_of(w0 + at, rows_w * a.w_stride - at), fx = buffer_of(x0 + at, rows_x * a.x_stride - at);
+    const __amdgpu_buffer_rsrc_t fw = buffer_of(w0 + at, rows_w * a.w_stride - at), fx = buffer_of(a.x + at, rows_x * a.x_stride - at);
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
       const int group = wave + i * NWV;
@@ -181,13 +180,13 @@ __global__ void __launch_bounds__(64 * WN * WM) product_kernel(ProductArgs a) {
 #pragma unroll
     for (int u = 0; u < UM; ++u) acc[t][u] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
   }
-  const int at_w = (wn * 64 + 16 * (r >> 2) + (r & 3)) * kBlock + ((g ^ (r & 7)) * 16);
-  const int at_x = (TN + wm * 16 * UM + r) * kBlock + ((g ^ (r & 7)) * 16);
-  const int64_t sn = (n0 + wn * 64 < a.N ? n0 + wn * 64 : a.N - 1) / kBlock;
+  const int at_w = (wave * 64 + 16 * (r >> 2) + (r & 3)) * kBlock + ((g ^ (r & 7)) * 16);
+  const int at_x = (TN + r) * kBlock + ((g ^ (r & 7)) * 16);
+  const int64_t sn = (n0 + wave * 64 < a.N ? n0 + wave * 64 : a.N - 1) / kBlock;
   int64_t sm[UM];
 #pragma unroll
   for (int u = 0; u < UM; ++u) {
-    const int64_t m = m0 + wm * 16 * UM + 16 * u + r;
+    const int64_t m = 16 * u + r;
     sm[u] = (m < a.M ? m : a.M - 1) * a.xs_stride;
   }
 
@@ -245,7 +244,7 @@ __global__ void __launch_bounds__(64 * WN * WM) product_kernel(ProductArgs a) {
   if (a.splits > 1) out += (int64_t)split * a.M * a.out_stride * (int64_t)sizeof(typename El<OUT>::T);
 #pragma unroll
   for (int u = 0; u < UM; ++u) {
-    const int64_t m = m0 + wm * 16 * UM + 16 * u + r;
+    const int64_t m = 16 * u + r;
     if (m >= a.M) continue;
     float v[16];
 #pragma unroll
@@ -253,16 +252,15 @@ __global__ void __launch_bounds__(64 * WN * WM) product_kernel(ProductArgs a) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) v[4 * t + i] = acc[t][u][i];
     }
-    put_row16<OUT>(out + m * a.out_stride * (int64_t)sizeof(typename El<OUT>::T), n0 + wn * 64 + 16 * g, a.N, v);
+    put_row16<OUT>(out + m * a.out_stride * (int64_t)sizeof(typename El<OUT>::T), n0 + wave * 64 + 16 * g, a.N, v);
   }
 }
 
-// Few rows of x (16 UM at most): what bounds them is the reading of w.  A
-// workgroup takes 64 rows of w, each of its four waves every fourth block of
+// Few rows of x (16 UM at most) and a w that is not long: a workgroup takes 64 rows of w, each of its four waves every fourth block of
 // 128 columns, straight from memory into registers one block ahead, without a
 // barrier; the waves' sums meet in LDS at the end.
 template <int UM, int ST, bool WIDE, int OUT>
-__global__ void __launch_bounds__(256) product_few_kernel(ProductArgs a) {
+__global__ void __launch_bounds__(256) product_direct_kernel(ProductArgs a) {
   constexpr int TM = 16 * UM, PITCH = 68;  // (a row's 64 sums, and room that spreads rows over the banks)
   __shared__ __align__(16) float part[4][TM * PITCH];
   const int64_t b = block_number(a.tiles_m * a.tiles_n * a.splits);
