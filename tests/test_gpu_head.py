@@ -159,7 +159,7 @@ def test_product_of_long_rows(n, V, width, kind):
         _check(B.block_product(x, w, out), worth(x, 1), worth(w, 128), out)
 
 
-@pytest.mark.parametrize("n", [1, 16, 24, 64, 384])
+@pytest.mark.parametrize("n", [1, 16, 24, 32, 33, 64, 384])
 def test_product_of_a_full_vocabulary(n):
     V, width = 129280, 1024
     x = B.quantize_blocks(_x(n, width, torch.bfloat16, 5).to(dev), 1)
@@ -220,6 +220,24 @@ def test_nan_and_infinity_reach_their_row(kind):
     bad[[3, 7, 9]] = True
     assert y[bad].isnan().all() and y[~bad].isfinite().all()
     assert B.propose(wide(y.cpu(), dev))["status"].tolist() == [int(b) for b in bad]  # ROW_NAN
+
+
+@pytest.mark.parametrize("kind", ["f32", "pow2"])
+@pytest.mark.parametrize("n,V", [(3, 700), (40, 300), (200, 500)])
+def test_nan_scales(n, V, kind):
+    """A scale that is a NaN reaches the outputs of its rows, and no others, whatever its values are."""
+    x = B.quantize_blocks(_x(n, 512, torch.bfloat16, 1).to(dev), 1, KINDS[kind])
+    w = _weight(V, 512, kind, 2)
+    sx, sw = x["scales"].float(), w["scales"].float()
+    sx[n // 2, 2] = float("nan")
+    sw[1, 3] = float("nan")
+    bad = torch.zeros((n, V), dtype=torch.bool, device=dev)
+    bad[n // 2] = True
+    bad[:, 128:256] = True
+    q = [{"values": t["values"], "scales": s.to(KINDS[kind])} for t, s in ((x, sx), (w, sw))]
+    for out in (torch.float32, torch.bfloat16):
+        y = B.block_product(*q, out)
+        assert y[bad].isnan().all() and y[~bad].isfinite().all()
 
 
 @pytest.mark.parametrize("kind", ["f32", "pow2"])

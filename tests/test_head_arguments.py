@@ -27,6 +27,7 @@ def test_quantize_refusals():
     for bad in (_q(4, values=0x10008), _q(4, stride=264), _q(4, scales=0x20002)):
         assert _quantize(x, bad) == -2
     assert _quantize(B.Rows(0x40008, 1, 0, 4, 250, 256), _q(4)) == -2
+    assert _quantize(x, _q(4, values=0x40100)) == -1                             # onto the rows
     lib = B.load_library()
     assert lib.dspark_quantize_blocks(None, ctypes.byref(_q(4)), None) == -1
     assert lib.dspark_quantize_blocks(ctypes.byref(x), None, None) == -1
@@ -47,6 +48,7 @@ def test_product_refusals():
     assert _product(x, w, stride=1004) == -2                                     # 2,008 bytes
     assert _product(x, w, out=0x900008) == -2
     assert _product(x, w, out=0) == -1
+    assert _product(x, w, out=0x10010) == -1 and _product(_q(4, values=0x800000), _q(1000, rows=128, values=0x900100)) == -1  # onto an input
     assert _product(_q(0), w, out=0) == 0 and _product(x, _q(0, rows=128), out=0) == 0
     lib = B.load_library()
     assert lib.dspark_block_product(None, ctypes.byref(w), fake, 1, 1000, None, 0, None) == -1
@@ -75,6 +77,7 @@ def test_linear_refusals():
     assert call(B.Rows(0x40000, 1, 0, 4, 240, 256), w) == -1
     assert call(B.Rows(0x40000, 3, 0, 4, 250, 256), w) == -1
     assert call(x, w, stride=992) == -1 and call(x, w, stride=1004) == -2 and call(x, w, out=0x900004) == -2
+    assert call(x, w, out=0x40010) == -1 and call(x, _q(1000, rows=128, values=0x900100)) == -1
     assert call(x, w, ws=None) == -3 and call(x, w, nbytes=need - 1) == -3
     assert call(x, w, ws=ctypes.c_void_p(0x10004)) == -2
     assert call(B.Rows(None, 1, 0, 0, 250, 256), w, out=0, ws=None, nbytes=0) == 0

@@ -87,6 +87,16 @@ int check_product_out(int64_t M, int64_t N, const void* out, int32_t dtype, int6
   return DSPARK_SUCCESS;
 }
 
+// whether `bytes` bytes at p meet rows of out
+bool meet(const void* p, int64_t bytes, const void* out, int64_t rows, int64_t row_bytes, int64_t stride_bytes) {
+  const char *a = static_cast<const char*>(p), *b = static_cast<const char*>(out);
+  return rows > 0 && bytes > 0 && a < b + (rows - 1) * stride_bytes + row_bytes && b < a + bytes;
+}
+int64_t fp8_bytes(const dspark_fp8* q) { return q->n_rows > 0 ? (q->n_rows - 1) * q->row_stride + q->cols : 0; }
+int64_t rows_bytes(const dspark_rows* x) {
+  return x->n_rows > 0 ? ((x->n_rows - 1) * x->row_stride + x->vocab) * (x->dtype == DSPARK_BF16 ? 2 : 4) : 0;
+}
+
 enum ProductWay { kDirect, kStaged, kTiles };
 struct ProductPlan {
   ProductWay way;
@@ -264,6 +274,8 @@ int dspark_quantize_blocks(const dspark_rows* x, const dspark_fp8* out, void* st
   if (out->n_rows != x->n_rows) return fail(DSPARK_EINVAL, "the fp8 matrix has another number of rows");
   if (out->cols != up(x->vocab, 16)) return fail(DSPARK_EINVAL, "fp8 cols must be the rows' width rounded up to a multiple of 16");
   if (x->n_rows == 0) return DSPARK_SUCCESS;
+  if (meet(x->data, rows_bytes(x), out->values, out->n_rows, out->cols, out->row_stride))
+    return fail(DSPARK_EINVAL, "the fp8 matrix overlaps the rows");
   quantize(x, out, 1, static_cast<hipStream_t>(stream));
   return host_check_launch();
 }
@@ -284,6 +296,10 @@ int dspark_block_product(const dspark_fp8* x, const dspark_fp8* w, void* out, in
   rc = check_product_out(x->n_rows, w->n_rows, out, out_dtype, out_stride);
   if (rc) return rc;
   if (x->n_rows == 0 || w->n_rows == 0) return DSPARK_SUCCESS;
+  const int64_t es = out_dtype == DSPARK_BF16 ? 2 : 4;
+  if (meet(x->values, fp8_bytes(x), out, x->n_rows, w->n_rows * es, out_stride * es) ||
+      meet(w->values, fp8_bytes(w), out, x->n_rows, w->n_rows * es, out_stride * es))
+    return fail(DSPARK_EINVAL, "output rows overlap an input");
   rc = check_ws(product_bytes(x->n_rows, w->n_rows, x->cols), ws, ws_bytes);
   if (rc) return rc;
   product(x, 1, w, out, out_dtype, out_stride, ws, static_cast<hipStream_t>(stream));
@@ -305,6 +321,10 @@ int dspark_block_linear(const dspark_rows* x, const dspark_fp8* w, void* out, in
   rc = check_product_out(x->n_rows, w->n_rows, out, out_dtype, out_stride);
   if (rc) return rc;
   if (x->n_rows == 0 || w->n_rows == 0) return DSPARK_SUCCESS;
+  const int64_t es = out_dtype == DSPARK_BF16 ? 2 : 4;
+  if (meet(x->data, rows_bytes(x), out, x->n_rows, w->n_rows * es, out_stride * es) ||
+      meet(w->values, fp8_bytes(w), out, x->n_rows, w->n_rows * es, out_stride * es))
+    return fail(DSPARK_EINVAL, "output rows overlap an input");
   const LinearPlan p = linear_plan(x->n_rows, w->n_rows, x->vocab);
   rc = check_ws(p.bytes, ws, ws_bytes);
   if (rc) return rc;

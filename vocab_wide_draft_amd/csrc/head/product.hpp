@@ -453,11 +453,11 @@ __global__ void __launch_bounds__(512, 2) product_tile_kernel(ProductArgs a) {
     if (j < GW) {
       const int col = col_w ^ (j & 1 ? 64 : 0);
       load_lds_ahead<16>(buffer_words(from_w + at, left > 0 ? bytes_w - at : 0), to_w + (uint32_t)(buf * BUF + j * 1024),
-                     (col < left ? base_w + col : kPastEnd) + j * 8 * (int)a.w_stride);
+                     (int)((uint32_t)(col < left ? base_w + col : kPastEnd) + (uint32_t)(j * 8) * (uint32_t)a.w_stride));
     } else {
       j -= GW;
       load_lds_ahead<16>(buffer_words(from_x + at, left > 0 ? bytes_x - at : 0), to_x + (uint32_t)(buf * BUF + j * 1024),
-                     (col_x < left ? base_x + col_x : kPastEnd) + j * 8 * (int)a.x_stride);
+                     (int)((uint32_t)(col_x < left ? base_x + col_x : kPastEnd) + (uint32_t)(j * 8) * (uint32_t)a.x_stride));
     }
   };
   // a part's share of the fetches from `lo` to `hi`, after its u-th group of instructions
