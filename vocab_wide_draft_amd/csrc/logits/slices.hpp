@@ -18,9 +18,10 @@ __device__ __forceinline__ int64_t block_number(int64_t total) {
   return b < total ? b : -1;
 }
 
-// The row and slice of a workgroup of a grid laid out by row_slice_grid: the slices of one row go to workgroups eight apart, which run on one
-// of the eight XCDs, so that what they all read of the row stays in its L2.
-// False past the last row (uniform).
+// The row and slice of a workgroup of a grid laid out by row_slice_grid: the
+// slices of one row go to workgroups eight apart, which run on one of the eight
+// XCDs, so that what they all read of the row stays in its L2.  False past the
+// last row (uniform).
 __device__ __forceinline__ bool row_slice(int64_t n, int slices, int64_t& r, int& s) {
   const uint32_t x = blockIdx.x >> 3, rows = x / (uint32_t)slices;
   s = (int)(x - rows * (uint32_t)slices);
