@@ -130,8 +130,8 @@ ProductPlan product_plan(int64_t M, int64_t N, int64_t K, bool wide) {
     // 64 u rows 0.38 + 0.28 u us, and 0.86 us for its columns of w out of memory
     // shared by the tiles that read them; three steps for a tile's beginning and
     // end; the parts' way through memory.  (129,280 x 5,120, powers of two, us for
-    // u = 1, 2, 3, 4: 64 rows 133, 138, 162, 168; 128: 195, 152, 172, 176; 256:
-    // 308, 230, 276, 206; 384: 405, 308, 294, 304; 768: 741, 538, 509, 439; 5,120:
+    // u = 1, 2, 3, 4: 64 rows 133, 138, 153, 168; 128: 195, 152, 150, 176; 256:
+    // 308, 230, 255, 206; 384: 405, 308, 264, 304; 768: 741, 538, 508, 439; 5,120:
     // 4,500, 3,190, 2,870, 2,560.)
     p.way = kTiles;
     double best = 0.0;

@@ -402,18 +402,26 @@ __global__ void __launch_bounds__(256) product_direct_kernel(ProductArgs a) {
 //
 // Where U leaves room for three buffers a fetch has two steps to arrive (128
 // rows 172 -> 152 us, 64 rows 154 -> 133: what bounds those is the reading of
-// w).  The largest tiles are bound by power: with 65 % of the matrix cores'
-// cycles in use the clock falls from 2.4 to 1.9 GHz (2.56 ms, 2,645 TFLOP/s;
-// 2.22 ms at 2.2 GHz without the fetches).  A second barrier a step, which
-// gives a fetch more time, costs more than it gives there (2,867 us).
+// w), at 192 rows those of w alone, that of x one (192 rows, powers of two, 172
+// -> 159 us, 384 rows 282 -> 257; with scales of their own 177 and 292 either
+// way, 576 rows 410 -> 427, so those have two).  The largest tiles are bound by
+// power: with 65 % of the matrix cores' cycles in use the clock falls from 2.4
+// to 1.9 GHz (2.56 ms, 2,645 TFLOP/s; 2.22 ms at 2.2 GHz without the fetches).
+// A second barrier a step, which gives a fetch more time, costs more than it
+// gives there (2,867 us).
 template <int U, int ST, bool WIDE, int OUT>
 __global__ void __launch_bounds__(512, 2) product_tile_kernel(ProductArgs a) {
-  constexpr int TN = 256, TM = 64 * U, T = 8, BUF = (TN + TM) * kBlock, GW = 4, GX = U, FETCHES = GW + GX, EARLY = (FETCHES + 1) / 2;
-  constexpr int STAGES = U <= 2 ? 3 : 2;  // buffers that LDS has room for
+  constexpr int TN = 256, TM = 64 * U, T = 8, GW = 4, GX = U, FETCHES = GX + GW, EARLY = (FETCHES + 1) / 2;
+  // buffers of w and of x: as many of both that a pair is one piece of LDS, or all of w's and then x's
+  constexpr int WS = U <= 2 || (U == 3 && ST == DSPARK_SCALE_E8M0) ? 3 : 2, XS = U <= 2 ? 3 : 2;
+  constexpr bool PAIRS = WS == XS;
+  constexpr int BUF_W = (PAIRS ? TN + TM : TN) * kBlock, BUF_X = (PAIRS ? TN + TM : TM) * kBlock, X_AT = (PAIRS ? TN : WS * TN) * kBlock;
+  // fetches that may still be on their way when a step's have to be there
+  constexpr int AHEAD = PAIRS ? (WS - 2) * (FETCHES + 1) : GW;
   constexpr int AT_ONCE = 2, PARTS = T / AT_ONCE;  // rows of 16 of w between two reads
   constexpr int SE = ST == DSPARK_SCALE_F32 ? 4 : 1;
-  __shared__ __align__(16) uint8_t lds[STAGES][BUF];
-  __shared__ uint32_t scales[STAGES][TM + 128];  // of x's rows, of w's two blocks, and room that nobody reads
+  __shared__ __align__(16) uint8_t lds[(WS * TN + XS * TM) * kBlock];
+  __shared__ uint32_t scales[XS][TM + 128];  // of x's rows, of w's two blocks, and room that nobody reads
   const int64_t total = a.tiles_m * a.tiles_n * a.splits;
   int64_t b = block_number(total);
   if (b < 0) return;
@@ -445,26 +453,30 @@ __global__ void __launch_bounds__(512, 2) product_tile_kernel(ProductArgs a) {
   const int64_t bytes_w = rows_w * a.w_stride, bytes_x = rows_x * a.x_stride;
   const int col_x = ((lane & 7) ^ sub) * 16, col_w = ((lane & 7) ^ (sub & 3)) * 16;
   const int base_w = w_row * (int)a.w_stride, base_x = x_row * (int)a.x_stride;
-  const uint32_t to_w = lds_address(&lds[0][wave * 8 * GW * kBlock]), to_x = lds_address(&lds[0][(TN + wave * 8 * GX) * kBlock]);
-  // the j-th of a wave's GW + GX fetches of a step
-  const auto fetch = [&](int step, int buf, int j) {
-    const int64_t at = (int64_t)step * kBlock;
-    const int left = step < last ? a.K - (int)at : 0;
-    if (j < GW) {
-      const int col = col_w ^ (j & 1 ? 64 : 0);
-      load_lds_ahead<16>(buffer_words(from_w + at, left > 0 ? bytes_w - at : 0), to_w + (uint32_t)(buf * BUF + j * 1024),
-                     (int)((uint32_t)(col < left ? base_w + col : kPastEnd) + (uint32_t)(j * 8) * (uint32_t)a.w_stride));
-    } else {
-      j -= GW;
-      load_lds_ahead<16>(buffer_words(from_x + at, left > 0 ? bytes_x - at : 0), to_x + (uint32_t)(buf * BUF + j * 1024),
+  const uint32_t to_w = lds_address(&lds[wave * 8 * GW * kBlock]), to_x = lds_address(&lds[X_AT + wave * 8 * GX * kBlock]);
+  // the j-th of a wave's fetches of x and w, for steps and into buffers of their own
+  const auto fetch = [&](int step_x, int buf_x, int step_w, int buf_w, int j) {
+    if constexpr (PAIRS) j = j < GW ? j + GX : j - GW;  // (otherwise x first: it has less time)
+    if (j < GX) {
+      const int64_t at = (int64_t)step_x * kBlock;
+      const int left = step_x < last ? a.K - (int)at : 0;
+      load_lds_ahead<16>(buffer_words(from_x + at, left > 0 ? bytes_x - at : 0), to_x + (uint32_t)(buf_x * BUF_X + j * 1024),
                      (int)((uint32_t)(col_x < left ? base_x + col_x : kPastEnd) + (uint32_t)(j * 8) * (uint32_t)a.x_stride));
+    } else {
+      j -= GX;
+      const int64_t at = (int64_t)step_w * kBlock;
+      const int left = step_w < last ? a.K - (int)at : 0;
+      const int col = col_w ^ (j & 1 ? 64 : 0);
+      load_lds_ahead<16>(buffer_words(from_w + at, left > 0 ? bytes_w - at : 0), to_w + (uint32_t)(buf_w * BUF_W + j * 1024),
+                     (int)((uint32_t)(col < left ? base_w + col : kPastEnd) + (uint32_t)(j * 8) * (uint32_t)a.w_stride));
     }
   };
-  // a part's share of the fetches from `lo` to `hi`, after its u-th group of instructions
-  const auto share = [&](int step, int buf, int lo, int hi, int u) {
+  // a part's share of the fetches from `lo` to `hi`, after its u-th group of instructions: those that step
+  // `after` leaves its buffers to
+  const auto share = [&](int after, int buf_x, int buf_w, int lo, int hi, int u) {
 #pragma unroll
     for (int j = 0; j < FETCHES; ++j)
-      if (j >= lo + (hi - lo) * u / U && j < lo + (hi - lo) * (u + 1) / U) fetch(step, buf, j);
+      if (j >= lo + (hi - lo) * u / U && j < lo + (hi - lo) * (u + 1) / U) fetch(after + XS, buf_x, after + WS, buf_w, j);
   };
   // Scales: the first U waves' lanes a row of x each, the next wave's first two
   // lanes a block of w each (the rest fetch nothing, into room for it).
@@ -488,13 +500,13 @@ __global__ void __launch_bounds__(512, 2) product_tile_kernel(ProductArgs a) {
     for (int u = 0; u < U; ++u) acc[t][u] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
   }
   const int at_w = (wn * 128 + 8 * (r >> 2) + (r & 3)) * kBlock + ((g ^ (r & 7)) * 16);
-  const int at_x = (TN + wm * 16 * U + r) * kBlock + ((g ^ (r & 7)) * 16);
+  const int at_x = X_AT + (wm * 16 * U + r) * kBlock + ((g ^ (r & 7)) * 16);
   // the matrix instruction's row 4 g + i of its t-th 16 is row 32 (t / 2) + 8 g
   // + 4 (t % 2) + i, so that a lane holds eight neighbours of an output row and
   // four lanes 64 or 128 bytes of it
   const auto row_of = [](int t) { return 32 * (t >> 1) + 4 * (t & 1); };
   const auto frag = [&](int buf, int at) {
-    const v4i lo = *reinterpret_cast<const v4i*>(&lds[0][buf * BUF + at]), hi = *reinterpret_cast<const v4i*>(&lds[0][buf * BUF + (at ^ 64)]);
+    const v4i lo = *reinterpret_cast<const v4i*>(&lds[buf + at]), hi = *reinterpret_cast<const v4i*>(&lds[buf + (at ^ 64)]);
     return v8i{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
   };
 
@@ -560,7 +572,7 @@ __global__ void __launch_bounds__(512, 2) product_tile_kernel(ProductArgs a) {
   };
   const auto read_w = [&](int buf, int part, int to) {
 #pragma unroll
-    for (int i = 0; i < AT_ONCE; ++i) fw[to][i] = frag(buf, at_w + row_of(part * AT_ONCE + i) * kBlock);
+    for (int i = 0; i < AT_ONCE; ++i) fw[to][i] = frag(buf * BUF_W, at_w + row_of(part * AT_ONCE + i) * kBlock);
   };
   const auto part = [&](int p, auto between) {
 #pragma unroll
@@ -572,30 +584,33 @@ __global__ void __launch_bounds__(512, 2) product_tile_kernel(ProductArgs a) {
   const auto nothing = [](int) {};
 
   if (first < last) {
+    // as if steps had come before the first
 #pragma unroll
-    for (int s = 0; s < STAGES; ++s) {
-      fetch_scales(first + s, s);
+    for (int s = -WS; s < 0; ++s) {
+      if (s + XS >= 0) fetch_scales(first + s + XS, s + XS);
 #pragma unroll
-      for (int j = 0; j < (s < STAGES - 1 ? FETCHES : EARLY); ++j) fetch(first + s, s, j);
+      for (int j = 0; j < (s < -1 ? FETCHES : EARLY); ++j)
+        if (s + XS >= 0 || j >= GX) fetch(first + s + XS, s + XS, first + s + WS, s + WS, j);
     }
-    loads_but<(STAGES - 2) * (FETCHES + 1) + 1 + EARLY>();
+    loads_but<AHEAD + 1 + EARLY>();
     group_barrier();
     read_scales(0);
 #pragma unroll
     for (int u = 0; u < U; ++u) fx[u] = frag(0, at_x + u * 16 * kBlock);
     read_w(0, 0, 0);
-    int buf = 0;
+    int buf_x = 0, buf_w = 0;
     for (int step = first; step + 1 < last; ++step) {
-      const int next = buf + 1 < STAGES ? buf + 1 : 0, before = buf > 0 ? buf - 1 : STAGES - 1;
+      const int next_x = buf_x + 1 < XS ? buf_x + 1 : 0, before_x = buf_x > 0 ? buf_x - 1 : XS - 1;
+      const int next_w = PAIRS ? next_x : buf_w + 1 < WS ? buf_w + 1 : 0, before_w = PAIRS ? before_x : buf_w > 0 ? buf_w - 1 : WS - 1;
       widen_x();
 #pragma unroll
       for (int p = 0; p < PARTS - 1; ++p) {
-        read_w(buf, p + 1, (p + 1) & 1);
+        read_w(buf_w, p + 1, (p + 1) & 1);
         __builtin_amdgcn_sched_barrier(0);
         if (p == 0) {
           part(p, [&](int u) {
             __builtin_amdgcn_sched_barrier(0);
-            share(step + STAGES - 1, before, EARLY, FETCHES, u);
+            share(step - 1, before_x, before_w, EARLY, FETCHES, u);
             __builtin_amdgcn_sched_barrier(0);
           });
         } else {
@@ -603,26 +618,27 @@ __global__ void __launch_bounds__(512, 2) product_tile_kernel(ProductArgs a) {
         }
         __builtin_amdgcn_sched_barrier(0);
       }
-      loads_but<(STAGES - 2) * (FETCHES + 1)>();
-      group_barrier();  // the next step's buffer has arrived, this one has been read
-      read_w(next, 0, PARTS & 1);
-      fetch_scales(step + STAGES, buf);
+      loads_but<AHEAD>();
+      group_barrier();  // the next step's buffers have arrived, this one's have been read
+      read_w(next_w, 0, PARTS & 1);
+      fetch_scales(step + XS, buf_x);
       __builtin_amdgcn_sched_barrier(0);
       part(PARTS - 1, [&](int u) {
         __builtin_amdgcn_sched_barrier(0);
-        fx[u] = frag(next, at_x + u * 16 * kBlock);
-        share(step + STAGES, buf, 0, EARLY, u);
+        fx[u] = frag(next_x * BUF_X, at_x + u * 16 * kBlock);
+        share(step, buf_x, buf_w, 0, EARLY, u);
         __builtin_amdgcn_sched_barrier(0);
       });
       if constexpr (LATER) add_late(T - AT_ONCE, U - 1);
       __builtin_amdgcn_sched_barrier(0);
-      read_scales(next);
-      buf = next;
+      read_scales(next_x);
+      buf_x = next_x;
+      buf_w = next_w;
     }
     widen_x();
 #pragma unroll
     for (int p = 0; p < PARTS; ++p) {
-      if (p + 1 < PARTS) read_w(buf, p + 1, (p + 1) & 1);
+      if (p + 1 < PARTS) read_w(buf_w, p + 1, (p + 1) & 1);
       part(p, nothing);
     }
     if constexpr (LATER) add_late(T - AT_ONCE, U - 1);
