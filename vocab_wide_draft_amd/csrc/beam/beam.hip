@@ -23,7 +23,7 @@ BeamPlan beam_plan_of(int64_t n, int64_t V, int n_out, int slice) {
   BeamPlan p{};
   p.slice = slice;
   p.slices = (int)((V + slice - 1) / slice);
-  p.cap = 2 * n_out + 64;
+  p.cap = beam_cap(n_out);
   p.part_at = (size_t)n * (size_t)p.slices * (size_t)p.cap * sizeof(uint64_t);
   p.bytes = p.part_at + (size_t)n * (size_t)p.slices * sizeof(BeamPart);
   return p;

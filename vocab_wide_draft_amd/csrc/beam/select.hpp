@@ -14,9 +14,9 @@
 // the log-sum-exp.  Between beams it hangs on their log-sum-exps, which
 // binary32 exponentials give to kLseOff at most: an exponent t in base 2 is
 // rounded by |t| 2^-24, and as much again by half from log2(e), the hardware
-// exponential is off by 2^-23, and eight terms are added in binary32 before
-// binary64 takes them; the weights' mean |t| is below 18 for 2^20 logits, so
-// that is 2^-24 (0.7 * 1.5 * 18 + 2 + 8) = 1.8e-6.  Where two neighbours in the
+// exponential is off by 2^-23, and a term is in at most twelve sums of a thread
+// and six of a wave before binary64 takes them; the weights' mean |t| is below
+// 18 for 2^20 logits, so that is 2^-24 (0.7 * 1.5 * 18 + 2 + 18) = 2.4e-6.  Where two neighbours in the
 // merged order of different beams lie closer than twice kLseOff, their beams'
 // log-sum-exps are computed again in binary64 and what decides is compared again
 // (60 us more where two beams of 129,280 ids are alike; random requests come so
@@ -29,7 +29,10 @@ namespace dspark {
 
 constexpr int kBeams = 64;      // beams of a request: a lane each
 constexpr int kBeamOut = 128;   // candidates selected
-constexpr double kLseOff = 2e-6;
+constexpr double kLseOff = 2.5e-6;
+// candidates of a slice's list that there is room for
+__host__ __device__ constexpr int beam_cap(int n_out) { return 2 * n_out + 64; }
+constexpr int kBeamCap = beam_cap(kBeamOut);
 
 struct BeamPart {
   float m;              // the slice's maximum
@@ -91,8 +94,9 @@ __device__ __forceinline__ uint32_t reached_by(uint4 v, int n) {
 
 template <int DT, int U>
 __global__ void __launch_bounds__(kSliceBS) beam_slice_kernel(BeamArgs a) {
-  constexpr int N = kVec<DT>, WORDS = (U * N + 31) / 32;
+  constexpr int N = kVec<DT>;
   __shared__ __align__(16) uint32_t most[kSliceBS];
+  __shared__ uint64_t near[kSliceNW][kBeamCap];  // a wave's candidates
   __shared__ float wave_m[kSliceNW];
   __shared__ uint32_t any_flags, held, counts[kSliceNW];
   typedef typename El<DT>::T XT;
@@ -114,10 +118,7 @@ __global__ void __launch_bounds__(kSliceBS) beam_slice_kernel(BeamArgs a) {
       for (int w = 0; w < 4; ++w) raw[i].w[w] = DT == DSPARK_F32 ? 0xff800000u : 0xff80ff80u;
     }
   }
-  if (tid == 0) {
-    any_flags = 0u;
-    held = 0u;
-  }
+  if (tid == 0) any_flags = 0u;
   float x[U][N];
 #pragma unroll
   for (int i = 0; i < U; ++i) unpack<DT, N>(raw[i], x[i]);
@@ -137,22 +138,24 @@ __global__ void __launch_bounds__(kSliceBS) beam_slice_kernel(BeamArgs a) {
   // the threshold, by every wave for itself: -inf is no candidate
   float t = top_key_value<DSPARK_BF16>(reached_by(*reinterpret_cast<const uint4*>(most + 4 * lane_id()), a.n_out));
   t = t >= -3.4028235e38f ? t : -3.4028235e38f;
-  uint32_t mask[WORDS];  // element l of vector i at bit N i + N - 1 - l
+  uint32_t n = 0;  // the wave's candidates (uniform); their order does not matter
 #pragma unroll
-  for (int w = 0; w < WORDS; ++w) mask[w] = 0u;
+  for (int i = 0; i < U; ++i) {
 #pragma unroll
-  for (int i = U - 1; i >= 0; --i) {
-#pragma unroll
-    for (int l = 0; l < N; ++l) push_ge(mask[i * N / 32], x[i][l], t);
+    for (int l = 0; l < N; ++l) {
+      const uint64_t reach = __ballot(x[i][l] >= t);
+      if (reach) {  // (uniform)
+        const uint32_t at = n + __builtin_amdgcn_mbcnt_hi((uint32_t)(reach >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)reach, 0u));
+        if (x[i][l] >= t && at < (uint32_t)a.cap) near[wave_id()][at] = beam_key(x[i][l], start + (i * kSliceBS + tid) * N + l);
+        n += (uint32_t)__builtin_popcountll(reach);
+      }
+    }
   }
-  uint32_t mine = 0;
-#pragma unroll
-  for (int w = 0; w < WORDS; ++w) mine += (uint32_t)__builtin_popcount(mask[w]);
-  const uint32_t at = mine ? atomicAdd(&held, mine) : 0u;  // in any order: the keys have one
+  if (lane_id() == 0) counts[wave_id()] = n;
   const float ref = M == -__builtin_inff() ? 0.0f : M;
-  double sum = 0.0;
+  float sum = 0.0f;
 #pragma unroll
-  for (int i = 0; i < U; ++i) sum += (double)exp_sum(a.x, ref, x[i]);
+  for (int i = 0; i < U; ++i) sum += exp_sum(a.x, ref, x[i]);
   if (sum != sum || M == __builtin_inff()) {  // a NaN or a +inf in this thread, or the slice's
     uint32_t flags = 0;
 #pragma unroll
@@ -162,66 +165,69 @@ __global__ void __launch_bounds__(kSliceBS) beam_slice_kernel(BeamArgs a) {
     }
     if (flags) atomicOr(&any_flags, flags);
   }
-  const double wsum = wave_sum(sum);
-  if (lane_id() == 63) p.sum[wave_id()] = (float)wsum;
+  sum = wave_sum(sum);
+  if (lane_id() == 63) p.sum[wave_id()] = sum;
   __syncthreads();
   uint64_t* list = a.cand + (r * a.slices + s) * a.cap;
-  const uint32_t total = held;
+  uint32_t total = 0, before = 0;
+#pragma unroll
+  for (int w = 0; w < kSliceNW; ++w) {
+    if (w < wave_id()) before += counts[w];
+    total += counts[w];
+  }
   if (tid == 0) {
     p.m = M;
     p.flags = (int32_t)any_flags;
     p.count = total <= (uint32_t)a.cap ? (int)total : a.n_out;
   }
   if (total <= (uint32_t)a.cap) {  // (uniform)
-    uint32_t pos = at;
-#pragma unroll
-    for (int w = 0; w < WORDS; ++w) {
-      for (uint32_t left = mask[w]; left; left &= left - 1) {
-        const int bit = __builtin_ctz(left), e = w * 32 + (bit & ~(N - 1)) + (N - 1 - (bit & (N - 1)));  // vector and element
-        float v = x[0][0];
-#pragma unroll
-        for (int i = 0; i < U; ++i) {
-#pragma unroll
-          for (int l = 0; l < N; ++l) v = e == i * N + l ? x[i][l] : v;
-        }
-        list[pos++] = beam_key(v, start + (e / N * kSliceBS + tid) * N + e % N);
-      }
-    }
+    for (uint32_t i = (uint32_t)lane_id(); i < n; i += 64) list[before + i] = near[wave_id()][i];
     return;
   }
-  // too many (equal logits): the key that exactly n_out of them reach, by
-  // halving (uniform; a sum over the workgroup each time)
-  uint64_t lo = (uint64_t)key32(t) << 32, hi = ~0ull, least;  // reached by more than n_out, by fewer
-  for (;;) {
-    least = lo + ((hi - lo) >> 1);
-    mine = 0;
+  // too many (equal logits): the largest logit that n_out reach, then of its
+  // equals the lowest ids, each by halving (uniform; sums over the workgroup)
+  const auto reaching = [&](auto reaches) {
+    uint32_t mine = 0;
 #pragma unroll
     for (int i = 0; i < U; ++i) {
 #pragma unroll
-      for (int l = 0; l < N; ++l)
-        mine += x[i][l] >= t && beam_key(x[i][l], start + (i * kSliceBS + tid) * N + l) >= least ? 1u : 0u;
+      for (int l = 0; l < N; ++l) mine += (uint32_t)__builtin_popcountll(__ballot(reaches(x[i][l], (i * kSliceBS) * N + l)));
     }
-    const uint32_t w = wave_sum(mine);
     __syncthreads();
-    if (lane_id() == 0) counts[wave_id()] = w;
+    if (lane_id() == 0) counts[wave_id()] = mine;
     __syncthreads();
-    uint32_t reach = 0;
+    uint32_t sum_of = 0;
 #pragma unroll
-    for (int v = 0; v < kSliceNW; ++v) reach += counts[v];
-    if (reach == (uint32_t)a.n_out || hi - lo <= 1) break;  // (no two keys are alike: the former comes)
-    if (reach > (uint32_t)a.n_out) lo = least;
-    else hi = least;
+    for (int w = 0; w < kSliceNW; ++w) sum_of += counts[w];
+    return (uint32_t)__builtin_amdgcn_readfirstlane((int)sum_of);
+  };
+  uint32_t low = (uint32_t)__builtin_amdgcn_readfirstlane((int)key32(t)), high = (uint32_t)__builtin_amdgcn_readfirstlane((int)key32(M));  // keys that n_out reach, and that hold the one looked for
+  while (low < high) {
+    const uint32_t mid = low + ((high - low) >> 1) + 1;
+    const float f = top_key_value<DSPARK_F32>(mid);
+    if (reaching([&](float v, int) { return v >= f; }) >= (uint32_t)a.n_out) low = mid;
+    else high = mid - 1;
+  }
+  float f = top_key_value<DSPARK_F32>(low);
+  const uint32_t equal = (uint32_t)a.n_out - reaching([&](float v, int) { return v > f; });
+  int from = 0, to = a.length;  // ids below which fewer than `equal` of them lie, or as many
+  while (to - from > 1) {
+    const int mid = from + ((to - from) >> 1);
+    asm volatile("" : "+v"(f));  // (comparisons with it are not to be kept over the rounds)
+    if (reaching([&](float v, int id) { return v == f && tid * N < mid - id; }) >= equal) to = mid;
+    else from = mid;
   }
   if (tid == 0) held = 0u;
   __syncthreads();
+  asm volatile("" : "+v"(f));
 #pragma unroll
   for (int i = 0; i < U; ++i) {
 #pragma unroll
     for (int l = 0; l < N; ++l) {
-      const uint64_t k = beam_key(x[i][l], start + (i * kSliceBS + tid) * N + l);
-      if (x[i][l] >= t && k >= least) {
-        const uint32_t to = atomicAdd(&held, 1u);
-        if (to < (uint32_t)a.cap) list[to] = k;
+      const int id = (i * kSliceBS + tid) * N + l;
+      if (x[i][l] > f || (x[i][l] == f && id < to)) {
+        const uint32_t place = atomicAdd(&held, 1u);
+        if (place < (uint32_t)a.cap) list[place] = beam_key(x[i][l], start + id);
       }
     }
   }
