@@ -5,21 +5,23 @@
 // be among the row's best -- those that reach the n_out-th largest of its
 // threads' maxima, or of 64 groups' of four.  A second kernel joins a request:
 // its waves join their beams' slices into log-sum-exps, and its threads select
-// among all beams' candidates.  Reading bounds the first kernel (256 requests of
-// 8 beams, 2,048 bf16 rows of 129,280 ids: 117 us, 4.5 TB/s); the second is a
-// chain of one workgroup's latencies (8 us for one request of 4 beams, 12 us
-// for 256 of 8, 25 us for 8 of 32 with 64 selected).
+// among all beams' candidates.  The first kernel is bound by vector instructions
+// and reading alike (256 requests of 8 beams, 0.45 GB of bf16 rows of 129,280
+// ids: 94 us, 4.7 TB/s, 90 % of the cycles issue; 107 us while each thread picked
+// its candidates out of its registers; float32 rows 5.4 TB/s); the second is a
+// chain of one workgroup's latencies (8 us for one request of 4 beams, 11 us for
+// 256 of 8, 25 us for 8 of 32 with 64 selected).
 //
 // Order.  Within a beam the order of scores is the order of logits, whatever
 // the log-sum-exp.  Between beams it hangs on their log-sum-exps, which
 // binary32 exponentials give to kLseOff at most: an exponent t in base 2 is
 // rounded by |t| 2^-24, and as much again by half from log2(e), the hardware
-// exponential is off by 2^-23, and a term is in at most twelve sums of a thread
-// and six of a wave before binary64 takes them; the weights' mean |t| is below
-// 18 for 2^20 logits, so that is 2^-24 (0.7 * 1.5 * 18 + 2 + 18) = 2.4e-6.  Where two neighbours in the
+// exponential is off by 2^-23, and a term is in six sums of a thread and six of
+// a wave before binary64 takes them; the weights' mean |t| is below 18 for 2^20
+// logits, so that is 2^-24 (0.7 * 1.5 * 18 + 2 + 12) = 1.96e-6.  Where two neighbours in the
 // merged order of different beams lie closer than twice kLseOff, their beams'
 // log-sum-exps are computed again in binary64 and what decides is compared again
-// (60 us more where two beams of 129,280 ids are alike; random requests come so
+// (44 us more where two beams of 129,280 ids are alike; random requests come so
 // close once in some thousands).
 #pragma once
 #include "../logits/slices.hpp"
@@ -29,7 +31,7 @@ namespace dspark {
 
 constexpr int kBeams = 64;      // beams of a request: a lane each
 constexpr int kBeamOut = 128;   // candidates selected
-constexpr double kLseOff = 2.5e-6;
+constexpr double kLseOff = 2e-6;
 // candidates of a slice's list that there is room for
 __host__ __device__ constexpr int beam_cap(int n_out) { return 2 * n_out + 64; }
 constexpr int kBeamCap = beam_cap(kBeamOut);
@@ -92,8 +94,31 @@ __device__ __forceinline__ uint32_t reached_by(uint4 v, int n) {
   return T;
 }
 
+// the sum of the exponentials of N logits relative to m, quads first
+template <int N>
+__device__ __forceinline__ float beam_exp_sum(const TopArgs& a, float m, const float (&x)[N]) {
+  float sum[N / 4];
+  if (reference_fits(a, m)) {  // (uniform)
+    const float K = m * a.c;
+#pragma unroll
+    for (int l = 0; l < N; ++l) {
+      const float w = __builtin_amdgcn_exp2f(__builtin_fmaf(x[l], a.c, -K));
+      sum[l / 4] = l % 4 ? sum[l / 4] + w : w;
+    }
+  } else {
+#pragma unroll
+    for (int l = 0; l < N; ++l) {
+      const float w = __builtin_amdgcn_exp2f((x[l] - m) * a.c);
+      sum[l / 4] = l % 4 ? sum[l / 4] + w : w;
+    }
+  }
+  return N == 8 ? sum[0] + sum[N / 4 - 1] : sum[0];
+}
+
+// (Seven waves a SIMD: with the three registers more that leave it six, the case
+// above takes 106 us instead of 100.)
 template <int DT, int U>
-__global__ void __launch_bounds__(kSliceBS) beam_slice_kernel(BeamArgs a) {
+__global__ void __launch_bounds__(kSliceBS, 7) beam_slice_kernel(BeamArgs a) {
   constexpr int N = kVec<DT>;
   __shared__ __align__(16) uint32_t most[kSliceBS];
   __shared__ uint64_t near[kSliceNW][kBeamCap];  // a wave's candidates
@@ -153,9 +178,15 @@ __global__ void __launch_bounds__(kSliceBS) beam_slice_kernel(BeamArgs a) {
   }
   if (lane_id() == 0) counts[wave_id()] = n;
   const float ref = M == -__builtin_inff() ? 0.0f : M;
-  float sum = 0.0f;
+  float sum_of[U];
 #pragma unroll
-  for (int i = 0; i < U; ++i) sum += exp_sum(a.x, ref, x[i]);
+  for (int i = 0; i < U; ++i) sum_of[i] = beam_exp_sum(a.x, ref, x[i]);
+#pragma unroll
+  for (int d = 1; d < U; d *= 2) {
+#pragma unroll
+    for (int i = 0; i < U; i += 2 * d) sum_of[i] += sum_of[i + d];
+  }
+  float sum = sum_of[0];
   if (sum != sum || M == __builtin_inff()) {  // a NaN or a +inf in this thread, or the slice's
     uint32_t flags = 0;
 #pragma unroll
@@ -201,7 +232,8 @@ __global__ void __launch_bounds__(kSliceBS) beam_slice_kernel(BeamArgs a) {
     for (int w = 0; w < kSliceNW; ++w) sum_of += counts[w];
     return (uint32_t)__builtin_amdgcn_readfirstlane((int)sum_of);
   };
-  uint32_t low = (uint32_t)__builtin_amdgcn_readfirstlane((int)key32(t)), high = (uint32_t)__builtin_amdgcn_readfirstlane((int)key32(M));  // keys that n_out reach, and that hold the one looked for
+  // keys: one that n_out reach, and the largest that they may
+  uint32_t low = (uint32_t)__builtin_amdgcn_readfirstlane((int)key32(t)), high = (uint32_t)__builtin_amdgcn_readfirstlane((int)key32(M));
   while (low < high) {
     const uint32_t mid = low + ((high - low) >> 1) + 1;
     const float f = top_key_value<DSPARK_F32>(mid);
@@ -272,6 +304,18 @@ __device__ __forceinline__ uint64_t beam_cut(const uint64_t (&key)[PER], int n, 
   }
 }
 
+// e^y of y <= 0 to some 2^-51 of its value (the series of 2^f on |f| <= 1/2, up to f^12), 0 far below
+__device__ __forceinline__ double beam_exp(double y) {
+  const double t = (y > -1000.0 ? y : -1000.0) * 1.4426950408889634;
+  const double n = __builtin_rint(t), f = (t - n) * 0.6931471805599453;
+  double p = 1.0 / 479001600.0;
+  constexpr double c[12] = {1.0,         1.0,          1.0 / 2.0,     1.0 / 6.0,      1.0 / 24.0,      1.0 / 120.0,
+                            1.0 / 720.0, 1.0 / 5040.0, 1.0 / 40320.0, 1.0 / 362880.0, 1.0 / 3628800.0, 1.0 / 39916800.0};
+#pragma unroll
+  for (int i = 11; i >= 0; --i) p = __builtin_fma(p, f, c[i]);
+  return __builtin_ldexp(p, (int)n);
+}
+
 // binary64 log-sum-exp of a row by the whole workgroup (every thread calls
 // and gets it)
 template <int DT, int NWV>
@@ -279,11 +323,20 @@ __device__ double beam_exact_lse(const BeamArgs& a, int64_t r, float M, double* 
   constexpr int N = kVec<DT>;
   const typename El<DT>::T* row = static_cast<const typename El<DT>::T*>(a.x.x) + r * a.x.stride;
   double sum = 0.0;
-  for (int v = (int)threadIdx.x * N; v < a.x.V; v += NWV * 64 * N) {
-    float x[N];
-    load_vec<DT, N>(row, v, a.x.V, x);
+  constexpr int AT_ONCE = 8, STEP = NWV * 64 * N;  // vectors on their way
+  for (int v0 = (int)threadIdx.x * N; v0 < a.x.V; v0 += AT_ONCE * STEP) {
+    Raw<DT, N> raw[AT_ONCE];
 #pragma unroll
-    for (int l = 0; l < N; ++l) sum += exp((double)x[l] - (double)M);
+    for (int j = 0; j < AT_ONCE; ++j)
+      if (v0 + j * STEP < a.x.V) raw[j] = raw_vec<DT, N, false>(row, v0 + j * STEP, a.x.V);
+#pragma unroll
+    for (int j = 0; j < AT_ONCE; ++j) {
+      if (v0 + j * STEP >= a.x.V) break;
+      float x[N];
+      unpack<DT, N>(raw[j], x);
+#pragma unroll
+      for (int l = 0; l < N; ++l) sum += beam_exp((double)x[l] - (double)M);
+    }
   }
   sum = group_reduce<NWV>(sum, 0.0, [](double u, double v) { return u + v; }, scratch);
   return (double)M + log(sum);
