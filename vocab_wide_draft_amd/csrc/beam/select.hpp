@@ -18,11 +18,11 @@
 // rounded by |t| 2^-24, and as much again by half from log2(e), the hardware
 // exponential is off by 2^-23, and a term is in six sums of a thread and six of
 // a wave before binary64 takes them; the weights' mean |t| is below 18 for 2^20
-// logits, so that is 2^-24 (0.7 * 1.5 * 18 + 2 + 12) = 1.96e-6.  Where two neighbours in the
-// merged order of different beams lie closer than twice kLseOff, their beams'
-// log-sum-exps are computed again in binary64 and what decides is compared again
-// (44 us more where two beams of 129,280 ids are alike; random requests come so
-// close once in some thousands).
+// logits, so that is 2^-24 (0.7 * 1.5 * 18 + 2 + 12) = 1.96e-6.  Where two
+// neighbours in the merged order of different beams lie closer than twice
+// kLseOff, their beams' log-sum-exps are computed again in binary64 and what
+// decides is compared again (44 us more where two beams of 129,280 ids are
+// alike; random requests come so close once in some thousands).
 #pragma once
 #include "../logits/slices.hpp"
 #include "../logits/top.hpp"
@@ -304,7 +304,7 @@ __device__ __forceinline__ uint64_t beam_cut(const uint64_t (&key)[PER], int n, 
   }
 }
 
-// e^y of y <= 0 to some 2^-51 of its value (the series of 2^f on |f| <= 1/2, up to f^12), 0 far below
+// e^y of y <= 0, off by |y| 2^-52 of its value at most (the series of e^f on |f| <= ln(2) / 2, up to f^12), 0 far below
 __device__ __forceinline__ double beam_exp(double y) {
   const double t = (y > -1000.0 ? y : -1000.0) * 1.4426950408889634;
   const double n = __builtin_rint(t), f = (t - n) * 0.6931471805599453;
