@@ -100,3 +100,16 @@ def test_rows_on_the_cpu_are_refused():
         B.quantize_blocks(torch.zeros(2, 128))
     with pytest.raises(ValueError):
         B.block_linear(torch.zeros(2, 128), {"values": torch.zeros(4, 128).to(torch.float8_e4m3fn), "scales": torch.ones(1, 1)})
+
+
+def test_scales_apart():
+    """Outputs onto scales, and scales onto values or rows, are refused."""
+    x = B.Rows(0x40000, 1, 0, 4, 250, 256)
+    assert _quantize(x, _q(4, scales=0x40004)) == -1                             # a matrix's scales onto the rows
+    assert _quantize(x, _q(4, scales=0x10100)) == -1 and _quantize(x, _q(4, scales=0x0fffc)) == -1  # onto its values
+    x, w = _q(4), _q(1000, rows=128, scales=0x30000, values=0x100000)
+    assert _product(x, w, out=0x20010) == -1 and _product(x, w, out=0x1fff0) == -1
+    assert _product(x, w, out=0x30010) == -1
+    rows = B.Rows(0x40000, 1, 0, 4, 250, 256)
+    ws = ctypes.c_void_p(0x800000)
+    assert B.load_library().dspark_block_linear(ctypes.byref(rows), ctypes.byref(w), ctypes.c_void_p(0x30010), 1, 1000, ws, 1 << 20, None) == -1

@@ -97,6 +97,12 @@ int64_t rows_bytes(const dspark_rows* x) {
   return x->n_rows > 0 ? ((x->n_rows - 1) * x->row_stride + x->vocab) * (x->dtype == DSPARK_BF16 ? 2 : 4) : 0;
 }
 
+// bytes from the first scale to the last
+int64_t scale_bytes(const dspark_fp8* q) {
+  const int64_t rows = (q->n_rows + q->block_rows - 1) / q->block_rows;
+  return rows > 0 ? ((rows - 1) * q->scale_stride + (q->cols + kBlock - 1) / kBlock) * (q->scale_dtype == DSPARK_SCALE_F32 ? 4 : 1) : 0;
+}
+
 enum ProductWay { kDirect, kStaged, kTiles };
 struct ProductPlan {
   ProductWay way;
@@ -274,8 +280,11 @@ int dspark_quantize_blocks(const dspark_rows* x, const dspark_fp8* out, void* st
   if (out->n_rows != x->n_rows) return fail(DSPARK_EINVAL, "the fp8 matrix has another number of rows");
   if (out->cols != up(x->vocab, 16)) return fail(DSPARK_EINVAL, "fp8 cols must be the rows' width rounded up to a multiple of 16");
   if (x->n_rows == 0) return DSPARK_SUCCESS;
-  if (meet(x->data, rows_bytes(x), out->values, out->n_rows, out->cols, out->row_stride))
+  if (meet(x->data, rows_bytes(x), out->values, out->n_rows, out->cols, out->row_stride) ||
+      meet(x->data, rows_bytes(x), out->scales, 1, scale_bytes(out), 0))
     return fail(DSPARK_EINVAL, "the fp8 matrix overlaps the rows");
+  if (meet(out->scales, scale_bytes(out), out->values, out->n_rows, out->cols, out->row_stride))
+    return fail(DSPARK_EINVAL, "the fp8 matrix's scales overlap its values");
   quantize(x, out, 1, static_cast<hipStream_t>(stream));
   return host_check_launch();
 }
@@ -298,7 +307,9 @@ int dspark_block_product(const dspark_fp8* x, const dspark_fp8* w, void* out, in
   if (x->n_rows == 0 || w->n_rows == 0) return DSPARK_SUCCESS;
   const int64_t es = out_dtype == DSPARK_BF16 ? 2 : 4;
   if (meet(x->values, fp8_bytes(x), out, x->n_rows, w->n_rows * es, out_stride * es) ||
-      meet(w->values, fp8_bytes(w), out, x->n_rows, w->n_rows * es, out_stride * es))
+      meet(w->values, fp8_bytes(w), out, x->n_rows, w->n_rows * es, out_stride * es) ||
+      meet(x->scales, scale_bytes(x), out, x->n_rows, w->n_rows * es, out_stride * es) ||
+      meet(w->scales, scale_bytes(w), out, x->n_rows, w->n_rows * es, out_stride * es))
     return fail(DSPARK_EINVAL, "output rows overlap an input");
   rc = check_ws(product_bytes(x->n_rows, w->n_rows, x->cols), ws, ws_bytes);
   if (rc) return rc;
@@ -323,7 +334,8 @@ int dspark_block_linear(const dspark_rows* x, const dspark_fp8* w, void* out, in
   if (x->n_rows == 0 || w->n_rows == 0) return DSPARK_SUCCESS;
   const int64_t es = out_dtype == DSPARK_BF16 ? 2 : 4;
   if (meet(x->data, rows_bytes(x), out, x->n_rows, w->n_rows * es, out_stride * es) ||
-      meet(w->values, fp8_bytes(w), out, x->n_rows, w->n_rows * es, out_stride * es))
+      meet(w->values, fp8_bytes(w), out, x->n_rows, w->n_rows * es, out_stride * es) ||
+      meet(w->scales, scale_bytes(w), out, x->n_rows, w->n_rows * es, out_stride * es))
     return fail(DSPARK_EINVAL, "output rows overlap an input");
   const LinearPlan p = linear_plan(x->n_rows, w->n_rows, x->vocab);
   rc = check_ws(p.bytes, ws, ws_bytes);
