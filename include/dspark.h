@@ -548,9 +548,10 @@ int dspark_quantize_blocks(const dspark_rows* x, const dspark_fp8* out, void* st
  * token) or, for the gradient of the hidden states, its transpose; both of
  * the same cols and scale_dtype.  out: x->n_rows rows of w->n_rows values,
  * out_stride elements apart, 16-byte aligned, apart from the inputs; what lies
- * between rows is not written.  A row of x with a NaN gives NaN throughout, which every later
- * step refuses.  ws: dspark_block_product_workspace() bytes, 16-byte aligned
- * (NULL where it is 0); it is free again when the call's work is done. */
+ * between rows is not written.  A row of x with a NaN gives NaN throughout,
+ * which every later step refuses.  ws: dspark_block_product_workspace() bytes,
+ * 16-byte aligned (NULL where it is 0); it is free again when the call's work
+ * is done. */
 size_t dspark_block_product_workspace(int64_t x_rows, int64_t w_rows, int64_t cols);
 int dspark_block_product(const dspark_fp8* x, const dspark_fp8* w, void* out, int32_t out_dtype, int64_t out_stride,
                          void* ws, size_t ws_bytes, void* stream);
@@ -586,8 +587,8 @@ int dspark_block_linear(const dspark_rows* x, const dspark_fp8* w, void* out, in
  * none; finished must then be NULL).  req_status[r]: OK, ROW_NAN or
  * ROW_POSINF for a row that is read, or BAD_SCORE; a refused request has len 0
  * and empty slots.  The outputs lie apart from the inputs.  ws:
- * dspark_beam_select_workspace() bytes, 16-byte aligned;
- * one for n rows serves fewer rows as well. */
+ * dspark_beam_select_workspace() bytes, 16-byte aligned; one for n rows serves
+ * fewer rows as well. */
 #define DSPARK_BEAM_MAX 64
 #define DSPARK_BEAM_OUT_MAX 128
 size_t dspark_beam_select_workspace(int64_t n_rows, int64_t vocab, int32_t n_out);

@@ -2,7 +2,7 @@
 
 Tolerances.  Whole outputs are equal.  A score is s + (x - lse) in binary64 with the log-sum-exp from binary32
 exponentials, off by at most 2e-6 (each exponential by (|t| 0.7 + 2) 2^-24 of itself, t its exponent in base 2, whose
-weighted mean is below 18; eight of them are added in binary32), rounded to binary32: half a step, 2^-24 of itself."""
+weighted mean is below 18; a term is in twelve binary32 sums), rounded to binary32: half a step, 2^-24 of itself."""
 import numpy as np
 import pytest
 import torch

@@ -930,7 +930,7 @@ def head_logits(x: torch.Tensor, head, out_dtype=None) -> torch.Tensor:
 
 
 def beam_select(rows: torch.Tensor, scores: torch.Tensor, n_out: int | None = None, *, finished=None, end_token: int = -1):
-    """The n_out (default: twice the beams, at most BEAM_OUT_MAX) best
+    """The n_out (default: twice the beams, or as many as a call may select) best
     continuations of each request's beams (see dspark_beam_select).  rows
     [requests * beams, V]; scores float32 [requests, beams], -inf for an empty
     slot; finished int32 [requests, beams], nonzero for an ended beam, which
@@ -942,7 +942,7 @@ def beam_select(rows: torch.Tensor, scores: torch.Tensor, n_out: int | None = No
     if scores.dim() != 2 or scores.numel() != n:
         raise ValueError("scores must be [requests, beams] with a row of logits for each")
     R, beams = scores.shape
-    k = min(2 * beams, BEAM_OUT_MAX) if n_out is None else int(n_out)
+    k = min(2 * beams, BEAM_OUT_MAX, 4096 // max(beams, 1)) if n_out is None else int(n_out)
     i32 = torch.int32
     s, f = _arg(scores, "scores", torch.float32, (R, beams), dev), _arg(finished, "finished", i32, (R, beams), dev)
     # (few allocations: each costs the host as much as a tenth of a small call)
