@@ -71,3 +71,26 @@ def test_default_count(beams, count):
     x = torch.randn((beams, 300), generator=torch.Generator().manual_seed(beams)).to(dev)
     got = B.beam_select(x, torch.zeros((1, beams), device=dev))
     assert got["parent"].shape == (1, count) and int(got["len"][0]) == count
+
+
+def test_most_beams_over_the_longest_rows():
+    """64 beams of 2^20 ids, all masked but some."""
+    beams, V, n_out = 64, 1 << 20, 64
+    g = torch.Generator().manual_seed(1)
+    x = torch.full((beams, V), -np.inf, dtype=torch.bfloat16)
+    for r in range(beams):
+        x[r, torch.randint(0, V, (2000,), generator=g)] = (torch.randn(2000, generator=g) * 3).to(torch.bfloat16)
+    s = (-3 - torch.rand((1, beams), generator=g)).float()
+    got = {k: v.cpu().numpy() for k, v in B.beam_select(x.to(dev), s.to(dev), n_out).items()}
+    parent, token, _, ended, length, status = O.select(x.float().numpy(), s.numpy(), n_out)
+    for name, want in (("status", status), ("len", length), ("parent", parent), ("token", token), ("finished", ended)):
+        np.testing.assert_array_equal(got[name], want, name)
+
+
+def test_a_transposed_head_of_another_size_is_refused_at_once():
+    w = B.quantize_blocks(torch.ones((200, 64), device=dev), 128)
+    x = torch.ones((3, 64), device=dev, requires_grad=True)
+    for t in (B.quantize_blocks(torch.ones((64, 176), device=dev), 128), B.quantize_blocks(torch.ones((48, 200), device=dev), 128)):
+        with pytest.raises(ValueError, match="transposed"):
+            B.head_logits(x, {"weight": w, "transposed": t})
+    assert B.head_logits(x, {"weight": w, "transposed": B.transpose_blocks(w, 64)}).shape == (3, 200)

@@ -918,8 +918,10 @@ def head_logits(x: torch.Tensor, head, out_dtype=None) -> torch.Tensor:
         t = head.get("transposed")
         if t is None:
             raise ValueError('the gradient needs head["transposed"] (see transpose_blocks)')
-        if t["values"].shape[0] != x.shape[1]:
+        if x.dim() != 2 or t["values"].shape[0] != x.shape[1]:
             raise ValueError('head["transposed"] must have a row for each channel of x')
+        if t["values"].shape[1] != -(-head["weight"]["values"].shape[0] // 16) * 16:
+            raise ValueError('head["transposed"] must have a column for each token, filled up to a multiple of 16')
         if any(q[k].requires_grad for q in (head["weight"], t) for k in ("values", "scales")):
             raise ValueError("the head is constant: detach it")
         return _HeadLogits.apply(x, head, out_dtype)
