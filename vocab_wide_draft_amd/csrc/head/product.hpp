@@ -409,36 +409,25 @@ __global__ void __launch_bounds__(256) product_direct_kernel(ProductArgs a) {
 // to 1.9 GHz (2.56 ms, 2,645 TFLOP/s; 2.22 ms at 2.2 GHz without the fetches).
 // A second barrier a step, which gives a fetch more time, costs more than it
 // gives there (2,867 us).
-template <int U, int ST, bool WIDE, int OUT>
-__global__ void __launch_bounds__(512, 2) product_tile_kernel(ProductArgs a) {
-  constexpr int TN = 256, TM = 64 * U, T = 8, GW = 4, GX = U, FETCHES = GX + GW, EARLY = (FETCHES + 1) / 2;
+template <int U, int ST>
+struct Tile {
+  static constexpr int TN = 256, TM = 64 * U;
   // buffers of w and of x: as many of both that a pair is one piece of LDS, or all of w's and then x's
-  constexpr int WS = U <= 2 || (U == 3 && ST == DSPARK_SCALE_E8M0) ? 3 : 2, XS = U <= 2 ? 3 : 2;
+  static constexpr int WS = U <= 2 || (U == 3 && ST == DSPARK_SCALE_E8M0) ? 3 : 2, XS = U <= 2 ? 3 : 2;
+  static constexpr int BYTES = (WS * TN + XS * TM) * kBlock;
+  static constexpr int SCALES = TM + 128;  // of x's rows, of w's two blocks, and room that nobody reads
+};
+template <int U, int ST, bool WIDE, int OUT>
+__device__ __forceinline__ void product_tile(const ProductArgs& a, int64_t m0, int64_t n0, int split, uint8_t* lds, uint32_t* scales) {
+  constexpr int TN = 256, TM = 64 * U, T = 8, GW = 4, GX = U, FETCHES = GX + GW, EARLY = (FETCHES + 1) / 2;
+  constexpr int WS = Tile<U, ST>::WS, XS = Tile<U, ST>::XS;
   constexpr bool PAIRS = WS == XS;
   constexpr int BUF_W = (PAIRS ? TN + TM : TN) * kBlock, BUF_X = (PAIRS ? TN + TM : TM) * kBlock, X_AT = (PAIRS ? TN : WS * TN) * kBlock;
   // fetches that may still be on their way when a step's have to be there
   constexpr int AHEAD = PAIRS ? (WS - 2) * (FETCHES + 1) : GW;
   constexpr int AT_ONCE = 2, PARTS = T / AT_ONCE;  // rows of 16 of w between two reads
   constexpr int SE = ST == DSPARK_SCALE_F32 ? 4 : 1;
-  __shared__ __align__(16) uint8_t lds[(WS * TN + XS * TM) * kBlock];
-  __shared__ uint32_t scales[XS][TM + 128];  // of x's rows, of w's two blocks, and room that nobody reads
-  const int64_t total = a.tiles_m * a.tiles_n * a.splits;
-  int64_t b = block_number(total);
-  if (b < 0) return;
-  // Workgroups go to the eight XCDs in turn: each takes a stretch of tiles,
-  // in groups of kTogether by all of m, so that those in work at a time share
-  // rows of both matrices in its L2.
-  if (total >= 64) {
-    const int64_t each = total / 8, more = total % 8, xcd = b & 7;
-    b = xcd * each + (xcd < more ? xcd : more) + (b >> 3);
-  }
-  constexpr int kTogether = 4;
-  const int64_t plane = a.tiles_m * a.tiles_n;
-  const int split = (int)(b / plane);
-  b -= split * plane;
-  const int64_t group = b / (a.tiles_m * kTogether), in = b - group * a.tiles_m * kTogether;
-  const int64_t across = a.tiles_n - group * kTogether < kTogether ? a.tiles_n - group * kTogether : kTogether;
-  const int64_t m0 = in / across * TM, n0 = (group * kTogether + in % across) * TN;
+  constexpr int SCALES = Tile<U, ST>::SCALES;
   const int first = split * a.split_steps, last = first + a.split_steps < a.steps ? first + a.split_steps : a.steps;
   const int rows_w = a.N - n0 < TN ? (int)(a.N - n0) : TN, rows_x = a.M - m0 < TM ? (int)(a.M - m0) : TM;
   const int tid = (int)threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -487,10 +476,10 @@ __global__ void __launch_bounds__(512, 2) product_tile_kernel(ProductArgs a) {
   const int64_t scale_step = (of_x ? a.xs_step : 1) * SE;
   const int scale_at = of_x ? (wave * 64 + lane < rows_x ? lane * (int)a.xs_stride * SE : kPastEnd)
                             : of_w && lane < 2 && block_w + lane <= last_w ? lane * (int)a.ws_stride * SE : kPastEnd;
-  const uint32_t scale_to = lds_address(&scales[0][of_x ? wave * 64 : of_w ? TM : TM + 64]);
+  const uint32_t scale_to = lds_address(scales + (of_x ? wave * 64 : of_w ? TM : TM + 64));
   const auto fetch_scales = [&](int step, int buf) {
     load_lds_ahead<SE>(buffer_words(scale_from + step * scale_step, step < last ? 0x40000000 : 0),
-                       scale_to + (uint32_t)(buf * (int)sizeof(scales[0])), scale_at);
+                       scale_to + (uint32_t)(buf * SCALES * 4), scale_at);
   };
 
   v4f acc[T][U];
@@ -514,9 +503,9 @@ __global__ void __launch_bounds__(512, 2) product_tile_kernel(ProductArgs a) {
   v8b wx[WIDE ? U : 1][4];  // a step's rows of x in bf16
   uint32_t sx[U], sw;
   const auto read_scales = [&](int buf) {
-    sw = scales[buf][TM + wn];
+    sw = scales[buf * SCALES + TM + wn];
 #pragma unroll
-    for (int u = 0; u < U; ++u) sx[u] = scales[buf][wm * 16 * U + 16 * u + r];
+    for (int u = 0; u < U; ++u) sx[u] = scales[buf * SCALES + wm * 16 * U + 16 * u + r];
     if constexpr (WIDE && ST == DSPARK_SCALE_E8M0) {
       const float w = e8m0_value(sw);
 #pragma unroll
@@ -659,6 +648,51 @@ __global__ void __launch_bounds__(512, 2) product_tile_kernel(ProductArgs a) {
       put_row8<OUT>(row, n0 + wn * 128 + row_of(t) + 8 * g, a.N, v);
     }
   }
+}
+
+// LDS for a tile of 64 U rows or any fewer
+template <int U, int ST>
+constexpr int tile_bytes() {
+  if constexpr (U == 1) return Tile<1, ST>::BYTES;
+  else return Tile<U, ST>::BYTES > tile_bytes<U - 1, ST>() ? Tile<U, ST>::BYTES : tile_bytes<U - 1, ST>();
+}
+static_assert(tile_bytes<4, DSPARK_SCALE_F32>() == Tile<2, DSPARK_SCALE_F32>::BYTES && tile_bytes<4, DSPARK_SCALE_E8M0>() == Tile<3, DSPARK_SCALE_E8M0>::BYTES &&
+              Tile<3, DSPARK_SCALE_E8M0>::BYTES + 3 * 4 * Tile<4, DSPARK_SCALE_E8M0>::SCALES <= 160 * 1024, "what LDS holds");
+// Tiles of 64 U rows of x, but for the last, which has as many 64s as are left
+// (129,280 x 5,120, powers of two: 264 rows 253 -> 239 us, 600 rows 419 -> 403,
+// 900 rows 576 -> 554; full tiles as before).
+template <int U, int ST, bool WIDE, int OUT>
+__global__ void __launch_bounds__(512, 2) product_tile_kernel(ProductArgs a) {
+  __shared__ __align__(16) uint8_t lds[tile_bytes<U, ST>()];
+  __shared__ uint32_t scales[3 * Tile<U, ST>::SCALES];
+  const int64_t total = a.tiles_m * a.tiles_n * a.splits;
+  int64_t b = block_number(total);
+  if (b < 0) return;
+  // Workgroups go to the eight XCDs in turn: each takes a stretch of tiles,
+  // in groups of kTogether by all of m, so that those in work at a time share
+  // rows of both matrices in its L2.
+  if (total >= 64) {
+    const int64_t each = total / 8, more = total % 8, xcd = b & 7;
+    b = xcd * each + (xcd < more ? xcd : more) + (b >> 3);
+  }
+  constexpr int kTogether = 4;
+  const int64_t plane = a.tiles_m * a.tiles_n;
+  const int split = (int)(b / plane);
+  b -= split * plane;
+  const int64_t group = b / (a.tiles_m * kTogether), in = b - group * a.tiles_m * kTogether;
+  const int64_t across = a.tiles_n - group * kTogether < kTogether ? a.tiles_n - group * kTogether : kTogether;
+  const int64_t m0 = in / across * (64 * U), n0 = (group * kTogether + in % across) * 256;
+  const int64_t left = a.M - m0;  // (uniform)
+  if constexpr (U > 1) {
+    if (left <= 64) return product_tile<1, ST, WIDE, OUT>(a, m0, n0, split, lds, scales);
+  }
+  if constexpr (U > 2) {
+    if (left <= 128) return product_tile<2, ST, WIDE, OUT>(a, m0, n0, split, lds, scales);
+  }
+  if constexpr (U > 3) {
+    if (left <= 192) return product_tile<3, ST, WIDE, OUT>(a, m0, n0, split, lds, scales);
+  }
+  product_tile<U, ST, WIDE, OUT>(a, m0, n0, split, lds, scales);
 }
 
 // The parts of a product, added in order.
