@@ -94,3 +94,10 @@ def test_a_transposed_head_of_another_size_is_refused_at_once():
         with pytest.raises(ValueError, match="transposed"):
             B.head_logits(x, {"weight": w, "transposed": t})
     assert B.head_logits(x, {"weight": w, "transposed": B.transpose_blocks(w, 64)}).shape == (3, 200)
+
+
+@pytest.mark.parametrize("kind", ["f32", "pow2"])
+@pytest.mark.parametrize("width", [16, 400])
+@pytest.mark.parametrize("n", [193, 257, 264, 330, 400, 450, 520, 600, 700])
+def test_a_narrower_last_tile(n, width, kind):
+    test_tiles_of_every_width_and_few_steps(n, width, kind)
