@@ -516,7 +516,9 @@ int dspark_distill_step(const dspark_rows* student, const dspark_teacher* teache
  *   scales: (n_rows + block_rows - 1) / block_rows rows of (cols + 127) / 128
  *           scales, scale_stride scales apart: float (DSPARK_SCALE_F32) or the
  *           exponent byte of a power of two, 2^(byte - 127), 255 a NaN
- *           (DSPARK_SCALE_E8M0).  0 <= n_rows <= 2^24, 16 <= cols <= 2^20. */
+ *           (DSPARK_SCALE_E8M0).
+ * 0 <= n_rows <= 2^24, 16 <= cols <= 2^20, row_stride <= 2^22, scale_stride
+ * <= 2^20. */
 typedef enum { DSPARK_SCALE_F32 = 0, DSPARK_SCALE_E8M0 = 1 } dspark_scale;
 typedef struct {
   void* values;
