@@ -582,8 +582,8 @@ int dspark_block_linear(const dspark_rows* x, const dspark_fp8* w, void* out, in
  * scores compared in binary64 with the log-sum-exp exact to binary64's
  * rounding wherever it decides.  parent, token, score, out_finished ([n_out]
  * a request): the candidate's beam in the request, its token, its score
- * rounded to binary32, and whether it comes from an ended beam or its token is
- * end_token; len[r] of them, behind which stand empty slots (parent -1, token
+ * rounded to binary32 (-inf below its range: the next step takes that slot as
+ * empty), and whether it comes from an ended beam or its token is end_token; len[r] of them, behind which stand empty slots (parent -1, token
  * 0, score -inf, finished 0).  beams in [1, DSPARK_BEAM_MAX], n_out in [1,
  * DSPARK_BEAM_OUT_MAX], beams * n_out <= 4096, end_token in [-1, vocab) (-1:
  * none; finished must then be NULL).  req_status[r]: OK, ROW_NAN or

@@ -578,7 +578,9 @@ __global__ void __launch_bounds__(64 * NWV) beam_join_kernel(BeamArgs a) {
     }
 #pragma unroll
     for (int j = 0; j < 2; ++j)
-      if (j * 64 + lane < a.slices) best[b * a.slices + j * 64 + lane] = m[j] > kNone ? half((float)((double)s + ((double)m[j] - lse))) : 0;
+      // (a score below binary32 counts as its lowest value: the half key of -inf stands for no number)
+      if (j * 64 + lane < a.slices)
+        best[b * a.slices + j * 64 + lane] = m[j] > kNone ? half(__builtin_fmaxf((float)((double)s + ((double)m[j] - lse)), -3.4028235e38f)) : 0;
     if (lane == 0) {
       sh.flags[b] = (int)f;
       sh.n_list[b] = M > kNone ? 1 : 0;
