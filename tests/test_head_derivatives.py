@@ -1,0 +1,29 @@
+"""Derivatives that head_logits does not have are refused before any device work; so none is lost in silence."""
+import pytest
+import torch
+import torch.autograd.forward_ad as forward_ad
+
+from vocab_wide_draft_amd import binding as B
+
+
+def _head(width=128, V=16):
+    w = {"values": torch.zeros(V, width).to(torch.float8_e4m3fn), "scales": torch.ones(1, -(-width // 128))}
+    return {"weight": w, "transposed": B.transpose_blocks(w, width)}
+
+
+@pytest.mark.parametrize("grad", [True, False])
+@pytest.mark.parametrize("out", [None, torch.float32])
+def test_forward_mode_tangents_are_refused(out, grad):
+    x, t = torch.ones(2, 128), torch.ones(2, 128)
+    with forward_ad.dual_level(), torch.set_grad_enabled(grad):
+        with pytest.raises(NotImplementedError, match="forward-mode"):
+            B.head_logits(forward_ad.make_dual(x, t), _head(), out)
+        with pytest.raises(ValueError, match="on the GPU"):  # without a tangent the call goes on to its other checks
+            B.head_logits(x, _head(), out)
+
+
+def test_forward_mode_through_functions_of_functions():
+    x = torch.ones(2, 128)
+    for derivative in (lambda f: torch.func.jvp(f, (x,), (x,)), lambda f: torch.func.jacfwd(f)(x)):
+        with pytest.raises(NotImplementedError, match="forward-mode"):
+            derivative(lambda t: B.head_logits(t, _head()))

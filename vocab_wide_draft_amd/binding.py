@@ -10,6 +10,7 @@ import os
 import struct
 
 import torch
+from torch.autograd import forward_ad
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _LIB = None
@@ -907,13 +908,21 @@ class _HeadLogits(torch.autograd.Function):
         return _head_grad(ctx, grad)
 
 
+def _has_tangent(x):
+    # (outside of a dual level, which is where calls are but for forward mode, there is none: a tenth of unpack_dual's time)
+    return getattr(forward_ad, "_current_level", 0) >= 0 and forward_ad.unpack_dual(x).tangent is not None
+
+
 def head_logits(x: torch.Tensor, head, out_dtype=None) -> torch.Tensor:
     """Logits [n, V] of hidden states x [n, width] (float32 or bf16, rows
     16-byte aligned) and a head {"weight": a quantised matrix [V, width],
     "transposed": transpose_blocks(weight, width)}, a differentiable function
     of x: the logits' gradient is quantised in blocks of 128 tokens, as x is in
     blocks of 128 channels, and multiplied with the transposed head.  The head
-    is constant; without a gradient "transposed" is not needed."""
+    is constant; without a gradient "transposed" is not needed.  There is no
+    forward-mode derivative, nor a second one."""
+    if _has_tangent(x):
+        raise NotImplementedError("head_logits has no forward-mode derivative")
     if x.requires_grad and torch.is_grad_enabled():
         t = head.get("transposed")
         if t is None:
