@@ -27,3 +27,20 @@ def test_forward_mode_through_functions_of_functions():
     for derivative in (lambda f: torch.func.jvp(f, (x,), (x,)), lambda f: torch.func.jacfwd(f)(x)):
         with pytest.raises(NotImplementedError, match="forward-mode"):
             derivative(lambda t: B.head_logits(t, _head()))
+
+
+@pytest.mark.parametrize("part", ["weight", "transposed"])
+def test_the_head_is_constant_whatever_x_needs(part):
+    """A head that a derivative is asked of is refused, also where x itself needs none; without derivatives it is taken."""
+    x, head = torch.ones(2, 128), _head()
+    head[part]["scales"].requires_grad_()
+    for t in (x, x.clone().requires_grad_()):
+        with pytest.raises(ValueError, match="constant"):
+            B.head_logits(t, head)
+    with torch.no_grad(), pytest.raises(ValueError, match="on the GPU"):
+        B.head_logits(x, head)
+    head[part]["scales"].requires_grad_(False)
+    with forward_ad.dual_level():
+        head[part] = {"values": head[part]["values"], "scales": forward_ad.make_dual(head[part]["scales"], torch.ones_like(head[part]["scales"]))}
+        with pytest.raises(ValueError, match="constant"):
+            B.head_logits(x, head)

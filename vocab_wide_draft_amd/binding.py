@@ -908,9 +908,11 @@ class _HeadLogits(torch.autograd.Function):
         return _head_grad(ctx, grad)
 
 
-def _has_tangent(x):
-    # (outside of a dual level, which is where calls are but for forward mode, there is none: a tenth of unpack_dual's time)
-    return getattr(forward_ad, "_current_level", 0) >= 0 and forward_ad.unpack_dual(x).tangent is not None
+def _no_tangents(x, w, t):
+    if forward_ad.unpack_dual(x).tangent is not None:
+        raise NotImplementedError("head_logits has no forward-mode derivative")
+    if any(forward_ad.unpack_dual(q[k]).tangent is not None for q in (w, t) if q is not None for k in ("values", "scales")):
+        raise ValueError("the head is constant: detach it")
 
 
 def head_logits(x: torch.Tensor, head, out_dtype=None) -> torch.Tensor:
@@ -921,18 +923,19 @@ def head_logits(x: torch.Tensor, head, out_dtype=None) -> torch.Tensor:
     blocks of 128 channels, and multiplied with the transposed head.  The head
     is constant; without a gradient "transposed" is not needed.  There is no
     forward-mode derivative, nor a second one."""
-    if _has_tangent(x):
-        raise NotImplementedError("head_logits has no forward-mode derivative")
-    if x.requires_grad and torch.is_grad_enabled():
-        t = head.get("transposed")
+    w, t, grad = head["weight"], head.get("transposed"), torch.is_grad_enabled()
+    if getattr(forward_ad, "_current_level", 0) >= 0:  # (without a dual level there is none: not looked for, 3 us less)
+        _no_tangents(x, w, t)
+    if grad and (w["values"].requires_grad or w["scales"].requires_grad or
+                 (t is not None and (t["values"].requires_grad or t["scales"].requires_grad))):
+        raise ValueError("the head is constant: detach it")
+    if x.requires_grad and grad:
         if t is None:
             raise ValueError('the gradient needs head["transposed"] (see transpose_blocks)')
         if x.dim() != 2 or t["values"].shape[0] != x.shape[1]:
             raise ValueError('head["transposed"] must have a row for each channel of x')
         if t["values"].shape[1] != -(-head["weight"]["values"].shape[0] // 16) * 16:
             raise ValueError('head["transposed"] must have a column for each token, filled up to a multiple of 16')
-        if any(q[k].requires_grad for q in (head["weight"], t) for k in ("values", "scales")):
-            raise ValueError("the head is constant: detach it")
         return _HeadLogits.apply(x, head, out_dtype)
     return block_linear(x, head["weight"], out_dtype)
 
