@@ -605,7 +605,9 @@ int dspark_beam_select(const dspark_rows* rows, const float* scores, const int32
  * apart (all strides in bytes).  rows 0: the state has no positions and is one
  * row of row_bytes.  out: the same layout with strides of its own; out == in
  * (with the same strides) reorders in place, other memory must lie apart.
- * Parts of different beams, and different states, do not overlap. */
+ * Parts of different beams do not overlap, and what one state writes is apart
+ * from what any other reads or writes (views that lie between each other, as
+ * keys and values in one tensor, are apart); others are refused. */
 typedef struct {
   const void* in;
   void* out;

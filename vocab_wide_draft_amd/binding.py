@@ -1002,7 +1002,10 @@ def beam_reorder(states, parent: torch.Tensor, length=None, *, axis: int = 2, ou
     say), reordered in place, or into `out`, tensors of the same shapes and
     types; parent int32 [requests, beams].  length int32 [requests]: only the
     first length[r] positions, which dimension `axis` counts; states of fewer
-    dimensions are taken whole.  Returns {"states", "status"}."""
+    dimensions are taken whole.  A tensor that is written shares no element with
+    any other of them (views beside each other in one tensor are fine, two
+    sets of caches exchanged within one call are not).  Returns {"states",
+    "status"}."""
     lib = load_library()
     states = list(states)
     if not states:

@@ -4,9 +4,12 @@
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
+#include <memory>
+#include <new>
 
 #include "../host_checks.hpp"
 #include "dspark.h"
+#include "regions.hpp"
 #include "reorder.hpp"
 #include "select.hpp"
 
@@ -49,14 +52,14 @@ void launch_select(const BeamArgs& a, int slice, hipStream_t s) {
                      beam_join_bytes(a.beams, a.slices, a.n_out, 8), s, a);
 }
 
-// the bytes that a state's layout spans; -1 where parts overlap
+// the bytes that a state's layout spans; -1 where parts overlap, or it is longer than any memory
 int64_t span(const int64_t (&size)[4], const int64_t (&stride)[4], int64_t row_bytes, bool apart) {
   int order[4] = {0, 1, 2, 3};
   std::sort(order, order + 4, [&](int a, int b) { return stride[a] < stride[b]; });
   int64_t reach = row_bytes;
   for (int i : order) {
     if (size[i] <= 1) continue;
-    if (stride[i] < 0 || (apart && stride[i] < reach)) return -1;
+    if (stride[i] < 0 || (apart && stride[i] < reach) || stride[i] > (int64_t(1) << 56) / size[i]) return -1;
     reach += stride[i] * (size[i] - 1);
   }
   return reach;
@@ -141,6 +144,14 @@ int dspark_beam_reorder(const dspark_state* states, int32_t n_states, int64_t re
   if (beams < 1 || beams > DSPARK_BEAM_MAX) return fail(DSPARK_EINVAL, "beams must be in [1, DSPARK_BEAM_MAX]");
   const bool in_place = states[0].in == states[0].out;
   int64_t least = INT64_MAX;
+  // what the states read and write
+  constexpr int kFew = 64;
+  Region few[kFew];
+  const int64_t pieces = requests > 0 ? (in_place ? 1 : 2) * (int64_t)n_states : 0;
+  std::unique_ptr<Region[]> many(pieces > kFew ? new (std::nothrow) Region[pieces] : nullptr);
+  Region* const region = pieces > kFew ? many.get() : few;
+  if (!region) return fail(DSPARK_EINVAL, "too many states for the host's memory");
+  int n_regions = 0;
   for (int i = 0; i < n_states; ++i) {
     const dspark_state& t = states[i];
     if (t.outer < 1 || t.rows < 0 || t.row_bytes < 1 || t.row_bytes > INT32_MAX || t.outer > (1 << 24) || t.rows > INT32_MAX ||
@@ -160,10 +171,13 @@ int dspark_beam_reorder(const dspark_state* states, int32_t n_states, int64_t re
       const char *x = static_cast<const char*>(t.in), *y = static_cast<const char*>(t.out);
       if (x < y + out_span && y < x + in_span) return fail(DSPARK_EINVAL, "a state's output overlaps its input");
     }
-    for (int j = 0; j < i; ++j)
-      if (requests > 0 && states[j].out == t.out) return fail(DSPARK_EINVAL, "a state is listed twice");
+    if (requests > 0) {
+      region[n_regions++] = region_of(t.out, size, out, t.row_bytes, i, true);
+      if (!in_place) region[n_regions++] = region_of(t.in, size, in, t.row_bytes, i, false);
+    }
     if (t.rows > 0) least = std::min(least, t.rows);
   }
+  if (any_meet(region, n_regions)) return fail(DSPARK_EINVAL, "a state overlaps another one that is written");
   if (requests == 0) return DSPARK_SUCCESS;
   if (!parent || !req_status) return fail(DSPARK_EINVAL, "NULL parent or req_status");
   // 16 bytes of every beam to a thread, fewer where that would be too many registers
