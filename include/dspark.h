@@ -583,14 +583,15 @@ int dspark_block_linear(const dspark_rows* x, const dspark_fp8* w, void* out, in
  * rounding wherever it decides.  parent, token, score, out_finished ([n_out]
  * a request): the candidate's beam in the request, its token, its score
  * rounded to binary32 (-inf below its range: the next step takes that slot as
- * empty), and whether it comes from an ended beam or its token is end_token; len[r] of them, behind which stand empty slots (parent -1, token
+ * empty), and whether it comes from an ended beam or its token is end_token;
+ * len[r] of them, behind which stand empty slots (parent -1, token
  * 0, score -inf, finished 0).  beams in [1, DSPARK_BEAM_MAX], n_out in [1,
  * DSPARK_BEAM_OUT_MAX], beams * n_out <= 4096, end_token in [-1, vocab) (-1:
  * none; finished must then be NULL).  req_status[r]: OK, ROW_NAN or
  * ROW_POSINF for a row that is read, or BAD_SCORE; a refused request has len 0
- * and empty slots.  The outputs lie apart from the inputs.  ws:
- * dspark_beam_select_workspace() bytes, 16-byte aligned; one for n rows serves
- * fewer rows as well. */
+ * and empty slots.  The outputs and the workspace lie apart from the inputs and
+ * from each other (others are refused).  ws: dspark_beam_select_workspace()
+ * bytes, 16-byte aligned; one for n rows serves fewer rows as well. */
 #define DSPARK_BEAM_MAX 64
 #define DSPARK_BEAM_OUT_MAX 128
 size_t dspark_beam_select_workspace(int64_t n_rows, int64_t vocab, int32_t n_out);

@@ -107,6 +107,14 @@ int dspark_beam_select(const dspark_rows* rows, const float* scores, const int32
   const BeamPlan p = beam_plan(rows->n_rows, rows->vocab, n_out);
   if (!aligned16(ws)) return fail(DSPARK_EALIGN, "workspace must be 16-byte aligned");
   if (!ws || ws_bytes < p.bytes) return fail(DSPARK_EWORKSPACE, "workspace smaller than dspark_beam_select_workspace()");
+  const int64_t requests = rows->n_rows / beams, all = requests * n_out * 4, es = rows->dtype == DSPARK_BF16 ? 2 : 4;
+  const int64_t row_count[4] = {rows->n_rows, 1, 1, 1}, row_step[4] = {rows->row_stride * es, 0, 0, 0};
+  Region region[] = {region_of(rows->data, row_count, row_step, rows->vocab * es, 0, false),
+                     piece_of(scores, rows->n_rows * 4, 1, false), piece_of(finished, rows->n_rows * 4, 2, false),
+                     piece_of(parent, all, 3, true), piece_of(token, all, 4, true), piece_of(score, all, 5, true),
+                     piece_of(out_finished, all, 6, true), piece_of(len, requests * 4, 7, true),
+                     piece_of(req_status, requests * 4, 8, true), piece_of(ws, (int64_t)p.bytes, 9, true)};
+  if (any_meet(region, sizeof region / sizeof *region)) return fail(DSPARK_EINVAL, "an output or the workspace overlaps an input or another output");
   BeamArgs a{};
   a.x.n = rows->n_rows;
   a.x.x = rows->data;
@@ -119,7 +127,7 @@ int dspark_beam_select(const dspark_rows* rows, const float* scores, const int32
   a.beams = beams;
   a.n_out = n_out;
   a.end_token = end_token;
-  a.requests = rows->n_rows / beams;
+  a.requests = requests;
   a.parent = parent;
   a.token = token;
   a.score = score;

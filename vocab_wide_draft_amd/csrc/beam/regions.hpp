@@ -53,6 +53,12 @@ inline Region region_of(const void* base, const int64_t (&size)[4], const int64_
   return r;
 }
 
+// one piece of memory (NULL: none)
+inline Region piece_of(const void* base, int64_t bytes, int state, bool written) {
+  constexpr int64_t one[4] = {1, 1, 1, 1}, none[4] = {0, 0, 0, 0};
+  return region_of(base, one, none, base ? bytes : 0, state, written);
+}
+
 // Whether two regions share a byte: whether whole numbers c_k in [lo_k, hi_k]
 // (differences of the two sides' indices along a stride) have a sum of c_k *
 // stride_k between first and last, the distances of the bases at which pieces
