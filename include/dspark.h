@@ -624,7 +624,8 @@ typedef struct {
  * 1 <= beams <= DSPARK_BEAM_MAX; all states are in place, or none.
  * req_status[r]: OK, BAD_PARENT (outside [-1, beams)) or BAD_LENGTH (outside
  * [0, the least `rows` of the states that have positions]); the states of a
- * refused request are left as they are. */
+ * refused request are left as they are.  parent, length and req_status lie apart
+ * from what is written (others are refused). */
 int dspark_beam_reorder(const dspark_state* states, int32_t n_states, int64_t requests, int32_t beams,
                         const int32_t* parent, const int32_t* length, int32_t* req_status, void* stream);
 

@@ -116,3 +116,20 @@ def test_against_sets_of_bytes(seed):
         assert (message is not None) == want
         met += want
     assert met > 20
+
+
+def test_parents_lengths_and_status():
+    """What the call reads of the requests, and the status that it writes, apart from the states and from each other."""
+    lib = B.load_library()
+
+    def refused(parent, length, status):
+        s = _plain(AT)
+        assert lib.dspark_beam_reorder(ctypes.byref(s), 1, R, Bm, parent, length, status, None) == -1
+        message = lib.dspark_last_error().decode()
+        assert "overlaps another" in message or message == "NULL parent or req_status"
+        return "overlaps" in message
+
+    far = AT + 4 * SIZE
+    assert refused(AT + 4, None, far) and refused(AT - 4, None, None) and refused(far, AT + SIZE - 4, far + 64)
+    assert refused(far, far + 64, AT + 8) and refused(far, None, far + 4 * R * Bm - 4) and refused(far, far + 64, far + 68)
+    assert not refused(None, far, far + 4 * R) and not refused(far, far + 4 * R * Bm, None)

@@ -152,14 +152,19 @@ int dspark_beam_reorder(const dspark_state* states, int32_t n_states, int64_t re
   if (beams < 1 || beams > DSPARK_BEAM_MAX) return fail(DSPARK_EINVAL, "beams must be in [1, DSPARK_BEAM_MAX]");
   const bool in_place = states[0].in == states[0].out;
   int64_t least = INT64_MAX;
-  // what the states read and write
+  // what the call reads and writes
   constexpr int kFew = 64;
   Region few[kFew];
-  const int64_t pieces = requests > 0 ? (in_place ? 1 : 2) * (int64_t)n_states : 0;
+  const int64_t pieces = (in_place ? 1 : 2) * (int64_t)n_states + 3;
   std::unique_ptr<Region[]> many(pieces > kFew ? new (std::nothrow) Region[pieces] : nullptr);
   Region* const region = pieces > kFew ? many.get() : few;
   if (!region) return fail(DSPARK_EINVAL, "too many states for the host's memory");
   int n_regions = 0;
+  if (requests > 0) {
+    region[n_regions++] = piece_of(parent, requests * beams * 4, -1, false);
+    region[n_regions++] = piece_of(length, requests * 4, -2, false);
+    region[n_regions++] = piece_of(req_status, requests * 4, -3, true);
+  }
   for (int i = 0; i < n_states; ++i) {
     const dspark_state& t = states[i];
     if (t.outer < 1 || t.rows < 0 || t.row_bytes < 1 || t.row_bytes > INT32_MAX || t.outer > (1 << 24) || t.rows > INT32_MAX ||
@@ -185,7 +190,7 @@ int dspark_beam_reorder(const dspark_state* states, int32_t n_states, int64_t re
     }
     if (t.rows > 0) least = std::min(least, t.rows);
   }
-  if (any_meet(region, n_regions)) return fail(DSPARK_EINVAL, "a state overlaps another one that is written");
+  if (any_meet(region, n_regions)) return fail(DSPARK_EINVAL, "a state, parent, length or req_status overlaps another one that is written");
   if (requests == 0) return DSPARK_SUCCESS;
   if (!parent || !req_status) return fail(DSPARK_EINVAL, "NULL parent or req_status");
   // 16 bytes of every beam to a thread, fewer where that would be too many registers
