@@ -265,6 +265,11 @@ int check_ws(size_t need, const void* ws, size_t ws_bytes) {
   return DSPARK_SUCCESS;
 }
 
+// whether a workspace of `bytes` bytes meets a matrix
+bool meets(const void* ws, size_t bytes, const dspark_fp8* q) {
+  return meet(ws, (int64_t)bytes, q->values, q->n_rows, q->cols, q->row_stride) || meet(ws, (int64_t)bytes, q->scales, 1, scale_bytes(q), 0);
+}
+
 }  // namespace
 }  // namespace dspark
 
@@ -311,8 +316,11 @@ int dspark_block_product(const dspark_fp8* x, const dspark_fp8* w, void* out, in
       meet(x->scales, scale_bytes(x), out, x->n_rows, w->n_rows * es, out_stride * es) ||
       meet(w->scales, scale_bytes(w), out, x->n_rows, w->n_rows * es, out_stride * es))
     return fail(DSPARK_EINVAL, "output rows overlap an input");
-  rc = check_ws(product_bytes(x->n_rows, w->n_rows, x->cols), ws, ws_bytes);
+  const size_t need = product_bytes(x->n_rows, w->n_rows, x->cols);
+  rc = check_ws(need, ws, ws_bytes);
   if (rc) return rc;
+  if (meets(ws, need, x) || meets(ws, need, w) || meet(ws, (int64_t)need, out, x->n_rows, w->n_rows * es, out_stride * es))
+    return fail(DSPARK_EINVAL, "the workspace overlaps an input or the output");
   product(x, 1, w, out, out_dtype, out_stride, ws, static_cast<hipStream_t>(stream));
   return host_check_launch();
 }
@@ -340,6 +348,9 @@ int dspark_block_linear(const dspark_rows* x, const dspark_fp8* w, void* out, in
   const LinearPlan p = linear_plan(x->n_rows, w->n_rows, x->vocab);
   rc = check_ws(p.bytes, ws, ws_bytes);
   if (rc) return rc;
+  if (meet(ws, (int64_t)p.bytes, x->data, 1, rows_bytes(x), 0) || meets(ws, p.bytes, w) ||
+      meet(ws, (int64_t)p.bytes, out, x->n_rows, w->n_rows * es, out_stride * es))
+    return fail(DSPARK_EINVAL, "the workspace overlaps an input or the output");
   char* at = static_cast<char*>(ws);
   // (its scales by blocks: a tile's rows lie next to each other)
   dspark_fp8 q{at, at + p.scales_at, w->scale_dtype, 1, x->n_rows, p.cols, p.cols, 1};
