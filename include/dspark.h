@@ -552,8 +552,9 @@ int dspark_quantize_blocks(const dspark_rows* x, const dspark_fp8* out, void* st
  * out_stride elements apart, 16-byte aligned, apart from the inputs; what lies
  * between rows is not written.  A row of x with a NaN gives NaN throughout,
  * which every later step refuses.  ws: dspark_block_product_workspace() bytes,
- * 16-byte aligned (NULL where it is 0), apart from the inputs and out; it is
- * free again when the call's work is done. */
+ * 16-byte aligned (NULL where it is 0), apart from the inputs and out; one for
+ * x_rows rows serves fewer rows as well, and it is free again when the call's
+ * work is done. */
 size_t dspark_block_product_workspace(int64_t x_rows, int64_t w_rows, int64_t cols);
 int dspark_block_product(const dspark_fp8* x, const dspark_fp8* w, void* out, int32_t out_dtype, int64_t out_stride,
                          void* ws, size_t ws_bytes, void* stream);

@@ -32,3 +32,12 @@ def test_onto_inputs_and_outputs():
         for start, bytes_ in own.items():
             for at in (start, (start + bytes_ - 1) // 16 * 16, (start - size) // 16 * 16 + 16):
                 assert "workspace overlaps" in _message(call, at), hex(at)
+
+
+def test_a_workspace_of_more_rows_serves_fewer():
+    lib = B.load_library()
+    rows = [*range(1, 700), *range(700, 6000, 29), 1 << 16, 1 << 24]
+    for N, K in ((150, 9000), (1, 1 << 20), (5120, 129280), (640, 1 << 20), (1000, 3000), (27489, 28027), (129280, 5120), (20003, 1000)):
+        for query in (lib.dspark_block_product_workspace, lib.dspark_block_linear_workspace):
+            sizes = [query(n, N, K) for n in rows]
+            assert sizes == sorted(sizes)

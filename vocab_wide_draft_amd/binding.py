@@ -849,6 +849,11 @@ def _product_out(n, V, out, out_dtype, dev):
     return out, DTYPE_F32 if out_dtype == torch.float32 else DTYPE_BF16, out.stride(0) if n > 1 else max(out.stride(0), V)
 
 
+@functools.lru_cache(maxsize=1024)
+def _head_workspace(call, n, V, cols):
+    return getattr(load_library(), f"dspark_{call}_workspace")(n, V, cols)
+
+
 def block_product(x, w, out_dtype=torch.bfloat16, out=None) -> torch.Tensor:
     """Logit rows [n, V] of quantised rows x (a scale for each row's blocks)
     and a quantised matrix w of V rows (a scale for blocks of 128 rows), both
@@ -857,7 +862,7 @@ def block_product(x, w, out_dtype=torch.bfloat16, out=None) -> torch.Tensor:
     dev = x["values"].device
     fx, fw = _fp8(x, "x", 1, dev), _fp8(w, "w", 128, dev)
     o, dt, stride = _product_out(fx.n_rows, fw.n_rows, out, out_dtype, dev)
-    nbytes = lib.dspark_block_product_workspace(fx.n_rows, fw.n_rows, fx.cols)
+    nbytes = _head_workspace("block_product", fx.n_rows, fw.n_rows, fx.cols)
     ws = torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
     _call(dev, lib.dspark_block_product, ctypes.byref(fx), ctypes.byref(fw), o.data_ptr(), dt, stride,
           ws.data_ptr() if nbytes else None, nbytes)
@@ -873,7 +878,7 @@ def block_linear(x: torch.Tensor, w, out_dtype=None, out=None) -> torch.Tensor:
     n, dev = x.shape[0], x.device
     fw = _fp8(w, "w", 128, dev)
     o, dt, stride = _product_out(n, fw.n_rows, out, out_dtype or (x.dtype if out is None else out.dtype), dev)
-    nbytes = lib.dspark_block_linear_workspace(n, fw.n_rows, x.shape[1])
+    nbytes = _head_workspace("block_linear", n, fw.n_rows, x.shape[1])
     ws = torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
     _call(dev, lib.dspark_block_linear, ctypes.byref(r), ctypes.byref(fw), o.data_ptr(), dt, stride,
           ws.data_ptr() if nbytes else None, nbytes)

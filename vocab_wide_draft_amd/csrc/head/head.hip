@@ -166,6 +166,24 @@ size_t product_bytes(int64_t M, int64_t N, int64_t K) {
   return std::max(product_plan(M, N, K, false).bytes, product_plan(M, N, K, true).bytes);
 }
 
+// The same for any number of rows up to M: where a long product has fewer
+// parts with more rows, fewer rows take more.  Among as many 64s of rows (which
+// is all that a plan's tiles and their cost hang on, but for the parts' way
+// through memory, which grows with the rows) the first has the most parts.
+size_t most_product_bytes(int64_t M, int64_t N, int64_t K) {
+  const int64_t steps = (K + kBlock - 1) / kBlock, tiles_n = (N + 255) / 256, row_bytes = up(N, 4) * 4;
+  size_t most = std::max({product_bytes(M, N, K), product_bytes(std::min<int64_t>(M, 16), N, K), product_bytes(std::min<int64_t>(M, 32), N, K)});
+  for (int64_t first = 33; first <= M; first = up(first, 64) + 1) {
+    const int64_t last = std::min(up(first, 64), M), tiles = (first + 255) / 256 * tiles_n;  // (of the largest tiles)
+    const int64_t parts = std::min<int64_t>({16, steps / 8, 1 + 1023 / tiles});
+    if (parts < 2) break;
+    if ((size_t)(parts * last * row_bytes) <= most) continue;
+    const int splits = std::max(product_plan(first, N, K, false).splits, product_plan(first, N, K, true).splits);
+    if (splits > 1) most = std::max(most, (size_t)(splits * last * row_bytes));
+  }
+  return most;
+}
+
 template <int ST, bool WIDE, int OUT, int U>
 void launch_tile(const ProductArgs& a, hipStream_t s) {
   hipLaunchKernelGGL(HIP_KERNEL_NAME(product_tile_kernel<U, ST, WIDE, OUT>), grid_of(a.tiles_m * a.tiles_n * a.splits),
@@ -295,7 +313,7 @@ int dspark_quantize_blocks(const dspark_rows* x, const dspark_fp8* out, void* st
 }
 
 size_t dspark_block_product_workspace(int64_t x_rows, int64_t w_rows, int64_t cols) {
-  return product_sizes(x_rows, w_rows, cols) ? product_bytes(x_rows, w_rows, up(cols, 16)) : 0;
+  return product_sizes(x_rows, w_rows, cols) ? most_product_bytes(x_rows, w_rows, up(cols, 16)) : 0;
 }
 
 int dspark_block_product(const dspark_fp8* x, const dspark_fp8* w, void* out, int32_t out_dtype, int64_t out_stride,
@@ -326,7 +344,7 @@ int dspark_block_product(const dspark_fp8* x, const dspark_fp8* w, void* out, in
 }
 
 size_t dspark_block_linear_workspace(int64_t x_rows, int64_t w_rows, int64_t cols) {
-  return product_sizes(x_rows, w_rows, cols) ? linear_plan(x_rows, w_rows, cols).bytes : 0;
+  return product_sizes(x_rows, w_rows, cols) ? linear_plan(x_rows, w_rows, cols).ws_at + most_product_bytes(x_rows, w_rows, up(cols, 16)) : 0;
 }
 
 int dspark_block_linear(const dspark_rows* x, const dspark_fp8* w, void* out, int32_t out_dtype, int64_t out_stride,
