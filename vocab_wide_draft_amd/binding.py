@@ -1026,7 +1026,7 @@ def beam_reorder(states, parent: torch.Tensor, length=None, *, axis: int = 2, ou
         raise ValueError("axis counts from the dimensions after requests and beams: 2 or more")
     if len(into) != len(states):
         raise ValueError("out must be as many tensors as states")
-    laid = []  # State records, field by field
+    laid, fewest = [], None  # State records, field by field; the positions of those that hold nothing
     for x, y in zip(states, into):
         size = x.shape
         if len(size) < 2 or size[0] != R or size[1] != beams or x.device != dev:
@@ -1041,9 +1041,17 @@ def beam_reorder(states, parent: torch.Tensor, length=None, *, axis: int = 2, ou
             to = _layout(size, y.stride(), es, axis)[0]
         if x.numel():
             laid += (x.data_ptr(), y.data_ptr(), *strides, *to, *counts)
+        elif len(size) > axis:
+            fewest = size[axis] if fewest is None else min(fewest, size[axis])
     st = _i32(R, dev)
-    if not laid:
+    if not parent.numel():
         return {"states": into, "status": st.zero_()}
+    if fewest is not None and length is not None:  # (the library does not see those states: their limit is put into the lengths)
+        length = torch.where(length <= fewest, length, -1)
+    if not laid:  # parents and lengths are still checked, with a byte for each beam in the states' place
+        nothing = torch.empty((R, beams), dtype=torch.uint8, device=dev)
+        strides, counts = _layout(nothing.shape, nothing.stride(), 1, axis)
+        laid += (nothing.data_ptr(), nothing.data_ptr(), *strides, *strides, *counts)
     _call(dev, lib.dspark_beam_reorder, struct.pack(f"{len(laid)}q", *laid), len(laid) // 13, R, beams,
           _arg(parent, "parent", torch.int32, (R, beams), dev), _arg(length, "length", torch.int32, (R,), dev), st.data_ptr())
     torch.autograd.graph.increment_version(into)  # (as _written does)
