@@ -810,7 +810,8 @@ def quantize_blocks(x: torch.Tensor, block_rows: int = 1, scale_dtype=torch.floa
     """Rows x [n, width] in e4m3 with a scale for each 128 columns of
     block_rows (1 or 128) rows (see dspark_quantize_blocks): {"values"
     float8_e4m3fn [n, width rounded up to a multiple of 16], "scales"}.
-    scale_dtype: float32, or float8_e8m0fnu for powers of two."""
+    scale_dtype: float32, or float8_e8m0fnu for powers of two.  No gradient
+    flows through it."""
     lib = load_library()
     r = _rows(x)
     if block_rows not in (1, 128):
@@ -857,7 +858,8 @@ def _head_workspace(call, n, V, cols):
 def block_product(x, w, out_dtype=torch.bfloat16, out=None) -> torch.Tensor:
     """Logit rows [n, V] of quantised rows x (a scale for each row's blocks)
     and a quantised matrix w of V rows (a scale for blocks of 128 rows), both
-    with scales of one type (see dspark_block_product).  out: rows to write."""
+    with scales of one type (see dspark_block_product).  out: rows to write.
+    No gradient flows through it."""
     lib = load_library()
     dev = x["values"].device
     fx, fw = _fp8(x, "x", 1, dev), _fp8(w, "w", 128, dev)
@@ -872,7 +874,9 @@ def block_product(x, w, out_dtype=torch.bfloat16, out=None) -> torch.Tensor:
 
 def block_linear(x: torch.Tensor, w, out_dtype=None, out=None) -> torch.Tensor:
     """The same from rows x [n, width] in float32 or bf16, quantised on the
-    way (see dspark_block_linear); out_dtype: x's type by default."""
+    way (see dspark_block_linear); out_dtype: x's type by default.  No gradient
+    flows through it, whatever x requires: head_logits is the differentiable
+    form."""
     lib = load_library()
     r = _rows(x)
     n, dev = x.shape[0], x.device
@@ -925,9 +929,12 @@ def head_logits(x: torch.Tensor, head, out_dtype=None) -> torch.Tensor:
     16-byte aligned) and a head {"weight": a quantised matrix [V, width],
     "transposed": transpose_blocks(weight, width)}, a differentiable function
     of x: the logits' gradient is quantised in blocks of 128 tokens, as x is in
-    blocks of 128 channels, and multiplied with the transposed head.  The head
-    is constant; without a gradient "transposed" is not needed.  There is no
-    forward-mode derivative, nor a second one."""
+    blocks of 128 channels, and multiplied with the transposed head.  (An entry
+    below a 460,000th of its block's largest, a label's, say, becomes zero: see
+    dspark_block_linear.)  The head is constant; without a gradient "transposed"
+    is not needed.  There is no forward-mode derivative, nor a second one.  It
+    may be captured into a graph with its backward pass, while no eager graph of
+    the same leaves is alive."""
     w, t, grad = head["weight"], head.get("transposed"), torch.is_grad_enabled()
     if getattr(forward_ad, "_current_level", 0) >= 0:  # (without a dual level there is none: not looked for, 3 us less)
         _no_tangents(x, w, t)
