@@ -8,7 +8,11 @@
 // what a slot keeps is neither read nor written.  Memory bounds it: 32 requests
 // of eight beams, four states of up to 2,048 positions of 2 KB, move 5.07 GB
 // into other states in 1,070 us (4.7 TB/s, a copy's rate), 2.34 GB in place in
-// 460 us; with one vector a thread 1,590 and 970 us.
+// 460 us; with one vector a thread 1,590 and 970 us.  More beams leave fewer waves
+// a SIMD (registers for a vector of each), and from 17 beams on vectors of 8 or 4
+// bytes: two states of 2,048 positions of 2 KB, 256 beams in all, in place / into
+// others, TB/s: 4 beams a request 5.7 / 5.3, 8 5.2 / 4.8, 12 4.0 / 4.3, 16 4.3 / 4.1,
+// 32 4.5 / 3.9, 64 3.7 / 4.2.
 #pragma once
 #include "../logits/slices.hpp"
 

@@ -116,11 +116,17 @@ ProductPlan product_plan(int64_t M, int64_t N, int64_t K, bool wide) {
   const int64_t tiles_n = (N + 255) / 256;
   // Few rows go straight from memory while w is short, and through LDS (whole
   // lines of w at a time) where bandwidth counts, unless tiles do as well;
-  // direct / staged / tiles, float scales, bf16 results, w out of the caches, us:
-  // 20 MB of w, 1 row 8.7 / 11.8, 32 rows 11.9 / 18 / 14, 48 rows 16.3 / 20 / 14;
-  // 60 MB 16.4 / 19.5, 22 / 28 / 24, 28 / 32 / 24; 102 MB 25 / 25, 31 / 33 / 27;
-  // 131 MB 33 / 32, 40 / 38 / 32; 205 MB 56 / 50, 70 / 51 / 51; 662 MB 129 / 115,
-  // 186 / 121 / 124.  float32 results, 662 MB, 32 rows: staged 130, tiles 165.
+  // direct / staged / tiles, float scales, bf16 results, w out of the caches, us of
+  // a call: 20,003 x 1,008 (20 MB), 1 row 8.4 / 11.6 / 12.6, 32 rows 11.7 / 16.3 /
+  // 13.5; 60,000 x 1,008 15.7 / 18.3 / 15.7, 21 / 27 / 17; 102,000 x 1,008 24 / 26 /
+  // 28, 33 / 31 / 30; 129,280 x 1,024 (132 MB) 27 / 27 / 28, 37 / 30 / 30; 40,000 x
+  // 5,120 (205 MB) 49 / 41 / 43, 69 / 51 / 49; 129,280 x 5,120 128 / 113 / 113,
+  // 184 / 122 / 121.  Longer rows would have the border lower than the bytes do:
+  // 4,000 x 5,120 11.3 / 12.9 / 13.4, 14.4 / 17.0 / 15.7; 12,000 x 5,120 20 / 18 / 17,
+  // 28 / 24 / 19; 20,000 x 5,120 (102 MB) 32 / 25 / 24, 46 / 32 / 27.  float32 results
+  // of 17 rows and more stay staged, as tiles have the slower instruction: 32 rows of
+  // 129,280 x 1,024 33.7 / 36.4 (staged / tiles), 40,000 x 5,120 52 / 56, 129,280 x
+  // 5,120 130 / 144.
   const int64_t bytes = N * K;
   const bool direct = M <= 32 && bytes <= 112 << 20;
   if (direct || M <= 16 || (M <= 32 && (wide || bytes > 300 << 20))) {
@@ -136,9 +142,15 @@ ProductPlan product_plan(int64_t M, int64_t N, int64_t K, bool wide) {
     // 64 u rows 0.38 + 0.28 u us, and 0.86 us for its columns of w out of memory
     // shared by the tiles that read them; three steps for a tile's beginning and
     // end; the parts' way through memory.  (129,280 x 5,120, powers of two, us for
-    // u = 1, 2, 3, 4: 64 rows 133, 138, 153, 168; 128: 195, 152, 150, 176; 256:
-    // 308, 230, 255, 206; 384: 405, 308, 264, 304; 768: 741, 538, 508, 439; 5,120:
-    // 4,500, 3,190, 2,870, 2,560.)
+    // u = 1, 2, 3, 4, the last tile as narrow as what is left: 64 rows 129, 127, 127,
+    // 127; 128: 184, 144, 144, 144; 256: 304, 223, 223, 194; 384: 400, 306, 262, 276;
+    // 768: 753, 547, 482, 447; 5,120: 4,623, 3,315, 3,021, 2,700.)  The constants are
+    // fitted to these.  Float scales, and float32 results with twice the time of
+    // matrix instructions, order the choices alike (float scales, u = 1, 2, 3, 4: 384
+    // rows 443, 339, 298, 308; 5,120 5,280, 3,906, 3,486, 3,191; float32 results, u =
+    // 1, 2: 64 rows 149, 152; 128: 259, 203; 384: 701, 532; 5,120: 8,870, 6,528; a
+    // gradient, 384 rows x 5,120 x 129,280, u = 2 in 4, 6, 8, 12, 16 parts 543, 623,
+    // 530, 546, 539, the rule's 518): its choice is within 3 % of the best of those.
     p.way = kTiles;
     double best = 0.0;
     for (int u = wide ? 2 : 4; u >= 1; --u) {

@@ -65,6 +65,9 @@ __device__ __forceinline__ v8b widen(int lo, int hi) {
 
 // The same, not waited for by what reads LDS afterwards (the compiler waits
 // for every load into an array before any read of it): loads_but() does.
+// (m0 is named as written, so that nothing else is taken to be there; the compiler
+// warns that it does not restore such a register, which nobody needs: no other
+// instruction of the kernels that use this reads it.)
 template <int BYTES>
 __device__ __forceinline__ void load_lds_ahead(v4i from, uint32_t to, int offset) {
   static_assert(BYTES == 16 || BYTES == 4 || BYTES == 1, "of a lane (a byte becomes a word)");
@@ -410,8 +413,9 @@ __global__ void __launch_bounds__(256) product_direct_kernel(ProductArgs a) {
 // w), at 192 rows those of w alone, that of x one (192 rows, powers of two, 172
 // -> 159 us, 384 rows 282 -> 257; with scales of their own 177 and 292 either
 // way, 576 rows 410 -> 427, so those have two).  The largest tiles are bound by
-// power: with 65 % of the matrix cores' cycles in use the clock falls from 2.4
-// to 1.9 GHz (2.56 ms, 2,645 TFLOP/s; 2.22 ms at 2.2 GHz without the fetches).
+// power: with 64 % of the matrix cores' cycles in use the clock falls from 2.4
+// to 1.9 GHz (2.62 to 2.72 ms from one card to another, 2,490 to 2,590 TFLOP/s;
+// without the fetches, on a card where they take 2.56 ms, 2.22 ms at 2.2 GHz).
 // A second barrier a step, which gives a fetch more time, costs more than it
 // gives there (2,867 us).
 template <int U, int ST>
