@@ -41,3 +41,12 @@ def test_a_workspace_of_more_rows_serves_fewer():
         for query in (lib.dspark_block_product_workspace, lib.dspark_block_linear_workspace):
             sizes = [query(n, N, K) for n in rows]
             assert sizes == sorted(sizes)
+
+
+def test_a_workspace_of_a_few_dozen_rows_serves_fewer():
+    """Lengths of w for which 17 to 32 rows, too, are taken in tiles."""
+    lib = B.load_library()
+    for N, K in ((98253, 3120), (1000, 125000), (640, 300000), (12000, 20000), (40000, 5120), (300, 1 << 19), (2000, 150000)):
+        for query in (lib.dspark_block_product_workspace, lib.dspark_block_linear_workspace):
+            sizes = [query(n, N, K) for n in range(1, 130)]
+            assert sizes == sorted(sizes)

@@ -1051,7 +1051,7 @@ def beam_reorder(states, parent: torch.Tensor, length=None, *, axis: int = 2, ou
         elif len(size) > axis:
             fewest = size[axis] if fewest is None else min(fewest, size[axis])
     st = _i32(R, dev)
-    if not parent.numel():
+    if not (R and beams):
         return {"states": into, "status": st.zero_()}
     if fewest is not None and length is not None:  # (the library does not see those states: their limit is put into the lengths)
         length = torch.where(length <= fewest, length, -1)

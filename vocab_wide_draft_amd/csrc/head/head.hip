@@ -185,10 +185,12 @@ size_t product_bytes(int64_t M, int64_t N, int64_t K) {
 size_t most_product_bytes(int64_t M, int64_t N, int64_t K) {
   const int64_t steps = (K + kBlock - 1) / kBlock, tiles_n = (N + 255) / 256, row_bytes = up(N, 4) * 4;
   size_t most = std::max({product_bytes(M, N, K), product_bytes(std::min<int64_t>(M, 16), N, K), product_bytes(std::min<int64_t>(M, 32), N, K)});
-  for (int64_t first = 33; first <= M; first = up(first, 64) + 1) {
-    const int64_t last = std::min(up(first, 64), M), tiles = (first + 255) / 256 * tiles_n;  // (of the largest tiles)
+  int64_t last = 0;
+  for (int64_t first = 17; first <= M; first = last + 1) {
+    last = std::min(first == 17 ? 32 : up(first, 64), M);  // (17 to 32 rows: tiles only for some lengths of w)
+    const int64_t tiles = (first + 255) / 256 * tiles_n;  // (of the largest ones)
     const int64_t parts = std::min<int64_t>({16, steps / 8, 1 + 1023 / tiles});
-    if (parts < 2) break;
+    if (parts < 2 && first > 17) break;
     if ((size_t)(parts * last * row_bytes) <= most) continue;
     const int splits = std::max(product_plan(first, N, K, false).splits, product_plan(first, N, K, true).splits);
     if (splits > 1) most = std::max(most, (size_t)(splits * last * row_bytes));
