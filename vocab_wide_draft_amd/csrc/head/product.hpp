@@ -414,7 +414,7 @@ __global__ void __launch_bounds__(256) product_direct_kernel(ProductArgs a) {
 // -> 159 us, 384 rows 282 -> 257; with scales of their own 177 and 292 either
 // way, 576 rows 410 -> 427, so those have two).  The largest tiles are bound by
 // power: with 64 % of the matrix cores' cycles in use the clock falls from 2.4
-// to 1.9 GHz (2.62 to 2.72 ms from one card to another, 2,490 to 2,590 TFLOP/s;
+// to 1.9 GHz (2.62 to 2.76 ms from one card to another, 2,460 to 2,590 TFLOP/s;
 // without the fetches, on a card where they take 2.56 ms, 2.22 ms at 2.2 GHz).
 // A second barrier a step, which gives a fetch more time, costs more than it
 // gives there (2,867 us).
